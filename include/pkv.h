@@ -157,7 +157,7 @@ PKV_API int pkv_pool_wrap(const pkv_config* cfg, int num_pages, void* k, void* v
  * finish using it.  NULL is accepted and ignored. */
 PKV_API int pkv_pool_free(pkv_pool* pool);
 
-/* The pool's K and V device pointers and its number of slots
+/* The pool's K and V device pointers (null for a 4-bit pool) and its number of slots
  * (num_pages * page_size).  Any output pointer may be NULL. */
 PKV_API int pkv_pool_kv(const pkv_pool* pool, void** k, void** v, int64_t* num_slots);
 
@@ -378,6 +378,141 @@ PKV_API int pkv_decode_static(pkv_pool* pool, const void* q, const void* k, cons
                               const void* k_norm_w, const int32_t* positions, const int32_t* table, int rows,
                               int pages, void* out, void* stream);
 
+/* ---- a page pool in 4 bits -----------------------------------------------------------------
+ * The pool of decode_paged (README.md, Entries) with K and V quantised as they are
+ * written: 72 bytes a head vector instead of 256, so that a decode step reads 0.28 of
+ * the bytes and the same memory holds 3.5 times the context.
+ *
+ * Values.  Each head vector of 128 dims is 8 groups of 16 consecutive dims; a value is
+ *   code * scale * s
+ * with code one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives (4 bits: sign, two
+ * exponent bits, one mantissa bit), scale the group's in 8 bits (e4m3) and s the pool's
+ * k_scale or v_scale.  For the values x of a group -- the bf16 values a bf16 pool would
+ * hold: k after QK-norm and RoPE rounded to bf16, v as given --
+ *   scale = e4m3(max |x| / (6 s)),   code = e2m1(x / (scale s)),
+ * each rounded to nearest, ties to even, scale at most 448; a group whose scale rounds to
+ * 0 is 0.  A group holding an Inf or a NaN is stored as NaN.  k_scale and v_scale are
+ * powers of two from 2^-60 to 2^60 (they move the range of the scales, 2^-9 .. 448, to
+ * that of the data; 1 suits values of order 0.01 to 1000).
+ *
+ * Layout.  uint8 [num_pages][kv_heads][9216]: page_size positions in 4 blocks of 16, a
+ * block's 2304 bytes being K codes [16][64], V codes [16][64], K scales [128], V scales
+ * [128].  With b = (i >> 2) & 1 and c = (i & 3) ^ b for position i of a block, dims 2j
+ * (low half) and 2j + 1 of it are byte 64 i + (j ^ (32 * ((i >> 1) & 1))) of the codes, its
+ * K scale of group g is byte 16 (2c + b) + 4 (g >> 1) + (g & 1) + 2 (i >> 3) and its V scale
+ * byte 16 g + 4 c + b + 2 (i >> 3) of the scales.
+ *
+ * A 4-bit pool is a pkv_pool: pkv_pool_free, pkv_check_errors, pkv_set_ctas,
+ * pkv_set_wait_limit, the kernel timer, pkv_linear, pkv_qkv_proj, pkv_output_gate,
+ * pkv_norm_rope and pkv_pool_set_rope take it as any other; pkv_pool_kv gives null k and
+ * v; pkv_workspace_bytes gives what pkv_q4_decode needs (PKV_ENOTIMPL for
+ * prefill_tokens > 0).  The entries that read or write a bf16 pool (pkv_decode,
+ * pkv_decode_static, pkv_step, pkv_prefill, pkv_qkv_proj_append, pkv_decode_appended)
+ * return PKV_EINVAL for it, and the pkv_q4 entries do so for a bf16 pool.
+ *
+ * A prompt: pkv_prefill over a bf16 pool of scratch pages, then pkv_q4_append of the same
+ * k and v; before a later chunk of it, pkv_q4_read brings the row's prefix back to the
+ * scratch pages.
+ *
+ * pkv_q4_pool_bytes: bytes of a pool's pages.  pkv_q4_pool_alloc / pkv_q4_pool_wrap: as
+ * pkv_pool_alloc (zeroed pages) and pkv_pool_wrap (caller's pages, 256-byte aligned), with
+ * PKV_EINVAL also for a scale that is not such a power of two.  pkv_q4_pool_data: the
+ * pages' device pointer and bytes (either output may be NULL). */
+PKV_API int pkv_q4_pool_bytes(const pkv_config* cfg, int num_pages, size_t* bytes);
+PKV_API int pkv_q4_pool_alloc(const pkv_config* cfg, int num_pages, float k_scale, float v_scale, void* stream,
+                              pkv_pool** out);
+PKV_API int pkv_q4_pool_wrap(const pkv_config* cfg, int num_pages, void* data, float k_scale, float v_scale,
+                             void* stream, pkv_pool** out);
+PKV_API int pkv_q4_pool_data(const pkv_pool* pool, void** data, size_t* bytes);
+
+/* Quantise k and v into the pool as they are written, for `tokens` tokens of any rows
+ * (prompt chunks packed end to end, or one token per row): token t sits at position
+ * positions[t] of table row prow[t] and is written at
+ *   slot = table[prow[t]][positions[t] / page_size] * page_size + positions[t] % page_size.
+ * k is QK-normed and roped first (as pkv_decode does), v is quantised as given.
+ *   k, v       device bf16 [tokens][kv_heads][head_dim], 16-byte aligned
+ *   k_norm_w   device bf16 [head_dim]
+ *   positions  device int32 [tokens]; -1 = nothing to write
+ *   prow       device int32 [tokens], or NULL: token t is row t (rows >= tokens)
+ *   table      device int32 [rows][pages], or NULL: contiguous rows
+ * Slots must be distinct (PKV_CHECK=1 checks).  Only the written positions change.
+ * Tokens with a bad row, position or page are skipped and set their error bit.
+ * rows * pages < 2^30 here and in the two calls below (PKV_ERANGE). */
+PKV_API int pkv_q4_append(pkv_pool* pool, const void* k, const void* v, const void* k_norm_w,
+                          const int32_t* positions, const int32_t* prow, const int32_t* table, int tokens, int rows,
+                          int pages, void* stream);
+
+/* Read cached k and v back: the values that position positions[t] of row prow[t] holds,
+ * for `tokens` tokens, as bf16 (exact while in bf16's range).  Element (t, kv head g, dim d)
+ * goes to k[t * token_stride + g * head_stride + d] and the same of v; strides in elements.
+ * [tokens][kv_heads][128] is (kv_heads * 128, 128); a bf16 pool's contiguous slots from slot s
+ * on are k = K + s * 128 with (128, num_slots * 128).
+ *   positions, prow, table as pkv_q4_append; position -1 gives zeros, a bad row, position or
+ *   page gives zeros and sets its error bit
+ *   k, v  device bf16, 16-byte aligned, strides multiples of 8 (PKV_EINVAL); vectors must not overlap */
+PKV_API int pkv_q4_read(pkv_pool* pool, const int32_t* positions, const int32_t* prow, const int32_t* table,
+                        int tokens, int rows, int pages, void* k, void* v, int64_t token_stride, int64_t head_stride,
+                        void* stream);
+
+/* decode_paged over a 4-bit pool: pkv_decode's steps, with k and v quantised as they are
+ * appended and the attention over the values the pool holds (the new position's own
+ * quantised values included).  Arguments, skipped rows and error bits as pkv_decode, out
+ * 16-byte aligned; all writes of the call happen before any attention, so rows may read
+ * each other's new slots.  Results are the same from run to run. */
+PKV_API int pkv_q4_decode(pkv_pool* pool, const void* q, const void* k, const void* v, const void* q_norm_w,
+                          const void* k_norm_w, const int32_t* positions, const int32_t* table, int rows, int pages,
+                          void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- QK-norm and RoPE of a batch of tokens, and the rotation's frequencies ----------------------
+ * qwen3-8b Nest files, src/norm.linnet (RmsNorm), src/rope.linnet (tables): the per-head
+ * norm and the rotation of q and k in one pass, without an attention,
+ *   y = rope(x / sqrt(mean(x^2) + eps) * w),
+ * computed in fp32 and rounded once to the output's type.
+ *   q, k       device bf16, heads of 128 contiguous elements; q_stride, k_stride: elements
+ *              between tokens (>= heads * 128, kv_heads * 128; a multiple of 4), so that both may
+ *              lie in one row of a projection.  Either may be NULL, with its output.
+ *   q_norm_w, k_norm_w  device bf16 [head_dim], or NULL: no norm, only the rotation
+ *   positions  device int32 [tokens]; -1 gives zeros, another value outside [0, max_seq)
+ *              gives zeros and sets PKV_DEVERR_POSITION
+ *   layout     PKV_ROPE_HALF: pairs (i, i + R/2), the layout of every other entry;
+ *              PKV_ROPE_INTERLEAVED: pairs (2i, 2i + 1); R = rotary_dim, dims from R on unrotated
+ *   out_type   PKV_BF16 or PKV_F32 (fp32 q with q_out_stride heads * 128 is pkv_decode_appended's q_hat)
+ *   q_out, k_out  device, strides as the inputs', in elements.  An output may be its own input
+ *              (PKV_BF16, same stride); otherwise outputs must not overlap inputs.
+ * Pointers 8-byte aligned, fp32 outputs 16. */
+#define PKV_ROPE_HALF 0
+#define PKV_ROPE_INTERLEAVED 1
+#define PKV_BF16 0
+#define PKV_F32 1
+PKV_API int pkv_norm_rope(pkv_pool* pool, const void* q, const void* k, const void* q_norm_w, const void* k_norm_w,
+                          const int32_t* positions, int tokens, int layout, int out_type, int64_t q_stride,
+                          int64_t k_stride, void* q_out, void* k_out, int64_t q_out_stride, int64_t k_out_stride,
+                          void* stream);
+
+/* Frequencies for contexts `factor` (>= 1) times the trained one.  Host only: fills
+ * inv_freq[R/2] (R = rotary_dim) and the factor on cos and sin.  f_i = theta^(-2i/R):
+ *   PKV_ROPE_NONE    f_i
+ *   PKV_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   PKV_ROPE_BASE    theta * factor^(R/(R-2)) in theta's place: the slowest pair is divided by factor
+ *   PKV_ROPE_RAMP    f_i where the pair turns 32 times or more over the `trained` positions,
+ *                    f_i / factor where it turns once or less, a linear ramp over the pair's index
+ *                    between (its ends rounded outwards); *mscale = 0.1 ln(factor) + 1
+ * *mscale = 1 but for the ramp.  Errors: PKV_EINVAL (null, unknown scaling, factor < 1 or not
+ * finite, trained <= 0 for the ramp), and pkv_pool_alloc's for the config. */
+#define PKV_ROPE_NONE 0
+#define PKV_ROPE_LINEAR 1
+#define PKV_ROPE_BASE 2
+#define PKV_ROPE_RAMP 3
+PKV_API int pkv_rope_frequencies(const pkv_config* cfg, int scaling, double factor, int trained, double* inv_freq,
+                                 double* mscale);
+
+/* Replace the pool's RoPE tables: pair i turns by position * inv_freq[i] (host, rotary_dim/2 of
+ * them, >= 0 and finite) and cos and sin are multiplied by mscale (> 0).  Every entry of this
+ * pool uses them from then on; what the pool already holds is not rotated again.  Waits for the
+ * device's work and is not for a stream under capture (PKV_EINVAL).  Errors: PKV_EINVAL,
+ * PKV_EDEVICE, PKV_ENOMEM, PKV_ECUDA. */
+PKV_API int pkv_pool_set_rope(pkv_pool* pool, const double* inv_freq, double mscale, void* stream);
+
 /* ---- errors ------------------------------------------------------------------------------
  * Synchronise `stream`, then read and clear the pool's sticky device error
  * word (PKV_DEVERR_* bits of every call since the last read) into *flags.
@@ -413,6 +548,7 @@ PKV_API int pkv_set_wait_limit(pkv_pool* pool, int64_t ns);
  * returns the summed duration in milliseconds and the number of timed
  * launches since the timer was last enabled, and keeps the timer running.
  * At most 4096 launches are kept (later ones overwrite the oldest).
+ * pkv_q4_decode is timed as pkv_decode is.
  * enable: 0 off, 1 every launch named above, 2 the attention launches only
  * (not pkv_linear / pkv_qkv_proj / pkv_qkv_proj_append); PKV_EINVAL otherwise.  Host
  * threads sharing a pool take distinct event slots; pkv_timer_enable and

@@ -11,6 +11,7 @@ PyTorch provides device memory and streams only.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -28,7 +29,12 @@ ABI_SYMBOLS = ("pkv_config_default", "pkv_strerror", "pkv_pool_alloc", "pkv_pool
                "pkv_pool_kv", "pkv_workspace_bytes", "pkv_decode", "pkv_step", "pkv_prefill", "pkv_check_errors",
                "pkv_set_ctas", "pkv_set_wait_limit", "pkv_timer_enable", "pkv_timer_read", "pkv_decode_static",
                "pkv_linear_workspace_bytes", "pkv_linear", "pkv_qkv_proj", "pkv_qkv_proj_append",
-               "pkv_decode_appended", "pkv_output_gate")
+               "pkv_decode_appended", "pkv_output_gate", "pkv_q4_pool_bytes", "pkv_q4_pool_alloc", "pkv_q4_pool_wrap",
+               "pkv_q4_pool_data", "pkv_q4_append", "pkv_q4_read", "pkv_q4_decode", "pkv_norm_rope",
+               "pkv_rope_frequencies", "pkv_pool_set_rope")
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}                  # PKV_ROPE_HALF, PKV_ROPE_INTERLEAVED
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}  # PKV_ROPE_NONE ...
 
 # Size of the scratch array pkv_decode_static uses in place of a workspace.
 PKV_STATIC_SCRATCH_BYTES = 32 << 20
@@ -86,6 +92,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "pkv_qkv_proj_append": ([vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, vp, vp], i32),
         "pkv_decode_appended": ([vp, vp, vp, vp, i32, i32, vp, vp, sz, vp], i32),
         "pkv_output_gate": ([vp, vp, vp, i32, vp], i32),
+        "pkv_q4_pool_bytes": ([cfgp, i32, ctypes.POINTER(sz)], i32),
+        "pkv_q4_pool_alloc": ([cfgp, i32, ctypes.c_float, ctypes.c_float, vp, ctypes.POINTER(vp)], i32),
+        "pkv_q4_pool_wrap": ([cfgp, i32, vp, ctypes.c_float, ctypes.c_float, vp, ctypes.POINTER(vp)], i32),
+        "pkv_q4_pool_data": ([vp, ctypes.POINTER(vp), ctypes.POINTER(sz)], i32),
+        "pkv_q4_append": ([vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp], i32),
+        "pkv_q4_read": ([vp, vp, vp, vp, i32, i32, i32, vp, vp, i64, i64, vp], i32),
+        "pkv_q4_decode": ([vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, vp, sz, vp], i32),
+        "pkv_norm_rope": ([vp, vp, vp, vp, vp, vp, i32, i32, i32, i64, i64, vp, vp, i64, i64, vp], i32),
+        "pkv_rope_frequencies": ([cfgp, i32, ctypes.c_double, i32, ctypes.POINTER(ctypes.c_double),
+                                  ctypes.POINTER(ctypes.c_double)], i32),
+        "pkv_pool_set_rope": ([vp, ctypes.POINTER(ctypes.c_double), ctypes.c_double, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -106,6 +123,11 @@ def _stream(stream) -> ctypes.c_void_p:
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
+
+
+def _on(stream):
+    """Allocations inside are ordered on `stream` (a torch stream; anything else: the current stream)."""
+    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
 
 
 def _dev(t: torch.Tensor | None, dtype: torch.dtype, what: str, allow_none: bool = False) -> ctypes.c_void_p:
@@ -304,6 +326,129 @@ def pkv_output_gate(pool, out, gate, stream=None) -> None:
                                           int(out.shape[0]), _stream(stream)), "pkv_output_gate")
 
 
+# ---- 4-bit pools
+
+def pkv_q4_pool_bytes(cfg, num_pages: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().pkv_q4_pool_bytes(ctypes.byref(_cfg(cfg)), int(num_pages), ctypes.byref(n)),
+           "pkv_q4_pool_bytes")
+    return n.value
+
+
+def pkv_q4_pool_alloc(cfg, num_pages: int, k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> ctypes.c_void_p:
+    out = ctypes.c_void_p()
+    _check(load_library().pkv_q4_pool_alloc(ctypes.byref(_cfg(cfg)), int(num_pages), float(k_scale), float(v_scale),
+                                            _stream(stream), ctypes.byref(out)), "pkv_q4_pool_alloc")
+    return out
+
+
+def pkv_q4_pool_wrap(cfg, num_pages: int, data: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0,
+                     stream=None) -> ctypes.c_void_p:
+    out = ctypes.c_void_p()
+    _check(load_library().pkv_q4_pool_wrap(ctypes.byref(_cfg(cfg)), int(num_pages), _dev(data, torch.uint8, "data"),
+                                           float(k_scale), float(v_scale), _stream(stream), ctypes.byref(out)),
+           "pkv_q4_pool_wrap")
+    return out
+
+
+def pkv_q4_pool_data(pool):
+    p, n = ctypes.c_void_p(), ctypes.c_size_t()
+    _check(load_library().pkv_q4_pool_data(pool, ctypes.byref(p), ctypes.byref(n)), "pkv_q4_pool_data")
+    return p.value, n.value
+
+
+def _prow(prow, tokens):
+    if prow is not None and prow.shape[0] != tokens:
+        raise ValueError(f"prow has {prow.shape[0]} tokens, positions {tokens}")
+    return _dev(prow, torch.int32, "prow", allow_none=True)
+
+
+def pkv_q4_append(pool, k, v, k_norm_w, positions, prow, table, stream=None, rows=None, pages=None) -> None:
+    """Quantise k, v [tokens][kv_heads][head_dim] into the pool; ``prow=None``: token t is row t."""
+    tokens = int(positions.shape[0])
+    if k.shape != v.shape or k.shape[0] != tokens:
+        raise ValueError(f"k {tuple(k.shape)}, v {tuple(v.shape)} and {tokens} positions do not match")
+    tp, rows, pages = _table(table, rows, pages)
+    _check(load_library().pkv_q4_append(
+        pool, _dev(k, torch.bfloat16, "k"), _dev(v, torch.bfloat16, "v"), _dev(k_norm_w, torch.bfloat16, "k_norm_w"),
+        _dev(positions, torch.int32, "positions"), _prow(prow, tokens), tp, tokens, rows, pages, _stream(stream)),
+        "pkv_q4_append")
+
+
+def pkv_q4_read(pool, positions, prow, table, k, v, stream=None, rows=None, pages=None) -> None:
+    """Cached k and v of the tokens, into views [tokens][kv_heads][head_dim] whose heads are contiguous
+    (a bf16 pool's K[:, s:s+n].transpose(0, 1) is one)."""
+    tokens = int(positions.shape[0])
+    for name, x in (("k", k), ("v", v)):
+        if x.dtype != torch.bfloat16 or not x.is_cuda:
+            raise TypeError(f"{name} must be a bf16 CUDA tensor")
+        if x.dim() != 3 or x.shape[0] != tokens or x.stride(2) != 1 or x.stride() != k.stride() or x.shape != k.shape:
+            raise ValueError(f"{name} must be [{tokens}][kv_heads][head_dim] with contiguous heads, k and v alike")
+    tp, rows, pages = _table(table, rows, pages)
+    _check(load_library().pkv_q4_read(
+        pool, _dev(positions, torch.int32, "positions"), _prow(prow, tokens), tp, tokens, rows, pages,
+        ctypes.c_void_p(k.data_ptr()), ctypes.c_void_p(v.data_ptr()), k.stride(0), k.stride(1), _stream(stream)),
+        "pkv_q4_read")
+
+
+def pkv_q4_decode(pool, q, k, v, q_norm_w, k_norm_w, positions, table, out, workspace, stream=None,
+                  pages=None) -> None:
+    """decode_paged over a 4-bit pool; ``table=None`` with ``pages`` is the contiguous-row layout."""
+    tp, rows, pages = _table(table, positions.shape[0], pages)
+    _check(load_library().pkv_q4_decode(
+        pool, _dev(q, torch.bfloat16, "q"), _dev(k, torch.bfloat16, "k"), _dev(v, torch.bfloat16, "v"),
+        _dev(q_norm_w, torch.bfloat16, "q_norm_w"), _dev(k_norm_w, torch.bfloat16, "k_norm_w"),
+        _dev(positions, torch.int32, "positions"), tp, rows, pages, _dev(out, torch.bfloat16, "out"),
+        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "pkv_q4_decode")
+
+
+# ---- norm + rotation
+
+def pkv_norm_rope(pool, q, k, q_norm_w, k_norm_w, positions, q_out, k_out, layout="half", stream=None) -> None:
+    """QK-norm and RoPE of q [tokens][heads][head_dim] and k [tokens][kv_heads][head_dim] (heads contiguous, any
+    token stride) into q_out and k_out (both bf16 or both fp32).  q or k may be None; no weights: no norm."""
+    tokens, kinds, ptrs, strides = int(positions.shape[0]), set(), [], []
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if (x is None) != (y is None):
+            raise ValueError(f"{name} and {name}_out are given together")
+        for what, t in ((name, x), (name + "_out", y)):
+            if t is None:
+                ptrs.append(None)
+                strides.append(0)
+                continue
+            if not t.is_cuda or t.dtype not in (torch.bfloat16, torch.float32) or (t is x and t.dtype != torch.bfloat16):
+                raise TypeError(f"{what} must be a CUDA tensor, inputs bf16 and outputs bf16 or fp32")
+            if t.dim() != 3 or t.shape != x.shape or t.shape[0] != tokens or t.stride(2) != 1 \
+                    or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+                raise ValueError(f"{what} must be [{tokens}][heads][head_dim] with heads contiguous, as its input")
+            ptrs.append(ctypes.c_void_p(t.data_ptr()))
+            strides.append(t.stride(0) if tokens > 1 else t.shape[1] * t.shape[2])
+            if t is y:
+                kinds.add(t.dtype)
+    if len(kinds) != 1:
+        raise TypeError("q_out and k_out must have one type")
+    _check(load_library().pkv_norm_rope(
+        pool, ptrs[0], ptrs[2], _dev(q_norm_w, torch.bfloat16, "q_norm_w", allow_none=True),
+        _dev(k_norm_w, torch.bfloat16, "k_norm_w", allow_none=True), _dev(positions, torch.int32, "positions"), tokens,
+        ROPE_LAYOUTS[layout], int(kinds == {torch.float32}), strides[0], strides[2], ptrs[1], ptrs[3], strides[1],
+        strides[3], _stream(stream)), "pkv_norm_rope")
+
+
+def pkv_rope_frequencies(cfg, scaling="none", factor: float = 1.0, trained: int = 0):
+    """(inverse frequencies of the rotated pairs, factor on cos and sin) of a scaled rotation."""
+    c = _cfg(cfg)
+    freq = (ctypes.c_double * max(1, (c.rotary_dim or c.head_dim) // 2))()
+    m = ctypes.c_double()
+    _check(load_library().pkv_rope_frequencies(ctypes.byref(c), ROPE_SCALINGS[scaling], float(factor), int(trained),
+                                               freq, ctypes.byref(m)), "pkv_rope_frequencies")
+    return list(freq), m.value
+
+
+def pkv_pool_set_rope(pool, inv_freq, mscale: float = 1.0, stream=None) -> None:
+    _check(load_library().pkv_pool_set_rope(pool, (ctypes.c_double * len(inv_freq))(*inv_freq), float(mscale),
+                                            _stream(stream)), "pkv_pool_set_rope")
+
+
 def pkv_check_errors(pool, stream=None) -> int:
     f = ctypes.c_uint32()
     _check(load_library().pkv_check_errors(pool, _stream(stream), ctypes.byref(f)), "pkv_check_errors")
@@ -331,7 +476,54 @@ def pkv_timer_read(pool):
 
 # ------------------------------------------------------------------ convenience (marshalling only)
 
-class PagedKVPool:
+class _Pool:
+    """What pools of either format share: the workspace, norm + rotation, errors, closing."""
+
+    handle = None
+    _ws = None
+
+    def workspace(self, rows: int, pages: int, prefill_tokens: int = 0) -> torch.Tensor:
+        n = pkv_workspace_bytes(self.handle, rows, pages, prefill_tokens)
+        if self._ws is None or self._ws.numel() < n:
+            self._ws = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
+        return self._ws
+
+    def set_rope(self, inv_freq, mscale: float = 1.0, stream=None) -> None:
+        """Other frequencies for this pool's rotation (see pkv_rope_frequencies)."""
+        if len(inv_freq) != (self.cfg.rotary_dim or self.cfg.head_dim) // 2:
+            raise ValueError(f"{len(inv_freq)} frequencies for a rotation of {self.cfg.rotary_dim} dims")
+        pkv_pool_set_rope(self.handle, inv_freq, mscale, stream)
+
+    def norm_rope(self, q, k, q_norm_w, k_norm_w, positions, layout="half", q_out=None, k_out=None,
+                  dtype=torch.bfloat16, stream=None):
+        """(q, k) normed over each head and rotated; fp32 q is what pkv_decode_appended takes."""
+        c = self.cfg
+        for name, x, h in (("q", q, c.heads), ("k", k, c.kv_heads)):
+            if x is not None and tuple(x.shape[1:]) != (h, c.head_dim):
+                raise ValueError(f"{name} must be [tokens][{h}][{c.head_dim}], got {tuple(x.shape)}")
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=dtype, device=k.device)
+        pkv_norm_rope(self.handle, q, k, q_norm_w, k_norm_w, positions, q_out, k_out, layout, stream)
+        return q_out, k_out
+
+    def check_errors(self, stream=None) -> int:
+        return pkv_check_errors(self.handle, stream)
+
+    def close(self):
+        if self.handle is not None and self.handle.value:
+            pkv_pool_free(self.handle)
+        self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class PagedKVPool(_Pool):
     """A pool over caller-owned K/V torch tensors [kv_heads][num_pages*page_size][head_dim] (bf16)."""
 
     def __init__(self, K: torch.Tensor, V: torch.Tensor, cfg=None, stream=None):
@@ -341,15 +533,9 @@ class PagedKVPool:
             raise ValueError(f"K/V must be [kv_heads][num_pages*page_size][head_dim], got {tuple(K.shape)}")
         self.K, self.V, self.cfg = K, V, c
         self.num_pages = K.shape[1] // c.page_size
+        self.device = K.device
         self.handle = pkv_pool_wrap(c, self.num_pages, K, V, stream)
-        self._ws = None
         self._lws = None
-
-    def workspace(self, rows: int, pages: int, prefill_tokens: int = 0) -> torch.Tensor:
-        n = pkv_workspace_bytes(self.handle, rows, pages, prefill_tokens)
-        if self._ws is None or self._ws.numel() < n:
-            self._ws = torch.empty(max(n, 256), dtype=torch.uint8, device=self.K.device)
-        return self._ws
 
     def decode(self, q, k, v, q_norm_w, k_norm_w, positions, table, out=None, stream=None,
                pages=None) -> torch.Tensor:
@@ -419,16 +605,71 @@ class PagedKVPool:
         pkv_decode_appended(self.handle, q_hat, positions, table, out, ws, stream, pages=pages)
         return out
 
-    def check_errors(self, stream=None) -> int:
-        return pkv_check_errors(self.handle, stream)
 
-    def close(self):
-        if self.handle is not None and self.handle.value:
-            pkv_pool_free(self.handle)
-        self.handle = None
+class Q4KVPool(_Pool):
+    """A 4-bit pool over a caller-owned uint8 tensor [num_pages][kv_heads][...] (pkv_q4_pool_bytes bytes; zeros are
+    an empty pool, and ``Q4KVPool.empty`` makes one).  k_scale and v_scale are powers of two."""
 
-    def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
+    def __init__(self, data: torch.Tensor, cfg=None, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+        c = _cfg(cfg)
+        per_page = pkv_q4_pool_bytes(c, 1)
+        if data.dtype != torch.uint8 or data.numel() == 0 or data.numel() % per_page:
+            raise ValueError(f"data must be uint8, a multiple of {per_page} bytes, got {data.dtype} x {data.numel()}")
+        self.data, self.cfg, self.device, self._streams = data, c, data.device, {}
+        self.num_pages = data.numel() // per_page
+        self.handle = pkv_q4_pool_wrap(c, self.num_pages, data, k_scale, v_scale, stream)
+
+    @classmethod
+    def empty(cls, num_pages: int, cfg=None, k_scale: float = 1.0, v_scale: float = 1.0, device="cuda", stream=None):
+        data = torch.zeros(pkv_q4_pool_bytes(cfg, num_pages), dtype=torch.uint8, device=device)
+        return cls(data, cfg, k_scale, v_scale, stream)
+
+    def _scratch(self, rows: int, pages: int, stream) -> torch.Tensor:
+        """A workspace for one call on `stream`: one kept per stream, and a captured call's own (it belongs to its
+        graph, so that graphs and eager calls may run at the same time)."""
+        n = pkv_workspace_bytes(self.handle, rows, pages, 0)
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        with _on(s):
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(n, dtype=torch.uint8, device=self.device)
+            key = s.cuda_stream if isinstance(s, torch.cuda.Stream) else int(s)
+            ws = self._streams.get(key)
+            if ws is None or ws.numel() < n:
+                ws = self._streams[key] = torch.empty(n, dtype=torch.uint8, device=self.device)
+            return ws
+
+    def _shapes(self, **tensors):
+        c = self.cfg
+        for name, x in tensors.items():
+            h = c.heads if name in ("q", "out") else c.kv_heads
+            if x.dim() != 3 or x.shape[1] != h or x.shape[2] != c.head_dim:
+                raise ValueError(f"{name} must be [tokens][{h}][{c.head_dim}], got {tuple(x.shape)}")
+
+    def append(self, k, v, k_norm_w, positions, prow, table, stream=None, rows=None, pages=None) -> None:
+        """k normed and roped, then k and v quantised into their slots (prow None: token t is row t)."""
+        self._shapes(k=k, v=v)
+        pkv_q4_append(self.handle, k, v, k_norm_w, positions, prow, table, stream, rows=rows, pages=pages)
+
+    def read(self, positions, prow, table, k=None, v=None, stream=None, rows=None, pages=None):
+        """(k, v) [tokens][kv_heads][head_dim] that the pool holds at the tokens' positions."""
+        c, shape = self.cfg, (positions.shape[0], self.cfg.kv_heads, self.cfg.head_dim)
+        with _on(stream):
+            k = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if k is None else k
+            v = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if v is None else v
+        self._shapes(k=k, v=v)
+        pkv_q4_read(self.handle, positions, prow, table, k, v, stream, rows=rows, pages=pages)
+        return k, v
+
+    def decode(self, q, k, v, q_norm_w, k_norm_w, positions, table, out=None, stream=None, pages=None) -> torch.Tensor:
+        """One step of every row: append its k and v, attend over its cached positions."""
+        if out is None:
+            with _on(stream):
+                out = torch.empty_like(q)
+        self._shapes(q=q, k=k, v=v, out=out)
+        rows = positions.shape[0]
+        if q.shape[0] != rows or k.shape[0] != rows or v.shape[0] != rows or out.shape[0] != rows:
+            raise ValueError(f"q, k, v and out must have {rows} tokens, as positions")
+        pages = table.shape[1] if table is not None else pages
+        pkv_q4_decode(self.handle, q, k, v, q_norm_w, k_norm_w, positions, table, out,
+                      self._scratch(rows, pages, stream), stream, pages=pages)
+        return out

@@ -183,34 +183,67 @@ static int check_config(const pkv_config* c)
     return PKV_OK;
 }
 
+static int rotary_dims(const pkv_config& c) { return c.rotary_dim > 0 ? c.rotary_dim : c.head_dim; }
+
+// Frequencies of the rotated pairs, theta^(-2i/R), scaled for a context of
+// `factor` times the trained one (see pkv.h), and the factor on cos and sin.
+static void rope_frequencies(const pkv_config& c, int scaling, double factor, int trained, double* inv, double* mscale)
+{
+    const int R = rotary_dims(c);
+    const double theta = scaling == PKV_ROPE_BASE ? c.rope_theta * std::pow(factor, (double)R / (R - 2.0)) : c.rope_theta;
+    for (int i = 0; i < R / 2; ++i) inv[i] = std::pow(theta, -2.0 * i / (double)R);
+    *mscale = 1.0;
+    if (scaling == PKV_ROPE_LINEAR)
+        for (int i = 0; i < R / 2; ++i) inv[i] /= factor;
+    if (scaling == PKV_ROPE_RAMP) {
+        // pairs up to the one that turns 32 times over the trained context keep their
+        // frequency, from the one that turns once on it is divided, a ramp between
+        auto pair = [&](double turns) {
+            return R * std::log(trained / (turns * 2.0 * 3.14159265358979323846)) / (2.0 * std::log(c.rope_theta));
+        };
+        const double low = std::max(std::floor(pair(32.0)), 0.0), high = std::min(std::ceil(pair(1.0)), R - 1.0);
+        for (int i = 0; i < R / 2; ++i) {
+            const double ramp = std::min(std::max((i - low) / std::max(high - low, 0.001), 0.0), 1.0);
+            inv[i] = inv[i] / factor * ramp + inv[i] * (1.0 - ramp);
+        }
+        *mscale = 0.1 * std::log(factor) + 1.0;
+    }
+}
+
 // RoPE tables: (cos, sin) of pos * theta^(-2i/head_dim), i < head_dim/2, for
 // every position < max_seq, computed in double (qwen3-8b Nest files,
 // src/rope.linnet tables; the pages evaluate the angle in f32, which at
 // position 40959 is off by up to ~2e-3 rad) and kept as two fp32 tables: hi,
 // the nearest fp32 values (q uses these), and lo, the remainders (k uses
 // hi + lo, so its rotation keeps the double table's accuracy).
-// (cos, sin) of pos * theta^(-2i/R) for i < R/2 (R = rotary dims), in double,
-// kept as the nearest fp32 pair plus the fp32 of the remainder; entries past
-// R/2 (partial rotation) are the identity (1, 0).
-static void rope_tables(const pkv_config& c, std::vector<float2>& hi, std::vector<float2>& lo)
+// (cos, sin) of pos * inv[i] for i < R/2 (R = rotary dims), times mscale, in
+// double, kept as the nearest fp32 pair plus the fp32 of the remainder; entries
+// past R/2 (partial rotation) are the identity (1, 0).
+static void rope_tables(const pkv_config& c, const double* inv, double mscale, std::vector<float2>& hi,
+                        std::vector<float2>& lo)
 {
-    const int half = c.head_dim / 2, R = c.rotary_dim > 0 ? c.rotary_dim : c.head_dim, rhalf = R / 2;
+    const int half = c.head_dim / 2, rhalf = rotary_dims(c) / 2;
     hi.assign((size_t)c.max_seq * half, make_float2(1.f, 0.f));
     lo.assign((size_t)c.max_seq * half, make_float2(0.f, 0.f));
-    std::vector<double> inv(rhalf);
-    for (int i = 0; i < rhalf; ++i) inv[i] = std::pow(c.rope_theta, -2.0 * i / (double)R);
     for (int p = 0; p < c.max_seq; ++p)
         for (int i = 0; i < rhalf; ++i) {
             const double a = (double)p * inv[i];
-            const double cs = std::cos(a), sn = std::sin(a);
+            const double cs = std::cos(a) * mscale, sn = std::sin(a) * mscale;
             const float ch = (float)cs, sh = (float)sn;
             hi[(size_t)p * half + i] = make_float2(ch, sh);
             lo[(size_t)p * half + i] = make_float2((float)(cs - (double)ch), (float)(sn - (double)sh));
         }
 }
 
+// The scales of a 4-bit pool, and its pages where the caller owns them.
+struct Q4Spec {
+    void* data;
+    float k_scale, v_scale;
+};
+
+// q4: a 4-bit pool (k and v unused), or null.
 static int create_pool(const pkv_config* cfg, int num_pages, void* k, void* v, bool owns, void* stream,
-                       pkv_pool** out)
+                       pkv_pool** out, const Q4Spec* q4 = nullptr)
 {
     if (!cfg || !out || num_pages <= 0) return PKV_EINVAL;
     *out = nullptr;
@@ -236,9 +269,15 @@ static int create_pool(const pkv_config* cfg, int num_pages, void* k, void* v, b
     p->owns_kv = owns;
     p->wait_ns = 1000000000ull;
     const size_t kv_bytes = (size_t)cfg->kv_heads * num_slots * cfg->head_dim * 2;
+    const size_t q4_bytes = (size_t)num_pages * cfg->kv_heads * kQ4PageBytes;
     const size_t tab = (size_t)cfg->max_seq * (cfg->head_dim / 2) * sizeof(float2);
     bool fail = false;
-    if (owns) {
+    if (q4) {
+        p->k_scale = q4->k_scale;
+        p->v_scale = q4->v_scale;
+        p->q4 = q4->data;
+        fail |= owns && cudaMalloc(&p->q4, q4_bytes) != cudaSuccess;
+    } else if (owns) {
         fail |= cudaMalloc(&p->k, kv_bytes) != cudaSuccess;
         fail |= !fail && cudaMalloc(&p->v, kv_bytes) != cudaSuccess;
     } else {
@@ -256,9 +295,19 @@ static int create_pool(const pkv_config* cfg, int num_pages, void* k, void* v, b
     p->claims = p->err + 32;
     static_assert(32 + kClaimSlots <= 256 / 4, "the claim counters share the error word's allocation");
     std::vector<float2> rhi, rlo;
-    rope_tables(*cfg, rhi, rlo);
+    try {
+        std::vector<double> inv(rotary_dims(*cfg) / 2);
+        double mscale = 1.0;
+        rope_frequencies(*cfg, PKV_ROPE_NONE, 1.0, 0, inv.data(), &mscale);
+        rope_tables(*cfg, inv.data(), mscale, rhi, rlo);
+    } catch (const std::bad_alloc&) {
+        pkv_pool_free(p);
+        return PKV_ENOMEM;
+    }
     bool ok = true;
-    if (owns) {
+    if (owns && q4) {
+        ok &= cudaMemsetAsync(p->q4, 0, q4_bytes, s) == cudaSuccess;
+    } else if (owns) {
         ok &= cudaMemsetAsync(p->k, 0, kv_bytes, s) == cudaSuccess;
         ok &= cudaMemsetAsync(p->v, 0, kv_bytes, s) == cudaSuccess;
     }
@@ -266,8 +315,12 @@ static int create_pool(const pkv_config* cfg, int num_pages, void* k, void* v, b
     ok &= cudaMemcpyAsync(p->rope_lo, rlo.data(), tab, cudaMemcpyHostToDevice, s) == cudaSuccess;
     ok &= cudaMemsetAsync(p->err, 0, 256, s) == cudaSuccess;
     ok &= cudaStreamSynchronize(s) == cudaSuccess;  // the host vectors die with this call
-    ok &= make_tmap(&p->tmap_k, p->k, num_slots, cfg->kv_heads);
-    ok &= make_tmap(&p->tmap_v, p->v, num_slots, cfg->kv_heads);
+    if (q4) {
+        ok &= configure_q4() == cudaSuccess;
+    } else {
+        ok &= make_tmap(&p->tmap_k, p->k, num_slots, cfg->kv_heads);
+        ok &= make_tmap(&p->tmap_v, p->v, num_slots, cfg->kv_heads);
+    }
     ok &= configure_kernels() == cudaSuccess;
     ok &= configure_prefill() == cudaSuccess;
     p->ctas_per_sm = attn_ctas_per_sm();
@@ -367,6 +420,7 @@ int host_precheck(const pkv_pool* pool, const StepArgs& a, cudaStream_t s)
 
 static int run_step(pkv_pool* pool, const StepArgs& a, size_t ws_bytes, void* stream)
 {
+    if (pool->q4) return PKV_EINVAL;  // a 4-bit pool has entries of its own
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev != pool->device) return PKV_EDEVICE;
     // contiguous rows (no table): every row's pages must be in the pool
@@ -436,6 +490,7 @@ int pkv_pool_free(pkv_pool* p)
     if (p->owns_kv) {
         if (p->k) cudaFree(p->k);
         if (p->v) cudaFree(p->v);
+        if (p->q4) cudaFree(p->q4);
     }
     if (p->rope_hi) cudaFree(p->rope_hi);
     if (p->rope_lo) cudaFree(p->rope_lo);
@@ -467,6 +522,11 @@ int pkv_workspace_bytes(const pkv_pool* pool, int rows, int pages, int prefill_t
     if (!pool || !bytes || rows < 0 || prefill_tokens < 0 || rows + prefill_tokens <= 0 || pages <= 0)
         return PKV_EINVAL;
     if ((int64_t)rows + prefill_tokens > (1 << 20) || (int64_t)rows * pages > INT32_MAX) return PKV_ERANGE;
+    if (pool->q4) {  // prompt tokens are appended without a workspace
+        if (prefill_tokens > 0) return PKV_ENOTIMPL;
+        *bytes = make_q4_plan(pool, rows).total;
+        return PKV_OK;
+    }
     *bytes = make_plan(pool, rows + prefill_tokens, pages, prefill_tokens).total;
     return PKV_OK;
 }
@@ -500,6 +560,7 @@ int pkv_qkv_proj_append(pkv_pool* pool, const void* x, const void* w_qkv, int to
     if (!aligned(x, 16) || !aligned(w_qkv, 16) || !aligned(q_hat, 16) || !aligned(q_norm_w, 8) ||
         !aligned(k_norm_w, 8) || !aligned(positions, 4) || !aligned(table, 4))
         return PKV_EINVAL;
+    if (pool->q4) return PKV_EINVAL;
     if (!table && (int64_t)tokens * pages > pool->num_pages) return PKV_ERANGE;
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev != pool->device) return PKV_EDEVICE;
@@ -523,6 +584,7 @@ int pkv_decode_appended(pkv_pool* pool, const float* q_hat, const int32_t* posit
     if (rows > (1 << 20) || (int64_t)rows * pages > INT32_MAX) return PKV_ERANGE;
     if (!aligned(q_hat, 16) || !aligned(out, 8) || !aligned(positions, 4) || !aligned(table, 4)) return PKV_EINVAL;
     if (workspace && !aligned(workspace, 256)) return PKV_EINVAL;
+    if (pool->q4) return PKV_EINVAL;
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev != pool->device) return PKV_EDEVICE;
     if (!table && (int64_t)rows * pages > pool->num_pages) return PKV_ERANGE;
@@ -630,6 +692,203 @@ int pkv_output_gate(pkv_pool* pool, void* out, const void* gate, int tokens, voi
     if (cudaGetDevice(&dev) != cudaSuccess || dev != pool->device) return PKV_EDEVICE;
     const int64_t n = (int64_t)tokens * pool->cfg.heads * pool->cfg.head_dim;
     return launch_gate(pool, out, gate, n, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+// ---- 4-bit pools -------------------------------------------------------------------------
+static bool power_of_two(float x)
+{
+    int e = 0;
+    return std::isfinite(x) && x > 0.f && std::frexp(x, &e) == 0.5f && e >= -59 && e <= 61;  // 2^-60 .. 2^60
+}
+
+int pkv_q4_pool_bytes(const pkv_config* cfg, int num_pages, size_t* bytes)
+{
+    if (!cfg || !bytes || num_pages <= 0) return PKV_EINVAL;
+    const int rc = check_config(cfg);
+    if (rc != PKV_OK) return rc;
+    if ((int64_t)num_pages * cfg->page_size >= (int64_t(1) << 31)) return PKV_ERANGE;
+    *bytes = (size_t)num_pages * cfg->kv_heads * kQ4PageBytes;
+    return PKV_OK;
+}
+
+int pkv_q4_pool_alloc(const pkv_config* cfg, int num_pages, float k_scale, float v_scale, void* stream, pkv_pool** out)
+{
+    if (!power_of_two(k_scale) || !power_of_two(v_scale)) return PKV_EINVAL;
+    const Q4Spec q4 = {nullptr, k_scale, v_scale};
+    return create_pool(cfg, num_pages, nullptr, nullptr, true, stream, out, &q4);
+}
+
+int pkv_q4_pool_wrap(const pkv_config* cfg, int num_pages, void* data, float k_scale, float v_scale, void* stream,
+                     pkv_pool** out)
+{
+    if (!data || !aligned(data, 256) || !power_of_two(k_scale) || !power_of_two(v_scale)) return PKV_EINVAL;
+    const Q4Spec q4 = {data, k_scale, v_scale};
+    return create_pool(cfg, num_pages, nullptr, nullptr, false, stream, out, &q4);
+}
+
+int pkv_q4_pool_data(const pkv_pool* pool, void** data, size_t* bytes)
+{
+    if (!pool || !pool->q4) return PKV_EINVAL;
+    if (data) *data = pool->q4;
+    if (bytes) *bytes = (size_t)pool->num_pages * pool->cfg.kv_heads * kQ4PageBytes;
+    return PKV_OK;
+}
+
+// What every call over a 4-bit pool's page table checks.
+static int q4_checks(const pkv_pool* pool, const int32_t* positions, const int32_t* prow, const int32_t* table,
+                     int tokens, int rows, int pages)
+{
+    if (!pool || !pool->q4 || !positions || tokens <= 0 || rows <= 0 || pages <= 0) return PKV_EINVAL;
+    if (!prow && rows < tokens) return PKV_EINVAL;  // token t is table row t
+    if (tokens > (1 << 20) || rows > (1 << 20) || (int64_t)rows * pages > INT32_MAX / 2) return PKV_ERANGE;
+    if (!aligned(positions, 4) || !aligned(prow, 4) || !aligned(table, 4)) return PKV_EINVAL;
+    if (!table && (int64_t)rows * pages > pool->num_pages) return PKV_ERANGE;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != pool->device) return PKV_EDEVICE;
+    return PKV_OK;
+}
+
+// PKV_CHECK=1: the written slots must be distinct (every write of a call is ordered before its reads).
+static int q4_precheck(const pkv_pool* pool, const int32_t* positions, const int32_t* prow, const int32_t* table,
+                       int tokens, int rows, int pages, cudaStream_t s)
+{
+    if (!check_enabled()) return PKV_OK;
+    StepArgs a = {};
+    a.table = table;
+    a.rows = rows;
+    a.pages = pages;
+    if (prow) {
+        a.positions = positions;
+        a.prow = prow;
+        a.P = tokens;
+    } else {
+        a.step_positions = positions;
+        a.steps = tokens;
+        a.q_hat = reinterpret_cast<const float*>(positions);  // not null: no ordering between rows to check
+    }
+    try {
+        return host_precheck(pool, a, s);
+    } catch (const std::bad_alloc&) {
+        return PKV_ENOMEM;
+    }
+}
+
+int pkv_q4_append(pkv_pool* pool, const void* k, const void* v, const void* k_norm_w, const int32_t* positions,
+                  const int32_t* prow, const int32_t* table, int tokens, int rows, int pages, void* stream)
+{
+    NvtxRange range("pkv_q4_append");
+    if (!k || !v || !k_norm_w || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_norm_w, 8)) return PKV_EINVAL;
+    int rc = q4_checks(pool, positions, prow, table, tokens, rows, pages);
+    if (rc == PKV_OK) rc = q4_precheck(pool, positions, prow, table, tokens, rows, pages, static_cast<cudaStream_t>(stream));
+    if (rc != PKV_OK) return rc;
+    return launch_q4_append(pool, k, v, k_norm_w, positions, prow, table, tokens, rows, pages,
+                            static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ECUDA;
+}
+
+int pkv_q4_read(pkv_pool* pool, const int32_t* positions, const int32_t* prow, const int32_t* table, int tokens,
+                int rows, int pages, void* k, void* v, int64_t token_stride, int64_t head_stride, void* stream)
+{
+    NvtxRange range("pkv_q4_read");
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || token_stride % 8 || head_stride % 8) return PKV_EINVAL;
+    const int rc = q4_checks(pool, positions, prow, table, tokens, rows, pages);
+    if (rc != PKV_OK) return rc;
+    return launch_q4_read(pool, positions, prow, table, tokens, rows, pages, k, v, token_stride, head_stride,
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ECUDA;
+}
+
+int pkv_q4_decode(pkv_pool* pool, const void* q, const void* k, const void* v, const void* q_norm_w,
+                  const void* k_norm_w, const int32_t* positions, const int32_t* table, int rows, int pages, void* out,
+                  void* workspace, size_t workspace_bytes, void* stream)
+{
+    NvtxRange range("pkv_q4_decode");
+    if (!q || !k || !v || !q_norm_w || !k_norm_w || !out) return PKV_EINVAL;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(q_norm_w, 8) ||
+        !aligned(k_norm_w, 8))
+        return PKV_EINVAL;
+    if (workspace && !aligned(workspace, 256)) return PKV_EINVAL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = q4_checks(pool, positions, nullptr, table, rows, rows, pages);
+    if (rc == PKV_OK) rc = q4_precheck(pool, positions, nullptr, table, rows, rows, pages, s);
+    if (rc != PKV_OK) return rc;
+    const StepArgs a = {q, k, v, q_norm_w, k_norm_w, nullptr, nullptr, nullptr, positions, table,
+                        0, rows, pages, rows, out, static_cast<char*>(workspace)};
+    const Q4Plan plan = make_q4_plan(pool, rows);
+    if (!workspace || workspace_bytes < plan.total) return PKV_EWORKSPACE;
+    return launch_q4_decode(pool, a, plan, s) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+// ---- norm + rotation, and the rotation's frequencies -------------------------------------------
+int pkv_rope_frequencies(const pkv_config* cfg, int scaling, double factor, int trained, double* inv_freq, double* mscale)
+{
+    if (!cfg || !inv_freq || !mscale) return PKV_EINVAL;
+    const int rc = check_config(cfg);
+    if (rc != PKV_OK) return rc;
+    if (scaling < PKV_ROPE_NONE || scaling > PKV_ROPE_RAMP) return PKV_EINVAL;
+    if (scaling != PKV_ROPE_NONE && !(factor >= 1.0 && std::isfinite(factor))) return PKV_EINVAL;
+    if (scaling == PKV_ROPE_RAMP && (trained <= 0 || !(cfg->rope_theta > 1.0))) return PKV_EINVAL;
+    rope_frequencies(*cfg, scaling, factor, trained, inv_freq, mscale);
+    return PKV_OK;
+}
+
+int pkv_pool_set_rope(pkv_pool* pool, const double* inv_freq, double mscale, void* stream)
+{
+    if (!pool || !inv_freq || !(mscale > 0.0) || !std::isfinite(mscale)) return PKV_EINVAL;
+    for (int i = 0; i < rotary_dims(pool->cfg) / 2; ++i)
+        if (!(inv_freq[i] >= 0.0) || !std::isfinite(inv_freq[i])) return PKV_EINVAL;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != pool->device) return PKV_EDEVICE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return PKV_ECUDA;
+    if (cs != cudaStreamCaptureStatusNone) return PKV_EINVAL;
+    std::vector<float2> hi, lo;
+    try {
+        rope_tables(pool->cfg, inv_freq, mscale, hi, lo);
+    } catch (const std::bad_alloc&) {
+        return PKV_ENOMEM;
+    }
+    const size_t tab = hi.size() * sizeof(float2);
+    if (cudaDeviceSynchronize() != cudaSuccess) return PKV_ECUDA;  // calls in flight read the old tables
+    if (cudaMemcpyAsync(pool->rope_hi, hi.data(), tab, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+        cudaMemcpyAsync(pool->rope_lo, lo.data(), tab, cudaMemcpyHostToDevice, s) != cudaSuccess)
+        return PKV_ECUDA;
+    return cudaStreamSynchronize(s) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+int pkv_norm_rope(pkv_pool* pool, const void* q, const void* k, const void* q_norm_w, const void* k_norm_w,
+                  const int32_t* positions, int tokens, int layout, int out_type, int64_t q_stride, int64_t k_stride,
+                  void* q_out, void* k_out, int64_t q_out_stride, int64_t k_out_stride, void* stream)
+{
+    NvtxRange range("pkv_norm_rope");
+    if (!pool || !positions || tokens <= 0 || (!q && !k) || !q != !q_out || !k != !k_out) return PKV_EINVAL;
+    if ((layout != PKV_ROPE_HALF && layout != PKV_ROPE_INTERLEAVED) || (out_type != PKV_BF16 && out_type != PKV_F32))
+        return PKV_EINVAL;
+    if (tokens > (1 << 24)) return PKV_ERANGE;
+    const size_t out_align = out_type == PKV_F32 ? 16 : 8;
+    if (!aligned(q, 8) || !aligned(k, 8) || !aligned(q_norm_w, 8) || !aligned(k_norm_w, 8) || !aligned(positions, 4) ||
+        !aligned(q_out, out_align) || !aligned(k_out, out_align))
+        return PKV_EINVAL;
+    const int64_t qw = (int64_t)pool->cfg.heads * kHeadDim, kw = (int64_t)pool->cfg.kv_heads * kHeadDim;
+    auto bad = [](const void* x, int64_t stride, int64_t width) { return x && (stride < width || stride % 4); };
+    if (bad(q, q_stride, qw) || bad(k, k_stride, kw) || bad(q_out, q_out_stride, qw) || bad(k_out, k_out_stride, kw))
+        return PKV_EINVAL;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != pool->device) return PKV_EDEVICE;
+    NormRope a;
+    a.x[0] = q, a.x[1] = k;
+    a.w[0] = q_norm_w, a.w[1] = k_norm_w;
+    a.y[0] = q_out, a.y[1] = k_out;
+    a.x_stride[0] = q_stride, a.x_stride[1] = k_stride;
+    a.y_stride[0] = q_out_stride, a.y_stride[1] = k_out_stride;
+    a.positions = positions;
+    a.tokens = tokens;
+    a.interleaved = layout == PKV_ROPE_INTERLEAVED;
+    a.f32 = out_type == PKV_F32;
+    return launch_norm_rope(pool, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
 int pkv_check_errors(pkv_pool* pool, void* stream, uint32_t* flags)

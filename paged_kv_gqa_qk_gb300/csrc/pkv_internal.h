@@ -21,6 +21,8 @@ constexpr int kPageSize = 64;
 constexpr int kGroup = 4;                                  // query heads per kv head
 constexpr int kPageBytes = kPageSize * kHeadDim * 2;       // one page of K (or V) for one kv head
 constexpr int kRopeHalf = kHeadDim / 2;
+// One page of one kv head of a 4-bit pool: K and V, 64 bytes of codes and 8 of scales a position each.
+constexpr int kQ4PageBytes = 2 * kPageSize * (kHeadDim / 2 + kHeadDim / 16);
 // The score scale the prompt attention's queries carry: log2(e) / sqrt(128), so that
 // its scores are in base-2 units.
 constexpr float kQScale = 1.4426950408889634f * 0.088388347648318440f;
@@ -42,8 +44,10 @@ struct pkv_pool {
     int num_pages;
     int64_t num_slots;
     bool owns_kv;
-    void* k;               // bf16 [kv_heads][num_slots][head_dim]
+    void* k;               // bf16 [kv_heads][num_slots][head_dim] (null: a 4-bit pool)
     void* v;
+    void* q4;              // 4-bit pool: [num_pages][kv_heads][kQ4PageBytes] (null: a bf16 pool)
+    float k_scale, v_scale;  // 4-bit pool: the powers of two on every value
     float2* rope_hi;       // (cos, sin) [max_seq][head_dim/2]: fp32 nearest to the double values
     float2* rope_lo;       // the double values minus rope_hi, in fp32
     uint32_t* err;         // sticky device error word (word 0 of a 256-byte allocation)
@@ -175,6 +179,35 @@ cudaError_t launch_qkv_append(pkv_pool* pool, const void* x, const void* w_qkv, 
 
 // out *= sigmoid(gate) over n bf16 elements (n % 8 == 0, 16-byte aligned).
 cudaError_t launch_gate(const pkv_pool* pool, void* out, const void* gate, int64_t n, cudaStream_t s);
+
+// ---- 4-bit pools (pkv_q4.cu) ----
+// Workspace of one pkv_q4_decode call (offsets 256-byte aligned).
+struct Q4Plan {
+    int ctas;           // attention grid size
+    size_t off_len, off_prefix, off_qhat, off_qmul, off_po, off_plse;
+    size_t total;
+};
+Q4Plan make_q4_plan(const pkv_pool* pool, int rows);
+cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v, const void* k_norm_w,
+                             const int32_t* positions, const int32_t* prow, const int32_t* table, int tokens, int rows,
+                             int pages, cudaStream_t s);
+cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& plan, cudaStream_t s);
+cudaError_t launch_q4_read(const pkv_pool* pool, const int32_t* positions, const int32_t* prow, const int32_t* table,
+                           int tokens, int rows, int pages, void* k, void* v, int64_t token_stride, int64_t head_stride,
+                           cudaStream_t s);
+cudaError_t configure_q4();
+
+// ---- pkv_norm_rope (pkv_norm_rope.cu): q and k (index 0 and 1; null: not given) ----
+struct NormRope {
+    const void* x[2];
+    const void* w[2];
+    void* y[2];
+    int64_t x_stride[2], y_stride[2];
+    const int32_t* positions;
+    int tokens;
+    bool interleaved, f32;
+};
+cudaError_t launch_norm_rope(const pkv_pool* pool, const NormRope& a, cudaStream_t s);
 
 // Per-device kernel attributes (dynamic shared memory); called with the
 // pool's device current when a pool is created.

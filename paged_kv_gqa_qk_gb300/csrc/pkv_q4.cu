@@ -1,0 +1,883 @@
+// A page pool in 4 bits: appending to it, reading it back, and the decode
+// attention over it (sm_103a).  The format is in pkv_q4.cuh.
+//
+//   q4_append_kernel  QK-norm + RoPE of k, quantise k and v, write them to their
+//                     slots; in front of the attention also each token's check,
+//                     its attended length and its prepared query heads
+//   q4_attn_kernel    split attention: every warp streams its own share of the
+//                     call's 32-position chunks through its own ring of bulk
+//                     copies and keeps its own softmax state
+//   q4_combine_kernel merge of the pieces of a (token, kv head) that several
+//                     warps shared
+//   q4_read_kernel    cached k and v of a list of tokens as bf16
+//
+// Source of the computation (as the bf16 pool's): qwen3-8b Nest files,
+// src/attention.linnet, GroupedQueryAttention.decode_paged.
+#include <math_constants.h>
+
+#include "pkv_internal.h"
+#include "pkv_ptx.cuh"
+#include "pkv_q4.cuh"
+
+namespace pkv {
+
+// =====================================================================================
+// q4_append_kernel
+// =====================================================================================
+struct Q4AppendParams {
+    const __nv_bfloat16* q;     // decode: [tokens][heads][128]
+    const __nv_bfloat16* k;     // [tokens][kv_heads][128]
+    const __nv_bfloat16* v;
+    const __nv_bfloat16* qw;
+    const __nv_bfloat16* kw;
+    const int32_t* positions;   // [tokens]; -1: nothing to do
+    const int32_t* prow;        // [tokens], or null: token t is table row t
+    const int32_t* table;       // [rows][pages], or null: contiguous rows
+    const float2* rope_hi;
+    const float2* rope_lo;
+    uint8_t* data;
+    __half* q_hat;              // decode: [tokens][heads][128], each head times a power of two
+    float* q_mul;               // decode: [tokens][heads], what a score of it is multiplied with
+    int32_t* tok_len;           // decode: [tokens], 0: skip
+    uint32_t* err;
+    int tokens, rows, pages, num_pages, max_seq, heads, kv_heads, rot;
+    float eps, k_scale, v_scale;
+    float2 eps2;                // eps as a pair of floats
+};
+
+constexpr int kQ4AppendWarps = 4;
+
+// One CTA per token; warp w takes kv heads w, w + 4, ... (and their query heads).
+template <bool kDecode>
+__global__ void __launch_bounds__(32 * kQ4AppendWarps) q4_append_kernel(Q4AppendParams p)
+{
+    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_launch_dependents();
+    const int pos = p.positions[t];
+    const int row = p.prow ? p.prow[t] : t;
+    const bool active = pos != -1;
+    uint32_t e = 0;
+    if (active) {
+        if (row < 0 || row >= p.rows)
+            e = PKV_DEVERR_ROW;
+        else if (pos < 0 || pos >= p.max_seq || pos / kPageSize >= p.pages)
+            e = PKV_DEVERR_POSITION;
+    }
+    int page = 0;
+    if (active && !e) {
+        // the written page, and before an attention every page that it will read
+        const int npg = pos / kPageSize + 1;
+        int bad = 0;
+        for (int i = kDecode ? (int)threadIdx.x : npg - 1; i < npg; i += kDecode ? (int)blockDim.x : 1) {
+            const int id = page_of(p.table, p.pages, row, i);
+            bad |= id < 0 || id >= p.num_pages;
+        }
+        if (kDecode ? __syncthreads_or(bad) : bad) e = PKV_DEVERR_PAGE;
+        page = page_of(p.table, p.pages, row, npg - 1);
+    }
+    const bool ok = active && !e;
+    if (threadIdx.x == 0) {
+        if (kDecode) p.tok_len[t] = ok ? pos + 1 : 0;
+        if (e) atomicOr(p.err, e);
+    }
+    if (!ok) return;
+
+    float2 rh[4], rl[4];
+    {
+        const int f0 = krope(lane, p.rot).f0;
+        const float4* h4 = reinterpret_cast<const float4*>(p.rope_hi + (int64_t)pos * kRopeHalf + f0);
+        const float4* l4 = reinterpret_cast<const float4*>(p.rope_lo + (int64_t)pos * kRopeHalf + f0);
+        const float4 a = h4[0], b = h4[1], c = l4[0], d = l4[1];
+        rh[0] = make_float2(a.x, a.y), rh[1] = make_float2(a.z, a.w), rh[2] = make_float2(b.x, b.y),
+        rh[3] = make_float2(b.z, b.w);
+        rl[0] = make_float2(c.x, c.y), rl[1] = make_float2(c.z, c.w), rl[2] = make_float2(d.x, d.y),
+        rl[3] = make_float2(d.z, d.w);
+    }
+    float wk[4];
+    unpack4(*reinterpret_cast<const uint2*>(p.kw + 4 * lane), wk);
+    const int i = pos % kQ4Block;
+    for (int g = warp; g < p.kv_heads; g += kQ4AppendWarps) {
+        const int64_t src = ((int64_t)t * p.kv_heads + g) * kHeadDim + 4 * lane;
+        const uint2 kraw = *reinterpret_cast<const uint2*>(p.k + src);
+        const uint2 vraw = *reinterpret_cast<const uint2*>(p.v + src);
+        uint8_t* block = p.data + q4_block(page, p.kv_heads, g, pos % kPageSize);
+        float x[4];
+        norm_rope_k_paired(kraw, wk, rh, rl, p.eps2, lane, p.rot, x);
+        q4_store(block, false, i, x, p.k_scale, lane);
+        unpack4(vraw, x);
+        q4_store(block, true, i, x, p.v_scale, lane);
+    }
+    if constexpr (kDecode) {
+        // the query heads, each scaled by a power of two to largest value in [1, 2), so that fp16
+        // keeps 11 bits of it whatever its size; the attention's scores take the inverse
+        float wq[4];
+        unpack4(*reinterpret_cast<const uint2*>(p.qw + 4 * lane), wq);
+        for (int h = warp; h < p.heads; h += kQ4AppendWarps) {
+            const int64_t src = ((int64_t)t * p.heads + h) * kHeadDim + 4 * lane;
+            const float4 y = norm_rope_q_regs(*reinterpret_cast<const uint2*>(p.q + src), wq, rh, p.eps, lane, p.rot);
+            float top = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            const int ex = min(max((int)(__float_as_uint(top) >> 23), 1), 253);  // 2^(ex - 127) <= top < twice that
+            const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+            const __half2 lo = __floats2half2_rn(y.x * down, y.y * down), hi = __floats2half2_rn(y.z * down, y.w * down);
+            uint2 r;
+            r.x = *reinterpret_cast<const uint32_t*>(&lo);
+            r.y = *reinterpret_cast<const uint32_t*>(&hi);
+            *reinterpret_cast<uint2*>(p.q_hat + src) = r;
+            if (lane == 0) p.q_mul[(int64_t)t * p.heads + h] = __uint_as_float((uint32_t)ex << 23) * kQScale * p.k_scale;
+        }
+    }
+}
+
+static Q4AppendParams append_params(const pkv_pool* pool)
+{
+    Q4AppendParams p = {};
+    p.rope_hi = pool->rope_hi;
+    p.rope_lo = pool->rope_lo;
+    p.data = static_cast<uint8_t*>(pool->q4);
+    p.err = pool->err;
+    p.num_pages = pool->num_pages;
+    p.max_seq = pool->cfg.max_seq;
+    p.heads = pool->cfg.heads;
+    p.kv_heads = pool->cfg.kv_heads;
+    p.rot = pool->cfg.rotary_dim > 0 ? pool->cfg.rotary_dim : kHeadDim;
+    p.eps = (float)pool->cfg.eps;
+    p.eps2 = make_float2(p.eps, (float)(pool->cfg.eps - (double)p.eps));
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
+    return p;
+}
+
+cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v, const void* k_norm_w,
+                             const int32_t* positions, const int32_t* prow, const int32_t* table, int tokens, int rows,
+                             int pages, cudaStream_t s)
+{
+    Q4AppendParams p = append_params(pool);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.kw = static_cast<const __nv_bfloat16*>(k_norm_w);
+    p.positions = positions;
+    p.prow = prow;
+    p.table = table;
+    p.tokens = tokens;
+    p.rows = rows;
+    p.pages = pages;
+    q4_append_kernel<false><<<tokens, 32 * kQ4AppendWarps, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+// =====================================================================================
+// q4_attn_kernel
+// =====================================================================================
+//
+// Work.  A (token, kv head) unit's positions are cut into chunks of 32 (half a
+// page, 4608 contiguous bytes); units in order, kv heads within tokens, make one
+// sequence of T chunks, and warp w of W streams chunks [w T / W, (w + 1) T / W).
+// Warps of one CTA are far apart in that sequence (w = warp * CTAs + CTA): a small
+// call spreads over all SMs.  A unit inside one warp's share is written out; the
+// pieces of the others go to index u + w of the partials (unique: units and warps
+// both increase along the sequence) and q4_combine_kernel merges them in order.
+// No warp waits for another: 16 warps a CTA with 3 stages of 4608 bytes keep
+// ~150 KB in flight on an SM.
+//
+// Per 16 positions (a block), with lane = 4 r + c:
+//   S[16 pos][8] = K[16][128] q[128][8], m16n8k16 fp16: column h = query head h of the
+//     group (columns 4-7 are zero), row i = position pi(i), row i + 8 = pi(i) + 8,
+//     pi(2c + b) = (c ^ b) + 4b.  Lane (r, c) holds dims 32c..32c+31 of rows r and r + 8:
+//     one 16-byte read of codes each, two scales each.
+//   O^T[128][8] += V^T[128][16 pos] P[16][8]: lane (r, c) holds dims 16r..16r+15 (one
+//     group) of positions pi(2c), pi(2c + 1) and the same + 8: four 8-byte reads, four scales.
+// The codes become fp16 by the conversion instruction and are multiplied by their
+// scales as fp16 pairs, exactly; V's are first regrouped so that one byte holds a
+// dim's codes of two positions.  P is turned between the fragments by movmatrix.
+constexpr int kQ4Warps = 16;
+constexpr int kQ4Stages = 3;
+constexpr int kQ4Chunk = 32;                                     // positions
+constexpr int kQ4ChunkBytes = kQ4Chunk / kQ4Block * kQ4BlockBytes;  // 4608
+
+struct Q4AttnParams {
+    const __half* q_hat;
+    const float* q_mul;
+    const int32_t* tok_len;
+    const int32_t* table;
+    const uint8_t* data;
+    __nv_bfloat16* out;
+    float* part_o;      // [U + W][4][128]
+    float* part_lse;    // [U + W][4]
+    int32_t* prefix;    // [ntok + 1], written by CTA 0 for the combine
+    uint32_t* err;
+    int ntok, pages, heads, kv_heads;
+    float v_scale;
+    uint64_t wait_ns;
+};
+
+struct Q4Smem {
+    static constexpr int kRing = 0;
+    static constexpr int kBars = kQ4Warps * kQ4Stages * kQ4ChunkBytes;
+    static constexpr int kT0 = kBars + 8 * kQ4Warps * kQ4Stages;
+    static constexpr int kP0 = kT0 + 4 * 32 * kQ4Warps;
+    static constexpr int kScan = kP0 + 4 * 32 * kQ4Warps;
+    static constexpr int kBytes = kScan + 4 * kQ4Warps;
+    static constexpr int kAlloc = kBytes + 128;  // slack to align the base
+};
+static_assert(Q4Smem::kAlloc <= 227 * 1024, "the ring fits");
+
+__device__ __forceinline__ int q4_chunks(int len) { return (len + kQ4Chunk - 1) / kQ4Chunk; }
+
+// Warp-wide: the token holding chunk x (x < T), and the chunks of one kv head before it.
+__device__ __forceinline__ void q4_find(const Q4AttnParams& p, const int* sT0, const int* sP0, int64_t x, int lane,
+                                        int& t_out, int& pre_out)
+{
+    const int G = p.kv_heads;
+    int lo = 0, hi = 32 * kQ4Warps - 1;
+    while (lo < hi) {  // last run of tokens whose prefix is at or before x
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)G * sP0[mid] <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    int t = sT0[lo], pre = sP0[lo];
+    for (; t < p.ntok; t += 32) {
+        const int n = t + lane < p.ntok ? q4_chunks(p.tok_len[t + lane]) : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const int before = pre + incl - n;
+        const unsigned m = __ballot_sync(kFull, n > 0 && (int64_t)G * before <= x && x < (int64_t)G * (before + n));
+        if (m) {
+            const int l = __ffs(m) - 1;
+            t_out = t + l;
+            pre_out = __shfl_sync(kFull, before, l);
+            return;
+        }
+        pre += __shfl_sync(kFull, incl, 31);
+    }
+    t_out = p.ntok - 1;  // not reached: x < T lies in some token
+    pre_out = pre;
+}
+
+// A place in the sequence of chunks: chunk j of n of unit (t, g).
+struct Q4Cursor {
+    int t, g, j, n, len;
+};
+
+__device__ __forceinline__ void q4_next(const Q4AttnParams& p, Q4Cursor& c, bool more)
+{
+    if (++c.j < c.n || !more) return;
+    c.j = 0;
+    if (++c.g < p.kv_heads) return;
+    c.g = 0;
+    do {
+        ++c.t;
+        c.len = p.tok_len[c.t];  // more: another token with chunks follows
+    } while (c.len == 0);
+    c.n = q4_chunks(c.len);
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of 16-bit elements (lane 4i + j: row i, columns 2j, 2j + 1).
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 127u) & ~127u;
+    uint8_t* sbase = smem_raw + (base - raw);
+    int* sT0 = reinterpret_cast<int*>(sbase + Q4Smem::kT0);
+    int* sP0 = reinterpret_cast<int*>(sbase + Q4Smem::kP0);
+    int* sScan = reinterpret_cast<int*>(sbase + Q4Smem::kScan);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = p.kv_heads, H = p.heads;
+    const uint32_t ring = base + warp * (kQ4Stages * kQ4ChunkBytes);
+    const uint32_t bars = base + Q4Smem::kBars + 8 * kQ4Stages * warp;
+    if (lane == 0) {
+        for (int i = 0; i < kQ4Stages; ++i) mbar_init(bars + 8 * i, 1);
+        fence_mbar_init();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // chunks per token and their prefix over tokens (one run of tokens a thread; every CTA computes it)
+    const int nt = p.ntok, per = (nt + 32 * kQ4Warps - 1) / (32 * kQ4Warps);
+    const int t0 = min(nt, tid * per), t1 = min(nt, t0 + per);
+    int local = 0;
+    for (int t = t0; t < t1; ++t) local += q4_chunks(p.tok_len[t]);
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sScan[warp] = incl;
+    __syncthreads();
+    int total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kQ4Warps; ++w) {
+        before += w < warp ? sScan[w] : 0;
+        total += sScan[w];
+    }
+    const int excl = before + incl - local;
+    sT0[tid] = t0;
+    sP0[tid] = excl;
+    if (blockIdx.x == 0) {
+        int run = excl;
+        for (int t = t0; t < t1; ++t) {
+            p.prefix[t] = run;
+            run += q4_chunks(p.tok_len[t]);
+        }
+        if (tid == 0) p.prefix[nt] = total;
+    }
+    __syncthreads();
+
+    const int64_t T = (int64_t)G * total;
+    const int64_t W = min((int64_t)gridDim.x * kQ4Warps, T);
+    const int w = warp * gridDim.x + blockIdx.x;
+    if (w >= W) return;
+    const int64_t xb = (int64_t)w * T / W, xe = (int64_t)(w + 1) * T / W;
+    const int count = (int)(xe - xb);
+
+    Q4Cursor cur;
+    {
+        int pre;
+        q4_find(p, sT0, sP0, xb, lane, cur.t, pre);
+        cur.len = p.tok_len[cur.t];
+        cur.n = q4_chunks(cur.len);
+        const int64_t off = xb - (int64_t)G * pre;
+        cur.g = (int)(off / cur.n);
+        cur.j = (int)(off % cur.n);
+    }
+    Q4Cursor iss = cur;
+    int issued = 0;
+    int entries = 0, ent_t = -1, ent_b = 0;  // table entries [32 ent_b, +32) of token ent_t, one a lane
+    auto issue = [&]() {
+        const int pg = iss.j >> 1;
+        if (ent_t != iss.t || ent_b != pg >> 5) {
+            ent_t = iss.t;
+            ent_b = pg >> 5;
+            const int e = 32 * ent_b + lane;
+            entries = e <= (iss.len - 1) / kPageSize ? page_of(p.table, p.pages, iss.t, e) : 0;
+        }
+        const int page = __shfl_sync(kFull, entries, pg & 31);
+        if (lane == 0) {
+            const int left = iss.len - iss.j * kQ4Chunk;
+            const uint32_t bytes = left > kQ4Block ? kQ4ChunkBytes : kQ4BlockBytes;
+            const int st = issued % kQ4Stages;
+            mbar_arrive_expect_tx(bars + 8 * st, bytes);
+            const uint8_t* src = p.data + ((int64_t)page * G + iss.g) * kQ4PageBytes + (iss.j & 1) * kQ4ChunkBytes;
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                    ring + st * kQ4ChunkBytes),
+                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bars + 8 * st)
+                : "memory");
+        }
+        ++issued;
+        q4_next(p, iss, issued < count);
+    };
+    for (int i = 0; i < kQ4Stages - 1 && i < count; ++i) issue();
+
+    const int r = lane >> 2, c = lane & 3;
+    const int pi_r = ((r >> 1) ^ (r & 1)) | ((r & 1) << 2);  // position of row r (see above)
+    const int pi_0 = c, pi_1 = (c ^ 1) | 4;                   // positions of k = 2c, 2c + 1
+    const uint32_t koff = 64 * pi_r + ((16 * c) ^ (((pi_r >> 1) & 1) << 5));
+    const uint32_t voff0 = kQ4VCodes + 64 * pi_0 + ((8 * r) ^ (((pi_0 >> 1) & 1) << 5));
+    const uint32_t voff1 = kQ4VCodes + 64 * pi_1 + ((8 * r) ^ (((pi_1 >> 1) & 1) << 5));
+    const uint32_t soff = 16 * r + 4 * c;
+
+    uint32_t bq[8][2];
+    float mulA = 0.f, mulB = 0.f;
+    float o[8][4];
+    float mA = 0.f, mB = 0.f, lA = 0.f, lB = 0.f;
+    bool fresh = true;   // the next chunk opens a segment
+    bool whole = false;  // the segment began with its unit's first chunk
+    bool ok = true;
+
+    for (int i = 0; i < count; ++i) {
+        if (issued < count) issue();
+        const int st = i % kQ4Stages;
+        if (fresh) {
+            const __half* qh = p.q_hat + ((int64_t)cur.t * H + cur.g * kGroup + (r & 3)) * kHeadDim + 32 * c;
+            uint4 x[4] = {};
+            if (r < kGroup) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = reinterpret_cast<const uint4*>(qh)[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bq[2 * k][0] = x[k].x;
+                bq[2 * k][1] = x[k].y;
+                bq[2 * k + 1][0] = x[k].z;
+                bq[2 * k + 1][1] = x[k].w;
+            }
+            const float2 mul = c < 2 ? *reinterpret_cast<const float2*>(p.q_mul + (int64_t)cur.t * H + cur.g * kGroup + 2 * c)
+                                     : make_float2(0.f, 0.f);
+            mulA = mul.x;
+            mulB = mul.y;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
+            mA = mB = -CUDART_INF_F;
+            lA = lB = 0.f;
+            whole = cur.j == 0;
+            fresh = false;
+        }
+        if (__any_sync(kFull, !mbar_wait(bars + 8 * st, (i / kQ4Stages) & 1, p.wait_ns))) {
+            ok = false;
+            break;
+        }
+        const uint32_t sb = ring + st * kQ4ChunkBytes;
+        const int left = cur.len - cur.j * kQ4Chunk;  // positions of the unit from this chunk on
+        const bool two = left > kQ4Block;
+
+        // ---- S = K q^T
+        float s[2][4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
+            if (b == 1 && !two) continue;
+            const uint32_t kb = sb + b * kQ4BlockBytes;
+            const uint4 k0 = lds128(kb + koff), k1 = lds128(kb + koff + 512);
+            const uint32_t sc = lds32(kb + kQ4KScales + soff);
+            const uint32_t s0 = e4m3x2_half2(sc & 0xffffu), s1 = e4m3x2_half2(sc >> 16);
+            const uint32_t sd[2][2] = {{__byte_perm(s0, s0, 0x1010), __byte_perm(s0, s0, 0x3232)},
+                                       {__byte_perm(s1, s1, 0x1010), __byte_perm(s1, s1, 0x3232)}};
+            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t h0[4], h1[4];
+                q4_unpack(w0[q], h0);
+                q4_unpack(w1[q], h1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h0[e] = mul_half2(h0[e], sd[0][q >> 1]);
+                    h1[e] = mul_half2(h1[e], sd[1][q >> 1]);
+                }
+                mma_f16_16816(s[b], h0[0], h1[0], h0[1], h1[1], bq[2 * q][0], bq[2 * q][1]);
+                mma_f16_16816(s[b], h0[2], h1[2], h0[3], h1[3], bq[2 * q + 1][0], bq[2 * q + 1][1]);
+            }
+        }
+
+        // ---- softmax, base 2: s[b][0], [1]: heads 2c, 2c + 1 at position pi_r of block b; [2], [3]: at pi_r + 8
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            s[b][0] *= mulA;
+            s[b][1] *= mulB;
+            s[b][2] *= mulA;
+            s[b][3] *= mulB;
+        }
+        if (left < kQ4Chunk) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (16 * b + pi_r >= left) s[b][0] = s[b][1] = -CUDART_INF_F;
+                if (16 * b + pi_r + 8 >= left) s[b][2] = s[b][3] = -CUDART_INF_F;
+            }
+        }
+        float nA = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+        float nB = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            nA = fmaxf(nA, __shfl_xor_sync(kFull, nA, d));
+            nB = fmaxf(nB, __shfl_xor_sync(kFull, nB, d));
+        }
+        if (__any_sync(kFull, nA > mA || nB > mB)) {
+            nA = fmaxf(nA, mA);
+            nB = fmaxf(nB, mB);
+            // (a maximum still at -inf -- scores that are all NaN -- leaves nothing to rescale)
+            const float aA = nA == -CUDART_INF_F ? 1.f : ex2(mA - nA), aB = nB == -CUDART_INF_F ? 1.f : ex2(mB - nB);
+            mA = nA;
+            mB = nB;
+            lA *= aA;
+            lB *= aB;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                o[k][0] *= aA;
+                o[k][1] *= aB;
+                o[k][2] *= aA;
+                o[k][3] *= aB;
+            }
+        }
+        uint32_t pb[2][2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            float e[4];
+            e[0] = ex2(s[b][0] - mA);
+            e[1] = ex2(s[b][1] - mB);
+            e[2] = ex2(s[b][2] - mA);
+            e[3] = ex2(s[b][3] - mB);
+            lA += e[0] + e[2];
+            lB += e[1] + e[3];
+            const __half2 lo = __floats2half2_rn(e[0], e[1]), hi = __floats2half2_rn(e[2], e[3]);
+            pb[b][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&lo));
+            pb[b][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&hi));
+        }
+
+        // ---- O^T += V^T P
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            if (b == 1 && !two) continue;
+            const uint32_t vb = sb + b * kQ4BlockBytes;
+            const uint2 v0 = lds64(vb + voff0), v1 = lds64(vb + voff1);
+            const uint2 v2 = lds64(vb + voff0 + 512), v3 = lds64(vb + voff1 + 512);
+            uint32_t sc = lds32(vb + kQ4VScales + soff);
+            if (left < kQ4Chunk) {  // positions past the row's end: whatever their bytes are, a scale of 0 (codes are finite)
+                const int at = left - 16 * b;
+                if (pi_0 >= at) sc &= 0xffffff00u;
+                if (pi_1 >= at) sc &= 0xffff00ffu;
+                if (pi_0 + 8 >= at) sc &= 0xff00ffffu;
+                if (pi_1 + 8 >= at) sc &= 0x00ffffffu;
+            }
+            const uint32_t s01 = e4m3x2_half2(sc & 0xffffu), s23 = e4m3x2_half2(sc >> 16);
+            const uint32_t a0[2] = {v0.x, v0.y}, a1[2] = {v1.x, v1.y}, a2[2] = {v2.x, v2.y}, a3[2] = {v3.x, v3.y};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+                uint32_t e01[4], d01[4], e23[4], d23[4];  // even and odd dims of the two pairs of positions
+                q4_unpack((a0[q] & kLow) | ((a1[q] << 4) & ~kLow), e01);
+                q4_unpack(((a0[q] >> 4) & kLow) | (a1[q] & ~kLow), d01);
+                q4_unpack((a2[q] & kLow) | ((a3[q] << 4) & ~kLow), e23);
+                q4_unpack(((a2[q] >> 4) & kLow) | (a3[q] & ~kLow), d23);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    mma_f16_16816(o[4 * q + e], mul_half2(e01[e], s01), mul_half2(d01[e], s01), mul_half2(e23[e], s23),
+                                  mul_half2(d23[e], s23), pb[b][0], pb[b][1]);
+            }
+        }
+        __syncwarp();  // every lane has read the stage: it may be filled again
+
+        const bool last = cur.j == cur.n - 1;
+        if (last || i == count - 1) {  // end of the segment
+            float LA = lA, LB = lB;
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                LA += __shfl_xor_sync(kFull, LA, d);
+                LB += __shfl_xor_sync(kFull, LB, d);
+            }
+            if (c < 2) {
+                const float iA = p.v_scale / LA, iB = p.v_scale / LB;
+                const int hA = cur.g * kGroup + 2 * c;
+                // o[j][0], [2]: dims 16r + 2j, + 1 of head A; [1], [3] of head B
+                if (whole && last) {
+                    __nv_bfloat16* dst = p.out + ((int64_t)cur.t * H + hA) * kHeadDim + 16 * r;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t a[4], b[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            a[e] = pack_bf16(__float2bfloat16_rn(o[4 * k + e][0] * iA), __float2bfloat16_rn(o[4 * k + e][2] * iA));
+                            b[e] = pack_bf16(__float2bfloat16_rn(o[4 * k + e][1] * iB), __float2bfloat16_rn(o[4 * k + e][3] * iB));
+                        }
+                        *reinterpret_cast<uint4*>(dst + 8 * k) = make_uint4(a[0], a[1], a[2], a[3]);
+                        *reinterpret_cast<uint4*>(dst + kHeadDim + 8 * k) = make_uint4(b[0], b[1], b[2], b[3]);
+                    }
+                } else {
+                    const int64_t u = (int64_t)cur.t * G + cur.g + w;
+                    float* po = p.part_o + (u * kGroup + 2 * c) * kHeadDim + 16 * r;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        *reinterpret_cast<float4*>(po + 4 * k) = make_float4(o[2 * k][0] * iA, o[2 * k][2] * iA,
+                                                                              o[2 * k + 1][0] * iA, o[2 * k + 1][2] * iA);
+                        *reinterpret_cast<float4*>(po + kHeadDim + 4 * k) = make_float4(
+                            o[2 * k][1] * iB, o[2 * k][3] * iB, o[2 * k + 1][1] * iB, o[2 * k + 1][3] * iB);
+                    }
+                    if (r == 0)
+                        *reinterpret_cast<float2*>(p.part_lse + u * kGroup + 2 * c) = make_float2(mA + log2f(LA), mB + log2f(LB));
+                }
+            }
+            fresh = true;
+        }
+        q4_next(p, cur, i + 1 < count);
+    }
+    if (!ok) {  // the awaited copy is late: report, and let the copies in flight land before the CTA may exit
+        if (lane == 0) {
+            atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+            for (int k = max(0, issued - kQ4Stages); k < issued; ++k)
+                mbar_wait(bars + 8 * (k % kQ4Stages), (k / kQ4Stages) & 1, kWaitLimitNs);
+        }
+        __syncwarp();
+    }
+}
+
+// =====================================================================================
+// q4_combine_kernel: one CTA per (token, kv head) unit, warp = query head, lane = 4 dims
+// =====================================================================================
+struct Q4CombineParams {
+    const int32_t* prefix;
+    const float* part_o;
+    const float* part_lse;
+    __nv_bfloat16* out;
+    int ntok, heads, kv_heads, warps;  // warps: of the attention's grid
+};
+
+__global__ void __launch_bounds__(32 * kGroup) q4_combine_kernel(Q4CombineParams p)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.kv_heads;
+    const int u = blockIdx.x, t = u / G, g = u % G;
+    pdl_wait();
+    const int pre = p.prefix[t], n = p.prefix[t + 1] - pre, total = p.prefix[p.ntok];
+    __nv_bfloat16* dst = p.out + ((int64_t)t * p.heads + g * kGroup + warp) * kHeadDim + 4 * lane;
+    if (n == 0) {  // a skipped token
+        *reinterpret_cast<uint2*>(dst) = make_uint2(0u, 0u);
+        return;
+    }
+    const int64_t T = (int64_t)G * total, W = min((int64_t)p.warps, T);
+    const int64_t xb = (int64_t)G * pre + (int64_t)g * n;
+    // warp w holds chunks [w T / W, (w + 1) T / W): the one holding chunk x is ((x + 1) W - 1) / T
+    const int64_t wf = ((xb + 1) * W - 1) / T, wl = ((xb + n) * W - 1) / T;
+    if (wf == wl) return;  // one warp held it and wrote it out
+    const int np = (int)(wl - wf + 1);
+    const float* lse = p.part_lse + ((int64_t)u + wf) * kGroup + warp;
+    const float* po = p.part_o + (((int64_t)u + wf) * kGroup + warp) * kHeadDim + 4 * lane;
+    float M = -CUDART_INF_F;
+    for (int k = lane; k < np; k += 32) M = fmaxf(M, lse[(int64_t)k * kGroup]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int kBatch = 8;
+    for (int k0 = 0; k0 < np; k0 += kBatch) {
+        float4 x[kBatch];
+        float l[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int at = min(k0 + k, np - 1);
+            x[k] = *reinterpret_cast<const float4*>(po + (int64_t)at * kGroup * kHeadDim);
+            l[k] = k0 + k < np ? lse[(int64_t)at * kGroup] : -CUDART_INF_F;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (k0 + k >= np) break;
+            const float f = exp2f(l[k] - M);
+            sum += f;
+            acc[0] += f * x[k].x;
+            acc[1] += f * x[k].y;
+            acc[2] += f * x[k].z;
+            acc[3] += f * x[k].w;
+        }
+    }
+    const float inv = 1.f / sum;
+    const float y[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+    *reinterpret_cast<uint2*>(dst) = pack4(y);
+}
+
+// =====================================================================================
+// the decode call
+// =====================================================================================
+Q4Plan make_q4_plan(const pkv_pool* pool, int rows)
+{
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    Q4Plan pl;
+    pl.ctas = pool->ctas_override > 0 ? pool->ctas_override : pool->num_sms;
+    const size_t units = (size_t)rows * pool->cfg.kv_heads, slots = units + (size_t)pl.ctas * kQ4Warps;
+    const size_t heads = (size_t)rows * pool->cfg.heads;
+    size_t off = 0;
+    pl.off_len = off, off = up(off + sizeof(int32_t) * rows);
+    pl.off_prefix = off, off = up(off + sizeof(int32_t) * (rows + 1));
+    pl.off_qhat = off, off = up(off + sizeof(__half) * heads * kHeadDim);
+    pl.off_qmul = off, off = up(off + sizeof(float) * heads);
+    pl.off_po = off, off = up(off + sizeof(float) * slots * kGroup * kHeadDim);
+    pl.off_plse = off, off = up(off + sizeof(float) * slots * kGroup);
+    pl.total = off;
+    return pl;
+}
+
+cudaError_t configure_q4()
+{
+    return cudaFuncSetAttribute(q4_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4Smem::kAlloc);
+}
+
+cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& plan, cudaStream_t s)
+{
+    Q4AppendParams ap = append_params(pool);
+    ap.q = static_cast<const __nv_bfloat16*>(a.q);
+    ap.k = static_cast<const __nv_bfloat16*>(a.k);
+    ap.v = static_cast<const __nv_bfloat16*>(a.v);
+    ap.qw = static_cast<const __nv_bfloat16*>(a.q_norm_w);
+    ap.kw = static_cast<const __nv_bfloat16*>(a.k_norm_w);
+    ap.positions = a.step_positions;
+    ap.table = a.table;
+    ap.tokens = ap.rows = a.rows;
+    ap.pages = a.pages;
+    ap.q_hat = reinterpret_cast<__half*>(a.ws + plan.off_qhat);
+    ap.q_mul = reinterpret_cast<float*>(a.ws + plan.off_qmul);
+    ap.tok_len = reinterpret_cast<int32_t*>(a.ws + plan.off_len);
+    q4_append_kernel<true><<<a.rows, 32 * kQ4AppendWarps, 0, s>>>(ap);
+    cudaError_t rc = cudaGetLastError();
+    if (rc != cudaSuccess) return rc;
+
+    Q4AttnParams p;
+    p.q_hat = ap.q_hat;
+    p.q_mul = ap.q_mul;
+    p.tok_len = ap.tok_len;
+    p.table = a.table;
+    p.data = ap.data;
+    p.out = static_cast<__nv_bfloat16*>(a.out);
+    p.part_o = reinterpret_cast<float*>(a.ws + plan.off_po);
+    p.part_lse = reinterpret_cast<float*>(a.ws + plan.off_plse);
+    p.prefix = reinterpret_cast<int32_t*>(a.ws + plan.off_prefix);
+    p.err = pool->err;
+    p.ntok = a.rows;
+    p.pages = a.pages;
+    p.heads = pool->cfg.heads;
+    p.kv_heads = pool->cfg.kv_heads;
+    p.v_scale = pool->v_scale;
+    p.wait_ns = pool->wait_ns;
+    const bool timed = pool->timer_on != 0;
+    const int slot = timed ? (int)(pool->timer_count.fetch_add(1) % kTimerSlots) : 0;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)plan.ctas);
+    cfg.blockDim = dim3(32 * kQ4Warps);
+    cfg.dynamicSmemBytes = Q4Smem::kAlloc;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = timed ? 0 : 1;  // timed: the attention alone between the events
+    if (timed && (rc = cudaEventRecord(pool->ev_start[slot], s)) != cudaSuccess) return rc;
+    if ((rc = cudaLaunchKernelEx(&cfg, q4_attn_kernel, p)) != cudaSuccess) return rc;
+    if (timed && (rc = cudaEventRecord(pool->ev_stop[slot], s)) != cudaSuccess) return rc;
+
+    Q4CombineParams cp;
+    cp.prefix = p.prefix;
+    cp.part_o = p.part_o;
+    cp.part_lse = p.part_lse;
+    cp.out = p.out;
+    cp.ntok = a.rows;
+    cp.heads = p.heads;
+    cp.kv_heads = p.kv_heads;
+    cp.warps = plan.ctas * kQ4Warps;
+    cfg.gridDim = dim3((unsigned)((int64_t)a.rows * p.kv_heads));
+    cfg.blockDim = dim3(32 * kGroup);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, q4_combine_kernel, cp);
+}
+
+// =====================================================================================
+// q4_read_kernel: 16 lanes a (token, kv head), 8 for k and 8 for v, a group of 16 dims a lane
+// =====================================================================================
+struct Q4ReadParams {
+    const uint8_t* data;
+    const int32_t* positions;
+    const int32_t* prow;
+    const int32_t* table;
+    __nv_bfloat16* k;
+    __nv_bfloat16* v;
+    uint32_t* err;
+    int64_t token_stride, head_stride, items;
+    int rows, pages, num_pages, max_seq, kv_heads;
+    float k_scale, v_scale;
+};
+
+__global__ void __launch_bounds__(256) q4_read_kernel(Q4ReadParams p)
+{
+    const int64_t item = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    if (item >= p.items) return;
+    const int grp = (int)(item & 7), is_v = (int)((item >> 3) & 1);
+    const int64_t tg = item >> 4;
+    const int t = (int)(tg / p.kv_heads), g = (int)(tg % p.kv_heads);
+    const int pos = p.positions[t];
+    const int row = p.prow ? p.prow[t] : t;
+    uint32_t e = 0;
+    int page = -1;
+    if (pos != -1) {
+        if (row < 0 || row >= p.rows) {
+            e = PKV_DEVERR_ROW;
+        } else if (pos < 0 || pos >= p.max_seq || pos / kPageSize >= p.pages) {
+            e = PKV_DEVERR_POSITION;
+        } else {
+            page = page_of(p.table, p.pages, row, pos / kPageSize);
+            if (page < 0 || page >= p.num_pages) e = PKV_DEVERR_PAGE, page = -1;
+        }
+    }
+    if (e && (item & 15) == 0 && g == 0) atomicOr(p.err, e);
+    uint32_t r[8] = {};
+    if (page >= 0) {
+        const uint8_t* block = p.data + q4_block(page, p.kv_heads, g, pos % kPageSize);
+        const int i = pos % kQ4Block;
+        const uint2 w = *reinterpret_cast<const uint2*>(block + (is_v ? kQ4VCodes : 0) + q4_code_row(i, 8 * grp));
+        const uint32_t sc = block[is_v ? q4_v_scale(i, grp) : q4_k_scale(i, grp)];
+        const uint32_t s2 = e4m3x2_half2(sc | sc << 8);
+        const float s = is_v ? p.v_scale : p.k_scale;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t h[4];
+            q4_unpack(q ? w.y : w.x, h);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // code * scale has 6 bits: exact in fp16, and times s in bf16
+                const uint32_t m = mul_half2(h[k], s2);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+                r[4 * q + k] = pack_bf16(__float2bfloat16_rn(f.x * s), __float2bfloat16_rn(f.y * s));
+            }
+        }
+    }
+    uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + t * p.token_stride + g * p.head_stride + 16 * grp);
+    dst[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    dst[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+cudaError_t launch_q4_read(const pkv_pool* pool, const int32_t* positions, const int32_t* prow, const int32_t* table,
+                           int tokens, int rows, int pages, void* k, void* v, int64_t token_stride, int64_t head_stride,
+                           cudaStream_t s)
+{
+    Q4ReadParams p;
+    p.data = static_cast<const uint8_t*>(pool->q4);
+    p.positions = positions;
+    p.prow = prow;
+    p.table = table;
+    p.k = static_cast<__nv_bfloat16*>(k);
+    p.v = static_cast<__nv_bfloat16*>(v);
+    p.err = pool->err;
+    p.token_stride = token_stride;
+    p.head_stride = head_stride;
+    p.items = (int64_t)tokens * pool->cfg.kv_heads * 16;
+    p.rows = rows;
+    p.pages = pages;
+    p.num_pages = pool->num_pages;
+    p.max_seq = pool->cfg.max_seq;
+    p.kv_heads = pool->cfg.kv_heads;
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
+    q4_read_kernel<<<(unsigned)((p.items + 255) / 256), 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace pkv

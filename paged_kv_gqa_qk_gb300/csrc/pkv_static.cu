@@ -54,7 +54,7 @@ extern "C" int pkv_decode_static(pkv_pool* pool, const void* q, const void* k, c
 {
     pkv::NvtxRange range("pkv_decode_static");
     if (!pool || !q || !k || !v || !q_norm_w || !k_norm_w || !positions || !out) return PKV_EINVAL;
-    if (rows <= 0 || pages <= 0) return PKV_EINVAL;
+    if (rows <= 0 || pages <= 0 || pool->q4) return PKV_EINVAL;
     if (rows > (1 << 20) || (int64_t)rows * pages > INT32_MAX) return PKV_ERANGE;
     if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(out, 8) ||
         !aligned_to(q_norm_w, 8) || !aligned_to(k_norm_w, 8) || !aligned_to(positions, 4) || !aligned_to(table, 4))

@@ -388,7 +388,7 @@ PKV_API int pkv_decode_static(pkv_pool* pool, const void* q, const void* k, cons
  * with code one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives (4 bits: sign, two
  * exponent bits, one mantissa bit), scale the group's in 8 bits (e4m3) and s the pool's
  * k_scale or v_scale.  For the values x of a group -- the bf16 values a bf16 pool would
- * hold: k after QK-norm and RoPE rounded to bf16, v as given --
+ * hold: k after QK-norm and RoPE in fp32 (correctly rounded), rounded to bf16, v as given --
  *   scale = e4m3(max |x| / (6 s)),   code = e2m1(x / (scale s)),
  * each rounded to nearest, ties to even, scale at most 448; a group whose scale rounds to
  * 0 is 0.  A group holding an Inf or a NaN is stored as NaN.  k_scale and v_scale are

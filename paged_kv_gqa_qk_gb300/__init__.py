@@ -117,12 +117,18 @@ def _check(rc: int, what: str):
         raise PkvError(rc, what)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
+    """The stream's handle; None: the current device's current stream (asked for without making a torch stream)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
+
+
+def _capturing(stream) -> bool:
+    with _on(stream):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def _on(stream):
@@ -130,10 +136,10 @@ def _on(stream):
     return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
 
 
-def _dev(t: torch.Tensor | None, dtype: torch.dtype, what: str, allow_none: bool = False) -> ctypes.c_void_p:
+def _dev(t: torch.Tensor | None, dtype: torch.dtype, what: str, allow_none: bool = False) -> int | None:
     if t is None:
         if allow_none:
-            return ctypes.c_void_p(None)
+            return None
         raise ValueError(f"{what} is required")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch tensor")
@@ -143,7 +149,7 @@ def _dev(t: torch.Tensor | None, dtype: torch.dtype, what: str, allow_none: bool
         raise ValueError(f"{what} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 # ------------------------------------------------------------------ C ABI, one function each
@@ -206,10 +212,11 @@ def _table(table, rows, pages):
     if table is None:
         if rows is None or pages is None:
             raise ValueError("without a table, rows and pages are required")
-        return ctypes.c_void_p(None), int(rows), int(pages)
+        return None, int(rows), int(pages)
     if table.dim() != 2:
         raise ValueError(f"table must be [rows][pages], got {tuple(table.shape)}")
-    return _dev(table, torch.int32, "table"), int(table.shape[0]), int(table.shape[1])
+    rows, pages = table.shape
+    return _dev(table, torch.int32, "table"), rows, pages
 
 
 def pkv_decode(pool, q, k, v, q_norm_w, k_norm_w, positions, table, out, workspace, stream=None,
@@ -387,7 +394,7 @@ def pkv_q4_read(pool, positions, prow, table, k, v, stream=None, rows=None, page
     tp, rows, pages = _table(table, rows, pages)
     _check(load_library().pkv_q4_read(
         pool, _dev(positions, torch.int32, "positions"), _prow(prow, tokens), tp, tokens, rows, pages,
-        ctypes.c_void_p(k.data_ptr()), ctypes.c_void_p(v.data_ptr()), k.stride(0), k.stride(1), _stream(stream)),
+        k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), _stream(stream)),
         "pkv_q4_read")
 
 
@@ -407,31 +414,34 @@ def pkv_q4_decode(pool, q, k, v, q_norm_w, k_norm_w, positions, table, out, work
 def pkv_norm_rope(pool, q, k, q_norm_w, k_norm_w, positions, q_out, k_out, layout="half", stream=None) -> None:
     """QK-norm and RoPE of q [tokens][heads][head_dim] and k [tokens][kv_heads][head_dim] (heads contiguous, any
     token stride) into q_out and k_out (both bf16 or both fp32).  q or k may be None; no weights: no norm."""
-    tokens, kinds, ptrs, strides = int(positions.shape[0]), set(), [], []
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if (x is None) != (y is None):
-            raise ValueError(f"{name} and {name}_out are given together")
-        for what, t in ((name, x), (name + "_out", y)):
-            if t is None:
-                ptrs.append(None)
-                strides.append(0)
-                continue
-            if not t.is_cuda or t.dtype not in (torch.bfloat16, torch.float32) or (t is x and t.dtype != torch.bfloat16):
-                raise TypeError(f"{what} must be a CUDA tensor, inputs bf16 and outputs bf16 or fp32")
-            if t.dim() != 3 or t.shape != x.shape or t.shape[0] != tokens or t.stride(2) != 1 \
-                    or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-                raise ValueError(f"{what} must be [{tokens}][heads][head_dim] with heads contiguous, as its input")
-            ptrs.append(ctypes.c_void_p(t.data_ptr()))
-            strides.append(t.stride(0) if tokens > 1 else t.shape[1] * t.shape[2])
-            if t is y:
-                kinds.add(t.dtype)
-    if len(kinds) != 1:
-        raise TypeError("q_out and k_out must have one type")
+    tokens = positions.shape[0]
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q and q_out, and k and k_out, are given together")
+    kind = (k_out if q_out is None else q_out).dtype
+    if kind not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"outputs must be bf16 or fp32, got {kind}")
+    qp, qs = _heads(q, torch.bfloat16, "q", tokens, q)
+    kp, ks = _heads(k, torch.bfloat16, "k", tokens, k)
+    qo, qos = _heads(q_out, kind, "q_out", tokens, q)
+    ko, kos = _heads(k_out, kind, "k_out", tokens, k)
     _check(load_library().pkv_norm_rope(
-        pool, ptrs[0], ptrs[2], _dev(q_norm_w, torch.bfloat16, "q_norm_w", allow_none=True),
+        pool, qp, kp, _dev(q_norm_w, torch.bfloat16, "q_norm_w", allow_none=True),
         _dev(k_norm_w, torch.bfloat16, "k_norm_w", allow_none=True), _dev(positions, torch.int32, "positions"), tokens,
-        ROPE_LAYOUTS[layout], int(kinds == {torch.float32}), strides[0], strides[2], ptrs[1], ptrs[3], strides[1],
-        strides[3], _stream(stream)), "pkv_norm_rope")
+        ROPE_LAYOUTS[layout], kind is torch.float32, qs, ks, qo, ko, qos, kos, _stream(stream)), "pkv_norm_rope")
+
+
+def _heads(x, dtype, what, tokens, like):
+    """(pointer, token stride) of [tokens][heads][head_dim] with contiguous heads."""
+    if x is None:
+        return None, 0
+    if x.dtype != dtype or not x.is_cuda:
+        raise TypeError(f"{what} must be a {dtype} CUDA tensor, got {x.dtype}")
+    if x.dim() != 3 or x.shape != like.shape or x.shape[0] != tokens:
+        raise ValueError(f"{what} must be [{tokens}][heads][head_dim], as its input, got {tuple(x.shape)}")
+    st, (_, h, d) = x.stride(), x.shape
+    if st[2] != 1 or (h > 1 and st[1] != d):
+        raise ValueError(f"{what} must have contiguous heads, got strides {st}")
+    return x.data_ptr(), st[0] if tokens > 1 else h * d
 
 
 def pkv_rope_frequencies(cfg, scaling="none", factor: float = 1.0, trained: int = 0):
@@ -616,6 +626,7 @@ class Q4KVPool(_Pool):
         if data.dtype != torch.uint8 or data.numel() == 0 or data.numel() % per_page:
             raise ValueError(f"data must be uint8, a multiple of {per_page} bytes, got {data.dtype} x {data.numel()}")
         self.data, self.cfg, self.device, self._streams = data, c, data.device, {}
+        self._heads, self._kv_heads, self._dim = c.heads, c.kv_heads, c.head_dim
         self.num_pages = data.numel() // per_page
         self.handle = pkv_q4_pool_wrap(c, self.num_pages, data, k_scale, v_scale, stream)
 
@@ -624,52 +635,60 @@ class Q4KVPool(_Pool):
         data = torch.zeros(pkv_q4_pool_bytes(cfg, num_pages), dtype=torch.uint8, device=device)
         return cls(data, cfg, k_scale, v_scale, stream)
 
-    def _scratch(self, rows: int, pages: int, stream) -> torch.Tensor:
-        """A workspace for one call on `stream`: one kept per stream, and a captured call's own (it belongs to its
-        graph, so that graphs and eager calls may run at the same time)."""
-        n = pkv_workspace_bytes(self.handle, rows, pages, 0)
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        with _on(s):
-            if torch.cuda.is_current_stream_capturing():
-                return torch.empty(n, dtype=torch.uint8, device=self.device)
-            key = s.cuda_stream if isinstance(s, torch.cuda.Stream) else int(s)
-            ws = self._streams.get(key)
-            if ws is None or ws.numel() < n:
-                ws = self._streams[key] = torch.empty(n, dtype=torch.uint8, device=self.device)
-            return ws
-
-    def _shapes(self, **tensors):
-        c = self.cfg
-        for name, x in tensors.items():
-            h = c.heads if name in ("q", "out") else c.kv_heads
-            if x.dim() != 3 or x.shape[1] != h or x.shape[2] != c.head_dim:
-                raise ValueError(f"{name} must be [tokens][{h}][{c.head_dim}], got {tuple(x.shape)}")
+    def _shape(self, name, x, tokens, heads):
+        if x.shape != (tokens, heads, self._dim):
+            raise ValueError(f"{name} must be [{tokens}][{heads}][{self._dim}], got {tuple(x.shape)}")
 
     def append(self, k, v, k_norm_w, positions, prow, table, stream=None, rows=None, pages=None) -> None:
         """k normed and roped, then k and v quantised into their slots (prow None: token t is row t)."""
-        self._shapes(k=k, v=v)
+        n = positions.shape[0]
+        self._shape("k", k, n, self._kv_heads)
+        self._shape("v", v, n, self._kv_heads)
         pkv_q4_append(self.handle, k, v, k_norm_w, positions, prow, table, stream, rows=rows, pages=pages)
 
     def read(self, positions, prow, table, k=None, v=None, stream=None, rows=None, pages=None):
         """(k, v) [tokens][kv_heads][head_dim] that the pool holds at the tokens' positions."""
-        c, shape = self.cfg, (positions.shape[0], self.cfg.kv_heads, self.cfg.head_dim)
-        with _on(stream):
-            k = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if k is None else k
-            v = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if v is None else v
-        self._shapes(k=k, v=v)
+        n = positions.shape[0]
+        if k is None or v is None:
+            with _on(stream):
+                new = torch.empty(2, n, self._kv_heads, self._dim, dtype=torch.bfloat16, device=self.device)
+            k, v = new[0] if k is None else k, new[1] if v is None else v
+        self._shape("k", k, n, self._kv_heads)
+        self._shape("v", v, n, self._kv_heads)
         pkv_q4_read(self.handle, positions, prow, table, k, v, stream, rows=rows, pages=pages)
         return k, v
 
     def decode(self, q, k, v, q_norm_w, k_norm_w, positions, table, out=None, stream=None, pages=None) -> torch.Tensor:
-        """One step of every row: append its k and v, attend over its cached positions."""
+        """One step of every row: append its k and v, attend over its cached positions.
+
+        The workspace is the class's own: one kept per stream, and each captured call's in its graph, so that graphs
+        and calls on other streams may run at the same time."""
         if out is None:
             with _on(stream):
                 out = torch.empty_like(q)
-        self._shapes(q=q, k=k, v=v, out=out)
         rows = positions.shape[0]
-        if q.shape[0] != rows or k.shape[0] != rows or v.shape[0] != rows or out.shape[0] != rows:
-            raise ValueError(f"q, k, v and out must have {rows} tokens, as positions")
+        self._shape("q", q, rows, self._heads)
+        self._shape("k", k, rows, self._kv_heads)
+        self._shape("v", v, rows, self._kv_heads)
+        self._shape("out", out, rows, self._heads)
         pages = table.shape[1] if table is not None else pages
-        pkv_q4_decode(self.handle, q, k, v, q_norm_w, k_norm_w, positions, table, out,
-                      self._scratch(rows, pages, stream), stream, pages=pages)
+        raw = _stream(stream)
+        ws = self._streams.get(raw)
+        if ws is None or _capturing(stream):
+            ws = self._new_workspace(raw, rows, pages, stream)
+        try:
+            pkv_q4_decode(self.handle, q, k, v, q_norm_w, k_norm_w, positions, table, out, ws, raw, pages=pages)
+        except PkvError as e:
+            if e.code != PKV_EWORKSPACE:
+                raise
+            ws = self._new_workspace(raw, rows, pages, stream)   # more rows than any call on this stream so far
+            pkv_q4_decode(self.handle, q, k, v, q_norm_w, k_norm_w, positions, table, out, ws, raw, pages=pages)
         return out
+
+    def _new_workspace(self, raw: int, rows: int, pages: int, stream) -> torch.Tensor:
+        n = pkv_workspace_bytes(self.handle, rows, pages, 0)
+        with _on(stream):
+            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        if not _capturing(stream):
+            self._streams[raw] = ws
+        return ws

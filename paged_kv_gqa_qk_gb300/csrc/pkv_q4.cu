@@ -1,9 +1,9 @@
 // A page pool in 4 bits: appending to it, reading it back, and the decode
 // attention over it (sm_103a).  The format is in pkv_q4.cuh.
 //
-//   q4_append_kernel  QK-norm + RoPE of k, quantise k and v, write them to their
-//                     slots; in front of the attention also each token's check,
-//                     its attended length and its prepared query heads
+//   q4_append_kernel  QK-norm + RoPE of k, quantise k and v, write them to their slots
+//   q4_prep_kernel    the same in front of the attention, with each row's check, its
+//                     attended length and its prepared query heads
 //   q4_attn_kernel    split attention: every warp streams its own share of the
 //                     call's 32-position chunks through its own ring of bulk
 //                     copies and keeps its own softmax state
@@ -15,6 +15,8 @@
 // src/attention.linnet, GroupedQueryAttention.decode_paged.
 #include <math_constants.h>
 
+#include <algorithm>
+
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
 #include "pkv_q4.cuh"
@@ -22,7 +24,7 @@
 namespace pkv {
 
 // =====================================================================================
-// q4_append_kernel
+// q4_append_kernel, q4_prep_kernel
 // =====================================================================================
 struct Q4AppendParams {
     const __nv_bfloat16* q;     // decode: [tokens][heads][128]
@@ -41,92 +43,151 @@ struct Q4AppendParams {
     int32_t* tok_len;           // decode: [tokens], 0: skip
     uint32_t* err;
     int tokens, rows, pages, num_pages, max_seq, heads, kv_heads, rot;
-    float eps, k_scale, v_scale;
+    float eps, k_scale;
     float2 eps2;                // eps as a pair of floats
+    float k_inv6, k_inv, v_inv6, v_inv;  // 1 / (6 s) and 1 / s of the pool's scales
 };
+
+// The two 16-byte pieces of a head vector that lane j of 8 holds.
+__device__ __forceinline__ void load16(const __nv_bfloat16* head, int j, uint4 (&r)[2])
+{
+    r[0] = *reinterpret_cast<const uint4*>(head + 8 * j);
+    r[1] = *reinterpret_cast<const uint4*>(head + 64 + 8 * j);
+}
+
+// Position and row of token t: the error bit, or 0 (then, if `active`, the token's pages can be looked up).
+__device__ __forceinline__ uint32_t q4_token(const Q4AppendParams& p, int t, int& pos, int& row, bool& active)
+{
+    pos = p.positions[t];
+    row = p.prow ? p.prow[t] : t;
+    active = pos != -1;
+    if (!active) return 0;
+    if (row < 0 || row >= p.rows) return PKV_DEVERR_ROW;
+    if (pos < 0 || pos >= p.max_seq || pos / kPageSize >= p.pages) return PKV_DEVERR_POSITION;
+    return 0;
+}
+
+// k and v of up to 4 kv heads of one token, 8 lanes each (kraw, vraw: this lane's
+// pieces; g: its head; live: there is such a head).  All lanes take part.
+template <bool kFullRot>
+__device__ __forceinline__ void q4_append_heads(const Q4AppendParams& p, const uint4 (&kraw)[2], const uint4 (&vraw)[2],
+                                                const uint4 (&wk)[2], int g, bool live, int page, int pos, int lane)
+{
+    const int64_t at = (int64_t)pos * kRopeHalf;
+    float x[16], k[16];
+    unpack16(kraw[0], kraw[1], x);
+    norm_rope_k_paired<kFullRot>(x, wk, p.rope_hi + at, p.rope_lo + at, p.eps2, lane, p.rot, k);
+    unpack16(vraw[0], vraw[1], x);
+    // (heads beyond the last quantise zeros and store nothing: the shuffles want every lane)
+    uint8_t* block = p.data + q4_block(page, p.kv_heads, live ? g : 0, pos % kPageSize);
+    q4_store(block, false, pos % kQ4Block, k, p.k_inv6, p.k_inv, lane & 7, live);
+    q4_store(block, true, pos % kQ4Block, x, p.v_inv6, p.v_inv, lane & 7, live);
+}
 
 constexpr int kQ4AppendWarps = 4;
 
-// One CTA per token; warp w takes kv heads w, w + 4, ... (and their query heads).
-template <bool kDecode>
+// pkv_q4_append: a warp takes 4 kv heads of one token.
+template <bool kFullRot>
 __global__ void __launch_bounds__(32 * kQ4AppendWarps) q4_append_kernel(Q4AppendParams p)
 {
-    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_launch_dependents();
-    const int pos = p.positions[t];
-    const int row = p.prow ? p.prow[t] : t;
-    const bool active = pos != -1;
-    uint32_t e = 0;
-    if (active) {
-        if (row < 0 || row >= p.rows)
-            e = PKV_DEVERR_ROW;
-        else if (pos < 0 || pos >= p.max_seq || pos / kPageSize >= p.pages)
-            e = PKV_DEVERR_POSITION;
+    const int lane = threadIdx.x & 31, j = lane & 7, quads = (p.kv_heads + 3) / 4;
+    const int item = blockIdx.x * kQ4AppendWarps + (threadIdx.x >> 5), t = item / quads;
+    if (t >= p.tokens) return;
+    const int g = 4 * (item % quads) + (lane >> 3);
+    const bool live = g < p.kv_heads;
+    uint4 kraw[2] = {}, vraw[2] = {}, wk[2];
+    if (live) {
+        const int64_t src = ((int64_t)t * p.kv_heads + g) * kHeadDim;
+        load16(p.k + src, j, kraw);
+        load16(p.v + src, j, vraw);
     }
-    int page = 0;
+    load16(p.kw, j, wk);
+    int pos, row, page = 0;
+    bool active;
+    uint32_t e = q4_token(p, t, pos, row, active);
     if (active && !e) {
-        // the written page, and before an attention every page that it will read
-        const int npg = pos / kPageSize + 1;
-        int bad = 0;
-        for (int i = kDecode ? (int)threadIdx.x : npg - 1; i < npg; i += kDecode ? (int)blockDim.x : 1) {
+        page = page_of(p.table, p.pages, row, pos / kPageSize);
+        if (page < 0 || page >= p.num_pages) e = PKV_DEVERR_PAGE;
+    }
+    if (e && lane == 0) atomicOr(p.err, e);
+    if (!active || e) return;
+    q4_append_heads<kFullRot>(p, kraw, vraw, wk, g, live, page, pos, lane);
+}
+
+// In front of the attention: one CTA per row checks every page that the row will read,
+// writes its attended length, appends its k and v (items 0 .. quads - 1 of 4 kv heads)
+// and prepares its queries (items from there on, the 4 query heads of a kv head each).
+template <bool kFullRot>
+__global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
+{
+    const int t = blockIdx.x, lane = threadIdx.x & 31, j = lane & 7, sub = lane >> 3, warps = blockDim.x >> 5;
+    const int quads = (p.kv_heads + 3) / 4, items = quads + p.kv_heads;
+    pdl_launch_dependents();
+    // a warp's first item's inputs go out before anything that they do not depend on
+    int item = threadIdx.x >> 5;
+    uint4 a[2] = {}, b[2] = {}, w[2];
+    auto load = [&]() {
+        if (item < quads) {
+            const int g = 4 * item + sub;
+            if (g < p.kv_heads) {
+                const int64_t src = ((int64_t)t * p.kv_heads + g) * kHeadDim;
+                load16(p.k + src, j, a);
+                load16(p.v + src, j, b);
+            }
+            load16(p.kw, j, w);
+        } else if (item < items) {
+            load16(p.q + ((int64_t)t * p.heads + 4 * (item - quads) + sub) * kHeadDim, j, a);
+            load16(p.qw, j, w);
+        }
+    };
+    load();
+    int pos, row, page = 0;
+    bool active;
+    uint32_t e = q4_token(p, t, pos, row, active);
+    int bad = 0;
+    if (active && !e) {
+        const int last = pos / kPageSize;
+        page = page_of(p.table, p.pages, row, last);
+        for (int i = threadIdx.x; i <= last; i += blockDim.x) {
             const int id = page_of(p.table, p.pages, row, i);
             bad |= id < 0 || id >= p.num_pages;
         }
-        if (kDecode ? __syncthreads_or(bad) : bad) e = PKV_DEVERR_PAGE;
-        page = page_of(p.table, p.pages, row, npg - 1);
     }
+    if (__syncthreads_or(bad)) e = PKV_DEVERR_PAGE;
     const bool ok = active && !e;
     if (threadIdx.x == 0) {
-        if (kDecode) p.tok_len[t] = ok ? pos + 1 : 0;
+        p.tok_len[t] = ok ? pos + 1 : 0;
         if (e) atomicOr(p.err, e);
     }
     if (!ok) return;
-
-    float2 rh[4], rl[4];
-    {
-        const int f0 = krope(lane, p.rot).f0;
-        const float4* h4 = reinterpret_cast<const float4*>(p.rope_hi + (int64_t)pos * kRopeHalf + f0);
-        const float4* l4 = reinterpret_cast<const float4*>(p.rope_lo + (int64_t)pos * kRopeHalf + f0);
-        const float4 a = h4[0], b = h4[1], c = l4[0], d = l4[1];
-        rh[0] = make_float2(a.x, a.y), rh[1] = make_float2(a.z, a.w), rh[2] = make_float2(b.x, b.y),
-        rh[3] = make_float2(b.z, b.w);
-        rl[0] = make_float2(c.x, c.y), rl[1] = make_float2(c.z, c.w), rl[2] = make_float2(d.x, d.y),
-        rl[3] = make_float2(d.z, d.w);
-    }
-    float wk[4];
-    unpack4(*reinterpret_cast<const uint2*>(p.kw + 4 * lane), wk);
-    const int i = pos % kQ4Block;
-    for (int g = warp; g < p.kv_heads; g += kQ4AppendWarps) {
-        const int64_t src = ((int64_t)t * p.kv_heads + g) * kHeadDim + 4 * lane;
-        const uint2 kraw = *reinterpret_cast<const uint2*>(p.k + src);
-        const uint2 vraw = *reinterpret_cast<const uint2*>(p.v + src);
-        uint8_t* block = p.data + q4_block(page, p.kv_heads, g, pos % kPageSize);
-        float x[4];
-        norm_rope_k_paired(kraw, wk, rh, rl, p.eps2, lane, p.rot, x);
-        q4_store(block, false, i, x, p.k_scale, lane);
-        unpack4(vraw, x);
-        q4_store(block, true, i, x, p.v_scale, lane);
-    }
-    if constexpr (kDecode) {
-        // the query heads, each scaled by a power of two to largest value in [1, 2), so that fp16
-        // keeps 11 bits of it whatever its size; the attention's scores take the inverse
-        float wq[4];
-        unpack4(*reinterpret_cast<const uint2*>(p.qw + 4 * lane), wq);
-        for (int h = warp; h < p.heads; h += kQ4AppendWarps) {
-            const int64_t src = ((int64_t)t * p.heads + h) * kHeadDim + 4 * lane;
-            const float4 y = norm_rope_q_regs(*reinterpret_cast<const uint2*>(p.q + src), wq, rh, p.eps, lane, p.rot);
-            float top = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-            const int ex = min(max((int)(__float_as_uint(top) >> 23), 1), 253);  // 2^(ex - 127) <= top < twice that
-            const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
-            const __half2 lo = __floats2half2_rn(y.x * down, y.y * down), hi = __floats2half2_rn(y.z * down, y.w * down);
-            uint2 r;
-            r.x = *reinterpret_cast<const uint32_t*>(&lo);
-            r.y = *reinterpret_cast<const uint32_t*>(&hi);
-            *reinterpret_cast<uint2*>(p.q_hat + src) = r;
-            if (lane == 0) p.q_mul[(int64_t)t * p.heads + h] = __uint_as_float((uint32_t)ex << 23) * kQScale * p.k_scale;
+    for (; item < items; item += warps, load()) {
+        if (item < quads) {
+            const int g = 4 * item + sub;
+            q4_append_heads<kFullRot>(p, a, b, w, g, g < p.kv_heads, page, pos, lane);
+            continue;
         }
+        // a query head, scaled by a power of two to largest value in [1, 2), so that fp16 keeps
+        // 11 bits of it whatever its size; the attention's scores take the inverse
+        float x[16], y[16];
+        unpack16(a[0], a[1], x);
+        norm_rope_q16<kFullRot>(x, w, p.rope_hi + (int64_t)pos * kRopeHalf, p.eps, lane, p.rot, y);
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(y[k]));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        const int ex = min(max((int)(__float_as_uint(top) >> 23), 1), 253);  // 2^(ex - 127) <= top < twice that
+        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+        uint32_t r[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const __half2 h = __floats2half2_rn(y[2 * k] * down, y[2 * k + 1] * down);
+            r[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        const int64_t head = (int64_t)t * p.heads + 4 * (item - quads) + sub;
+        *reinterpret_cast<uint4*>(p.q_hat + head * kHeadDim + 8 * j) = make_uint4(r[0], r[1], r[2], r[3]);
+        *reinterpret_cast<uint4*>(p.q_hat + head * kHeadDim + 64 + 8 * j) = make_uint4(r[4], r[5], r[6], r[7]);
+        if (j == 0) p.q_mul[head] = __uint_as_float((uint32_t)ex << 23) * kQScale * p.k_scale;
     }
 }
 
@@ -145,7 +206,10 @@ static Q4AppendParams append_params(const pkv_pool* pool)
     p.eps = (float)pool->cfg.eps;
     p.eps2 = make_float2(p.eps, (float)(pool->cfg.eps - (double)p.eps));
     p.k_scale = pool->k_scale;
-    p.v_scale = pool->v_scale;
+    p.k_inv6 = (1.f / 6.f) / pool->k_scale;  // (the scales are powers of two)
+    p.k_inv = 1.f / pool->k_scale;
+    p.v_inv6 = (1.f / 6.f) / pool->v_scale;
+    p.v_inv = 1.f / pool->v_scale;
     return p;
 }
 
@@ -163,7 +227,8 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
     p.tokens = tokens;
     p.rows = rows;
     p.pages = pages;
-    q4_append_kernel<false><<<tokens, 32 * kQ4AppendWarps, 0, s>>>(p);
+    const unsigned grid = (unsigned)(((int64_t)tokens * ((p.kv_heads + 3) / 4) + kQ4AppendWarps - 1) / kQ4AppendWarps);
+    (p.rot == kHeadDim ? q4_append_kernel<true> : q4_append_kernel<false>)<<<grid, 32 * kQ4AppendWarps, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -638,7 +703,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
 }
 
 // =====================================================================================
-// q4_combine_kernel: one CTA per (token, kv head) unit, warp = query head, lane = 4 dims
+// q4_combine_kernel: one CTA per (token, kv head) unit; kSub warps share a query head's
+// pieces, a lane holds 4 dims
 // =====================================================================================
 struct Q4CombineParams {
     const int32_t* prefix;
@@ -648,15 +714,20 @@ struct Q4CombineParams {
     int ntok, heads, kv_heads, warps;  // warps: of the attention's grid
 };
 
-__global__ void __launch_bounds__(32 * kGroup) q4_combine_kernel(Q4CombineParams p)
+// out = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M).  Each warp takes every kSub-th piece,
+// kBatch of them in flight, and its own maximum; the warps' sums are joined in warp order.
+// Few units mean many pieces each, and few CTAs: they get 4 warps a head.
+template <int kSub, int kBatch>
+__global__ void __launch_bounds__(32 * kGroup * kSub) q4_combine_kernel(Q4CombineParams p)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.kv_heads;
+    const int head = warp % kGroup, sub = warp / kGroup;
     const int u = blockIdx.x, t = u / G, g = u % G;
     pdl_wait();
     const int pre = p.prefix[t], n = p.prefix[t + 1] - pre, total = p.prefix[p.ntok];
-    __nv_bfloat16* dst = p.out + ((int64_t)t * p.heads + g * kGroup + warp) * kHeadDim + 4 * lane;
+    __nv_bfloat16* dst = p.out + ((int64_t)t * p.heads + g * kGroup + head) * kHeadDim + 4 * lane;
     if (n == 0) {  // a skipped token
-        *reinterpret_cast<uint2*>(dst) = make_uint2(0u, 0u);
+        if (sub == 0) *reinterpret_cast<uint2*>(dst) = make_uint2(0u, 0u);
         return;
     }
     const int64_t T = (int64_t)G * total, W = min((int64_t)p.warps, T);
@@ -665,32 +736,55 @@ __global__ void __launch_bounds__(32 * kGroup) q4_combine_kernel(Q4CombineParams
     const int64_t wf = ((xb + 1) * W - 1) / T, wl = ((xb + n) * W - 1) / T;
     if (wf == wl) return;  // one warp held it and wrote it out
     const int np = (int)(wl - wf + 1);
-    const float* lse = p.part_lse + ((int64_t)u + wf) * kGroup + warp;
-    const float* po = p.part_o + (((int64_t)u + wf) * kGroup + warp) * kHeadDim + 4 * lane;
-    float M = -CUDART_INF_F;
-    for (int k = lane; k < np; k += 32) M = fmaxf(M, lse[(int64_t)k * kGroup]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    constexpr int kBatch = 8;
-    for (int k0 = 0; k0 < np; k0 += kBatch) {
+    const float* lse = p.part_lse + ((int64_t)u + wf) * kGroup + head;
+    const float* po = p.part_o + (((int64_t)u + wf) * kGroup + head) * kHeadDim + 4 * lane;
+    float M = -CUDART_INF_F, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k0 = sub; k0 < np; k0 += kSub * kBatch) {
         float4 x[kBatch];
-        float l[kBatch];
+        float l[kBatch], m = M;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int at = min(k0 + k, np - 1);
-            x[k] = *reinterpret_cast<const float4*>(po + (int64_t)at * kGroup * kHeadDim);
-            l[k] = k0 + k < np ? lse[(int64_t)at * kGroup] : -CUDART_INF_F;
+            const int64_t at = min(k0 + k * kSub, np - 1);
+            x[k] = *reinterpret_cast<const float4*>(po + at * kGroup * kHeadDim);
+            l[k] = k0 + k * kSub < np ? lse[at * kGroup] : -CUDART_INF_F;
         }
 #pragma unroll
+        for (int k = 0; k < kBatch; ++k) m = fmaxf(m, l[k]);
+        const float f0 = M == -CUDART_INF_F ? 0.f : exp2f(M - m);
+        sum *= f0;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) acc[d] *= f0;
+        M = m;
+#pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            if (k0 + k >= np) break;
-            const float f = exp2f(l[k] - M);
+            if (k0 + k * kSub >= np) break;
+            const float f = exp2f(l[k] - M);  // (all pieces NaN: M stays -inf, and this is NaN)
             sum += f;
             acc[0] += f * x[k].x;
             acc[1] += f * x[k].y;
             acc[2] += f * x[k].z;
             acc[3] += f * x[k].w;
+        }
+    }
+    if constexpr (kSub > 1) {
+        __shared__ float part[kSub][kGroup][6][32];
+        float(&mine)[6][32] = part[sub][head];
+        mine[0][lane] = acc[0], mine[1][lane] = acc[1], mine[2][lane] = acc[2], mine[3][lane] = acc[3];
+        mine[4][lane] = sum, mine[5][lane] = M;
+        __syncthreads();
+        if (sub != 0) return;
+        float all = -CUDART_INF_F;
+#pragma unroll
+        for (int q = 0; q < kSub; ++q) all = fmaxf(all, part[q][head][5][lane]);
+        sum = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+#pragma unroll
+        for (int q = 0; q < kSub; ++q) {
+            if (q >= np) break;  // no piece, no maximum
+            const float(&o)[6][32] = part[q][head];
+            const float f = exp2f(o[5][lane] - all);
+            sum += f * o[4][lane];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) acc[d] += f * o[d][lane];
         }
     }
     const float inv = 1.f / sum;
@@ -739,7 +833,8 @@ cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& pl
     ap.q_hat = reinterpret_cast<__half*>(a.ws + plan.off_qhat);
     ap.q_mul = reinterpret_cast<float*>(a.ws + plan.off_qmul);
     ap.tok_len = reinterpret_cast<int32_t*>(a.ws + plan.off_len);
-    q4_append_kernel<true><<<a.rows, 32 * kQ4AppendWarps, 0, s>>>(ap);
+    const int items = (ap.kv_heads + 3) / 4 + ap.kv_heads;
+    (ap.rot == kHeadDim ? q4_prep_kernel<true> : q4_prep_kernel<false>)<<<a.rows, 32 * std::min(items, 16), 0, s>>>(ap);
     cudaError_t rc = cudaGetLastError();
     if (rc != cudaSuccess) return rc;
 
@@ -785,14 +880,18 @@ cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& pl
     cp.heads = p.heads;
     cp.kv_heads = p.kv_heads;
     cp.warps = plan.ctas * kQ4Warps;
-    cfg.gridDim = dim3((unsigned)((int64_t)a.rows * p.kv_heads));
-    cfg.blockDim = dim3(32 * kGroup);
+    const int64_t units = (int64_t)a.rows * p.kv_heads;
+    const bool few = units < 2 * (int64_t)plan.ctas;
+    cfg.gridDim = dim3((unsigned)units);
+    cfg.blockDim = dim3(32 * kGroup * (few ? 4 : 1));
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, q4_combine_kernel, cp);
+    cfg.numAttrs = 1;
+    return few ? cudaLaunchKernelEx(&cfg, q4_combine_kernel<4, 8>, cp) : cudaLaunchKernelEx(&cfg, q4_combine_kernel<1, 8>, cp);
 }
 
 // =====================================================================================
-// q4_read_kernel: 16 lanes a (token, kv head), 8 for k and 8 for v, a group of 16 dims a lane
+// q4_read_kernel: a warp takes 4 kv heads of one token, 8 lanes each, lane j the dims
+// 8j .. 8j + 7 and 64 + 8j .. of k and v (as the append's lanes): 16-byte stores
 // =====================================================================================
 struct Q4ReadParams {
     const uint8_t* data;
@@ -802,18 +901,19 @@ struct Q4ReadParams {
     __nv_bfloat16* k;
     __nv_bfloat16* v;
     uint32_t* err;
-    int64_t token_stride, head_stride, items;
-    int rows, pages, num_pages, max_seq, kv_heads;
+    int64_t token_stride, head_stride;
+    int tokens, rows, pages, num_pages, max_seq, kv_heads;
     float k_scale, v_scale;
 };
 
-__global__ void __launch_bounds__(256) q4_read_kernel(Q4ReadParams p)
+constexpr int kQ4ReadWarps = 8;
+
+__global__ void __launch_bounds__(32 * kQ4ReadWarps) q4_read_kernel(Q4ReadParams p)
 {
-    const int64_t item = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-    if (item >= p.items) return;
-    const int grp = (int)(item & 7), is_v = (int)((item >> 3) & 1);
-    const int64_t tg = item >> 4;
-    const int t = (int)(tg / p.kv_heads), g = (int)(tg % p.kv_heads);
+    const int lane = threadIdx.x & 31, j = lane & 7, quads = (p.kv_heads + 3) / 4;
+    const int item = blockIdx.x * kQ4ReadWarps + (threadIdx.x >> 5), t = item / quads;
+    if (t >= p.tokens) return;
+    const int g = 4 * (item % quads) + (lane >> 3);
     const int pos = p.positions[t];
     const int row = p.prow ? p.prow[t] : t;
     uint32_t e = 0;
@@ -828,30 +928,38 @@ __global__ void __launch_bounds__(256) q4_read_kernel(Q4ReadParams p)
             if (page < 0 || page >= p.num_pages) e = PKV_DEVERR_PAGE, page = -1;
         }
     }
-    if (e && (item & 15) == 0 && g == 0) atomicOr(p.err, e);
-    uint32_t r[8] = {};
+    if (e && lane == 0) atomicOr(p.err, e);
+    if (g >= p.kv_heads) return;
+    uint32_t word[2][2] = {}, scale[2][2] = {};
     if (page >= 0) {
         const uint8_t* block = p.data + q4_block(page, p.kv_heads, g, pos % kPageSize);
         const int i = pos % kQ4Block;
-        const uint2 w = *reinterpret_cast<const uint2*>(block + (is_v ? kQ4VCodes : 0) + q4_code_row(i, 8 * grp));
-        const uint32_t sc = block[is_v ? q4_v_scale(i, grp) : q4_k_scale(i, grp)];
-        const uint32_t s2 = e4m3x2_half2(sc | sc << 8);
-        const float s = is_v ? p.v_scale : p.k_scale;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            uint32_t h[4];
-            q4_unpack(q ? w.y : w.x, h);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // code * scale has 6 bits: exact in fp16, and times s in bf16
-                const uint32_t m = mul_half2(h[k], s2);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
-                r[4 * q + k] = pack_bf16(__float2bfloat16_rn(f.x * s), __float2bfloat16_rn(f.y * s));
-            }
+        for (int h = 0; h < 2; ++h) {
+            word[0][h] = *reinterpret_cast<const uint32_t*>(block + q4_code_row(i, 32 * h + 4 * j));
+            word[1][h] = *reinterpret_cast<const uint32_t*>(block + kQ4VCodes + q4_code_row(i, 32 * h + 4 * j));
+            scale[0][h] = block[q4_k_scale(i, 4 * h + (j >> 1))];
+            scale[1][h] = block[q4_v_scale(i, 4 * h + (j >> 1))];
         }
     }
-    uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + t * p.token_stride + g * p.head_stride + 16 * grp);
-    dst[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    dst[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    const int64_t at = t * p.token_stride + g * p.head_stride + 8 * j;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const float s = which ? p.v_scale : p.k_scale;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t c[4], r[4];
+            q4_unpack(word[which][h], c);
+            const uint32_t s2 = e4m3x2_half2(scale[which][h] * 0x101u);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // code * scale has 6 bits: exact in fp16, and times s in bf16
+                const uint32_t m = mul_half2(c[k], s2);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+                r[k] = pack_bf16(__float2bfloat16_rn(f.x * s), __float2bfloat16_rn(f.y * s));
+            }
+            *reinterpret_cast<uint4*>((which ? p.v : p.k) + at + 64 * h) = make_uint4(r[0], r[1], r[2], r[3]);
+        }
+    }
 }
 
 cudaError_t launch_q4_read(const pkv_pool* pool, const int32_t* positions, const int32_t* prow, const int32_t* table,
@@ -868,7 +976,7 @@ cudaError_t launch_q4_read(const pkv_pool* pool, const int32_t* positions, const
     p.err = pool->err;
     p.token_stride = token_stride;
     p.head_stride = head_stride;
-    p.items = (int64_t)tokens * pool->cfg.kv_heads * 16;
+    p.tokens = tokens;
     p.rows = rows;
     p.pages = pages;
     p.num_pages = pool->num_pages;
@@ -876,7 +984,8 @@ cudaError_t launch_q4_read(const pkv_pool* pool, const int32_t* positions, const
     p.kv_heads = pool->cfg.kv_heads;
     p.k_scale = pool->k_scale;
     p.v_scale = pool->v_scale;
-    q4_read_kernel<<<(unsigned)((p.items + 255) / 256), 256, 0, s>>>(p);
+    const int64_t items = (int64_t)tokens * ((p.kv_heads + 3) / 4);
+    q4_read_kernel<<<(unsigned)((items + kQ4ReadWarps - 1) / kQ4ReadWarps), 32 * kQ4ReadWarps, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -9,16 +9,8 @@ LEVELS = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
 
 
 def bf16(x) -> np.ndarray:
-    """float64 values rounded to bf16 (ties to even, one rounding), as float64."""
-    x = np.asarray(x, np.float64)
-    f = x.astype(np.float32)
-    # round to odd in fp32 first, so that the two roundings are one
-    b = f.view(np.uint32).copy()
-    off = x - f.astype(np.float64)
-    fix = (off != 0) & ((b & 1) == 0) & np.isfinite(f)
-    away = (off > 0) == (f > 0)
-    b = np.where(fix, np.where(away, b + 1, b - 1), b).astype(np.uint32)
-    return torch.from_numpy(b.view(np.float32).copy()).to(torch.bfloat16).double().numpy()
+    """float64 values rounded to fp32 and then to bf16 (ties to even), as float64."""
+    return torch.from_numpy(np.asarray(x, np.float64).astype(np.float32)).to(torch.bfloat16).double().numpy()
 
 
 def e4m3(x) -> np.ndarray:

@@ -437,7 +437,7 @@ PKV_API int pkv_q4_pool_data(const pkv_pool* pool, void** data, size_t* bytes);
  *   table      device int32 [rows][pages], or NULL: contiguous rows
  * Slots must be distinct (PKV_CHECK=1 checks).  Only the written positions change.
  * Tokens with a bad row, position or page are skipped and set their error bit.
- * rows * pages < 2^30 here and in the two calls below (PKV_ERANGE). */
+ * rows * pages * kv_heads < 2^31 here and in the two calls below (PKV_ERANGE). */
 PKV_API int pkv_q4_append(pkv_pool* pool, const void* k, const void* v, const void* k_norm_w,
                           const int32_t* positions, const int32_t* prow, const int32_t* table, int tokens, int rows,
                           int pages, void* stream);
@@ -457,8 +457,8 @@ PKV_API int pkv_q4_read(pkv_pool* pool, const int32_t* positions, const int32_t*
 /* decode_paged over a 4-bit pool: pkv_decode's steps, with k and v quantised as they are
  * appended and the attention over the values the pool holds (the new position's own
  * quantised values included).  Arguments, skipped rows and error bits as pkv_decode, out
- * 16-byte aligned; all writes of the call happen before any attention, so rows may read
- * each other's new slots.  Results are the same from run to run. */
+ * 16-byte aligned; as there, slots must be distinct and a row's new slot must not be read by
+ * another row of the call (PKV_CHECK=1 checks both).  Results are the same from run to run. */
 PKV_API int pkv_q4_decode(pkv_pool* pool, const void* q, const void* k, const void* v, const void* q_norm_w,
                           const void* k_norm_w, const int32_t* positions, const int32_t* table, int rows, int pages,
                           void* out, void* workspace, size_t workspace_bytes, void* stream);

@@ -137,6 +137,8 @@ def _on(stream):
 
 
 def _dev(t: torch.Tensor | None, dtype: torch.dtype, what: str, allow_none: bool = False) -> int | None:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t is None:
         if allow_none:
             return None
@@ -147,9 +149,7 @@ def _dev(t: torch.Tensor | None, dtype: torch.dtype, what: str, allow_none: bool
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{what} must be contiguous")
 
 
 # ------------------------------------------------------------------ C ABI, one function each

@@ -740,7 +740,7 @@ static int q4_checks(const pkv_pool* pool, const int32_t* positions, const int32
 {
     if (!pool || !pool->q4 || !positions || tokens <= 0 || rows <= 0 || pages <= 0) return PKV_EINVAL;
     if (!prow && rows < tokens) return PKV_EINVAL;  // token t is table row t
-    if (tokens > (1 << 20) || rows > (1 << 20) || (int64_t)rows * pages > INT32_MAX / 2) return PKV_ERANGE;
+    if (tokens > (1 << 20) || rows > (1 << 20) || (int64_t)rows * pages > INT32_MAX / pool->cfg.kv_heads) return PKV_ERANGE;
     if (!aligned(positions, 4) || !aligned(prow, 4) || !aligned(table, 4)) return PKV_EINVAL;
     if (!table && (int64_t)rows * pages > pool->num_pages) return PKV_ERANGE;
     int dev = -1;
@@ -748,9 +748,9 @@ static int q4_checks(const pkv_pool* pool, const int32_t* positions, const int32
     return PKV_OK;
 }
 
-// PKV_CHECK=1: the written slots must be distinct (every write of a call is ordered before its reads).
+// PKV_CHECK=1: the written slots must be distinct, and (decode) no row may read another row's new slot.
 static int q4_precheck(const pkv_pool* pool, const int32_t* positions, const int32_t* prow, const int32_t* table,
-                       int tokens, int rows, int pages, cudaStream_t s)
+                       int tokens, int rows, int pages, bool decode, cudaStream_t s)
 {
     if (!check_enabled()) return PKV_OK;
     StepArgs a = {};
@@ -764,7 +764,7 @@ static int q4_precheck(const pkv_pool* pool, const int32_t* positions, const int
     } else {
         a.step_positions = positions;
         a.steps = tokens;
-        a.q_hat = reinterpret_cast<const float*>(positions);  // not null: no ordering between rows to check
+        if (!decode) a.q_hat = reinterpret_cast<const float*>(positions);  // not null: nothing is read
     }
     try {
         return host_precheck(pool, a, s);
@@ -779,7 +779,7 @@ int pkv_q4_append(pkv_pool* pool, const void* k, const void* v, const void* k_no
     NvtxRange range("pkv_q4_append");
     if (!k || !v || !k_norm_w || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_norm_w, 8)) return PKV_EINVAL;
     int rc = q4_checks(pool, positions, prow, table, tokens, rows, pages);
-    if (rc == PKV_OK) rc = q4_precheck(pool, positions, prow, table, tokens, rows, pages, static_cast<cudaStream_t>(stream));
+    if (rc == PKV_OK) rc = q4_precheck(pool, positions, prow, table, tokens, rows, pages, false, static_cast<cudaStream_t>(stream));
     if (rc != PKV_OK) return rc;
     return launch_q4_append(pool, k, v, k_norm_w, positions, prow, table, tokens, rows, pages,
                             static_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -812,7 +812,7 @@ int pkv_q4_decode(pkv_pool* pool, const void* q, const void* k, const void* v, c
     if (workspace && !aligned(workspace, 256)) return PKV_EINVAL;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int rc = q4_checks(pool, positions, nullptr, table, rows, rows, pages);
-    if (rc == PKV_OK) rc = q4_precheck(pool, positions, nullptr, table, rows, rows, pages, s);
+    if (rc == PKV_OK) rc = q4_precheck(pool, positions, nullptr, table, rows, rows, pages, true, s);
     if (rc != PKV_OK) return rc;
     const StepArgs a = {q, k, v, q_norm_w, k_norm_w, nullptr, nullptr, nullptr, positions, table,
                         0, rows, pages, rows, out, static_cast<char*>(workspace)};

@@ -5,7 +5,7 @@
 //   q4_prep_kernel    the same in front of the attention, with each row's check, its
 //                     attended length and its prepared query heads
 //   q4_attn_kernel    split attention: every warp streams its own share of the
-//                     call's 32-position chunks through its own ring of bulk
+//                     call's pages through its own ring of bulk
 //                     copies and keeps its own softmax state
 //   q4_combine_kernel merge of the pieces of a (token, kv head) that several
 //                     warps shared
@@ -22,6 +22,26 @@
 #include "pkv_q4.cuh"
 
 namespace pkv {
+
+// A launch that may start while the kernel before it on the stream drains: every kernel
+// here waits for that one (pdl_wait) before it reads or writes memory, and lets the
+// next start its own launch early.
+template <class P>
+static cudaError_t launch_dependent(void (*kernel)(P), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                                    const P& p, bool early = true)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 // =====================================================================================
 // q4_append_kernel, q4_prep_kernel
@@ -40,6 +60,7 @@ struct Q4AppendParams {
     uint8_t* data;
     __half* q_hat;              // decode: [tokens][heads][128], each head times a power of two
     float* q_mul;               // decode: [tokens][heads], what a score of it is multiplied with
+    __nv_bfloat16* out;         // decode: [tokens][heads][128], zeroed for skipped tokens
     int32_t* tok_len;           // decode: [tokens], 0: skip
     uint32_t* err;
     int tokens, rows, pages, num_pages, max_seq, heads, kv_heads, rot;
@@ -92,6 +113,8 @@ __global__ void __launch_bounds__(32 * kQ4AppendWarps) q4_append_kernel(Q4Append
 {
     const int lane = threadIdx.x & 31, j = lane & 7, quads = (p.kv_heads + 3) / 4;
     const int item = blockIdx.x * kQ4AppendWarps + (threadIdx.x >> 5), t = item / quads;
+    pdl_wait();
+    pdl_launch_dependents();
     if (t >= p.tokens) return;
     const int g = 4 * (item % quads) + (lane >> 3);
     const bool live = g < p.kv_heads;
@@ -115,14 +138,15 @@ __global__ void __launch_bounds__(32 * kQ4AppendWarps) q4_append_kernel(Q4Append
 }
 
 // In front of the attention: one CTA per row checks every page that the row will read,
-// writes its attended length, appends its k and v (items 0 .. quads - 1 of 4 kv heads)
+// writes its attended length (and the zeros of a skipped row's output), appends its k and v (items 0 .. quads - 1 of 4 kv heads)
 // and prepares its queries (items from there on, the 4 query heads of a kv head each).
 template <bool kFullRot>
 __global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
 {
     const int t = blockIdx.x, lane = threadIdx.x & 31, j = lane & 7, sub = lane >> 3, warps = blockDim.x >> 5;
     const int quads = (p.kv_heads + 3) / 4, items = quads + p.kv_heads;
-    pdl_launch_dependents();
+    pdl_wait();               // (launched while the kernel before this call drains)
+    pdl_launch_dependents();  // after the wait: the attention reads this call's inputs before it waits for this grid
     // a warp's first item's inputs go out before anything that they do not depend on
     int item = threadIdx.x >> 5;
     uint4 a[2] = {}, b[2] = {}, w[2];
@@ -159,7 +183,11 @@ __global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
         p.tok_len[t] = ok ? pos + 1 : 0;
         if (e) atomicOr(p.err, e);
     }
-    if (!ok) return;
+    if (!ok) {
+        uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)t * p.heads * kHeadDim);
+        for (int i = threadIdx.x; i < p.heads * kHeadDim / 8; i += blockDim.x) out[i] = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
     for (; item < items; item += warps, load()) {
         if (item < quads) {
             const int g = 4 * item + sub;
@@ -187,7 +215,8 @@ __global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
         const int64_t head = (int64_t)t * p.heads + 4 * (item - quads) + sub;
         *reinterpret_cast<uint4*>(p.q_hat + head * kHeadDim + 8 * j) = make_uint4(r[0], r[1], r[2], r[3]);
         *reinterpret_cast<uint4*>(p.q_hat + head * kHeadDim + 64 + 8 * j) = make_uint4(r[4], r[5], r[6], r[7]);
-        if (j == 0) p.q_mul[head] = __uint_as_float((uint32_t)ex << 23) * kQScale * p.k_scale;
+        // (never 0, which would make a masked score NaN; below 1e-30 the scores are 0 either way)
+        if (j == 0) p.q_mul[head] = fmaxf(__uint_as_float((uint32_t)ex << 23) * kQScale * p.k_scale, 1e-30f);
     }
 }
 
@@ -228,23 +257,28 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
     p.rows = rows;
     p.pages = pages;
     const unsigned grid = (unsigned)(((int64_t)tokens * ((p.kv_heads + 3) / 4) + kQ4AppendWarps - 1) / kQ4AppendWarps);
-    (p.rot == kHeadDim ? q4_append_kernel<true> : q4_append_kernel<false>)<<<grid, 32 * kQ4AppendWarps, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(p.rot == kHeadDim ? q4_append_kernel<true> : q4_append_kernel<false>, grid, 32 * kQ4AppendWarps, 0,
+                            s, p);
 }
 
 // =====================================================================================
 // q4_attn_kernel
 // =====================================================================================
 //
-// Work.  A (token, kv head) unit's positions are cut into chunks of 32 (half a
-// page, 4608 contiguous bytes); units in order, kv heads within tokens, make one
-// sequence of T chunks, and warp w of W streams chunks [w T / W, (w + 1) T / W).
-// Warps of one CTA are far apart in that sequence (w = warp * CTAs + CTA): a small
-// call spreads over all SMs.  A unit inside one warp's share is written out; the
-// pieces of the others go to index u + w of the partials (unique: units and warps
-// both increase along the sequence) and q4_combine_kernel merges them in order.
-// No warp waits for another: 16 warps a CTA with 3 stages of 4608 bytes keep
-// ~150 KB in flight on an SM.
+// Work.  A (token, kv head) unit's positions are cut into chunks of a page (9216
+// contiguous bytes); units in order, kv heads within tokens, make one sequence of T
+// chunks, and warp w of W streams chunks [w T / W, (w + 1) T / W).  Warps of one CTA
+// are far apart in that sequence (w = warp * CTAs + CTA): a small call spreads over
+// all SMs.  A unit inside one warp's share is written out; the pieces of the others
+// go to index u + w of the partials (unique: units and warps both increase along the
+// sequence).  A warp counts its pieces in when its share is done; the CTA of the
+// warp that was last at a unit merges its pieces, in an order that depends on the
+// sizes alone.  No warp waits for a warp of another CTA.
+//
+// The kernel starts beside q4_prep_kernel (programmatic launch): it splits the work
+// by the positions and starts its first copies at once -- all but a row's last chunk,
+// which holds the position that the preparation writes -- and waits for the
+// preparation before it needs the queries.
 //
 // Per 16 positions (a block), with lane = 4 r + c:
 //   S[16 pos][8] = K[16][128] q[128][8], m16n8k16 fp16: column h = query head h of the
@@ -256,23 +290,26 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
 // The codes become fp16 by the conversion instruction and are multiplied by their
 // scales as fp16 pairs, exactly; V's are first regrouped so that one byte holds a
 // dim's codes of two positions.  P is turned between the fragments by movmatrix.
-constexpr int kQ4Warps = 16;
-constexpr int kQ4Stages = 3;
-constexpr int kQ4Chunk = 32;                                     // positions
-constexpr int kQ4ChunkBytes = kQ4Chunk / kQ4Block * kQ4BlockBytes;  // 4608
+constexpr int kQ4Warps = 12;
+constexpr int kQ4Stages = 2;
+constexpr int kQ4Chunk = 64;                         // positions: a page
+constexpr int kQ4Blocks = kQ4Chunk / kQ4Block;
+constexpr int kQ4ChunkBytes = kQ4Blocks * kQ4BlockBytes;
+constexpr float kQ4Slack = 8.f;                      // base-2 exponent that a weight may reach (q4_attn_kernel)
 
 struct Q4AttnParams {
     const __half* q_hat;
     const float* q_mul;
-    const int32_t* tok_len;
+    const int32_t* positions;
+    const int32_t* tok_len;  // 0: a row that the preparation skipped
     const int32_t* table;
     const uint8_t* data;
     __nv_bfloat16* out;
     float* part_o;      // [U + W][4][128]
     float* part_lse;    // [U + W][4]
-    int32_t* prefix;    // [ntok + 1], written by CTA 0 for the combine
+    int32_t* prefix;    // [ntok + 1]: chunks before each token, written by CTA 0 for the combine
     uint32_t* err;
-    int ntok, pages, heads, kv_heads;
+    int ntok, pages, num_pages, max_seq, heads, kv_heads;
     float v_scale;
     uint64_t wait_ns;
 };
@@ -282,30 +319,59 @@ struct Q4Smem {
     static constexpr int kBars = kQ4Warps * kQ4Stages * kQ4ChunkBytes;
     static constexpr int kT0 = kBars + 8 * kQ4Warps * kQ4Stages;
     static constexpr int kP0 = kT0 + 4 * 32 * kQ4Warps;
-    static constexpr int kScan = kP0 + 4 * 32 * kQ4Warps;
+    static constexpr int kLen = kP0 + 4 * 32 * kQ4Warps;
+    static constexpr int kScan = kLen + 4 * 32 * kQ4Warps;
     static constexpr int kBytes = kScan + 4 * kQ4Warps;
     static constexpr int kAlloc = kBytes + 128;  // slack to align the base
 };
 static_assert(Q4Smem::kAlloc <= 227 * 1024, "the ring fits");
 
+// Attended length of token t and its chunks (rows with a bad page count: they are
+// streamed, with the page ids put in range, and not written out).
+__device__ __forceinline__ int q4_len(const Q4AttnParams& p, int t)
+{
+    const int pos = p.positions[t];
+    return pos >= 0 && pos < p.max_seq && pos / kPageSize < p.pages ? pos + 1 : 0;
+}
 __device__ __forceinline__ int q4_chunks(int len) { return (len + kQ4Chunk - 1) / kQ4Chunk; }
 
-// Warp-wide: the token holding chunk x (x < T), and the chunks of one kv head before it.
-__device__ __forceinline__ void q4_find(const Q4AttnParams& p, const int* sT0, const int* sP0, int64_t x, int lane,
-                                        int& t_out, int& pre_out)
+// The split of T chunks over W <= T warps: warp w has chunks [floor(w T / W), floor((w + 1) T / W)),
+// in 32-bit arithmetic (W is a few thousand: w rem < 2^31).
+struct Q4Split {
+    int T, W, q, rem;
+    __device__ __forceinline__ Q4Split(int T_, int W_) : T(T_), W(W_), q(W_ ? T_ / W_ : 0), rem(W_ ? T_ - q * W_ : 0) {}
+    __device__ __forceinline__ int start(int w) const { return w * q + (int)((uint32_t)w * (uint32_t)rem / (uint32_t)W); }
+    __device__ __forceinline__ int warp_of(int x) const  // the warp that has chunk x
+    {
+        int w = min(max((int)((float)x * ((float)W / (float)T)), 0), W - 1);
+        while (start(w) > x) --w;
+        while (w + 1 < W && start(w + 1) <= x) ++w;
+        return w;
+    }
+};
+
+// Warp-wide: the token holding chunk x (x < T), its length, and the chunks of one kv head before it.
+__device__ __forceinline__ void q4_find(const Q4AttnParams& p, const int* sT0, const int* sP0, const int* sLen,
+                                        int x, int lane, int& t_out, int& len_out, int& pre_out)
 {
     const int G = p.kv_heads;
     int lo = 0, hi = 32 * kQ4Warps - 1;
     while (lo < hi) {  // last run of tokens whose prefix is at or before x
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)G * sP0[mid] <= x)
+        if (G * sP0[mid] <= x)
             lo = mid;
         else
             hi = mid - 1;
     }
     int t = sT0[lo], pre = sP0[lo];
+    if (p.ntok <= 32 * kQ4Warps) {  // runs of one token: it is this one (those after it start beyond x)
+        t_out = t;
+        len_out = sLen[lo];
+        pre_out = pre;
+        return;
+    }
     for (; t < p.ntok; t += 32) {
-        const int n = t + lane < p.ntok ? q4_chunks(p.tok_len[t + lane]) : 0;
+        const int len = t + lane < p.ntok ? q4_len(p, t + lane) : 0, n = q4_chunks(len);
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -313,60 +379,25 @@ __device__ __forceinline__ void q4_find(const Q4AttnParams& p, const int* sT0, c
             if (lane >= o) incl += y;
         }
         const int before = pre + incl - n;
-        const unsigned m = __ballot_sync(kFull, n > 0 && (int64_t)G * before <= x && x < (int64_t)G * (before + n));
+        const unsigned m = __ballot_sync(kFull, n > 0 && G * before <= x && x < G * (before + n));
         if (m) {
             const int l = __ffs(m) - 1;
             t_out = t + l;
+            len_out = __shfl_sync(kFull, len, l);
             pre_out = __shfl_sync(kFull, before, l);
             return;
         }
         pre += __shfl_sync(kFull, incl, 31);
     }
     t_out = p.ntok - 1;  // not reached: x < T lies in some token
+    len_out = 1;
     pre_out = pre;
 }
 
-// A place in the sequence of chunks: chunk j of n of unit (t, g).
-struct Q4Cursor {
-    int t, g, j, n, len;
-};
-
-__device__ __forceinline__ void q4_next(const Q4AttnParams& p, Q4Cursor& c, bool more)
-{
-    if (++c.j < c.n || !more) return;
-    c.j = 0;
-    if (++c.g < p.kv_heads) return;
-    c.g = 0;
-    do {
-        ++c.t;
-        c.len = p.tok_len[c.t];  // more: another token with chunks follows
-    } while (c.len == 0);
-    c.n = q4_chunks(c.len);
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t a)
-{
-    uint32_t r;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
-    return r;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a)
-{
-    uint2 r;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
-    return r;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a)
-{
-    uint4 r;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
-    return r;
-}
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -392,6 +423,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
     uint8_t* sbase = smem_raw + (base - raw);
     int* sT0 = reinterpret_cast<int*>(sbase + Q4Smem::kT0);
     int* sP0 = reinterpret_cast<int*>(sbase + Q4Smem::kP0);
+    int* sLen = reinterpret_cast<int*>(sbase + Q4Smem::kLen);  // of each token, where every token has a thread
     int* sScan = reinterpret_cast<int*>(sbase + Q4Smem::kScan);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = p.kv_heads, H = p.heads;
@@ -402,13 +434,11 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
         fence_mbar_init();
     }
     pdl_launch_dependents();
-    pdl_wait();
-
     // chunks per token and their prefix over tokens (one run of tokens a thread; every CTA computes it)
     const int nt = p.ntok, per = (nt + 32 * kQ4Warps - 1) / (32 * kQ4Warps);
     const int t0 = min(nt, tid * per), t1 = min(nt, t0 + per);
-    int local = 0;
-    for (int t = t0; t < t1; ++t) local += q4_chunks(p.tok_len[t]);
+    int local = 0, tlen = 0;
+    for (int t = t0; t < t1; ++t) local += q4_chunks(tlen = q4_len(p, t));
     int incl = local;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -423,86 +453,103 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
         before += w < warp ? sScan[w] : 0;
         total += sScan[w];
     }
-    const int excl = before + incl - local;
     sT0[tid] = t0;
-    sP0[tid] = excl;
+    sP0[tid] = before + incl - local;
+    sLen[tid] = tlen;
     if (blockIdx.x == 0) {
-        int run = excl;
+        int run = before + incl - local;
         for (int t = t0; t < t1; ++t) {
             p.prefix[t] = run;
-            run += q4_chunks(p.tok_len[t]);
+            run += q4_chunks(q4_len(p, t));
         }
         if (tid == 0) p.prefix[nt] = total;
     }
     __syncthreads();
 
-    const int64_t T = (int64_t)G * total;
-    const int64_t W = min((int64_t)gridDim.x * kQ4Warps, T);
+    const int T = G * total;  // (the host bounds rows * pages * kv_heads)
+    const Q4Split sp(T, min((int)gridDim.x * kQ4Warps, T));
+    const int W = sp.W;
     const int w = warp * gridDim.x + blockIdx.x;
-    if (w >= W) return;
-    const int64_t xb = (int64_t)w * T / W, xe = (int64_t)(w + 1) * T / W;
-    const int count = (int)(xe - xb);
+    const int xb = w < W ? sp.start(w) : 0, count = w < W ? sp.start(w + 1) - xb : 0;
 
-    Q4Cursor cur;
-    {
+    // chunk j of n of unit (t, g): where the warp computes, and (the i... values) where it issues copies
+    int t = 0, g = 0, j = 0, n = 1, len = 0;
+    if (count > 0) {
         int pre;
-        q4_find(p, sT0, sP0, xb, lane, cur.t, pre);
-        cur.len = p.tok_len[cur.t];
-        cur.n = q4_chunks(cur.len);
-        const int64_t off = xb - (int64_t)G * pre;
-        cur.g = (int)(off / cur.n);
-        cur.j = (int)(off % cur.n);
+        q4_find(p, sT0, sP0, sLen, xb, lane, t, len, pre);
+        n = q4_chunks(len);
+        const int off = xb - G * pre;
+        g = off / n;
+        j = off - g * n;
     }
-    Q4Cursor iss = cur;
-    int issued = 0;
-    int entries = 0, ent_t = -1, ent_b = 0;  // table entries [32 ent_b, +32) of token ent_t, one a lane
+    auto next_unit = [&](int& t, int& g, int& j, int& n, int& len) {  // (only where chunks remain)
+        j = 0;
+        if (++g < G) return;
+        g = 0;
+        do {
+            len = q4_len(p, ++t);
+        } while (len == 0);
+        n = q4_chunks(len);
+    };
+    int it = t, ig = g, ij = j, in = n, ilen = len, issued = 0, ist = 0;
+    constexpr int kPerPage = kPageSize / kQ4Chunk;
+    int entries = 0;     // table entries 32 k .. 32 k + 31 of the row, one a lane
+    bool reload = true;
     auto issue = [&]() {
-        const int pg = iss.j >> 1;
-        if (ent_t != iss.t || ent_b != pg >> 5) {
-            ent_t = iss.t;
-            ent_b = pg >> 5;
-            const int e = 32 * ent_b + lane;
-            entries = e <= (iss.len - 1) / kPageSize ? page_of(p.table, p.pages, iss.t, e) : 0;
+        const int pg = ij / kPerPage;
+        if (reload || (ij % (32 * kPerPage)) == 0) {
+            const int e = (pg & ~31) + lane;
+            entries = e <= (ilen - 1) / kPageSize ? page_of(p.table, p.pages, it, e) : 0;
+            if (entries < 0 || entries >= p.num_pages) entries = 0;  // (then the row is not written out)
+            reload = false;
         }
         const int page = __shfl_sync(kFull, entries, pg & 31);
         if (lane == 0) {
-            const int left = iss.len - iss.j * kQ4Chunk;
-            const uint32_t bytes = left > kQ4Block ? kQ4ChunkBytes : kQ4BlockBytes;
-            const int st = issued % kQ4Stages;
-            mbar_arrive_expect_tx(bars + 8 * st, bytes);
-            const uint8_t* src = p.data + ((int64_t)page * G + iss.g) * kQ4PageBytes + (iss.j & 1) * kQ4ChunkBytes;
+            const uint32_t bytes = min((ilen - ij * kQ4Chunk + kQ4Block - 1) / kQ4Block, kQ4Blocks) * kQ4BlockBytes;
+            mbar_arrive_expect_tx(bars + 8 * ist, bytes);
+            const uint8_t* src = p.data + ((int64_t)page * G + ig) * kQ4PageBytes + (ij % kPerPage) * kQ4ChunkBytes;
             asm volatile(
                 "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                    ring + st * kQ4ChunkBytes),
-                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bars + 8 * st)
+                    ring + ist * kQ4ChunkBytes),
+                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bars + 8 * ist)
                 : "memory");
         }
         ++issued;
-        q4_next(p, iss, issued < count);
+        ist = ist == kQ4Stages - 1 ? 0 : ist + 1;
+        if (++ij == in && issued < count) {
+            next_unit(it, ig, ij, in, ilen);
+            reload = true;
+        }
     };
-    for (int i = 0; i < kQ4Stages - 1 && i < count; ++i) issue();
+    // before the preparation is waited for: what it does not write
+    while (issued < kQ4Stages - 1 && issued < count && ij != in - 1) issue();
+    pdl_wait();
+    while (issued < kQ4Stages - 1 && issued < count) issue();
 
     const int r = lane >> 2, c = lane & 3;
     const int pi_r = ((r >> 1) ^ (r & 1)) | ((r & 1) << 2);  // position of row r (see above)
     const int pi_0 = c, pi_1 = (c ^ 1) | 4;                   // positions of k = 2c, 2c + 1
+    const uint8_t* wring = sbase + warp * (kQ4Stages * kQ4ChunkBytes);
     const uint32_t koff = 64 * pi_r + ((16 * c) ^ (((pi_r >> 1) & 1) << 5));
     const uint32_t voff0 = kQ4VCodes + 64 * pi_0 + ((8 * r) ^ (((pi_0 >> 1) & 1) << 5));
     const uint32_t voff1 = kQ4VCodes + 64 * pi_1 + ((8 * r) ^ (((pi_1 >> 1) & 1) << 5));
-    const uint32_t soff = 16 * r + 4 * c;
+    const uint32_t soff = kQ4KScales + 16 * r + 4 * c;
 
     uint32_t bq[8][2];
-    float mulA = 0.f, mulB = 0.f;
+    float mulA = 1.f, mulB = 1.f;
     float o[8][4];
     float mA = 0.f, mB = 0.f, lA = 0.f, lB = 0.f;
     bool fresh = true;   // the next chunk opens a segment
     bool whole = false;  // the segment began with its unit's first chunk
+    bool live = false;   // its row has an output (the preparation found no fault with it)
     bool ok = true;
+    int st = 0;
+    uint32_t phase = 0;
 
     for (int i = 0; i < count; ++i) {
         if (issued < count) issue();
-        const int st = i % kQ4Stages;
         if (fresh) {
-            const __half* qh = p.q_hat + ((int64_t)cur.t * H + cur.g * kGroup + (r & 3)) * kHeadDim + 32 * c;
+            const __half* qh = p.q_hat + ((int64_t)t * H + g * kGroup + (r & 3)) * kHeadDim + 32 * c;
             uint4 x[4] = {};
             if (r < kGroup) {
 #pragma unroll
@@ -515,35 +562,34 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
                 bq[2 * k + 1][0] = x[k].z;
                 bq[2 * k + 1][1] = x[k].w;
             }
-            const float2 mul = c < 2 ? *reinterpret_cast<const float2*>(p.q_mul + (int64_t)cur.t * H + cur.g * kGroup + 2 * c)
-                                     : make_float2(0.f, 0.f);
-            mulA = mul.x;
-            mulB = mul.y;
+            if (c < 2) {
+                const float2 mul = *reinterpret_cast<const float2*>(p.q_mul + (int64_t)t * H + g * kGroup + 2 * c);
+                mulA = mul.x;
+                mulB = mul.y;
+            }
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
             mA = mB = -CUDART_INF_F;
             lA = lB = 0.f;
-            whole = cur.j == 0;
+            live = p.tok_len[t] > 0;
+            whole = j == 0;
             fresh = false;
         }
-        if (__any_sync(kFull, !mbar_wait(bars + 8 * st, (i / kQ4Stages) & 1, p.wait_ns))) {
+        if (__any_sync(kFull, !mbar_wait(bars + 8 * st, phase, p.wait_ns))) {
             ok = false;
             break;
         }
-        const uint32_t sb = ring + st * kQ4ChunkBytes;
-        const int left = cur.len - cur.j * kQ4Chunk;  // positions of the unit from this chunk on
-        const bool two = left > kQ4Block;
+        const uint8_t* sb = wring + st * kQ4ChunkBytes;
 
         // ---- S = K q^T
-        float s[2][4];
+        float s[kQ4Blocks][4];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kQ4Blocks; ++b) {
             s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
-            if (b == 1 && !two) continue;
-            const uint32_t kb = sb + b * kQ4BlockBytes;
-            const uint4 k0 = lds128(kb + koff), k1 = lds128(kb + koff + 512);
-            const uint32_t sc = lds32(kb + kQ4KScales + soff);
-            const uint32_t s0 = e4m3x2_half2(sc & 0xffffu), s1 = e4m3x2_half2(sc >> 16);
+            const uint8_t* kb = sb + b * kQ4BlockBytes;
+            const uint4 k0 = *reinterpret_cast<const uint4*>(kb + koff), k1 = *reinterpret_cast<const uint4*>(kb + koff + 512);
+            const uint32_t sc = *reinterpret_cast<const uint32_t*>(kb + soff);
+            const uint32_t s0 = e4m3x2_half2(sc), s1 = e4m3x2_half2(sc >> 16);
             const uint32_t sd[2][2] = {{__byte_perm(s0, s0, 0x1010), __byte_perm(s0, s0, 0x3232)},
                                        {__byte_perm(s1, s1, 0x1010), __byte_perm(s1, s1, 0x3232)}};
             const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
@@ -563,28 +609,38 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
         }
 
         // ---- softmax, base 2: s[b][0], [1]: heads 2c, 2c + 1 at position pi_r of block b; [2], [3]: at pi_r + 8
+        // Positions past the row's end: scores of -inf, and V scales of 0 (the codes are finite
+        // whatever lies there), in a row's last chunk only.
+        uint32_t vmask[kQ4Blocks];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            s[b][0] *= mulA;
-            s[b][1] *= mulB;
-            s[b][2] *= mulA;
-            s[b][3] *= mulB;
-        }
+        for (int b = 0; b < kQ4Blocks; ++b) vmask[b] = ~0u;
+        const int left = len - j * kQ4Chunk;  // positions of the unit from this chunk on
         if (left < kQ4Chunk) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (16 * b + pi_r >= left) s[b][0] = s[b][1] = -CUDART_INF_F;
-                if (16 * b + pi_r + 8 >= left) s[b][2] = s[b][3] = -CUDART_INF_F;
+            for (int b = 0; b < kQ4Blocks; ++b) {
+                const int at = left - kQ4Block * b;
+                if (pi_r >= at) s[b][0] = s[b][1] = -CUDART_INF_F;
+                if (pi_r + 8 >= at) s[b][2] = s[b][3] = -CUDART_INF_F;
+                vmask[b] = (pi_0 < at ? 0xffu : 0u) | (pi_1 < at ? 0xff00u : 0u) | (pi_0 + 8 < at ? 0xff0000u : 0u) |
+                           (pi_1 + 8 < at ? 0xff000000u : 0u);
             }
         }
-        float nA = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
-        float nB = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+        float nA = fmaxf(s[0][0], s[0][2]), nB = fmaxf(s[0][1], s[0][3]);
+#pragma unroll
+        for (int b = 1; b < kQ4Blocks; ++b) {
+            nA = fmaxf(nA, fmaxf(s[b][0], s[b][2]));
+            nB = fmaxf(nB, fmaxf(s[b][1], s[b][3]));
+        }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
             nA = fmaxf(nA, __shfl_xor_sync(kFull, nA, d));
             nB = fmaxf(nB, __shfl_xor_sync(kFull, nB, d));
         }
-        if (__any_sync(kFull, nA > mA || nB > mB)) {
+        nA *= mulA;
+        nB *= mulB;
+        // the running maximum follows only when it is passed by more than 2^kQ4Slack: weights stay below
+        // that, well inside fp16, and most chunks rescale nothing
+        if (__any_sync(kFull, nA > mA + kQ4Slack || nB > mB + kQ4Slack)) {
             nA = fmaxf(nA, mA);
             nB = fmaxf(nB, mB);
             // (a maximum still at -inf -- scores that are all NaN -- leaves nothing to rescale)
@@ -601,14 +657,14 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
                 o[k][3] *= aB;
             }
         }
-        uint32_t pb[2][2];
+        uint32_t pb[kQ4Blocks][2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kQ4Blocks; ++b) {
             float e[4];
-            e[0] = ex2(s[b][0] - mA);
-            e[1] = ex2(s[b][1] - mB);
-            e[2] = ex2(s[b][2] - mA);
-            e[3] = ex2(s[b][3] - mB);
+            e[0] = ex2(__fmaf_rn(s[b][0], mulA, -mA));
+            e[1] = ex2(__fmaf_rn(s[b][1], mulB, -mB));
+            e[2] = ex2(__fmaf_rn(s[b][2], mulA, -mA));
+            e[3] = ex2(__fmaf_rn(s[b][3], mulB, -mB));
             lA += e[0] + e[2];
             lB += e[1] + e[3];
             const __half2 lo = __floats2half2_rn(e[0], e[1]), hi = __floats2half2_rn(e[2], e[3]);
@@ -618,20 +674,12 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
 
         // ---- O^T += V^T P
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            if (b == 1 && !two) continue;
-            const uint32_t vb = sb + b * kQ4BlockBytes;
-            const uint2 v0 = lds64(vb + voff0), v1 = lds64(vb + voff1);
-            const uint2 v2 = lds64(vb + voff0 + 512), v3 = lds64(vb + voff1 + 512);
-            uint32_t sc = lds32(vb + kQ4VScales + soff);
-            if (left < kQ4Chunk) {  // positions past the row's end: whatever their bytes are, a scale of 0 (codes are finite)
-                const int at = left - 16 * b;
-                if (pi_0 >= at) sc &= 0xffffff00u;
-                if (pi_1 >= at) sc &= 0xffff00ffu;
-                if (pi_0 + 8 >= at) sc &= 0xff00ffffu;
-                if (pi_1 + 8 >= at) sc &= 0x00ffffffu;
-            }
-            const uint32_t s01 = e4m3x2_half2(sc & 0xffffu), s23 = e4m3x2_half2(sc >> 16);
+        for (int b = 0; b < kQ4Blocks; ++b) {
+            const uint8_t* vb = sb + b * kQ4BlockBytes;
+            const uint2 v0 = *reinterpret_cast<const uint2*>(vb + voff0), v1 = *reinterpret_cast<const uint2*>(vb + voff1);
+            const uint2 v2 = *reinterpret_cast<const uint2*>(vb + voff0 + 512), v3 = *reinterpret_cast<const uint2*>(vb + voff1 + 512);
+            const uint32_t sc = *reinterpret_cast<const uint32_t*>(vb + soff + 128) & vmask[b];
+            const uint32_t s01 = e4m3x2_half2(sc), s23 = e4m3x2_half2(sc >> 16);
             const uint32_t a0[2] = {v0.x, v0.y}, a1[2] = {v1.x, v1.y}, a2[2] = {v2.x, v2.y}, a3[2] = {v3.x, v3.y};
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -649,34 +697,38 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
         }
         __syncwarp();  // every lane has read the stage: it may be filled again
 
-        const bool last = cur.j == cur.n - 1;
-        if (last || i == count - 1) {  // end of the segment
+        if (++st == kQ4Stages) {
+            st = 0;
+            phase ^= 1;
+        }
+        const bool last = j == n - 1;
+        if ((last || i == count - 1) && live) {  // end of the segment
             float LA = lA, LB = lB;
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
                 LA += __shfl_xor_sync(kFull, LA, d);
                 LB += __shfl_xor_sync(kFull, LB, d);
             }
+            const int64_t u = (int64_t)t * G + g;
             if (c < 2) {
                 const float iA = p.v_scale / LA, iB = p.v_scale / LB;
-                const int hA = cur.g * kGroup + 2 * c;
+                const int hA = g * kGroup + 2 * c;
                 // o[j][0], [2]: dims 16r + 2j, + 1 of head A; [1], [3] of head B
                 if (whole && last) {
-                    __nv_bfloat16* dst = p.out + ((int64_t)cur.t * H + hA) * kHeadDim + 16 * r;
+                    __nv_bfloat16* dst = p.out + ((int64_t)t * H + hA) * kHeadDim + 16 * r;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        uint32_t a[4], b[4];
+                        uint32_t x[4], y[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            a[e] = pack_bf16(__float2bfloat16_rn(o[4 * k + e][0] * iA), __float2bfloat16_rn(o[4 * k + e][2] * iA));
-                            b[e] = pack_bf16(__float2bfloat16_rn(o[4 * k + e][1] * iB), __float2bfloat16_rn(o[4 * k + e][3] * iB));
+                            x[e] = pack_bf16(__float2bfloat16_rn(o[4 * k + e][0] * iA), __float2bfloat16_rn(o[4 * k + e][2] * iA));
+                            y[e] = pack_bf16(__float2bfloat16_rn(o[4 * k + e][1] * iB), __float2bfloat16_rn(o[4 * k + e][3] * iB));
                         }
-                        *reinterpret_cast<uint4*>(dst + 8 * k) = make_uint4(a[0], a[1], a[2], a[3]);
-                        *reinterpret_cast<uint4*>(dst + kHeadDim + 8 * k) = make_uint4(b[0], b[1], b[2], b[3]);
+                        *reinterpret_cast<uint4*>(dst + 8 * k) = make_uint4(x[0], x[1], x[2], x[3]);
+                        *reinterpret_cast<uint4*>(dst + kHeadDim + 8 * k) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 } else {
-                    const int64_t u = (int64_t)cur.t * G + cur.g + w;
-                    float* po = p.part_o + (u * kGroup + 2 * c) * kHeadDim + 16 * r;
+                    float* po = p.part_o + ((u + w) * kGroup + 2 * c) * kHeadDim + 16 * r;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         *reinterpret_cast<float4*>(po + 4 * k) = make_float4(o[2 * k][0] * iA, o[2 * k][2] * iA,
@@ -685,12 +737,13 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
                             o[2 * k][1] * iB, o[2 * k][3] * iB, o[2 * k + 1][1] * iB, o[2 * k + 1][3] * iB);
                     }
                     if (r == 0)
-                        *reinterpret_cast<float2*>(p.part_lse + u * kGroup + 2 * c) = make_float2(mA + log2f(LA), mB + log2f(LB));
+                        *reinterpret_cast<float2*>(p.part_lse + (u + w) * kGroup + 2 * c) =
+                            make_float2(mA + log2f(LA), mB + log2f(LB));
                 }
             }
-            fresh = true;
         }
-        q4_next(p, cur, i + 1 < count);
+        fresh |= last;
+        if (++j == n && i + 1 < count) next_unit(t, g, j, n, len);
     }
     if (!ok) {  // the awaited copy is late: report, and let the copies in flight land before the CTA may exit
         if (lane == 0) {
@@ -708,6 +761,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
 // =====================================================================================
 struct Q4CombineParams {
     const int32_t* prefix;
+    const int32_t* tok_len;
     const float* part_o;
     const float* part_lse;
     __nv_bfloat16* out;
@@ -724,18 +778,14 @@ __global__ void __launch_bounds__(32 * kGroup * kSub) q4_combine_kernel(Q4Combin
     const int head = warp % kGroup, sub = warp / kGroup;
     const int u = blockIdx.x, t = u / G, g = u % G;
     pdl_wait();
+    pdl_launch_dependents();
     const int pre = p.prefix[t], n = p.prefix[t + 1] - pre, total = p.prefix[p.ntok];
-    __nv_bfloat16* dst = p.out + ((int64_t)t * p.heads + g * kGroup + head) * kHeadDim + 4 * lane;
-    if (n == 0) {  // a skipped token
-        if (sub == 0) *reinterpret_cast<uint2*>(dst) = make_uint2(0u, 0u);
-        return;
-    }
-    const int64_t T = (int64_t)G * total, W = min((int64_t)p.warps, T);
-    const int64_t xb = (int64_t)G * pre + (int64_t)g * n;
-    // warp w holds chunks [w T / W, (w + 1) T / W): the one holding chunk x is ((x + 1) W - 1) / T
-    const int64_t wf = ((xb + 1) * W - 1) / T, wl = ((xb + n) * W - 1) / T;
+    if (p.tok_len[t] == 0) return;  // a skipped token: its zeros are there
+    const int T = G * total, x0 = G * pre + g * n;
+    const Q4Split sp(T, min(p.warps, T));
+    const int wf = sp.warp_of(x0), wl = sp.warp_of(x0 + n - 1);
     if (wf == wl) return;  // one warp held it and wrote it out
-    const int np = (int)(wl - wf + 1);
+    const int np = wl - wf + 1;
     const float* lse = p.part_lse + ((int64_t)u + wf) * kGroup + head;
     const float* po = p.part_o + (((int64_t)u + wf) * kGroup + head) * kHeadDim + 4 * lane;
     float M = -CUDART_INF_F, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -789,7 +839,7 @@ __global__ void __launch_bounds__(32 * kGroup * kSub) q4_combine_kernel(Q4Combin
     }
     const float inv = 1.f / sum;
     const float y[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
-    *reinterpret_cast<uint2*>(dst) = pack4(y);
+    *reinterpret_cast<uint2*>(p.out + ((int64_t)t * p.heads + g * kGroup + head) * kHeadDim + 4 * lane) = pack4(y);
 }
 
 // =====================================================================================
@@ -799,7 +849,7 @@ Q4Plan make_q4_plan(const pkv_pool* pool, int rows)
 {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     Q4Plan pl;
-    pl.ctas = pool->ctas_override > 0 ? pool->ctas_override : pool->num_sms;
+    pl.ctas = std::min(pool->ctas_override > 0 ? pool->ctas_override : pool->num_sms, 4096);  // (Q4Split's 32 bits)
     const size_t units = (size_t)rows * pool->cfg.kv_heads, slots = units + (size_t)pl.ctas * kQ4Warps;
     const size_t heads = (size_t)rows * pool->cfg.heads;
     size_t off = 0;
@@ -833,14 +883,16 @@ cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& pl
     ap.q_hat = reinterpret_cast<__half*>(a.ws + plan.off_qhat);
     ap.q_mul = reinterpret_cast<float*>(a.ws + plan.off_qmul);
     ap.tok_len = reinterpret_cast<int32_t*>(a.ws + plan.off_len);
+    ap.out = static_cast<__nv_bfloat16*>(a.out);
     const int items = (ap.kv_heads + 3) / 4 + ap.kv_heads;
-    (ap.rot == kHeadDim ? q4_prep_kernel<true> : q4_prep_kernel<false>)<<<a.rows, 32 * std::min(items, 16), 0, s>>>(ap);
-    cudaError_t rc = cudaGetLastError();
+    cudaError_t rc = launch_dependent(ap.rot == kHeadDim ? q4_prep_kernel<true> : q4_prep_kernel<false>, (unsigned)a.rows,
+                                      32 * std::min(items, 16), 0, s, ap);
     if (rc != cudaSuccess) return rc;
 
     Q4AttnParams p;
     p.q_hat = ap.q_hat;
     p.q_mul = ap.q_mul;
+    p.positions = a.step_positions;
     p.tok_len = ap.tok_len;
     p.table = a.table;
     p.data = ap.data;
@@ -851,28 +903,23 @@ cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& pl
     p.err = pool->err;
     p.ntok = a.rows;
     p.pages = a.pages;
+    p.num_pages = pool->num_pages;
+    p.max_seq = pool->cfg.max_seq;
     p.heads = pool->cfg.heads;
     p.kv_heads = pool->cfg.kv_heads;
     p.v_scale = pool->v_scale;
     p.wait_ns = pool->wait_ns;
     const bool timed = pool->timer_on != 0;
     const int slot = timed ? (int)(pool->timer_count.fetch_add(1) % kTimerSlots) : 0;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)plan.ctas);
-    cfg.blockDim = dim3(32 * kQ4Warps);
-    cfg.dynamicSmemBytes = Q4Smem::kAlloc;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = timed ? 0 : 1;  // timed: the attention alone between the events
     if (timed && (rc = cudaEventRecord(pool->ev_start[slot], s)) != cudaSuccess) return rc;
-    if ((rc = cudaLaunchKernelEx(&cfg, q4_attn_kernel, p)) != cudaSuccess) return rc;
+    // (timed: the attention alone between the events)
+    rc = launch_dependent(q4_attn_kernel, (unsigned)plan.ctas, 32 * kQ4Warps, Q4Smem::kAlloc, s, p, !timed);
+    if (rc != cudaSuccess) return rc;
     if (timed && (rc = cudaEventRecord(pool->ev_stop[slot], s)) != cudaSuccess) return rc;
 
     Q4CombineParams cp;
     cp.prefix = p.prefix;
+    cp.tok_len = p.tok_len;
     cp.part_o = p.part_o;
     cp.part_lse = p.part_lse;
     cp.out = p.out;
@@ -881,12 +928,9 @@ cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& pl
     cp.kv_heads = p.kv_heads;
     cp.warps = plan.ctas * kQ4Warps;
     const int64_t units = (int64_t)a.rows * p.kv_heads;
-    const bool few = units < 2 * (int64_t)plan.ctas;
-    cfg.gridDim = dim3((unsigned)units);
-    cfg.blockDim = dim3(32 * kGroup * (few ? 4 : 1));
-    cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;
-    return few ? cudaLaunchKernelEx(&cfg, q4_combine_kernel<4, 8>, cp) : cudaLaunchKernelEx(&cfg, q4_combine_kernel<1, 8>, cp);
+    return units < 2 * (int64_t)plan.ctas
+               ? launch_dependent(q4_combine_kernel<4, 8>, (unsigned)units, 32 * kGroup * 4, 0, s, cp)
+               : launch_dependent(q4_combine_kernel<1, 8>, (unsigned)units, 32 * kGroup, 0, s, cp);
 }
 
 // =====================================================================================
@@ -912,6 +956,8 @@ __global__ void __launch_bounds__(32 * kQ4ReadWarps) q4_read_kernel(Q4ReadParams
 {
     const int lane = threadIdx.x & 31, j = lane & 7, quads = (p.kv_heads + 3) / 4;
     const int item = blockIdx.x * kQ4ReadWarps + (threadIdx.x >> 5), t = item / quads;
+    pdl_wait();
+    pdl_launch_dependents();
     if (t >= p.tokens) return;
     const int g = 4 * (item % quads) + (lane >> 3);
     const int pos = p.positions[t];
@@ -985,8 +1031,7 @@ cudaError_t launch_q4_read(const pkv_pool* pool, const int32_t* positions, const
     p.k_scale = pool->k_scale;
     p.v_scale = pool->v_scale;
     const int64_t items = (int64_t)tokens * ((p.kv_heads + 3) / 4);
-    q4_read_kernel<<<(unsigned)((items + kQ4ReadWarps - 1) / kQ4ReadWarps), 32 * kQ4ReadWarps, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(q4_read_kernel, (unsigned)((items + kQ4ReadWarps - 1) / kQ4ReadWarps), 32 * kQ4ReadWarps, 0, s, p);
 }
 
 }  // namespace pkv

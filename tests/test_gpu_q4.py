@@ -244,13 +244,24 @@ def test_what_lies_behind_a_row_is_not_seen():
     pool.close()
 
 
-def test_rows_may_read_each_others_new_slots():
-    """Row 1 lists row 0's page and attends past the position that row 0 writes in this call."""
-    wl, cache = make([40, 41], 2)
-    wl.table[1] = wl.table[0]
+def test_precheck(monkeypatch):
+    """PKV_CHECK=1: a row that reads another row's new slot, and two rows that write one slot, are refused."""
+    monkeypatch.setenv("PKV_CHECK", "1")
+    wl, cache = make([40, 41, 90], 2)
     pool = pool_of(wl, cache)
-    out = pool.decode(*inputs(wl))
-    check(out, *reference(wl, cache)[:2])
+    q, k, v, qw, kw, pos, table = inputs(wl)
+    check(pool.decode(q, k, v, qw, kw, pos, table), *reference(wl, cache)[:2])
+    same = table.clone()
+    same[1, 0] = same[0, 0]               # row 1 attends past the position that row 0 writes
+    for p, tab in ((pos, same), (torch.tensor([39, 39, 89], dtype=torch.int32, device=DEV), same)):
+        with pytest.raises(pkv.PkvError) as e:
+            pool.decode(q, k, v, qw, kw, p, tab)
+        assert e.value.code == pkv.PKV_EINVAL
+    pool.append(k, v, kw, pos, None, same)    # distinct slots, and nothing is read
+    row = torch.zeros(3, dtype=torch.int32, device=DEV)
+    with pytest.raises(pkv.PkvError) as e:
+        pool.append(k, v, kw, row + 7, row, table)
+    assert e.value.code == pkv.PKV_EINVAL and pool.check_errors() == 0
     pool.close()
 
 

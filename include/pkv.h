@@ -458,7 +458,9 @@ PKV_API int pkv_q4_read(pkv_pool* pool, const int32_t* positions, const int32_t*
  * appended and the attention over the values the pool holds (the new position's own
  * quantised values included).  Arguments, skipped rows and error bits as pkv_decode, out
  * 16-byte aligned; as there, slots must be distinct and a row's new slot must not be read by
- * another row of the call (PKV_CHECK=1 checks both).  Results are the same from run to run. */
+ * another row of the call (PKV_CHECK=1 checks both).  Results are the same from run to run.
+ * Small calls run in one launch, larger ones in three (their results differ by rounding
+ * only); a grid size set by pkv_set_ctas, up to 4096 CTAs, always takes the latter. */
 PKV_API int pkv_q4_decode(pkv_pool* pool, const void* q, const void* k, const void* v, const void* q_norm_w,
                           const void* k_norm_w, const int32_t* positions, const int32_t* table, int rows, int pages,
                           void* out, void* workspace, size_t workspace_bytes, void* stream);

@@ -137,6 +137,27 @@ __global__ void __launch_bounds__(32 * kQ4AppendWarps) q4_append_kernel(Q4Append
     q4_append_heads<kFullRot>(p, kraw, vraw, wk, g, live, page, pos, lane);
 }
 
+// A query head over 8 lanes as fp16, times the power of two that brings its largest
+// value into [1, 2), so that fp16 keeps 11 bits of it whatever its size.  Returns what
+// a score of it is multiplied with: never 0, which would make a masked score NaN (below
+// 1e-30 the scores are 0 either way).
+__device__ __forceinline__ float q4_query(const float (&y)[16], float k_scale, uint32_t (&r)[8])
+{
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(y[k]));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    const int ex = min(max((int)(__float_as_uint(top) >> 23), 1), 253);  // 2^(ex - 127) <= top < twice that
+    const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const __half2 h = __floats2half2_rn(y[2 * k] * down, y[2 * k + 1] * down);
+        r[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return fmaxf(__uint_as_float((uint32_t)ex << 23) * kQScale * k_scale, 1e-30f);
+}
+
 // In front of the attention: one CTA per row checks every page that the row will read,
 // writes its attended length (and the zeros of a skipped row's output), appends its k and v (items 0 .. quads - 1 of 4 kv heads)
 // and prepares its queries (items from there on, the 4 query heads of a kv head each).
@@ -194,29 +215,15 @@ __global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
             q4_append_heads<kFullRot>(p, a, b, w, g, g < p.kv_heads, page, pos, lane);
             continue;
         }
-        // a query head, scaled by a power of two to largest value in [1, 2), so that fp16 keeps
-        // 11 bits of it whatever its size; the attention's scores take the inverse
         float x[16], y[16];
+        uint32_t r[8];
         unpack16(a[0], a[1], x);
         norm_rope_q16<kFullRot>(x, w, p.rope_hi + (int64_t)pos * kRopeHalf, p.eps, lane, p.rot, y);
-        float top = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(y[k]));
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-        const int ex = min(max((int)(__float_as_uint(top) >> 23), 1), 253);  // 2^(ex - 127) <= top < twice that
-        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
-        uint32_t r[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const __half2 h = __floats2half2_rn(y[2 * k] * down, y[2 * k + 1] * down);
-            r[k] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+        const float mul = q4_query(y, p.k_scale, r);
         const int64_t head = (int64_t)t * p.heads + 4 * (item - quads) + sub;
         *reinterpret_cast<uint4*>(p.q_hat + head * kHeadDim + 8 * j) = make_uint4(r[0], r[1], r[2], r[3]);
         *reinterpret_cast<uint4*>(p.q_hat + head * kHeadDim + 64 + 8 * j) = make_uint4(r[4], r[5], r[6], r[7]);
-        // (never 0, which would make a masked score NaN; below 1e-30 the scores are 0 either way)
-        if (j == 0) p.q_mul[head] = fmaxf(__uint_as_float((uint32_t)ex << 23) * kQScale * p.k_scale, 1e-30f);
+        if (j == 0) p.q_mul[head] = mul;
     }
 }
 
@@ -416,6 +423,191 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
+// What a lane keeps of its place in the fragments (lane = 4 r + c).
+struct Q4Lane {
+    int r, c;
+    int pi_r;         // position of row r
+    int pi_0, pi_1;   // positions of k = 2c, 2c + 1
+    uint32_t koff, voff0, voff1, soff;
+    __device__ __forceinline__ explicit Q4Lane(int lane)
+    {
+        r = lane >> 2;
+        c = lane & 3;
+        pi_r = ((r >> 1) ^ (r & 1)) | ((r & 1) << 2);
+        pi_0 = c;
+        pi_1 = (c ^ 1) | 4;
+        koff = 64 * pi_r + ((16 * c) ^ (((pi_r >> 1) & 1) << 5));
+        voff0 = kQ4VCodes + 64 * pi_0 + ((8 * r) ^ (((pi_0 >> 1) & 1) << 5));
+        voff1 = kQ4VCodes + 64 * pi_1 + ((8 * r) ^ (((pi_1 >> 1) & 1) << 5));
+        soff = kQ4KScales + 16 * r + 4 * c;
+    }
+};
+
+// A warp's attention of one (token, kv head) over some of its chunks.
+struct Q4State {
+    uint32_t bq[8][2];   // the queries' fragments
+    float mulA, mulB;    // what scores of heads 2c and 2c + 1 are multiplied with (c < 2)
+    float o[8][4];       // o[k][0], [2]: dims 16r + 2k, + 1 of head 2c; [1], [3] of head 2c + 1; not normalised
+    float mA, mB, lA, lB;  // running maximum (of the warp) and sum (of the lane)
+
+    // q_hat: 4 heads of 128 fp16; q_mul: their multipliers
+    __device__ __forceinline__ void open(const Q4Lane& L, const __half* q_hat, const float* q_mul)
+    {
+        uint4 x[4] = {};
+        if (L.r < kGroup) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = reinterpret_cast<const uint4*>(q_hat + L.r * kHeadDim + 32 * L.c)[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            bq[2 * k][0] = x[k].x;
+            bq[2 * k][1] = x[k].y;
+            bq[2 * k + 1][0] = x[k].z;
+            bq[2 * k + 1][1] = x[k].w;
+        }
+        mulA = mulB = 1.f;
+        if (L.c < 2) {
+            const float2 mul = *reinterpret_cast<const float2*>(q_mul + 2 * L.c);
+            mulA = mul.x;
+            mulB = mul.y;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
+        mA = mB = -CUDART_INF_F;
+        lA = lB = 0.f;
+    }
+
+    // One chunk in shared memory at sb, of which the unit has `left` positions (as many or more: all).
+    __device__ __forceinline__ void chunk(const Q4Lane& L, const uint8_t* sb, int left)
+    {
+        // ---- S = K q^T
+        float s[kQ4Blocks][4];
+#pragma unroll
+        for (int b = 0; b < kQ4Blocks; ++b) {
+            s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
+            const uint8_t* kb = sb + b * kQ4BlockBytes;
+            const uint4 k0 = *reinterpret_cast<const uint4*>(kb + L.koff), k1 = *reinterpret_cast<const uint4*>(kb + L.koff + 512);
+            const uint32_t sc = *reinterpret_cast<const uint32_t*>(kb + L.soff);
+            const uint32_t s0 = e4m3x2_half2(sc), s1 = e4m3x2_half2(sc >> 16);
+            const uint32_t sd[2][2] = {{__byte_perm(s0, s0, 0x1010), __byte_perm(s0, s0, 0x3232)},
+                                       {__byte_perm(s1, s1, 0x1010), __byte_perm(s1, s1, 0x3232)}};
+            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t h0[4], h1[4];
+                q4_unpack(w0[q], h0);
+                q4_unpack(w1[q], h1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h0[e] = mul_half2(h0[e], sd[0][q >> 1]);
+                    h1[e] = mul_half2(h1[e], sd[1][q >> 1]);
+                }
+                mma_f16_16816(s[b], h0[0], h1[0], h0[1], h1[1], bq[2 * q][0], bq[2 * q][1]);
+                mma_f16_16816(s[b], h0[2], h1[2], h0[3], h1[3], bq[2 * q + 1][0], bq[2 * q + 1][1]);
+            }
+        }
+
+        // ---- softmax, base 2: s[b][0], [1]: heads 2c, 2c + 1 at position L.pi_r of block b; [2], [3]: at L.pi_r + 8
+        // Positions past the row's end: scores of -inf, and V scales of 0 (the codes are finite
+        // whatever lies there), in a row's last chunk only.
+        uint32_t vmask[kQ4Blocks];
+#pragma unroll
+        for (int b = 0; b < kQ4Blocks; ++b) vmask[b] = ~0u;
+        if (left < kQ4Chunk) {
+#pragma unroll
+            for (int b = 0; b < kQ4Blocks; ++b) {
+                const int at = left - kQ4Block * b;
+                if (L.pi_r >= at) s[b][0] = s[b][1] = -CUDART_INF_F;
+                if (L.pi_r + 8 >= at) s[b][2] = s[b][3] = -CUDART_INF_F;
+                vmask[b] = (L.pi_0 < at ? 0xffu : 0u) | (L.pi_1 < at ? 0xff00u : 0u) | (L.pi_0 + 8 < at ? 0xff0000u : 0u) |
+                           (L.pi_1 + 8 < at ? 0xff000000u : 0u);
+            }
+        }
+        float nA = fmaxf(s[0][0], s[0][2]), nB = fmaxf(s[0][1], s[0][3]);
+#pragma unroll
+        for (int b = 1; b < kQ4Blocks; ++b) {
+            nA = fmaxf(nA, fmaxf(s[b][0], s[b][2]));
+            nB = fmaxf(nB, fmaxf(s[b][1], s[b][3]));
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            nA = fmaxf(nA, __shfl_xor_sync(kFull, nA, d));
+            nB = fmaxf(nB, __shfl_xor_sync(kFull, nB, d));
+        }
+        nA *= mulA;
+        nB *= mulB;
+        // the running maximum follows only when it is passed by more than 2^kQ4Slack: weights stay below
+        // that, well inside fp16, and most chunks rescale nothing
+        if (__any_sync(kFull, nA > mA + kQ4Slack || nB > mB + kQ4Slack)) {
+            nA = fmaxf(nA, mA);
+            nB = fmaxf(nB, mB);
+            // (a maximum still at -inf -- scores that are all NaN -- leaves nothing to rescale)
+            const float aA = nA == -CUDART_INF_F ? 1.f : ex2(mA - nA), aB = nB == -CUDART_INF_F ? 1.f : ex2(mB - nB);
+            mA = nA;
+            mB = nB;
+            lA *= aA;
+            lB *= aB;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                o[k][0] *= aA;
+                o[k][1] *= aB;
+                o[k][2] *= aA;
+                o[k][3] *= aB;
+            }
+        }
+        uint32_t pb[kQ4Blocks][2];
+#pragma unroll
+        for (int b = 0; b < kQ4Blocks; ++b) {
+            float e[4];
+            e[0] = ex2(__fmaf_rn(s[b][0], mulA, -mA));
+            e[1] = ex2(__fmaf_rn(s[b][1], mulB, -mB));
+            e[2] = ex2(__fmaf_rn(s[b][2], mulA, -mA));
+            e[3] = ex2(__fmaf_rn(s[b][3], mulB, -mB));
+            lA += e[0] + e[2];
+            lB += e[1] + e[3];
+            const __half2 lo = __floats2half2_rn(e[0], e[1]), hi = __floats2half2_rn(e[2], e[3]);
+            pb[b][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&lo));
+            pb[b][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&hi));
+        }
+
+        // ---- O^T += V^T P
+#pragma unroll
+        for (int b = 0; b < kQ4Blocks; ++b) {
+            const uint8_t* vb = sb + b * kQ4BlockBytes;
+            const uint2 v0 = *reinterpret_cast<const uint2*>(vb + L.voff0), v1 = *reinterpret_cast<const uint2*>(vb + L.voff1);
+            const uint2 v2 = *reinterpret_cast<const uint2*>(vb + L.voff0 + 512), v3 = *reinterpret_cast<const uint2*>(vb + L.voff1 + 512);
+            const uint32_t sc = *reinterpret_cast<const uint32_t*>(vb + L.soff + 128) & vmask[b];
+            const uint32_t s01 = e4m3x2_half2(sc), s23 = e4m3x2_half2(sc >> 16);
+            const uint32_t a0[2] = {v0.x, v0.y}, a1[2] = {v1.x, v1.y}, a2[2] = {v2.x, v2.y}, a3[2] = {v3.x, v3.y};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+                uint32_t e01[4], d01[4], e23[4], d23[4];  // even and odd dims of the two pairs of positions
+                q4_unpack((a0[q] & kLow) | ((a1[q] << 4) & ~kLow), e01);
+                q4_unpack(((a0[q] >> 4) & kLow) | (a1[q] & ~kLow), d01);
+                q4_unpack((a2[q] & kLow) | ((a3[q] << 4) & ~kLow), e23);
+                q4_unpack(((a2[q] >> 4) & kLow) | (a3[q] & ~kLow), d23);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    mma_f16_16816(o[4 * q + e], mul_half2(e01[e], s01), mul_half2(d01[e], s01), mul_half2(e23[e], s23),
+                                  mul_half2(d23[e], s23), pb[b][0], pb[b][1]);
+            }
+        }
+    }
+
+    // The sums over all lanes, for heads 2c and 2c + 1.
+    __device__ __forceinline__ void sums(float& LA, float& LB) const
+    {
+        LA = lA;
+        LB = lB;
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            LA += __shfl_xor_sync(kFull, LA, d);
+            LB += __shfl_xor_sync(kFull, LB, d);
+        }
+    }
+};
+
 __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -508,11 +700,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
             const uint32_t bytes = min((ilen - ij * kQ4Chunk + kQ4Block - 1) / kQ4Block, kQ4Blocks) * kQ4BlockBytes;
             mbar_arrive_expect_tx(bars + 8 * ist, bytes);
             const uint8_t* src = p.data + ((int64_t)page * G + ig) * kQ4PageBytes + (ij % kPerPage) * kQ4ChunkBytes;
-            asm volatile(
-                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                    ring + ist * kQ4ChunkBytes),
-                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bars + 8 * ist)
-                : "memory");
+            bulk_copy_g2s(ring + ist * kQ4ChunkBytes, src, bytes, bars + 8 * ist);
         }
         ++issued;
         ist = ist == kQ4Stages - 1 ? 0 : ist + 1;
@@ -526,19 +714,9 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
     pdl_wait();
     while (issued < kQ4Stages - 1 && issued < count) issue();
 
-    const int r = lane >> 2, c = lane & 3;
-    const int pi_r = ((r >> 1) ^ (r & 1)) | ((r & 1) << 2);  // position of row r (see above)
-    const int pi_0 = c, pi_1 = (c ^ 1) | 4;                   // positions of k = 2c, 2c + 1
+    const Q4Lane L(lane);
     const uint8_t* wring = sbase + warp * (kQ4Stages * kQ4ChunkBytes);
-    const uint32_t koff = 64 * pi_r + ((16 * c) ^ (((pi_r >> 1) & 1) << 5));
-    const uint32_t voff0 = kQ4VCodes + 64 * pi_0 + ((8 * r) ^ (((pi_0 >> 1) & 1) << 5));
-    const uint32_t voff1 = kQ4VCodes + 64 * pi_1 + ((8 * r) ^ (((pi_1 >> 1) & 1) << 5));
-    const uint32_t soff = kQ4KScales + 16 * r + 4 * c;
-
-    uint32_t bq[8][2];
-    float mulA = 1.f, mulB = 1.f;
-    float o[8][4];
-    float mA = 0.f, mB = 0.f, lA = 0.f, lB = 0.f;
+    Q4State S;
     bool fresh = true;   // the next chunk opens a segment
     bool whole = false;  // the segment began with its unit's first chunk
     bool live = false;   // its row has an output (the preparation found no fault with it)
@@ -549,28 +727,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
     for (int i = 0; i < count; ++i) {
         if (issued < count) issue();
         if (fresh) {
-            const __half* qh = p.q_hat + ((int64_t)t * H + g * kGroup + (r & 3)) * kHeadDim + 32 * c;
-            uint4 x[4] = {};
-            if (r < kGroup) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = reinterpret_cast<const uint4*>(qh)[k];
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                bq[2 * k][0] = x[k].x;
-                bq[2 * k][1] = x[k].y;
-                bq[2 * k + 1][0] = x[k].z;
-                bq[2 * k + 1][1] = x[k].w;
-            }
-            if (c < 2) {
-                const float2 mul = *reinterpret_cast<const float2*>(p.q_mul + (int64_t)t * H + g * kGroup + 2 * c);
-                mulA = mul.x;
-                mulB = mul.y;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
-            mA = mB = -CUDART_INF_F;
-            lA = lB = 0.f;
+            S.open(L, p.q_hat + ((int64_t)t * H + g * kGroup) * kHeadDim, p.q_mul + (int64_t)t * H + g * kGroup);
             live = p.tok_len[t] > 0;
             whole = j == 0;
             fresh = false;
@@ -579,122 +736,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
             ok = false;
             break;
         }
-        const uint8_t* sb = wring + st * kQ4ChunkBytes;
-
-        // ---- S = K q^T
-        float s[kQ4Blocks][4];
-#pragma unroll
-        for (int b = 0; b < kQ4Blocks; ++b) {
-            s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
-            const uint8_t* kb = sb + b * kQ4BlockBytes;
-            const uint4 k0 = *reinterpret_cast<const uint4*>(kb + koff), k1 = *reinterpret_cast<const uint4*>(kb + koff + 512);
-            const uint32_t sc = *reinterpret_cast<const uint32_t*>(kb + soff);
-            const uint32_t s0 = e4m3x2_half2(sc), s1 = e4m3x2_half2(sc >> 16);
-            const uint32_t sd[2][2] = {{__byte_perm(s0, s0, 0x1010), __byte_perm(s0, s0, 0x3232)},
-                                       {__byte_perm(s1, s1, 0x1010), __byte_perm(s1, s1, 0x3232)}};
-            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t h0[4], h1[4];
-                q4_unpack(w0[q], h0);
-                q4_unpack(w1[q], h1);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    h0[e] = mul_half2(h0[e], sd[0][q >> 1]);
-                    h1[e] = mul_half2(h1[e], sd[1][q >> 1]);
-                }
-                mma_f16_16816(s[b], h0[0], h1[0], h0[1], h1[1], bq[2 * q][0], bq[2 * q][1]);
-                mma_f16_16816(s[b], h0[2], h1[2], h0[3], h1[3], bq[2 * q + 1][0], bq[2 * q + 1][1]);
-            }
-        }
-
-        // ---- softmax, base 2: s[b][0], [1]: heads 2c, 2c + 1 at position pi_r of block b; [2], [3]: at pi_r + 8
-        // Positions past the row's end: scores of -inf, and V scales of 0 (the codes are finite
-        // whatever lies there), in a row's last chunk only.
-        uint32_t vmask[kQ4Blocks];
-#pragma unroll
-        for (int b = 0; b < kQ4Blocks; ++b) vmask[b] = ~0u;
-        const int left = len - j * kQ4Chunk;  // positions of the unit from this chunk on
-        if (left < kQ4Chunk) {
-#pragma unroll
-            for (int b = 0; b < kQ4Blocks; ++b) {
-                const int at = left - kQ4Block * b;
-                if (pi_r >= at) s[b][0] = s[b][1] = -CUDART_INF_F;
-                if (pi_r + 8 >= at) s[b][2] = s[b][3] = -CUDART_INF_F;
-                vmask[b] = (pi_0 < at ? 0xffu : 0u) | (pi_1 < at ? 0xff00u : 0u) | (pi_0 + 8 < at ? 0xff0000u : 0u) |
-                           (pi_1 + 8 < at ? 0xff000000u : 0u);
-            }
-        }
-        float nA = fmaxf(s[0][0], s[0][2]), nB = fmaxf(s[0][1], s[0][3]);
-#pragma unroll
-        for (int b = 1; b < kQ4Blocks; ++b) {
-            nA = fmaxf(nA, fmaxf(s[b][0], s[b][2]));
-            nB = fmaxf(nB, fmaxf(s[b][1], s[b][3]));
-        }
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-            nA = fmaxf(nA, __shfl_xor_sync(kFull, nA, d));
-            nB = fmaxf(nB, __shfl_xor_sync(kFull, nB, d));
-        }
-        nA *= mulA;
-        nB *= mulB;
-        // the running maximum follows only when it is passed by more than 2^kQ4Slack: weights stay below
-        // that, well inside fp16, and most chunks rescale nothing
-        if (__any_sync(kFull, nA > mA + kQ4Slack || nB > mB + kQ4Slack)) {
-            nA = fmaxf(nA, mA);
-            nB = fmaxf(nB, mB);
-            // (a maximum still at -inf -- scores that are all NaN -- leaves nothing to rescale)
-            const float aA = nA == -CUDART_INF_F ? 1.f : ex2(mA - nA), aB = nB == -CUDART_INF_F ? 1.f : ex2(mB - nB);
-            mA = nA;
-            mB = nB;
-            lA *= aA;
-            lB *= aB;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                o[k][0] *= aA;
-                o[k][1] *= aB;
-                o[k][2] *= aA;
-                o[k][3] *= aB;
-            }
-        }
-        uint32_t pb[kQ4Blocks][2];
-#pragma unroll
-        for (int b = 0; b < kQ4Blocks; ++b) {
-            float e[4];
-            e[0] = ex2(__fmaf_rn(s[b][0], mulA, -mA));
-            e[1] = ex2(__fmaf_rn(s[b][1], mulB, -mB));
-            e[2] = ex2(__fmaf_rn(s[b][2], mulA, -mA));
-            e[3] = ex2(__fmaf_rn(s[b][3], mulB, -mB));
-            lA += e[0] + e[2];
-            lB += e[1] + e[3];
-            const __half2 lo = __floats2half2_rn(e[0], e[1]), hi = __floats2half2_rn(e[2], e[3]);
-            pb[b][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&lo));
-            pb[b][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&hi));
-        }
-
-        // ---- O^T += V^T P
-#pragma unroll
-        for (int b = 0; b < kQ4Blocks; ++b) {
-            const uint8_t* vb = sb + b * kQ4BlockBytes;
-            const uint2 v0 = *reinterpret_cast<const uint2*>(vb + voff0), v1 = *reinterpret_cast<const uint2*>(vb + voff1);
-            const uint2 v2 = *reinterpret_cast<const uint2*>(vb + voff0 + 512), v3 = *reinterpret_cast<const uint2*>(vb + voff1 + 512);
-            const uint32_t sc = *reinterpret_cast<const uint32_t*>(vb + soff + 128) & vmask[b];
-            const uint32_t s01 = e4m3x2_half2(sc), s23 = e4m3x2_half2(sc >> 16);
-            const uint32_t a0[2] = {v0.x, v0.y}, a1[2] = {v1.x, v1.y}, a2[2] = {v2.x, v2.y}, a3[2] = {v3.x, v3.y};
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                constexpr uint32_t kLow = 0x0f0f0f0fu;
-                uint32_t e01[4], d01[4], e23[4], d23[4];  // even and odd dims of the two pairs of positions
-                q4_unpack((a0[q] & kLow) | ((a1[q] << 4) & ~kLow), e01);
-                q4_unpack(((a0[q] >> 4) & kLow) | (a1[q] & ~kLow), d01);
-                q4_unpack((a2[q] & kLow) | ((a3[q] << 4) & ~kLow), e23);
-                q4_unpack(((a2[q] >> 4) & kLow) | (a3[q] & ~kLow), d23);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    mma_f16_16816(o[4 * q + e], mul_half2(e01[e], s01), mul_half2(d01[e], s01), mul_half2(e23[e], s23),
-                                  mul_half2(d23[e], s23), pb[b][0], pb[b][1]);
-            }
-        }
+        S.chunk(L, wring + st * kQ4ChunkBytes, len - j * kQ4Chunk);
         __syncwarp();  // every lane has read the stage: it may be filled again
 
         if (++st == kQ4Stages) {
@@ -703,12 +745,10 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
         }
         const bool last = j == n - 1;
         if ((last || i == count - 1) && live) {  // end of the segment
-            float LA = lA, LB = lB;
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                LA += __shfl_xor_sync(kFull, LA, d);
-                LB += __shfl_xor_sync(kFull, LB, d);
-            }
+            float LA, LB;
+            S.sums(LA, LB);
+            const int r = L.r, c = L.c;
+            const float(&o)[8][4] = S.o;
             const int64_t u = (int64_t)t * G + g;
             if (c < 2) {
                 const float iA = p.v_scale / LA, iB = p.v_scale / LB;
@@ -738,7 +778,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
                     }
                     if (r == 0)
                         *reinterpret_cast<float2*>(p.part_lse + (u + w) * kGroup + 2 * c) =
-                            make_float2(mA + log2f(LA), mB + log2f(LB));
+                            make_float2(S.mA + log2f(LA), S.mB + log2f(LB));
                 }
             }
         }
@@ -843,6 +883,224 @@ __global__ void __launch_bounds__(32 * kGroup * kSub) q4_combine_kernel(Q4Combin
 }
 
 // =====================================================================================
+// q4_unit_kernel: a whole decode call in one launch, for small calls
+// =====================================================================================
+//
+// A cluster of CTAs per (token, kv head) unit; its warps take the unit's chunks in
+// turn (chunk j: warp j mod the cluster's warps, spread over its CTAs first).  Every
+// CTA checks the row and prepares the unit's queries; the warp that has the last chunk
+// quantises the row's k and v while that chunk is on its way, and puts them into the
+// pool and into the staged chunk.  The warps' sums meet in the first CTA, which reads
+// the others' through distributed shared memory.
+//
+// A call of few short rows is bound by its chain of latencies, not by bytes: this has
+// one launch and one trip to memory after the table, where preparation, split attention
+// and combine are three launches.  (Measured on one row of 700: 9 us a call instead of 14.)
+constexpr int kUnitWarps = 4;
+constexpr int kUnitStages = 2;
+
+struct Q4UnitSmem {
+    static constexpr int kBars = kUnitWarps * kUnitStages * kQ4ChunkBytes;
+    static constexpr int kQ = kBars + 8 * kUnitWarps * kUnitStages;  // __half [4][128]
+    static constexpr int kMul = kQ + 2 * kGroup * kHeadDim;          // float [4]
+    static constexpr int kML = kMul + 4 * kGroup;                    // float2 [warps][4]: maximum and sum
+    static constexpr int kBytes = kML + 8 * kUnitWarps * kGroup;
+    static constexpr int kAlloc = kBytes + 128;
+};
+static_assert(kUnitWarps == kGroup, "the merge has a warp a query head");
+
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+template <bool kFullRot>
+__global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams p, float v_scale, uint64_t wait_ns, int cs)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 127u) & ~127u;
+    uint8_t* sbase = smem_raw + (base - raw);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lj = lane & 7, sub = lane >> 3, G = p.kv_heads;
+    const int u = blockIdx.x / cs, t = u / G, g = u % G, rank = (int)cluster_rank();
+    const uint32_t bars = base + Q4UnitSmem::kBars + 8 * kUnitStages * warp;
+    uint8_t* ring = sbase + warp * (kUnitStages * kQ4ChunkBytes);
+    __half* sQ = reinterpret_cast<__half*>(sbase + Q4UnitSmem::kQ);
+    float* sMul = reinterpret_cast<float*>(sbase + Q4UnitSmem::kMul);
+    float2* sML = reinterpret_cast<float2*>(sbase + Q4UnitSmem::kML);
+    if (lane == 0) {
+        for (int i = 0; i < kUnitStages; ++i) mbar_init(bars + 8 * i, 1);
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // the inputs that depend on nothing: q (warp 0, 8 lanes a head), k and v (8 lanes, all four times)
+    uint4 qraw[2], kraw[2], vraw[2], wq[2], wk[2];
+    if (warp == 0) {
+        load16(p.q + ((int64_t)t * p.heads + g * kGroup + sub) * kHeadDim, lj, qraw);
+        load16(p.qw, lj, wq);
+    }
+    const int64_t kv = ((int64_t)t * G + g) * kHeadDim;
+    load16(p.k + kv, lj, kraw);
+    load16(p.v + kv, lj, vraw);
+    load16(p.kw, lj, wk);
+    int pos, row;
+    bool active;
+    uint32_t e = q4_token(p, t, pos, row, active);
+    const int n = active && !e ? pos / kPageSize + 1 : 0;  // chunks (pages)
+    int bad = 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int id = page_of(p.table, p.pages, row, i);
+        bad |= id < 0 || id >= p.num_pages;
+    }
+    if (__syncthreads_or(bad)) e = PKV_DEVERR_PAGE;
+    if (!active || e) {  // (the same for the whole cluster)
+        if (rank == 0) {
+            uint4* out = reinterpret_cast<uint4*>(p.out + ((int64_t)t * p.heads + g * kGroup) * kHeadDim);
+            if (threadIdx.x < kGroup * kHeadDim / 8) out[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+            if (e && g == 0 && threadIdx.x == 0) atomicOr(p.err, e);
+        }
+        return;
+    }
+
+    // this warp's chunks first, first + step, ...; the copies of the first stages
+    const int step = cs * kUnitWarps, first = warp * cs + rank;
+    int issued = first;
+    auto issue = [&](int st) {  // (one lane)
+        const int page = page_of(p.table, p.pages, row, issued);
+        const uint32_t bytes = min((pos - issued * kQ4Chunk) / kQ4Block + 1, kQ4Blocks) * kQ4BlockBytes;
+        mbar_arrive_expect_tx(bars + 8 * st, bytes);
+        bulk_copy_g2s(smem_u32(ring) + st * kQ4ChunkBytes, p.data + q4_block(page, G, g, 0), bytes, bars + 8 * st);
+    };
+    for (int st = 0; st < kUnitStages && issued < n; ++st, issued += step)
+        if (lane == 0) issue(st);
+
+    const int64_t at = (int64_t)pos * kRopeHalf;
+    if (warp == 0) {
+        float x[16], y[16];
+        uint32_t h[8];
+        unpack16(qraw[0], qraw[1], x);
+        norm_rope_q16<kFullRot>(x, wq, p.rope_hi + at, p.eps, lane, p.rot, y);
+        const float mul = q4_query(y, p.k_scale, h);
+        *reinterpret_cast<uint4*>(sQ + sub * kHeadDim + 8 * lj) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(sQ + sub * kHeadDim + 64 + 8 * lj) = make_uint4(h[4], h[5], h[6], h[7]);
+        if (lj == 0) sMul[sub] = mul;
+    }
+    const bool owner = first < n && (n - 1 - first) % step == 0;  // this warp has the last chunk
+    float xn[16];  // lanes of sub 0 and 1: the new k, of 2 and 3: v
+    if (owner) {
+        float x[16], k[16];
+        unpack16(kraw[0], kraw[1], x);
+        norm_rope_k_paired<kFullRot>(x, wk, p.rope_hi + at, p.rope_lo + at, p.eps2, lane, p.rot, k);
+        unpack16(vraw[0], vraw[1], x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) xn[i] = sub < 2 ? k[i] : x[i];
+    }
+    __syncthreads();
+
+    const Q4Lane L(lane);
+    Q4State S;
+    S.open(L, sQ, sMul);
+    bool ok = true;
+    int i = 0;
+    for (int j = first; j < n; j += step, ++i) {
+        const int st = i % kUnitStages;
+        if (__any_sync(kFull, !mbar_wait(bars + 8 * st, (i / kUnitStages) & 1, wait_ns))) {
+            ok = false;
+            break;
+        }
+        uint8_t* sb = ring + st * kQ4ChunkBytes;
+        if (j == n - 1) {  // the new position into the staged chunk (sub 0, 2) and into the pool (1, 3)
+            const int s = pos % kPageSize;
+            uint8_t* pool = p.data + q4_block(page_of(p.table, p.pages, row, j), G, g, s);
+            q4_store((sub & 1) ? pool : sb + s / kQ4Block * kQ4BlockBytes, sub >= 2, s % kQ4Block, xn,
+                     sub < 2 ? p.k_inv6 : p.v_inv6, sub < 2 ? p.k_inv : p.v_inv, lj, true);
+            __syncwarp();
+        }
+        S.chunk(L, sb, pos + 1 - j * kQ4Chunk);
+        __syncwarp();
+        if (issued < n) {
+            if (lane == 0) issue(st);
+            issued += step;
+        }
+    }
+    if (!ok) {  // the awaited copy is late: report, and let the copies in flight land
+        if (lane == 0) {
+            atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+            const int all = (issued - first) / step;
+            for (int k = max(0, all - kUnitStages); k < all; ++k)
+                mbar_wait(bars + 8 * (k % kUnitStages), (k / kUnitStages) & 1, kWaitLimitNs);
+        }
+        __syncwarp();
+    }
+
+    // ---- the warps' sums into their own ring (nothing in flight there any more), then one warp a head joins them
+    float LA, LB;
+    S.sums(LA, LB);
+    float* part = reinterpret_cast<float*>(ring);
+    if (L.c < 2 && first < n) {
+        float* pa = part + 2 * L.c * kHeadDim + 16 * L.r;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            *reinterpret_cast<float4*>(pa + 4 * k) = make_float4(S.o[2 * k][0], S.o[2 * k][2], S.o[2 * k + 1][0], S.o[2 * k + 1][2]);
+            *reinterpret_cast<float4*>(pa + kHeadDim + 4 * k) =
+                make_float4(S.o[2 * k][1], S.o[2 * k][3], S.o[2 * k + 1][1], S.o[2 * k + 1][3]);
+        }
+        if (L.r == 0) {
+            sML[warp * kGroup + 2 * L.c] = make_float2(S.mA, LA);
+            sML[warp * kGroup + 2 * L.c + 1] = make_float2(S.mB, LB);
+        }
+    }
+    if (cs > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (rank == 0) {
+        const int h = warp, parts = min(n, step);  // warp w of CTA r has chunk w cs + r first: parts are 0 .. parts - 1
+        // maxima and sums of the parts, one a lane
+        float2 ml = make_float2(-CUDART_INF_F, 0.f);
+        if (lane < parts) {
+            const uint32_t a = base + Q4UnitSmem::kML + 8 * (lane / cs * kGroup + h);
+            ml = ld_cluster_f32x2(cluster_map(a, lane % cs));
+        }
+        float M = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        const float f = lane < parts ? exp2f(ml.x - M) : 0.f;  // (NaN sums: M is theirs or above; f * NaN or NaN)
+        float sum = f * ml.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        constexpr int kBatch = 4;
+        for (int k0 = 0; k0 < parts; k0 += kBatch) {
+            float4 x[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int q = min(k0 + k, parts - 1);
+                const uint32_t a = base + q / cs * (kUnitStages * kQ4ChunkBytes) + 4 * (h * kHeadDim + 4 * lane);
+                x[k] = ld_cluster_f32x4(cluster_map(a, q % cs));
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const float fk = __shfl_sync(kFull, f, min(k0 + k, parts - 1));
+                if (k0 + k < parts) {
+                    acc[0] += fk * x[k].x;
+                    acc[1] += fk * x[k].y;
+                    acc[2] += fk * x[k].z;
+                    acc[3] += fk * x[k].w;
+                }
+            }
+        }
+        const float inv = v_scale / sum;
+        const float y[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+        *reinterpret_cast<uint2*>(p.out + ((int64_t)t * p.heads + g * kGroup + h) * kHeadDim + 4 * lane) = pack4(y);
+    }
+    if (cs > 1) cluster_sync();  // the others' shared memory is read until here
+}
+
+// =====================================================================================
 // the decode call
 // =====================================================================================
 Q4Plan make_q4_plan(const pkv_pool* pool, int rows)
@@ -863,9 +1121,53 @@ Q4Plan make_q4_plan(const pkv_pool* pool, int rows)
     return pl;
 }
 
+// The CTAs that each unit gets in q4_unit_kernel, or 0: the call goes through the split
+// attention.  A unit gets as many CTAs (up to a cluster's 8) as leave about one an SM,
+// and no more than its pages can use.  A CTA's life is about 6 us and 1.25 us more for
+// every further page of its warps; the split attention costs 10 us and the time of its
+// bytes, and more where few units are cut into many pieces.  Measured (us, units
+// against split): 1 row of 700 6.3 / 10.3, 1 of 30000 24 / 38, 4 of 8000 15.3 / 21.4, 16 of
+// 500-1500 11.8 / 16.6, 64 of 1-640 15.5 / 19.6; 32 of 500-1500 18.8 / 18.8, 128 of 1-640
+// 25.4 / 24.7, 256 of 1-64 27.6 / 17.6.  The rows' lengths are not known here: `pages`, the
+// table's width, stands for the longest.  A grid size set by pkv_set_ctas is the split
+// attention's.
+static int q4_unit_ctas(const pkv_pool* pool, int rows, int pages)
+{
+    if (pool->ctas_override > 0) return 0;
+    const int64_t units = (int64_t)rows * pool->cfg.kv_heads, sms = pool->num_sms;
+    int cs = 1;
+    while (cs < 8 && 3 * units * 2 * cs <= 4 * sms && cs * kUnitWarps < pages) cs *= 2;
+    const int rounds = (pages + cs * kUnitWarps - 1) / (cs * kUnitWarps);
+    if (3 * units * cs <= 4 * sms) return rounds <= 16 ? cs : 0;
+    return units <= 4 * sms && rounds <= 4 ? 1 : 0;
+}
+
 cudaError_t configure_q4()
 {
+    cudaError_t rc;
+    if ((rc = cudaFuncSetAttribute(q4_unit_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4UnitSmem::kAlloc)) != cudaSuccess ||
+        (rc = cudaFuncSetAttribute(q4_unit_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4UnitSmem::kAlloc)) != cudaSuccess)
+        return rc;
     return cudaFuncSetAttribute(q4_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4Smem::kAlloc);
+}
+
+static cudaError_t launch_q4_units(const pkv_pool* pool, const Q4AppendParams& ap, int cs, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cs;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ap.tokens * ap.kv_heads * cs));
+    cfg.blockDim = dim3(32 * kUnitWarps);
+    cfg.dynamicSmemBytes = Q4UnitSmem::kAlloc;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, ap.rot == kHeadDim ? q4_unit_kernel<true> : q4_unit_kernel<false>, ap, pool->v_scale,
+                              pool->wait_ns, cs);
 }
 
 cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& plan, cudaStream_t s)
@@ -884,8 +1186,16 @@ cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& pl
     ap.q_mul = reinterpret_cast<float*>(a.ws + plan.off_qmul);
     ap.tok_len = reinterpret_cast<int32_t*>(a.ws + plan.off_len);
     ap.out = static_cast<__nv_bfloat16*>(a.out);
+    cudaError_t rc;
+    const bool timed = pool->timer_on != 0;
+    const int slot = timed ? (int)(pool->timer_count.fetch_add(1) % kTimerSlots) : 0;
+    if (const int cs = q4_unit_ctas(pool, a.rows, a.pages)) {
+        if (timed && (rc = cudaEventRecord(pool->ev_start[slot], s)) != cudaSuccess) return rc;
+        if ((rc = launch_q4_units(pool, ap, cs, s)) != cudaSuccess) return rc;
+        return timed ? cudaEventRecord(pool->ev_stop[slot], s) : cudaSuccess;
+    }
     const int items = (ap.kv_heads + 3) / 4 + ap.kv_heads;
-    cudaError_t rc = launch_dependent(ap.rot == kHeadDim ? q4_prep_kernel<true> : q4_prep_kernel<false>, (unsigned)a.rows,
+    rc = launch_dependent(ap.rot == kHeadDim ? q4_prep_kernel<true> : q4_prep_kernel<false>, (unsigned)a.rows,
                                       32 * std::min(items, 16), 0, s, ap);
     if (rc != cudaSuccess) return rc;
 
@@ -909,8 +1219,6 @@ cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& pl
     p.kv_heads = pool->cfg.kv_heads;
     p.v_scale = pool->v_scale;
     p.wait_ns = pool->wait_ns;
-    const bool timed = pool->timer_on != 0;
-    const int slot = timed ? (int)(pool->timer_count.fetch_add(1) % kTimerSlots) : 0;
     if (timed && (rc = cudaEventRecord(pool->ev_start[slot], s)) != cudaSuccess) return rc;
     // (timed: the attention alone between the events)
     rc = launch_dependent(q4_attn_kernel, (unsigned)plan.ctas, 32 * kQ4Warps, Q4Smem::kAlloc, s, p, !timed);

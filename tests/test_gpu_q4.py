@@ -175,8 +175,9 @@ LENGTHS = [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 63, 64, 65, 0, 127, 128, 129, 7
 
 
 @pytest.mark.parametrize("kv_heads,ks,vs", [(8, 1.0, 1.0), (1, 0.25, 2.0 ** -8), (3, 2.0, 64.0)])
-@pytest.mark.parametrize("ctas", [0, 1, 7])
+@pytest.mark.parametrize("ctas", [0, 1, 7, 152])
 def test_decode(kv_heads, ks, vs, ctas):
+    """ctas 0: one launch for a call of this size; a set grid: the split attention."""
     wl, cache = make(LENGTHS, kv_heads, ks, vs, seed=kv_heads)
     pool = pool_of(wl, cache, ctas)
     out = pool.decode(*inputs(wl, vs))
@@ -190,25 +191,31 @@ def test_decode(kv_heads, ks, vs, ctas):
     pool.close()
 
 
-def test_decode_batches():
-    """Many short rows; the serving batch with shared prefixes; one row alone; few long rows."""
-    for lengths, kw in (([1 + (37 * i) % 90 for i in range(600)], dict(kv_heads=2)),
-                        ([512 + (997 * i) % 3000 for i in range(16)], dict(kv_heads=2, share_groups=8)),
-                        ([700], {}), ([3], dict(kv_heads=1)), ([4096, 4001], dict(kv_heads=2))):
-        wl, cache = make(lengths, seed=len(lengths), **kw)
-        pool = pool_of(wl, cache)
-        out = pool.decode(*inputs(wl))
-        assert pool.check_errors() == 0
-        ref, bound, after = reference(wl, cache)
-        check(out, ref, bound)
-        assert np.array_equal(pool.data.cpu().numpy().reshape(after.data.shape), after.data)
-        pool.close()
+@pytest.mark.parametrize("lengths,kw", [
+    ([1 + (37 * i) % 90 for i in range(600)], dict(kv_heads=2)),             # many short rows
+    ([512 + (997 * i) % 3000 for i in range(16)], dict(kv_heads=2, share_groups=8)),   # shared prefixes
+    ([700], {}), ([3], dict(kv_heads=1)), ([4096, 4001], dict(kv_heads=2)),  # few units, 8, 1 and 4
+    ([1, 64, 65, 0, 300, 256, 257], dict(kv_heads=6)),                       # one CTA a unit, more units than that
+    ([5, 100], dict(kv_heads=2, table_pages=700)),                           # a table far wider than the rows
+    ([2500, 40, 0, 2000], dict(kv_heads=1, table_pages=700)),
+])
+@pytest.mark.parametrize("ctas", [0, 152])
+def test_decode_batches(lengths, kw, ctas):
+    wl, cache = make(lengths, seed=len(lengths), **dict(kw))
+    pool = pool_of(wl, cache, ctas)
+    out = pool.decode(*inputs(wl))
+    assert pool.check_errors() == 0
+    ref, bound, after = reference(wl, cache)
+    check(out, ref, bound)
+    assert np.array_equal(pool.data.cpu().numpy().reshape(after.data.shape), after.data)
+    pool.close()
 
 
 @pytest.mark.parametrize("rot", [32, 64, 96])
-def test_decode_partial_rotation(rot):
+@pytest.mark.parametrize("ctas", [0, 152])
+def test_decode_partial_rotation(rot, ctas):
     wl, cache = make([5, 100, 333], 2, rot=rot)
-    pool = pool_of(wl, cache)
+    pool = pool_of(wl, cache, ctas)
     out = pool.decode(*inputs(wl))
     check(out, *reference(wl, cache)[:2])
     pool.close()
@@ -227,7 +234,8 @@ def test_decode_contiguous_rows():
     pool.close()
 
 
-def test_what_lies_behind_a_row_is_not_seen():
+@pytest.mark.parametrize("ctas", [0, 152])
+def test_what_lies_behind_a_row_is_not_seen(ctas):
     """Every byte of the pool that no row's positions own is 0xff: codes of -6 and scales of NaN."""
     wl, cache = make([1, 17, 40, 64, 90], 2)
     own = np.zeros(cache.data.shape, bool)
@@ -237,7 +245,7 @@ def test_what_lies_behind_a_row_is_not_seen():
             at = np.concatenate([_q4.CODE[i], 1024 + _q4.CODE[i], 2048 + _q4.KS[i], 2176 + _q4.VS[i]])
             own[wl.table[b, s // 64], :, s % 64 // 16][:, at] = True
     cache.data[~own] = 0xff
-    pool = pool_of(wl, cache)
+    pool = pool_of(wl, cache, ctas)
     out = pool.decode(*inputs(wl))
     assert pool.check_errors() == 0
     check(out, *reference(wl, cache)[:2])
@@ -265,14 +273,15 @@ def test_precheck(monkeypatch):
     pool.close()
 
 
-def test_bad_rows_give_zeros_and_leave_the_others():
+@pytest.mark.parametrize("ctas", [0, 152])
+def test_bad_rows_give_zeros_and_leave_the_others(ctas):
     wl, cache = make([100, 100, 70, 200, 9], 2, max_seq=300)
     wl.table[1, 0] = -5              # a page before the written one
     wl.table[2, 1] = wl.num_pages    # the written page
     wl.step_positions[3] = 256       # beyond the table
     wl.step_positions[4] = -7
     before = cache.data.copy()
-    pool = pool_of(wl, cache)
+    pool = pool_of(wl, cache, ctas)
     out = pool.decode(*inputs(wl))
     assert pool.check_errors() == pkv.PKV_DEVERR_PAGE | pkv.PKV_DEVERR_POSITION
     wl.step_positions[3:] = -1
@@ -283,25 +292,27 @@ def test_bad_rows_give_zeros_and_leave_the_others():
     pool.close()
 
 
-def test_nan_stays_in_its_row():
+@pytest.mark.parametrize("ctas", [0, 152])
+def test_nan_stays_in_its_row(ctas):
     wl, cache = make([80, 80, 80], 2)
     v = wl.v.clone()
     v[1, 0, 3] = float("nan")
     wl.v = v
-    pool = pool_of(wl, cache)
+    pool = pool_of(wl, cache, ctas)
     out = f64(pool.decode(*inputs(wl)))
     assert np.isnan(out[1, :4, :16]).all() and np.isfinite(out[1, 4:]).all() and np.isfinite(out[1, :4, 16:]).all()
     assert np.isfinite(out[[0, 2]]).all()
     pool.close()
 
 
-def test_sizes_of_q():
+@pytest.mark.parametrize("ctas", [0, 152])
+def test_sizes_of_q(ctas):
     """Queries of any size: weights of 2^-40 and 2^40 (scores near 0, and a one-hot softmax)."""
     wl, cache = make([300, 33], 2)
     small, big = wl.q_norm_w.clone() * 2.0 ** -40, wl.q_norm_w.clone() * 2.0 ** 6
     for w in (small, big):
         wl.q_norm_w = w
-        pool = pool_of(wl, cache)
+        pool = pool_of(wl, cache, ctas)
         out = pool.decode(*inputs(wl))
         check(out, *reference(wl, cache)[:2])
         pool.close()
@@ -374,12 +385,14 @@ def test_other_streams():
 
 
 def test_a_wait_that_runs_out_is_reported():
-    wl, cache = make([3000] * 4, 8)
+    """A limit of 0 gives up at the first copy that is not there yet (the cache is pushed out of L2 first)."""
+    wl, cache = make([3000] * 40, 2)
     pool = pool_of(wl, cache)
     args = inputs(wl)
     ref = pool.decode(*args)
     assert pool.check_errors() == 0
     pkv.pkv_set_wait_limit(pool.handle, 0)
+    torch.empty(1 << 28, dtype=torch.float32, device=DEV).fill_(1.0)
     pool.decode(*args)
     assert pool.check_errors() == pkv.PKV_DEVERR_TIMEOUT
     pkv.pkv_set_wait_limit(pool.handle, 10 ** 9)

@@ -127,6 +127,8 @@ def _stream(stream) -> int:
 
 
 def _capturing(stream) -> bool:
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
     with _on(stream):
         return torch.cuda.is_current_stream_capturing()
 
@@ -137,8 +139,11 @@ def _on(stream):
 
 
 def _dev(t: torch.Tensor | None, dtype: torch.dtype, what: str, allow_none: bool = False) -> int | None:
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if t is None:
         if allow_none:
             return None
@@ -365,14 +370,16 @@ def pkv_q4_pool_data(pool):
 
 
 def _prow(prow, tokens):
-    if prow is not None and prow.shape[0] != tokens:
+    if prow is None:
+        return None
+    if prow.shape[0] != tokens:
         raise ValueError(f"prow has {prow.shape[0]} tokens, positions {tokens}")
-    return _dev(prow, torch.int32, "prow", allow_none=True)
+    return _dev(prow, torch.int32, "prow")
 
 
 def pkv_q4_append(pool, k, v, k_norm_w, positions, prow, table, stream=None, rows=None, pages=None) -> None:
     """Quantise k, v [tokens][kv_heads][head_dim] into the pool; ``prow=None``: token t is row t."""
-    tokens = int(positions.shape[0])
+    tokens = positions.shape[0]
     if k.shape != v.shape or k.shape[0] != tokens:
         raise ValueError(f"k {tuple(k.shape)}, v {tuple(v.shape)} and {tokens} positions do not match")
     tp, rows, pages = _table(table, rows, pages)
@@ -385,16 +392,15 @@ def pkv_q4_append(pool, k, v, k_norm_w, positions, prow, table, stream=None, row
 def pkv_q4_read(pool, positions, prow, table, k, v, stream=None, rows=None, pages=None) -> None:
     """Cached k and v of the tokens, into views [tokens][kv_heads][head_dim] whose heads are contiguous
     (a bf16 pool's K[:, s:s+n].transpose(0, 1) is one)."""
-    tokens = int(positions.shape[0])
-    for name, x in (("k", k), ("v", v)):
-        if x.dtype != torch.bfloat16 or not x.is_cuda:
-            raise TypeError(f"{name} must be a bf16 CUDA tensor")
-        if x.dim() != 3 or x.shape[0] != tokens or x.stride(2) != 1 or x.stride() != k.stride() or x.shape != k.shape:
-            raise ValueError(f"{name} must be [{tokens}][kv_heads][head_dim] with contiguous heads, k and v alike")
+    tokens, strides = positions.shape[0], k.stride()
+    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or not k.is_cuda or not v.is_cuda:
+        raise TypeError("k and v must be bf16 CUDA tensors")
+    if len(strides) != 3 or strides[2] != 1 or v.stride() != strides or v.shape != k.shape or k.shape[0] != tokens:
+        raise ValueError(f"k and v must be [{tokens}][kv_heads][head_dim] with contiguous heads, both alike")
     tp, rows, pages = _table(table, rows, pages)
     _check(load_library().pkv_q4_read(
         pool, _dev(positions, torch.int32, "positions"), _prow(prow, tokens), tp, tokens, rows, pages,
-        k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), _stream(stream)),
+        k.data_ptr(), v.data_ptr(), strides[0], strides[1], _stream(stream)),
         "pkv_q4_read")
 
 
@@ -434,14 +440,14 @@ def _heads(x, dtype, what, tokens, like):
     """(pointer, token stride) of [tokens][heads][head_dim] with contiguous heads."""
     if x is None:
         return None, 0
-    if x.dtype != dtype or not x.is_cuda:
+    if x.dtype is not dtype or not x.is_cuda:
         raise TypeError(f"{what} must be a {dtype} CUDA tensor, got {x.dtype}")
-    if x.dim() != 3 or x.shape != like.shape or x.shape[0] != tokens:
-        raise ValueError(f"{what} must be [{tokens}][heads][head_dim], as its input, got {tuple(x.shape)}")
-    st, (_, h, d) = x.stride(), x.shape
-    if st[2] != 1 or (h > 1 and st[1] != d):
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != tokens or (x is not like and shape != like.shape):
+        raise ValueError(f"{what} must be [{tokens}][heads][head_dim], as its input, got {tuple(shape)}")
+    if st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"{what} must have contiguous heads, got strides {st}")
-    return x.data_ptr(), st[0] if tokens > 1 else h * d
+    return x.data_ptr(), st[0] if tokens > 1 else shape[1] * shape[2]
 
 
 def pkv_rope_frequencies(cfg, scaling="none", factor: float = 1.0, trained: int = 0):
@@ -507,10 +513,10 @@ class _Pool:
     def norm_rope(self, q, k, q_norm_w, k_norm_w, positions, layout="half", q_out=None, k_out=None,
                   dtype=torch.bfloat16, stream=None):
         """(q, k) normed over each head and rotated; fp32 q is what pkv_decode_appended takes."""
-        c = self.cfg
-        for name, x, h in (("q", q, c.heads), ("k", k, c.kv_heads)):
-            if x is not None and tuple(x.shape[1:]) != (h, c.head_dim):
-                raise ValueError(f"{name} must be [tokens][{h}][{c.head_dim}], got {tuple(x.shape)}")
+        n, c = positions.shape[0], self.cfg
+        if q is not None and q.shape != (n, c.heads, c.head_dim) or k is not None and k.shape != (n, c.kv_heads, c.head_dim):
+            raise ValueError(f"q must be [{n}][{c.heads}][{c.head_dim}] and k [{n}][{c.kv_heads}][{c.head_dim}], got "
+                             f"{None if q is None else tuple(q.shape)} and {None if k is None else tuple(k.shape)}")
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
         if k is not None and k_out is None:
@@ -635,26 +641,23 @@ class Q4KVPool(_Pool):
         data = torch.zeros(pkv_q4_pool_bytes(cfg, num_pages), dtype=torch.uint8, device=device)
         return cls(data, cfg, k_scale, v_scale, stream)
 
-    def _shape(self, name, x, tokens, heads):
-        if x.shape != (tokens, heads, self._dim):
-            raise ValueError(f"{name} must be [{tokens}][{heads}][{self._dim}], got {tuple(x.shape)}")
 
     def append(self, k, v, k_norm_w, positions, prow, table, stream=None, rows=None, pages=None) -> None:
         """k normed and roped, then k and v quantised into their slots (prow None: token t is row t)."""
-        n = positions.shape[0]
-        self._shape("k", k, n, self._kv_heads)
-        self._shape("v", v, n, self._kv_heads)
+        shape = (positions.shape[0], self._kv_heads, self._dim)
+        if k.shape != shape or v.shape != shape:
+            raise ValueError(f"k and v must be {list(shape)}, got {tuple(k.shape)} and {tuple(v.shape)}")
         pkv_q4_append(self.handle, k, v, k_norm_w, positions, prow, table, stream, rows=rows, pages=pages)
 
     def read(self, positions, prow, table, k=None, v=None, stream=None, rows=None, pages=None):
         """(k, v) [tokens][kv_heads][head_dim] that the pool holds at the tokens' positions."""
-        n = positions.shape[0]
+        shape = (positions.shape[0], self._kv_heads, self._dim)
         if k is None or v is None:
             with _on(stream):
-                new = torch.empty(2, n, self._kv_heads, self._dim, dtype=torch.bfloat16, device=self.device)
+                new = torch.empty(2, *shape, dtype=torch.bfloat16, device=self.device)
             k, v = new[0] if k is None else k, new[1] if v is None else v
-        self._shape("k", k, n, self._kv_heads)
-        self._shape("v", v, n, self._kv_heads)
+        if k.shape != shape:
+            raise ValueError(f"k and v must be {list(shape)}, got {tuple(k.shape)} and {tuple(v.shape)}")
         pkv_q4_read(self.handle, positions, prow, table, k, v, stream, rows=rows, pages=pages)
         return k, v
 
@@ -667,21 +670,21 @@ class Q4KVPool(_Pool):
             with _on(stream):
                 out = torch.empty_like(q)
         rows = positions.shape[0]
-        self._shape("q", q, rows, self._heads)
-        self._shape("k", k, rows, self._kv_heads)
-        self._shape("v", v, rows, self._kv_heads)
-        self._shape("out", out, rows, self._heads)
-        pages = table.shape[1] if table is not None else pages
+        qs, ks = (rows, self._heads, self._dim), (rows, self._kv_heads, self._dim)
+        if q.shape != qs or out.shape != qs or k.shape != ks or v.shape != ks:
+            raise ValueError(f"q and out must be {list(qs)}, k and v {list(ks)}, got {tuple(q.shape)}, "
+                             f"{tuple(out.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
         raw = _stream(stream)
         ws = self._streams.get(raw)
         if ws is None or _capturing(stream):
-            ws = self._new_workspace(raw, rows, pages, stream)
+            ws = self._new_workspace(raw, rows, table.shape[1] if table is not None else pages, stream)
         try:
             pkv_q4_decode(self.handle, q, k, v, q_norm_w, k_norm_w, positions, table, out, ws, raw, pages=pages)
         except PkvError as e:
             if e.code != PKV_EWORKSPACE:
                 raise
-            ws = self._new_workspace(raw, rows, pages, stream)   # more rows than any call on this stream so far
+            # more rows than any call on this stream so far
+            ws = self._new_workspace(raw, rows, table.shape[1] if table is not None else pages, stream)
             pkv_q4_decode(self.handle, q, k, v, q_norm_w, k_norm_w, positions, table, out, ws, raw, pages=pages)
         return out
 

@@ -836,7 +836,7 @@ int pkv_rope_frequencies(const pkv_config* cfg, int scaling, double factor, int 
 
 int pkv_pool_set_rope(pkv_pool* pool, const double* inv_freq, double mscale, void* stream)
 {
-    if (!pool || !inv_freq || !(mscale > 0.0) || !std::isfinite(mscale)) return PKV_EINVAL;
+    if (!pool || !inv_freq || !(mscale > 0.0) || !(mscale <= 1024.0)) return PKV_EINVAL;
     for (int i = 0; i < rotary_dims(pool->cfg) / 2; ++i)
         if (!(inv_freq[i] >= 0.0) || !std::isfinite(inv_freq[i])) return PKV_EINVAL;
     int dev = -1;
@@ -856,7 +856,9 @@ int pkv_pool_set_rope(pkv_pool* pool, const double* inv_freq, double mscale, voi
     if (cudaMemcpyAsync(pool->rope_hi, hi.data(), tab, cudaMemcpyHostToDevice, s) != cudaSuccess ||
         cudaMemcpyAsync(pool->rope_lo, lo.data(), tab, cudaMemcpyHostToDevice, s) != cudaSuccess)
         return PKV_ECUDA;
-    return cudaStreamSynchronize(s) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return PKV_ECUDA;
+    pool->rope_exp = std::max(0, (int)std::ceil(std::log2(mscale)));
+    return PKV_OK;
 }
 
 int pkv_norm_rope(pkv_pool* pool, const void* q, const void* k, const void* q_norm_w, const void* k_norm_w,

@@ -67,6 +67,7 @@ struct Q4AppendParams {
     float eps, k_scale;
     float2 eps2;                // eps as a pair of floats
     float k_inv6, k_inv, v_inv6, v_inv;  // 1 / (6 s) and 1 / s of the pool's scales
+    int rope_exp;               // |cos|, |sin| <= 2^rope_exp
 };
 
 // The two 16-byte pieces of a head vector that lane j of 8 holds.
@@ -95,14 +96,15 @@ __device__ __forceinline__ void q4_append_heads(const Q4AppendParams& p, const u
                                                 const uint4 (&wk)[2], int g, bool live, int page, int pos, int lane)
 {
     const int64_t at = (int64_t)pos * kRopeHalf;
-    float x[16], k[16];
-    unpack16(kraw[0], kraw[1], x);
-    norm_rope_k_paired<kFullRot>(x, wk, p.rope_hi + at, p.rope_lo + at, p.eps2, lane, p.rot, k);
-    unpack16(vraw[0], vraw[1], x);
+    float x[16];
+    uint32_t bits[8];
+    norm_rope_k_paired<kFullRot>(kraw, wk, p.rope_hi + at, p.rope_lo + at, p.eps2, p.rope_exp, lane, p.rot, x, bits);
     // (heads beyond the last quantise zeros and store nothing: the shuffles want every lane)
     uint8_t* block = p.data + q4_block(page, p.kv_heads, live ? g : 0, pos % kPageSize);
-    q4_store(block, false, pos % kQ4Block, k, p.k_inv6, p.k_inv, lane & 7, live);
-    q4_store(block, true, pos % kQ4Block, x, p.v_inv6, p.v_inv, lane & 7, live);
+    q4_store(block, false, pos % kQ4Block, x, bits, p.k_inv6, p.k_inv, lane & 7, live);
+    unpack16(vraw[0], vraw[1], x);
+    const uint32_t vbits[8] = {vraw[0].x, vraw[0].y, vraw[0].z, vraw[0].w, vraw[1].x, vraw[1].y, vraw[1].z, vraw[1].w};
+    q4_store(block, true, pos % kQ4Block, x, vbits, p.v_inv6, p.v_inv, lane & 7, live);
 }
 
 constexpr int kQ4AppendWarps = 4;
@@ -241,6 +243,7 @@ static Q4AppendParams append_params(const pkv_pool* pool)
     p.rot = pool->cfg.rotary_dim > 0 ? pool->cfg.rotary_dim : kHeadDim;
     p.eps = (float)pool->cfg.eps;
     p.eps2 = make_float2(p.eps, (float)(pool->cfg.eps - (double)p.eps));
+    p.rope_exp = pool->rope_exp;
     p.k_scale = pool->k_scale;
     p.k_inv6 = (1.f / 6.f) / pool->k_scale;  // (the scales are powers of two)
     p.k_inv = 1.f / pool->k_scale;
@@ -989,14 +992,15 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
         if (lj == 0) sMul[sub] = mul;
     }
     const bool owner = first < n && (n - 1 - first) % step == 0;  // this warp has the last chunk
-    float xn[16];  // lanes of sub 0 and 1: the new k, of 2 and 3: v
+    float xn[16];      // lanes of sub 0 and 1: the new k, of 2 and 3: v
+    uint32_t bits[8];  // the same as bf16
     if (owner) {
-        float x[16], k[16];
-        unpack16(kraw[0], kraw[1], x);
-        norm_rope_k_paired<kFullRot>(x, wk, p.rope_hi + at, p.rope_lo + at, p.eps2, lane, p.rot, k);
-        unpack16(vraw[0], vraw[1], x);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) xn[i] = sub < 2 ? k[i] : x[i];
+        norm_rope_k_paired<kFullRot>(kraw, wk, p.rope_hi + at, p.rope_lo + at, p.eps2, p.rope_exp, lane, p.rot, xn, bits);
+        if (sub >= 2) {
+            unpack16(vraw[0], vraw[1], xn);
+            bits[0] = vraw[0].x, bits[1] = vraw[0].y, bits[2] = vraw[0].z, bits[3] = vraw[0].w;
+            bits[4] = vraw[1].x, bits[5] = vraw[1].y, bits[6] = vraw[1].z, bits[7] = vraw[1].w;
+        }
     }
     __syncthreads();
 
@@ -1015,7 +1019,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
         if (j == n - 1) {  // the new position into the staged chunk (sub 0, 2) and into the pool (1, 3)
             const int s = pos % kPageSize;
             uint8_t* pool = p.data + q4_block(page_of(p.table, p.pages, row, j), G, g, s);
-            q4_store((sub & 1) ? pool : sb + s / kQ4Block * kQ4BlockBytes, sub >= 2, s % kQ4Block, xn,
+            q4_store((sub & 1) ? pool : sb + s / kQ4Block * kQ4BlockBytes, sub >= 2, s % kQ4Block, xn, bits,
                      sub < 2 ? p.k_inv6 : p.v_inv6, sub < 2 ? p.k_inv : p.v_inv, lj, true);
             __syncwarp();
         }

@@ -90,37 +90,45 @@ __device__ __forceinline__ void unpack16(uint4 lo, uint4 hi, float (&x)[16])
     }
 }
 
-// x rounded to 20 significant bits.
-__device__ __forceinline__ float snap20(float x) { return __uint_as_float((__float_as_uint(x) + 8u) & ~15u); }
-
-// Quantises the head vector (x: bf16 values in fp32) to position i of `block`.
-// s is a power of two.
-//   scale = e4m3(max |x| / (6 s)), codes = e2m1(x / (scale s)), both to nearest, ties to even.
-// Every quotient here has few enough bits for its ties to be told exactly: x has 8
-// significant bits, and a tie of a scale (5 bits) times 6 or of a code (3 bits) times
-// a scale (4 bits) at most 7, so a quotient that is not a tie is off it by more than
-// 2^-10 of its value.  The products with rounded inverses, off by 2^-23 at most, are
-// rounded to 20 bits, which puts the ties back in place.  A group that holds an Inf or
-// a NaN gets the scale NaN: the positions that read it are NaN, as with a bf16 pool.
-//   inv6s = 1 / (6 s) to nearest, inv_s = 1 / s
-__device__ __forceinline__ void q4_store(uint8_t* block, bool is_v, int i, const float (&x)[16], float inv6s,
-                                         float inv_s, int j, bool live)
+// The largest |x| of 8 bf16 (4 words of two) as its bits, sign cleared; Inf and NaN order above the rest.
+__device__ __forceinline__ uint32_t max8_bits(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    uint32_t top[2] = {0, 0};
-#pragma unroll
-    for (int k = 0; k < 16; ++k) top[k >> 3] = max(top[k >> 3], __float_as_uint(x[k]) & 0x7fffffffu);  // Inf, NaN on top
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    const uint32_t e = d & kAbs, m = __vimax3_u16x2(__vimax3_u16x2(a & kAbs, b & kAbs, c & kAbs), e, e);
+    return max(m >> 16, m & 0xffffu);
+}
+
+// Quantises the head vector (x: bf16 values in fp32, w: the same as they are) to
+// position i of `block`.  s is a power of two.
+//   scale = e4m3(max |x| / (6 s)), codes = e2m1(x / (scale s)), both to nearest, ties to even.
+// x has 8 significant bits, and a tie of a scale (5 bits) times 6 or of a code (3 bits)
+// times a scale (4 bits) at most 7, so a quotient that is not a tie is off it by more
+// than 2^-10 of its value: only the ties themselves need care.  Those of a scale come
+// out exact from the product with 1 / 6 to nearest (checked for all 32), those of a
+// code from the product with the inverse as a pair of floats.  A group that holds an
+// Inf or a NaN gets the scale NaN: the positions that read it are NaN, as with a bf16 pool.
+//   inv6s = 1 / (6 s) to nearest, inv_s = 1 / s
+__device__ __forceinline__ void q4_store(uint8_t* block, bool is_v, int i, const float (&x)[16], const uint32_t (&w)[8],
+                                         float inv6s, float inv_s, int j, bool live)
+{
     uint32_t word[2], scale[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        top[h] = max(top[h], __shfl_xor_sync(kFull, top[h], 1));
+        uint32_t top = max8_bits(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+        top = max(top, __shfl_xor_sync(kFull, top, 1));
         uint16_t sc;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(sc) : "f"(snap20(__uint_as_float(top[h]) * inv6s)));
-        scale[h] = top[h] >= 0x7f800000u ? 0x7fu : sc & 0xffu;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(sc) : "f"(__uint_as_float(top << 16) * inv6s));
+        scale[h] = top >= 0x7f80u ? 0x7fu : sc & 0xffu;
         const float step = __half2float(__ushort_as_half((unsigned short)(e4m3x2_half2(scale[h]) & 0xffffu)));
-        const float r = step > 0.f ? __frcp_rn(step) * inv_s : 0.f;  // (NaN: 0, any code will do)
+        float r = 0.f, rl = 0.f;
+        if (step > 0.f) {  // (NaN: 0, any code will do)
+            r = __frcp_rn(step);
+            rl = __fmaf_rn(-step, r, 1.f) * r * inv_s;
+            r *= inv_s;
+        }
         float y[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = snap20(x[8 * h + k] * r);
+        for (int k = 0; k < 8; ++k) y[k] = __fmaf_rn(x[8 * h + k], r, x[8 * h + k] * rl);
         asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
             "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
             "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
@@ -187,40 +195,46 @@ __device__ __forceinline__ void load_rope8(const float2* row, float2 (&t)[8])
     }
 }
 
-// u cos + up sin as a pair of floats (up: the partner with its sign): the products'
-// errors by fma, the sum's by two_sum, cos and sin with their low parts.
-__device__ __forceinline__ void rotate_paired(float u, float up, float2 hi, float2 lo, float& a, float& al)
+// u cos + up sin as a pair of floats, exact to about 2^-47 of `grid` (up: the partner with
+// its sign).  Added to `grid`, a power of two 8 times any such sum or more, both
+// products are rounded to its ulp; the additions are exact to take apart again, and
+// what the rounding left of each product is one fma.  cos and sin with their low parts.
+__device__ __forceinline__ void rotate_paired(float u, float up, float2 hi, float2 lo, float grid, float& a, float& al)
 {
-    const float p1 = __fmul_rn(u, hi.x), e1 = __fmaf_rn(u, hi.x, -p1);
-    const float p2 = __fmul_rn(up, hi.y), e2 = __fmaf_rn(up, hi.y, -p2);
-    float e3;
-    two_sum(p1, p2, a, e3);
-    al = __fmaf_rn(u, lo.x, __fmaf_rn(up, lo.y, __fadd_rn(__fadd_rn(e1, e2), e3)));
+    const float s1 = __fmaf_rn(u, hi.x, grid), s2 = __fmaf_rn(up, hi.y, s1);
+    const float e1 = __fmaf_rn(u, hi.x, -__fsub_rn(s1, grid)), e2 = __fmaf_rn(up, hi.y, -__fsub_rn(s2, s1));
+    a = __fsub_rn(s2, grid);
+    al = __fadd_rn(__fmaf_rn(u, lo.x, e1), __fmaf_rn(up, lo.y, e2));
 }
 
-// The bf16 values (in fp32) of the lanes' k head after QK-norm + RoPE: the fp32
-// nearest to the exact value, but for errors of about 2^-37, rounded to bf16.  A
-// bf16 that rounds the other way can move a code by a whole step, a third of its
-// value, so k is carried here in pairs of floats (hi + lo) to that rounding.
+// 2^e as a float, e kept within [lo, hi].
+__device__ __forceinline__ float pow2_clamped(int e, int lo, int hi)
+{
+    return __uint_as_float((uint32_t)(127 + min(max(e, lo), hi)) << 23);
+}
+
+// The bf16 values of the lanes' k head (kraw) after QK-norm + RoPE, as words of two
+// (out) and in fp32 (x): the fp32 nearest to the exact value, but for errors of about
+// 2^-36, rounded to bf16.  A bf16 that rounds the other way can move a code by a whole
+// step, a third of its value, so k is carried here in pairs of floats (hi + lo) to that
+// rounding.
 //   k = a inv,  a = u cos -/+ u' sin,  u = x w (exact),  inv = 1 / sqrt(mean(x^2) + eps)
 // The sum of squares: x^2 is exact in 32 bits; added to a power of two above the
 // lane's sum, each addition's rounding error is exact by one fma.  One Newton step
-// takes rsqrtf's inv to 2^-43; cos and sin come as hi + lo of the double values.
-//   row: lane's table entries (full rotation: 8j .. 8j + 7 of both tables);
-//   rot < 128: tables rhi, rlo of the position.
+// takes rsqrtf's inv to 2^-43; cos and sin come as hi + lo of the double values, |cos|
+// and |sin| at most 2^rope_exp.
 template <bool kFullRot>
-__device__ __forceinline__ void norm_rope_k_paired(const float (&x)[16], const uint4 (&w)[2], const float2* rhi,
-                                                   const float2* rlo, float2 eps, int lane, int rot, float (&out)[16])
+__device__ __forceinline__ void norm_rope_k_paired(const uint4 (&kraw)[2], const uint4 (&w)[2], const float2* rhi,
+                                                   const float2* rlo, float2 eps, int rope_exp, int lane, int rot,
+                                                   float (&x)[16], uint32_t (&out)[8])
 {
     const int j = lane & 7;
-    float wk[16];
-    unpack16(w[0], w[1], wk);
-    float big = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) big = fmaxf(big, fabsf(x[k]));
-    // 2^(2e + 6) > 16 big^2 for big < 2^(e + 1)
-    const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -60), 60);
-    const float base = __uint_as_float((uint32_t)(127 + 2 * ex + 6) << 23);
+    unpack16(kraw[0], kraw[1], x);
+    // 2^ex <= the lane's largest |x| < 2^(ex + 1), and the same of the weights
+    int ex = (int)(max(max8_bits(kraw[0].x, kraw[0].y, kraw[0].z, kraw[0].w),
+                       max8_bits(kraw[1].x, kraw[1].y, kraw[1].z, kraw[1].w)) >> 7) - 127;
+    int ew = (int)(max(max8_bits(w[0].x, w[0].y, w[0].z, w[0].w), max8_bits(w[1].x, w[1].y, w[1].z, w[1].w)) >> 7) - 127;
+    const float base = pow2_clamped(2 * ex + 6, -100, 126);  // above 16 (2^(ex + 1))^2
     float ss = base, sc = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
@@ -245,26 +259,37 @@ __device__ __forceinline__ void norm_rope_k_paired(const float (&x)[16], const u
     // r = 1 - (h + l) y^2, then inv = y (1 + r/2 + 3 r^2 / 8)
     const float r = __fmaf_rn(-l, p, __fmaf_rn(-h, pe, __fmaf_rn(-h, p, 1.f)));
     const float yl = __fmul_rn(y, __fmaf_rn(__fmul_rn(0.375f, r), r, __fmul_rn(0.5f, r)));
-    auto finish = [&](float a, float al) {  // (a + al) (y + yl)
-        const float q = __fmul_rn(a, y), qe = __fmaf_rn(a, y, -q);
-        return __bfloat162float(__float2bfloat16_rn(__fadd_rn(q, __fmaf_rn(a, yl, __fmaf_rn(al, y, qe)))));
-    };
+    // (a + al) (y + yl), rounded once
+    auto finish = [&](float a, float al) { return __fmaf_rn(a, y, __fmaf_rn(a, yl, __fmul_rn(al, y))); };
     float u[16];
+    {
+        float wk[16];
+        unpack16(w[0], w[1], wk);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) u[k] = __fmul_rn(x[k], wk[k]);
+        for (int k = 0; k < 16; ++k) u[k] = __fmul_rn(x[k], wk[k]);
+    }
     if constexpr (kFullRot) {
+        // |u| < 2^(ex + ew + 2), a sum of two terms < 2^(ex + ew + 3 + rope_exp)
+        const float grid = pow2_clamped(ex + ew + 6 + rope_exp, -100, 126);
         float2 ch[8], cl[8];
         load_rope8(rhi + 8 * j, ch);
         load_rope8(rlo + 8 * j, cl);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             float a, al;
-            rotate_paired(u[k], -u[8 + k], ch[k], cl[k], a, al);
-            out[k] = finish(a, al);
-            rotate_paired(u[8 + k], u[k], ch[k], cl[k], a, al);
-            out[8 + k] = finish(a, al);
+            rotate_paired(u[k], -u[8 + k], ch[k], cl[k], grid, a, al);
+            x[k] = finish(a, al);
+            rotate_paired(u[8 + k], u[k], ch[k], cl[k], grid, a, al);
+            x[8 + k] = finish(a, al);
         }
     } else {
+        // the partners lie in other lanes: the head's largest
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+            ex = max(ex, __shfl_xor_sync(kFull, ex, o));
+            ew = max(ew, __shfl_xor_sync(kFull, ew, o));
+        }
+        const float grid = pow2_clamped(ex + ew + 6 + rope_exp, -100, 126);
         const RopeBlock rb[2] = {rope_block(j, rot), rope_block(8 + j, rot)};
         float up[16];
         rope_partners(u, rb, lane, up);
@@ -276,10 +301,17 @@ __device__ __forceinline__ void norm_rope_k_paired(const float (&x)[16], const u
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 float a = u[8 * b + k], al = 0.f;
-                if (rb[b].sgn != 0.f) rotate_paired(u[8 * b + k], up[8 * b + k], ch[k], cl[k], a, al);
-                out[8 * b + k] = finish(a, al);
+                if (rb[b].sgn != 0.f) rotate_paired(u[8 * b + k], up[8 * b + k], ch[k], cl[k], grid, a, al);
+                x[8 * b + k] = finish(a, al);
             }
         }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        out[k] = *reinterpret_cast<const uint32_t*>(&b2);
+        x[2 * k] = __uint_as_float(out[k] << 16);
+        x[2 * k + 1] = __uint_as_float(out[k] & 0xffff0000u);
     }
 }
 

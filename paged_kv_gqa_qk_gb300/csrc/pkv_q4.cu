@@ -689,12 +689,21 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
     int it = t, ig = g, ij = j, in = n, ilen = len, issued = 0, ist = 0;
     constexpr int kPerPage = kPageSize / kQ4Chunk;
     int entries = 0;     // table entries 32 k .. 32 k + 31 of the row, one a lane
+    uint32_t shared = 0;  // which of them the row before or after lists too
     bool reload = true;
+    // pages are read once, but those of a prefix that rows share: these stay in L2, the rest go first
+    const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
     auto issue = [&]() {
         const int pg = ij / kPerPage;
         if (reload || (ij % (32 * kPerPage)) == 0) {
             const int e = (pg & ~31) + lane;
-            entries = e <= (ilen - 1) / kPageSize ? page_of(p.table, p.pages, it, e) : 0;
+            const bool in_row = e <= (ilen - 1) / kPageSize;
+            entries = in_row ? page_of(p.table, p.pages, it, e) : 0;
+            bool same = false;
+            if (in_row && p.table)
+                same = (it > 0 && page_of(p.table, p.pages, it - 1, e) == entries) ||
+                       (it + 1 < p.ntok && page_of(p.table, p.pages, it + 1, e) == entries);
+            shared = __ballot_sync(kFull, same);
             if (entries < 0 || entries >= p.num_pages) entries = 0;  // (then the row is not written out)
             reload = false;
         }
@@ -703,7 +712,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
             const uint32_t bytes = min((ilen - ij * kQ4Chunk + kQ4Block - 1) / kQ4Block, kQ4Blocks) * kQ4BlockBytes;
             mbar_arrive_expect_tx(bars + 8 * ist, bytes);
             const uint8_t* src = p.data + ((int64_t)page * G + ig) * kQ4PageBytes + (ij % kPerPage) * kQ4ChunkBytes;
-            bulk_copy_g2s(ring + ist * kQ4ChunkBytes, src, bytes, bars + 8 * ist);
+            bulk_copy_g2s_hint(ring + ist * kQ4ChunkBytes, src, bytes, bars + 8 * ist, (shared >> (pg & 31)) & 1 ? again : once);
         }
         ++issued;
         ist = ist == kQ4Stages - 1 ? 0 : ist + 1;

@@ -419,6 +419,12 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x)
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+__device__ __forceinline__ __half2 lows(uint32_t x) { return __low2half2(as_half2(x)); }
+__device__ __forceinline__ __half2 highs(uint32_t x) { return __high2half2(as_half2(x)); }
+constexpr uint32_t kOnes = 0x3c003c00u;  // two fp16 ones
+
 __device__ __forceinline__ float ex2(float x)
 {
     float r;
@@ -450,8 +456,9 @@ struct Q4Lane {
 struct Q4State {
     uint32_t bq[8][2];   // the queries' fragments
     float mulA, mulB;    // what scores of heads 2c and 2c + 1 are multiplied with (c < 2)
-    float o[8][4];       // o[k][0], [2]: dims 16r + 2k, + 1 of head 2c; [1], [3] of head 2c + 1; not normalised
-    float mA, mB, lA, lB;  // running maximum (of the warp) and sum (of the lane)
+    float o[9][4];       // o[k][0], [2]: dims 16r + 2k, + 1 of head 2c; [1], [3] of head 2c + 1; not normalised;
+                         // o[8]: the weights' sums (the product with ones), in every row
+    float mA, mB;        // running maximum
 
     // q_hat: 4 heads of 128 fp16; q_mul: their multipliers
     __device__ __forceinline__ void open(const Q4Lane& L, const __half* q_hat, const float* q_mul)
@@ -475,9 +482,8 @@ struct Q4State {
             mulB = mul.y;
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
+        for (int k = 0; k < 9; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
         mA = mB = -CUDART_INF_F;
-        lA = lB = 0.f;
     }
 
     // One chunk in shared memory at sb, of which the unit has `left` positions (as many or more: all).
@@ -492,8 +498,7 @@ struct Q4State {
             const uint4 k0 = *reinterpret_cast<const uint4*>(kb + L.koff), k1 = *reinterpret_cast<const uint4*>(kb + L.koff + 512);
             const uint32_t sc = *reinterpret_cast<const uint32_t*>(kb + L.soff);
             const uint32_t s0 = e4m3x2_half2(sc), s1 = e4m3x2_half2(sc >> 16);
-            const uint32_t sd[2][2] = {{__byte_perm(s0, s0, 0x1010), __byte_perm(s0, s0, 0x3232)},
-                                       {__byte_perm(s1, s1, 0x1010), __byte_perm(s1, s1, 0x3232)}};
+            const __half2 sd[2][2] = {{lows(s0), highs(s0)}, {lows(s1), highs(s1)}};
             const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -502,8 +507,8 @@ struct Q4State {
                 q4_unpack(w1[q], h1);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    h0[e] = mul_half2(h0[e], sd[0][q >> 1]);
-                    h1[e] = mul_half2(h1[e], sd[1][q >> 1]);
+                    h0[e] = as_u32(__hmul2(as_half2(h0[e]), sd[0][q >> 1]));
+                    h1[e] = as_u32(__hmul2(as_half2(h1[e]), sd[1][q >> 1]));
                 }
                 mma_f16_16816(s[b], h0[0], h1[0], h0[1], h1[1], bq[2 * q][0], bq[2 * q][1]);
                 mma_f16_16816(s[b], h0[2], h1[2], h0[3], h1[3], bq[2 * q + 1][0], bq[2 * q + 1][1]);
@@ -532,26 +537,24 @@ struct Q4State {
             nA = fmaxf(nA, fmaxf(s[b][0], s[b][2]));
             nB = fmaxf(nB, fmaxf(s[b][1], s[b][3]));
         }
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-            nA = fmaxf(nA, __shfl_xor_sync(kFull, nA, d));
-            nB = fmaxf(nB, __shfl_xor_sync(kFull, nB, d));
-        }
         nA *= mulA;
         nB *= mulB;
-        // the running maximum follows only when it is passed by more than 2^kQ4Slack: weights stay below
-        // that, well inside fp16, and most chunks rescale nothing
+        // the running maximum follows only when a lane's passes it by more than kQ4Slack: weights stay below
+        // 2^kQ4Slack, well inside fp16, and most chunks need no maximum over the lanes and rescale nothing
         if (__any_sync(kFull, nA > mA + kQ4Slack || nB > mB + kQ4Slack)) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                nA = fmaxf(nA, __shfl_xor_sync(kFull, nA, d));
+                nB = fmaxf(nB, __shfl_xor_sync(kFull, nB, d));
+            }
             nA = fmaxf(nA, mA);
             nB = fmaxf(nB, mB);
             // (a maximum still at -inf -- scores that are all NaN -- leaves nothing to rescale)
             const float aA = nA == -CUDART_INF_F ? 1.f : ex2(mA - nA), aB = nB == -CUDART_INF_F ? 1.f : ex2(mB - nB);
             mA = nA;
             mB = nB;
-            lA *= aA;
-            lB *= aB;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 9; ++k) {
                 o[k][0] *= aA;
                 o[k][1] *= aB;
                 o[k][2] *= aA;
@@ -566,8 +569,6 @@ struct Q4State {
             e[1] = ex2(__fmaf_rn(s[b][1], mulB, -mB));
             e[2] = ex2(__fmaf_rn(s[b][2], mulA, -mA));
             e[3] = ex2(__fmaf_rn(s[b][3], mulB, -mB));
-            lA += e[0] + e[2];
-            lB += e[1] + e[3];
             const __half2 lo = __floats2half2_rn(e[0], e[1]), hi = __floats2half2_rn(e[2], e[3]);
             pb[b][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&lo));
             pb[b][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&hi));
@@ -581,6 +582,7 @@ struct Q4State {
             const uint2 v2 = *reinterpret_cast<const uint2*>(vb + L.voff0 + 512), v3 = *reinterpret_cast<const uint2*>(vb + L.voff1 + 512);
             const uint32_t sc = *reinterpret_cast<const uint32_t*>(vb + L.soff + 128) & vmask[b];
             const uint32_t s01 = e4m3x2_half2(sc), s23 = e4m3x2_half2(sc >> 16);
+            mma_f16_16816(o[8], kOnes, kOnes, kOnes, kOnes, pb[b][0], pb[b][1]);
             const uint32_t a0[2] = {v0.x, v0.y}, a1[2] = {v1.x, v1.y}, a2[2] = {v2.x, v2.y}, a3[2] = {v3.x, v3.y};
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -592,21 +594,11 @@ struct Q4State {
                 q4_unpack(((a2[q] >> 4) & kLow) | (a3[q] & ~kLow), d23);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    mma_f16_16816(o[4 * q + e], mul_half2(e01[e], s01), mul_half2(d01[e], s01), mul_half2(e23[e], s23),
-                                  mul_half2(d23[e], s23), pb[b][0], pb[b][1]);
+                    mma_f16_16816(o[4 * q + e], as_u32(__hmul2(as_half2(e01[e]), as_half2(s01))),
+                                  as_u32(__hmul2(as_half2(d01[e]), as_half2(s01))),
+                                  as_u32(__hmul2(as_half2(e23[e]), as_half2(s23))),
+                                  as_u32(__hmul2(as_half2(d23[e]), as_half2(s23))), pb[b][0], pb[b][1]);
             }
-        }
-    }
-
-    // The sums over all lanes, for heads 2c and 2c + 1.
-    __device__ __forceinline__ void sums(float& LA, float& LB) const
-    {
-        LA = lA;
-        LB = lB;
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-            LA += __shfl_xor_sync(kFull, LA, d);
-            LB += __shfl_xor_sync(kFull, LB, d);
         }
     }
 };
@@ -757,10 +749,9 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
         }
         const bool last = j == n - 1;
         if ((last || i == count - 1) && live) {  // end of the segment
-            float LA, LB;
-            S.sums(LA, LB);
+            const float LA = S.o[8][0], LB = S.o[8][1];
             const int r = L.r, c = L.c;
-            const float(&o)[8][4] = S.o;
+            const float(&o)[9][4] = S.o;
             const int64_t u = (int64_t)t * G + g;
             if (c < 2) {
                 const float iA = p.v_scale / LA, iB = p.v_scale / LB;
@@ -1050,8 +1041,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
     }
 
     // ---- the warps' sums into their own ring (nothing in flight there any more), then one warp a head joins them
-    float LA, LB;
-    S.sums(LA, LB);
+    const float LA = S.o[8][0], LB = S.o[8][1];
     float* part = reinterpret_cast<float*>(ring);
     if (L.c < 2 && first < n) {
         float* pa = part + 2 * L.c * kHeadDim + 16 * L.r;

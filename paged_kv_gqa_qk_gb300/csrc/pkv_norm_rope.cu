@@ -7,6 +7,8 @@
 // pairs (i, i + R/2) of the first R dims (half layout) or (2i, 2i + 1)
 // (interleaved), the rest of the head as it is.  cos and sin are the pool's
 // fp32 tables; the arithmetic is fp32, rounded once to the output's type.
+#include <algorithm>
+
 #include "pkv_internal.h"
 #include "pkv_rope.cuh"
 
@@ -25,15 +27,19 @@ struct NormRopeParams {
     float eps;
 };
 
-constexpr int kNormRopeWarps = 4;
 constexpr int kNormRopeBatch = 5;  // heads a warp loads before the first use
 
-// One CTA per token; warp w takes heads w, w + 4, ... of q's and k's heads in one list.
-template <bool kInterleaved, bool kF32>
-__global__ void __launch_bounds__(32 * kNormRopeWarps) norm_rope_kernel(NormRopeParams p)
+// One CTA per token; of W warps, warp w takes heads w, w + W, ... of q's and k's heads in
+// one list.  Bound by memory for many tokens, where 4 warps measured best (8192 tokens of
+// 40 heads, fp32 out, 252 MB: 44 us; 8 warps 49, 10 warps 54), and by one token's latency
+// for few, where each warp gets at most 4 heads (one token: 3.0 us a call, 4.2 with 4 warps).
+template <bool kInterleaved, bool kF32, int kMaxWarps>
+__global__ void __launch_bounds__(32 * kMaxWarps) norm_rope_kernel(NormRopeParams p)
 {
-    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int nq = p.heads[0], all = nq + p.heads[1];
+    pdl_wait();  // (launched while the kernel before it drains)
+    pdl_launch_dependents();
     const int pos = p.positions[t];
     const bool ok = pos >= 0 && pos < p.max_seq;
     if (!ok && pos != -1 && threadIdx.x == 0) atomicOr(p.err, PKV_DEVERR_POSITION);
@@ -58,18 +64,18 @@ __global__ void __launch_bounds__(32 * kNormRopeWarps) norm_rope_kernel(NormRope
         w[i][0] = w[i][1] = w[i][2] = w[i][3] = 1.f;
         if (p.w[i]) unpack4(*reinterpret_cast<const uint2*>(p.w[i] + 4 * lane), w[i]);
     }
-    for (int h0 = warp; h0 < all; h0 += kNormRopeWarps * kNormRopeBatch) {
+    for (int h0 = warp; h0 < all; h0 += warps * kNormRopeBatch) {
         uint2 raw[kNormRopeBatch];
 #pragma unroll
         for (int b = 0; b < kNormRopeBatch; ++b) {
-            const int h = h0 + b * kNormRopeWarps, is_k = h >= nq;
+            const int h = h0 + b * warps, is_k = h >= nq;
             if (h < all)
                 raw[b] = *reinterpret_cast<const uint2*>((is_k ? p.x[1] + t * p.x_stride[1] - nq * kHeadDim : p.x[0] + t * p.x_stride[0]) +
                                                          h * kHeadDim + 4 * lane);
         }
 #pragma unroll
         for (int b = 0; b < kNormRopeBatch; ++b) {
-            const int h = h0 + b * kNormRopeWarps, is_k = h >= nq;
+            const int h = h0 + b * warps, is_k = h >= nq;
             if (h >= all) break;
             float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
             unpack4(raw[b], x);
@@ -120,12 +126,23 @@ cudaError_t launch_norm_rope(const pkv_pool* pool, const NormRope& a, cudaStream
     p.max_seq = pool->cfg.max_seq;
     p.rot = pool->cfg.rotary_dim > 0 ? pool->cfg.rotary_dim : kHeadDim;
     p.eps = (float)pool->cfg.eps;
-    const dim3 grid((unsigned)a.tokens), block(32 * kNormRopeWarps);
+    const int all = p.heads[0] + p.heads[1];
+    const bool few = a.tokens <= 2 * pool->num_sms;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.tokens);
+    cfg.blockDim = dim3(32 * (few ? std::min((all + 3) / 4, 16) : 4));
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto launch = [&](auto kernel_few, auto kernel) { return cudaLaunchKernelEx(&cfg, few ? kernel_few : kernel, p); };
     if (a.interleaved)
-        a.f32 ? norm_rope_kernel<true, true><<<grid, block, 0, s>>>(p) : norm_rope_kernel<true, false><<<grid, block, 0, s>>>(p);
-    else
-        a.f32 ? norm_rope_kernel<false, true><<<grid, block, 0, s>>>(p) : norm_rope_kernel<false, false><<<grid, block, 0, s>>>(p);
-    return cudaGetLastError();
+        return a.f32 ? launch(norm_rope_kernel<true, true, 16>, norm_rope_kernel<true, true, 4>)
+                     : launch(norm_rope_kernel<true, false, 16>, norm_rope_kernel<true, false, 4>);
+    return a.f32 ? launch(norm_rope_kernel<false, true, 16>, norm_rope_kernel<false, true, 4>)
+                 : launch(norm_rope_kernel<false, false, 16>, norm_rope_kernel<false, false, 4>);
 }
 
 }  // namespace pkv

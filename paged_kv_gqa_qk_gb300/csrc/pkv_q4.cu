@@ -1245,8 +1245,10 @@ cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& pl
 }
 
 // =====================================================================================
-// q4_read_kernel: a warp takes 4 kv heads of one token, 8 lanes each, lane j the dims
-// 8j .. 8j + 7 and 64 + 8j .. of k and v (as the append's lanes): 16-byte stores
+// q4_read_kernel: a warp takes kQuads times 4 kv heads of one token, 8 lanes a head, lane j
+// the dims 8j .. 8j + 7 and 64 + 8j .. of k and v (as the append's lanes): 16-byte stores.
+// Bound by its instructions next to memory: 8 heads a warp share a token's address
+// arithmetic.
 // =====================================================================================
 struct Q4ReadParams {
     const uint8_t* data;
@@ -1261,16 +1263,17 @@ struct Q4ReadParams {
     float k_scale, v_scale;
 };
 
-constexpr int kQ4ReadWarps = 8;
+constexpr int kQ4ReadWarps = 4;
 
+template <int kQuads>
 __global__ void __launch_bounds__(32 * kQ4ReadWarps) q4_read_kernel(Q4ReadParams p)
 {
-    const int lane = threadIdx.x & 31, j = lane & 7, quads = (p.kv_heads + 3) / 4;
-    const int item = blockIdx.x * kQ4ReadWarps + (threadIdx.x >> 5), t = item / quads;
+    const int lane = threadIdx.x & 31, j = lane & 7, groups = (p.kv_heads + 4 * kQuads - 1) / (4 * kQuads);
+    const int item = blockIdx.x * kQ4ReadWarps + (threadIdx.x >> 5), t = item / groups;
     pdl_wait();
     pdl_launch_dependents();
     if (t >= p.tokens) return;
-    const int g = 4 * (item % quads) + (lane >> 3);
+    const int g0 = 4 * kQuads * (item - t * groups) + (lane >> 3);  // this lane's heads: g0, g0 + 4, ...
     const int pos = p.positions[t];
     const int row = p.prow ? p.prow[t] : t;
     uint32_t e = 0;
@@ -1286,35 +1289,48 @@ __global__ void __launch_bounds__(32 * kQ4ReadWarps) q4_read_kernel(Q4ReadParams
         }
     }
     if (e && lane == 0) atomicOr(p.err, e);
-    if (g >= p.kv_heads) return;
-    uint32_t word[2][2] = {}, scale[2][2] = {};
+    uint32_t word[kQuads][2][2] = {}, scale[kQuads][2][2] = {};
     if (page >= 0) {
-        const uint8_t* block = p.data + q4_block(page, p.kv_heads, g, pos % kPageSize);
         const int i = pos % kQ4Block;
+        const uint8_t* block = p.data + q4_block(page, p.kv_heads, g0, pos % kPageSize);
+        const uint8_t* codes = block + q4_code_row(i, 4 * j);
+        const int other = q4_code_row(i, 32 + 4 * j) - q4_code_row(i, 4 * j);  // 32 or -32
+        const uint8_t *ks = block + q4_k_scale(i, j >> 1), *vs = block + q4_v_scale(i, j >> 1);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            word[0][h] = *reinterpret_cast<const uint32_t*>(block + q4_code_row(i, 32 * h + 4 * j));
-            word[1][h] = *reinterpret_cast<const uint32_t*>(block + kQ4VCodes + q4_code_row(i, 32 * h + 4 * j));
-            scale[0][h] = block[q4_k_scale(i, 4 * h + (j >> 1))];
-            scale[1][h] = block[q4_v_scale(i, 4 * h + (j >> 1))];
+        for (int q = 0; q < kQuads; ++q) {
+            if (g0 + 4 * q >= p.kv_heads) break;
+            const int at = 4 * q * kQ4PageBytes;
+            word[q][0][0] = *reinterpret_cast<const uint32_t*>(codes + at);
+            word[q][0][1] = *reinterpret_cast<const uint32_t*>(codes + at + other);
+            word[q][1][0] = *reinterpret_cast<const uint32_t*>(codes + at + kQ4VCodes);
+            word[q][1][1] = *reinterpret_cast<const uint32_t*>(codes + at + kQ4VCodes + other);
+            scale[q][0][0] = ks[at];  // (group g + 4: 8 bytes on for K, 64 for V)
+            scale[q][0][1] = ks[at + 8];
+            scale[q][1][0] = vs[at];
+            scale[q][1][1] = vs[at + 64];
         }
     }
-    const int64_t at = t * p.token_stride + g * p.head_stride + 8 * j;
+    __nv_bfloat16* dst[2] = {p.k + t * p.token_stride + g0 * p.head_stride + 8 * j,
+                             p.v + t * p.token_stride + g0 * p.head_stride + 8 * j};
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const float s = which ? p.v_scale : p.k_scale;
+    for (int q = 0; q < kQuads; ++q) {
+        if (g0 + 4 * q >= p.kv_heads) break;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t c[4], r[4];
-            q4_unpack(word[which][h], c);
-            const uint32_t s2 = e4m3x2_half2(scale[which][h] * 0x101u);
+        for (int which = 0; which < 2; ++which) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // code * scale has 6 bits: exact in fp16, and times s in bf16
-                const uint32_t m = mul_half2(c[k], s2);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
-                r[k] = pack_bf16(__float2bfloat16_rn(f.x * s), __float2bfloat16_rn(f.y * s));
+            for (int h = 0; h < 2; ++h) {
+                uint32_t c[4], r[4];
+                q4_unpack(word[q][which][h], c);
+                const float s = (which ? p.v_scale : p.k_scale) *
+                                __half2float(__ushort_as_half((unsigned short)e4m3x2_half2(scale[q][which][h])));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // code * scale has 6 bits: exact in bf16
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&c[k]));
+                    r[k] = pack_bf16(__float2bfloat16_rn(f.x * s), __float2bfloat16_rn(f.y * s));
+                }
+                __stcs(reinterpret_cast<uint4*>(dst[which] + 64 * h), make_uint4(r[0], r[1], r[2], r[3]));
             }
-            *reinterpret_cast<uint4*>((which ? p.v : p.k) + at + 64 * h) = make_uint4(r[0], r[1], r[2], r[3]);
+            dst[which] += 4 * p.head_stride;
         }
     }
 }
@@ -1341,8 +1357,11 @@ cudaError_t launch_q4_read(const pkv_pool* pool, const int32_t* positions, const
     p.kv_heads = pool->cfg.kv_heads;
     p.k_scale = pool->k_scale;
     p.v_scale = pool->v_scale;
-    const int64_t items = (int64_t)tokens * ((p.kv_heads + 3) / 4);
-    return launch_dependent(q4_read_kernel, (unsigned)((items + kQ4ReadWarps - 1) / kQ4ReadWarps), 32 * kQ4ReadWarps, 0, s, p);
+    // few tokens: 4 heads a warp, for the shorter chain; from about two warps a scheduler on, 8
+    const int quads = (p.kv_heads + 3) / 4, per = quads > 1 && (int64_t)tokens * quads >= 16 * (int64_t)pool->num_sms ? 2 : 1;
+    const int64_t items = (int64_t)tokens * ((quads + per - 1) / per);
+    const unsigned grid = (unsigned)((items + kQ4ReadWarps - 1) / kQ4ReadWarps);
+    return launch_dependent(per == 1 ? q4_read_kernel<1> : q4_read_kernel<2>, grid, 32 * kQ4ReadWarps, 0, s, p);
 }
 
 }  // namespace pkv

@@ -77,16 +77,22 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* head, int j, uint4 (
     r[1] = *reinterpret_cast<const uint4*>(head + 64 + 8 * j);
 }
 
-// Position and row of token t: the error bit, or 0 (then, if `active`, the token's pages can be looked up).
-__device__ __forceinline__ uint32_t q4_token(const Q4AppendParams& p, int t, int& pos, int& row, bool& active)
+// What is wrong with a token's position and row, as an error bit; 0: nothing, or no step (-1).
+__device__ __forceinline__ uint32_t q4_fault(const Q4AppendParams& p, int pos, int row)
 {
-    pos = p.positions[t];
-    row = p.prow ? p.prow[t] : t;
-    active = pos != -1;
-    if (!active) return 0;
+    if (pos == -1) return 0;
     if (row < 0 || row >= p.rows) return PKV_DEVERR_ROW;
     if (pos < 0 || pos >= p.max_seq || pos / kPageSize >= p.pages) return PKV_DEVERR_POSITION;
     return 0;
+}
+
+// The position's rows of the RoPE tables into L1 (512 bytes each), a line a thread.
+__device__ __forceinline__ void prefetch_rope(const Q4AppendParams& p, int pos, int thread)
+{
+    constexpr int kLines = kRopeHalf * (int)sizeof(float2) / 128;
+    if (thread < 2 * kLines)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"((thread < kLines ? p.rope_hi : p.rope_lo) + (int64_t)pos * kRopeHalf +
+                                                      thread % kLines * (128 / (int)sizeof(float2))));
 }
 
 // k and v of up to 4 kv heads of one token, 8 lanes each (kraw, vraw: this lane's
@@ -109,34 +115,38 @@ __device__ __forceinline__ void q4_append_heads(const Q4AppendParams& p, const u
 
 constexpr int kQ4AppendWarps = 4;
 
-// pkv_q4_append: a warp takes 4 kv heads of one token.
-template <bool kFullRot>
+// pkv_q4_append: a warp takes kQuads times 4 kv heads of one token.
+template <bool kFullRot, int kQuads>
 __global__ void __launch_bounds__(32 * kQ4AppendWarps) q4_append_kernel(Q4AppendParams p)
 {
-    const int lane = threadIdx.x & 31, j = lane & 7, quads = (p.kv_heads + 3) / 4;
-    const int item = blockIdx.x * kQ4AppendWarps + (threadIdx.x >> 5), t = item / quads;
+    const int lane = threadIdx.x & 31, j = lane & 7, groups = (p.kv_heads + 4 * kQuads - 1) / (4 * kQuads);
+    const int item = blockIdx.x * kQ4AppendWarps + (threadIdx.x >> 5), t = item / groups;
     pdl_wait();
     pdl_launch_dependents();
     if (t >= p.tokens) return;
-    const int g = 4 * (item % quads) + (lane >> 3);
-    const bool live = g < p.kv_heads;
-    uint4 kraw[2] = {}, vraw[2] = {}, wk[2];
-    if (live) {
-        const int64_t src = ((int64_t)t * p.kv_heads + g) * kHeadDim;
-        load16(p.k + src, j, kraw);
-        load16(p.v + src, j, vraw);
-    }
+    const int g0 = 4 * kQuads * (item - t * groups) + (lane >> 3);  // this lane's heads: g0, g0 + 4, ...
+    uint4 kraw[kQuads][2] = {}, vraw[kQuads][2] = {}, wk[2];
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q)
+        if (g0 + 4 * q < p.kv_heads) {
+            const int64_t src = ((int64_t)t * p.kv_heads + g0 + 4 * q) * kHeadDim;
+            load16(p.k + src, j, kraw[q]);
+            load16(p.v + src, j, vraw[q]);
+        }
     load16(p.kw, j, wk);
-    int pos, row, page = 0;
-    bool active;
-    uint32_t e = q4_token(p, t, pos, row, active);
+    const int pos = p.positions[t], row = p.prow ? p.prow[t] : t;
+    const bool active = pos != -1;
+    uint32_t e = q4_fault(p, pos, row);
+    int page = 0;
     if (active && !e) {
         page = page_of(p.table, p.pages, row, pos / kPageSize);
         if (page < 0 || page >= p.num_pages) e = PKV_DEVERR_PAGE;
     }
     if (e && lane == 0) atomicOr(p.err, e);
     if (!active || e) return;
-    q4_append_heads<kFullRot>(p, kraw, vraw, wk, g, live, page, pos, lane);
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q)
+        q4_append_heads<kFullRot>(p, kraw[q], vraw[q], wk, g0 + 4 * q, g0 + 4 * q < p.kv_heads, page, pos, lane);
 }
 
 // A query head over 8 lanes as fp16, times the power of two that brings its largest
@@ -188,11 +198,12 @@ __global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
         }
     };
     load();
-    int pos, row, page = 0;
-    bool active;
-    uint32_t e = q4_token(p, t, pos, row, active);
-    int bad = 0;
+    const int pos = p.positions[t], row = t;
+    const bool active = pos != -1;
+    uint32_t e = q4_fault(p, pos, row);
+    int page = 0, bad = 0;
     if (active && !e) {
+        prefetch_rope(p, pos, threadIdx.x);
         const int last = pos / kPageSize;
         page = page_of(p.table, p.pages, row, last);
         for (int i = threadIdx.x; i <= last; i += blockDim.x) {
@@ -266,9 +277,15 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
     p.tokens = tokens;
     p.rows = rows;
     p.pages = pages;
-    const unsigned grid = (unsigned)(((int64_t)tokens * ((p.kv_heads + 3) / 4) + kQ4AppendWarps - 1) / kQ4AppendWarps);
-    return launch_dependent(p.rot == kHeadDim ? q4_append_kernel<true> : q4_append_kernel<false>, grid, 32 * kQ4AppendWarps, 0,
-                            s, p);
+    // few tokens: 4 heads a warp, for the shorter chain (2048 tokens of 8 heads 6.7 us, 7.4 with 8 heads a warp);
+    // many: 8, which share the token's address arithmetic (16384 tokens 37.5 us with 4, 35.5 with 8)
+    const int quads = (p.kv_heads + 3) / 4, per = quads > 1 && (int64_t)tokens * quads >= 64 * (int64_t)pool->num_sms ? 2 : 1;
+    const int64_t items = (int64_t)tokens * ((quads + per - 1) / per);
+    const unsigned grid = (unsigned)((items + kQ4AppendWarps - 1) / kQ4AppendWarps);
+    const bool full = p.rot == kHeadDim;
+    return launch_dependent(per == 1 ? (full ? q4_append_kernel<true, 1> : q4_append_kernel<false, 1>)
+                                     : (full ? q4_append_kernel<true, 2> : q4_append_kernel<false, 2>),
+                            grid, 32 * kQ4AppendWarps, 0, s, p);
 }
 
 // =====================================================================================
@@ -949,11 +966,12 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
     load16(p.k + kv, lj, kraw);
     load16(p.v + kv, lj, vraw);
     load16(p.kw, lj, wk);
-    int pos, row;
-    bool active;
-    uint32_t e = q4_token(p, t, pos, row, active);
+    const int pos = p.positions[t], row = t;
+    const bool active = pos != -1;
+    uint32_t e = q4_fault(p, pos, row);
     const int n = active && !e ? pos / kPageSize + 1 : 0;  // chunks (pages)
     int bad = 0;
+    if (n) prefetch_rope(p, pos, threadIdx.x);
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const int id = page_of(p.table, p.pages, row, i);
         bad |= id < 0 || id >= p.num_pages;

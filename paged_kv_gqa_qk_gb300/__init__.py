@@ -56,6 +56,12 @@ class PkvError(RuntimeError):
 
 
 _lib = None
+_BF16, _I32 = torch.bfloat16, torch.int32
+
+
+def _raw_stream(device: int) -> int:
+    """Handle of the device's current stream, without making a torch stream of it."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -120,7 +126,7 @@ def _check(rc: int, what: str):
 def _stream(stream) -> int:
     """The stream's handle; None: the current device's current stream (asked for without making a torch stream)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -134,8 +140,12 @@ def _capturing(stream) -> bool:
 
 
 def _on(stream):
-    """Allocations inside are ordered on `stream` (a torch stream; anything else: the current stream)."""
-    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
+    """Allocations inside are ordered on `stream` (a torch stream or a handle; None: the current stream)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _dev(t: torch.Tensor | None, dtype: torch.dtype, what: str, allow_none: bool = False) -> int | None:
@@ -408,6 +418,8 @@ def pkv_q4_decode(pool, q, k, v, q_norm_w, k_norm_w, positions, table, out, work
                   pages=None) -> None:
     """decode_paged over a 4-bit pool; ``table=None`` with ``pages`` is the contiguous-row layout."""
     tp, rows, pages = _table(table, positions.shape[0], pages)
+    if positions.shape[0] != rows:
+        raise ValueError(f"table has {rows} rows, positions {positions.shape[0]}")
     _check(load_library().pkv_q4_decode(
         pool, _dev(q, torch.bfloat16, "q"), _dev(k, torch.bfloat16, "k"), _dev(v, torch.bfloat16, "v"),
         _dev(q_norm_w, torch.bfloat16, "q_norm_w"), _dev(k_norm_w, torch.bfloat16, "k_norm_w"),
@@ -633,6 +645,7 @@ class Q4KVPool(_Pool):
             raise ValueError(f"data must be uint8, a multiple of {per_page} bytes, got {data.dtype} x {data.numel()}")
         self.data, self.cfg, self.device, self._streams = data, c, data.device, {}
         self._heads, self._kv_heads, self._dim = c.heads, c.kv_heads, c.head_dim
+        self._lib, self._index = load_library(), data.get_device()
         self.num_pages = data.numel() // per_page
         self.handle = pkv_q4_pool_wrap(c, self.num_pages, data, k_scale, v_scale, stream)
 
@@ -641,24 +654,45 @@ class Q4KVPool(_Pool):
         data = torch.zeros(pkv_q4_pool_bytes(cfg, num_pages), dtype=torch.uint8, device=device)
         return cls(data, cfg, k_scale, v_scale, stream)
 
+    # The methods check what the functions of the same names check, in one place and once: these calls are short
+    # beside a Python function call.
 
     def append(self, k, v, k_norm_w, positions, prow, table, stream=None, rows=None, pages=None) -> None:
         """k normed and roped, then k and v quantised into their slots (prow None: token t is row t)."""
-        shape = (positions.shape[0], self._kv_heads, self._dim)
-        if k.shape != shape or v.shape != shape:
-            raise ValueError(f"k and v must be {list(shape)}, got {tuple(k.shape)} and {tuple(v.shape)}")
-        pkv_q4_append(self.handle, k, v, k_norm_w, positions, prow, table, stream, rows=rows, pages=pages)
+        n = positions.shape[0]
+        shape = (n, self._kv_heads, self._dim)
+        if k.shape != shape or v.shape != shape or k_norm_w.numel() != self._dim:
+            raise ValueError(f"k and v must be {list(shape)} and k_norm_w [{self._dim}], got {tuple(k.shape)}, "
+                             f"{tuple(v.shape)} and {tuple(k_norm_w.shape)}")
+        tp, rows, pages = _table(table, rows, pages)
+        rc = self._lib.pkv_q4_append(
+            self.handle, _dev(k, _BF16, "k"), _dev(v, _BF16, "v"), _dev(k_norm_w, _BF16, "k_norm_w"),
+            _dev(positions, _I32, "positions"), None if prow is None else _prow(prow, n), tp, n, rows, pages,
+            _raw_stream(self._index) if stream is None else _stream(stream))
+        if rc:
+            raise PkvError(rc, "pkv_q4_append")
 
     def read(self, positions, prow, table, k=None, v=None, stream=None, rows=None, pages=None):
         """(k, v) [tokens][kv_heads][head_dim] that the pool holds at the tokens' positions."""
-        shape = (positions.shape[0], self._kv_heads, self._dim)
+        n = positions.shape[0]
+        shape = (n, self._kv_heads, self._dim)
         if k is None or v is None:
             with _on(stream):
                 new = torch.empty(2, *shape, dtype=torch.bfloat16, device=self.device)
             k, v = new[0] if k is None else k, new[1] if v is None else v
-        if k.shape != shape:
-            raise ValueError(f"k and v must be {list(shape)}, got {tuple(k.shape)} and {tuple(v.shape)}")
-        pkv_q4_read(self.handle, positions, prow, table, k, v, stream, rows=rows, pages=pages)
+        strides = k.stride()
+        if k.shape != shape or v.shape != shape or v.stride() != strides or strides[2] != 1:
+            raise ValueError(f"k and v must be {list(shape)} with contiguous heads and the same strides, got "
+                             f"{tuple(k.shape)} by {strides} and {tuple(v.shape)} by {v.stride()}")
+        if k.dtype is not _BF16 or v.dtype is not _BF16 or not k.is_cuda or not v.is_cuda:
+            raise TypeError("k and v must be bf16 CUDA tensors")
+        tp, rows, pages = _table(table, rows, pages)
+        rc = self._lib.pkv_q4_read(
+            self.handle, _dev(positions, _I32, "positions"), None if prow is None else _prow(prow, n), tp, n, rows, pages,
+            k.data_ptr(), v.data_ptr(), strides[0], strides[1],
+            _raw_stream(self._index) if stream is None else _stream(stream))
+        if rc:
+            raise PkvError(rc, "pkv_q4_read")
         return k, v
 
     def decode(self, q, k, v, q_norm_w, k_norm_w, positions, table, out=None, stream=None, pages=None) -> torch.Tensor:
@@ -674,24 +708,26 @@ class Q4KVPool(_Pool):
         if q.shape != qs or out.shape != qs or k.shape != ks or v.shape != ks:
             raise ValueError(f"q and out must be {list(qs)}, k and v {list(ks)}, got {tuple(q.shape)}, "
                              f"{tuple(out.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
-        raw = _stream(stream)
+        if q_norm_w.numel() != self._dim or k_norm_w.numel() != self._dim:
+            raise ValueError(f"q_norm_w and k_norm_w must be [{self._dim}]")
+        tp, table_rows, pages = _table(table, rows, pages)
+        if table_rows != rows:
+            raise ValueError(f"table has {table_rows} rows, positions {rows}")
+        raw = _raw_stream(self._index) if stream is None else _stream(stream)
+        args = (self.handle, _dev(q, _BF16, "q"), _dev(k, _BF16, "k"), _dev(v, _BF16, "v"),
+                _dev(q_norm_w, _BF16, "q_norm_w"), _dev(k_norm_w, _BF16, "k_norm_w"), _dev(positions, _I32, "positions"),
+                tp, rows, pages, _dev(out, _BF16, "out"))
         ws = self._streams.get(raw)
-        if ws is None or _capturing(stream):
-            ws = self._new_workspace(raw, rows, table.shape[1] if table is not None else pages, stream)
-        try:
-            pkv_q4_decode(self.handle, q, k, v, q_norm_w, k_norm_w, positions, table, out, ws, raw, pages=pages)
-        except PkvError as e:
-            if e.code != PKV_EWORKSPACE:
-                raise
-            # more rows than any call on this stream so far
-            ws = self._new_workspace(raw, rows, table.shape[1] if table is not None else pages, stream)
-            pkv_q4_decode(self.handle, q, k, v, q_norm_w, k_norm_w, positions, table, out, ws, raw, pages=pages)
+        rc = PKV_EWORKSPACE
+        if ws is not None and (raw == 0 or not _capturing(stream)):   # (the default stream is never captured)
+            rc = self._lib.pkv_q4_decode(*args, ws[0], ws[1], raw)
+        if rc == PKV_EWORKSPACE:   # a first call, more rows than any call on this stream so far, or a capture
+            n = pkv_workspace_bytes(self.handle, rows, pages, 0)
+            with _on(stream):
+                buf = torch.empty(n, dtype=torch.uint8, device=self.device)
+            if not _capturing(stream):
+                self._streams[raw] = (buf.data_ptr(), n, buf)
+            rc = self._lib.pkv_q4_decode(*args, buf.data_ptr(), n, raw)
+        if rc:
+            raise PkvError(rc, "pkv_q4_decode")
         return out
-
-    def _new_workspace(self, raw: int, rows: int, pages: int, stream) -> torch.Tensor:
-        n = pkv_workspace_bytes(self.handle, rows, pages, 0)
-        with _on(stream):
-            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        if not _capturing(stream):
-            self._streams[raw] = ws
-        return ws

@@ -429,37 +429,47 @@ def pkv_q4_decode(pool, q, k, v, q_norm_w, k_norm_w, positions, table, out, work
 
 # ---- norm + rotation
 
-def pkv_norm_rope(pool, q, k, q_norm_w, k_norm_w, positions, q_out, k_out, layout="half", stream=None) -> None:
+def pkv_norm_rope(pool, q, k, q_norm_w, k_norm_w, positions, q_out, k_out, layout="half", stream=None,
+                  shape=None) -> None:
     """QK-norm and RoPE of q [tokens][heads][head_dim] and k [tokens][kv_heads][head_dim] (heads contiguous, any
-    token stride) into q_out and k_out (both bf16 or both fp32).  q or k may be None; no weights: no norm."""
+    token stride) into q_out and k_out (both bf16 or both fp32).  q or k may be None; no weights: no norm.
+    shape: the pool's (heads, kv_heads, head_dim), to be checked if given."""
     tokens = positions.shape[0]
     if (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("q and q_out, and k and k_out, are given together")
     kind = (k_out if q_out is None else q_out).dtype
-    if kind not in (torch.bfloat16, torch.float32):
+    if kind is not _BF16 and kind is not torch.float32:
         raise TypeError(f"outputs must be bf16 or fp32, got {kind}")
-    qp, qs = _heads(q, torch.bfloat16, "q", tokens, q)
-    kp, ks = _heads(k, torch.bfloat16, "k", tokens, k)
-    qo, qos = _heads(q_out, kind, "q_out", tokens, q)
-    ko, kos = _heads(k_out, kind, "k_out", tokens, k)
-    _check(load_library().pkv_norm_rope(
-        pool, qp, kp, _dev(q_norm_w, torch.bfloat16, "q_norm_w", allow_none=True),
-        _dev(k_norm_w, torch.bfloat16, "k_norm_w", allow_none=True), _dev(positions, torch.int32, "positions"), tokens,
-        ROPE_LAYOUTS[layout], kind is torch.float32, qs, ks, qo, ko, qos, kos, _stream(stream)), "pkv_norm_rope")
+    qp = qs = qo = qos = kp = ks = ko = kos = 0
+    if q is not None:
+        s = q.shape if shape is None else (tokens, shape[0], shape[2])
+        qp, qs = _heads(q, _BF16, "q", tokens, s)
+        qo, qos = _heads(q_out, kind, "q_out", tokens, s)
+    if k is not None:
+        s = k.shape if shape is None else (tokens, shape[1], shape[2])
+        kp, ks = _heads(k, _BF16, "k", tokens, s)
+        ko, kos = _heads(k_out, kind, "k_out", tokens, s)
+    for w in (q_norm_w, k_norm_w):
+        if w is not None and w.numel() != s[2]:
+            raise ValueError(f"norm weights must be [{s[2]}], got {tuple(w.shape)}")
+    rc = load_library().pkv_norm_rope(
+        pool, qp, kp, None if q_norm_w is None else _dev(q_norm_w, _BF16, "q_norm_w"),
+        None if k_norm_w is None else _dev(k_norm_w, _BF16, "k_norm_w"), _dev(positions, _I32, "positions"), tokens,
+        ROPE_LAYOUTS[layout], kind is not _BF16, qs, ks, qo, ko, qos, kos, _stream(stream))
+    if rc:
+        raise PkvError(rc, "pkv_norm_rope")
 
 
-def _heads(x, dtype, what, tokens, like):
-    """(pointer, token stride) of [tokens][heads][head_dim] with contiguous heads."""
-    if x is None:
-        return None, 0
+def _heads(x, dtype, what, tokens, shape):
+    """(pointer, token stride) of a tensor of that shape, [tokens][heads][head_dim], with contiguous heads."""
     if x.dtype is not dtype or not x.is_cuda:
         raise TypeError(f"{what} must be a {dtype} CUDA tensor, got {x.dtype}")
-    shape, st = x.shape, x.stride()
-    if len(shape) != 3 or shape[0] != tokens or (x is not like and shape != like.shape):
-        raise ValueError(f"{what} must be [{tokens}][heads][head_dim], as its input, got {tuple(shape)}")
-    if st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
-        raise ValueError(f"{what} must have contiguous heads, got strides {st}")
-    return x.data_ptr(), st[0] if tokens > 1 else shape[1] * shape[2]
+    if x.shape != shape or len(shape) != 3 or shape[0] != tokens:
+        raise ValueError(f"{what} must be {list(shape)} for {tokens} positions, got {tuple(x.shape)}")
+    token, head, dim = x.stride()
+    if dim != 1 or (head != shape[2] and shape[1] > 1):
+        raise ValueError(f"{what} must have contiguous heads, got strides {x.stride()}")
+    return x.data_ptr(), token if tokens > 1 else shape[1] * shape[2]
 
 
 def pkv_rope_frequencies(cfg, scaling="none", factor: float = 1.0, trained: int = 0):
@@ -509,6 +519,7 @@ class _Pool:
 
     handle = None
     _ws = None
+    _shape = None   # (heads, kv_heads, head_dim)
 
     def workspace(self, rows: int, pages: int, prefill_tokens: int = 0) -> torch.Tensor:
         n = pkv_workspace_bytes(self.handle, rows, pages, prefill_tokens)
@@ -525,15 +536,13 @@ class _Pool:
     def norm_rope(self, q, k, q_norm_w, k_norm_w, positions, layout="half", q_out=None, k_out=None,
                   dtype=torch.bfloat16, stream=None):
         """(q, k) normed over each head and rotated; fp32 q is what pkv_decode_appended takes."""
-        n, c = positions.shape[0], self.cfg
-        if q is not None and q.shape != (n, c.heads, c.head_dim) or k is not None and k.shape != (n, c.kv_heads, c.head_dim):
-            raise ValueError(f"q must be [{n}][{c.heads}][{c.head_dim}] and k [{n}][{c.kv_heads}][{c.head_dim}], got "
-                             f"{None if q is None else tuple(q.shape)} and {None if k is None else tuple(k.shape)}")
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+            with _on(stream):
+                q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
         if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=dtype, device=k.device)
-        pkv_norm_rope(self.handle, q, k, q_norm_w, k_norm_w, positions, q_out, k_out, layout, stream)
+            with _on(stream):
+                k_out = torch.empty(k.shape, dtype=dtype, device=k.device)
+        pkv_norm_rope(self.handle, q, k, q_norm_w, k_norm_w, positions, q_out, k_out, layout, stream, self._shape)
         return q_out, k_out
 
     def check_errors(self, stream=None) -> int:
@@ -561,7 +570,7 @@ class PagedKVPool(_Pool):
             raise ValueError(f"K/V must be [kv_heads][num_pages*page_size][head_dim], got {tuple(K.shape)}")
         self.K, self.V, self.cfg = K, V, c
         self.num_pages = K.shape[1] // c.page_size
-        self.device = K.device
+        self.device, self._shape = K.device, (c.heads, c.kv_heads, c.head_dim)
         self.handle = pkv_pool_wrap(c, self.num_pages, K, V, stream)
         self._lws = None
 
@@ -644,7 +653,7 @@ class Q4KVPool(_Pool):
         if data.dtype != torch.uint8 or data.numel() == 0 or data.numel() % per_page:
             raise ValueError(f"data must be uint8, a multiple of {per_page} bytes, got {data.dtype} x {data.numel()}")
         self.data, self.cfg, self.device, self._streams = data, c, data.device, {}
-        self._heads, self._kv_heads, self._dim = c.heads, c.kv_heads, c.head_dim
+        self._shape = self._heads, self._kv_heads, self._dim = c.heads, c.kv_heads, c.head_dim
         self._lib, self._index = load_library(), data.get_device()
         self.num_pages = data.numel() // per_page
         self.handle = pkv_q4_pool_wrap(c, self.num_pages, data, k_scale, v_scale, stream)

@@ -115,9 +115,12 @@ __device__ __forceinline__ void q4_append_heads(const Q4AppendParams& p, const u
 
 constexpr int kQ4AppendWarps = 4;
 
-// pkv_q4_append: a warp takes kQuads times 4 kv heads of one token.
+// pkv_q4_append: a warp takes kQuads times 4 kv heads of one token.  Bound by its
+// instructions: about 860 a quad, half of them k's norm and rotation in pairs of floats
+// (16384 tokens of 8 heads, 86 MB: 33.9 us, 2.5 TB/s, 0.67 of the issue slots).  Resident
+// CTAs by measurement: 6 an SM of the two-quad form (5: 35.8, 8: 36.9 us), 7 of the other.
 template <bool kFullRot, int kQuads>
-__global__ void __launch_bounds__(32 * kQ4AppendWarps) q4_append_kernel(Q4AppendParams p)
+__global__ void __launch_bounds__(32 * kQ4AppendWarps, !kFullRot ? 4 : kQuads == 1 ? 7 : 6) q4_append_kernel(Q4AppendParams p)
 {
     const int lane = threadIdx.x & 31, j = lane & 7, groups = (p.kv_heads + 4 * kQuads - 1) / (4 * kQuads);
     const int item = blockIdx.x * kQ4AppendWarps + (threadIdx.x >> 5), t = item / groups;
@@ -278,7 +281,7 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
     p.rows = rows;
     p.pages = pages;
     // few tokens: 4 heads a warp, for the shorter chain (2048 tokens of 8 heads 6.7 us, 7.4 with 8 heads a warp);
-    // many: 8, which share the token's address arithmetic (16384 tokens 37.5 us with 4, 35.5 with 8)
+    // many: 8, which share the token's address arithmetic (16384 tokens 37.4 us with 4, 33.9 with 8)
     const int quads = (p.kv_heads + 3) / 4, per = quads > 1 && (int64_t)tokens * quads >= 64 * (int64_t)pool->num_sms ? 2 : 1;
     const int64_t items = (int64_t)tokens * ((quads + per - 1) / per);
     const unsigned grid = (unsigned)((items + kQ4AppendWarps - 1) / kQ4AppendWarps);

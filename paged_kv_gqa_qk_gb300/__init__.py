@@ -56,6 +56,7 @@ class PkvError(RuntimeError):
 
 
 _lib = None
+_fast = None   # the module _pkv_torch (csrc/pkv_torch.cpp), if it was built for this torch
 _BF16, _I32 = torch.bfloat16, torch.int32
 
 
@@ -115,7 +116,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn.argtypes = args
         fn.restype = res
     _lib = lib
+    _load_fast(lib)
     return lib
+
+
+def _load_fast(lib) -> None:
+    """The calls of a few microseconds go through a CPython module where it was built: 0.5 us of checks in place of 4."""
+    global _fast
+    try:
+        from . import _pkv_torch as fast
+    except ImportError:
+        return
+    if fast.torch_version == torch.__version__:
+        fast.bind(*(ctypes.cast(getattr(lib, "pkv_" + name), ctypes.c_void_p).value
+                    for name in ("q4_decode", "q4_append", "q4_read", "norm_rope")))
+        _fast = fast
 
 
 def _check(rc: int, what: str):
@@ -437,6 +452,8 @@ def pkv_norm_rope(pool, q, k, q_norm_w, k_norm_w, positions, q_out, k_out, layou
     tokens = positions.shape[0]
     if (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("q and q_out, and k and k_out, are given together")
+    if q is None and k is None:
+        raise ValueError("q or k is required")
     kind = (k_out if q_out is None else q_out).dtype
     if kind is not _BF16 and kind is not torch.float32:
         raise TypeError(f"outputs must be bf16 or fp32, got {kind}")
@@ -520,6 +537,8 @@ class _Pool:
     handle = None
     _ws = None
     _shape = None   # (heads, kv_heads, head_dim)
+    _spec = None    # (device index, heads, kv_heads, head_dim)
+    _h = 0          # the handle's value
 
     def workspace(self, rows: int, pages: int, prefill_tokens: int = 0) -> torch.Tensor:
         n = pkv_workspace_bytes(self.handle, rows, pages, prefill_tokens)
@@ -542,6 +561,12 @@ class _Pool:
         if k is not None and k_out is None:
             with _on(stream):
                 k_out = torch.empty(k.shape, dtype=dtype, device=k.device)
+        if _fast is not None and layout in ROPE_LAYOUTS:
+            raw = _raw_stream(self._spec[0]) if stream is None else _stream(stream)
+            rc = _fast.norm_rope(self._h, self._spec, q, k, q_norm_w, k_norm_w, positions, ROPE_LAYOUTS[layout],
+                                 q_out, k_out, raw)
+            if rc == 0:
+                return q_out, k_out
         pkv_norm_rope(self.handle, q, k, q_norm_w, k_norm_w, positions, q_out, k_out, layout, stream, self._shape)
         return q_out, k_out
 
@@ -551,7 +576,7 @@ class _Pool:
     def close(self):
         if self.handle is not None and self.handle.value:
             pkv_pool_free(self.handle)
-        self.handle = None
+        self.handle, self._h = None, 0
 
     def __del__(self):
         try:
@@ -572,6 +597,7 @@ class PagedKVPool(_Pool):
         self.num_pages = K.shape[1] // c.page_size
         self.device, self._shape = K.device, (c.heads, c.kv_heads, c.head_dim)
         self.handle = pkv_pool_wrap(c, self.num_pages, K, V, stream)
+        self._h, self._spec = self.handle.value, (K.get_device(), *self._shape)
         self._lws = None
 
     def decode(self, q, k, v, q_norm_w, k_norm_w, positions, table, out=None, stream=None,
@@ -657,17 +683,22 @@ class Q4KVPool(_Pool):
         self._lib, self._index = load_library(), data.get_device()
         self.num_pages = data.numel() // per_page
         self.handle = pkv_q4_pool_wrap(c, self.num_pages, data, k_scale, v_scale, stream)
+        self._h, self._spec = self.handle.value, (self._index, *self._shape)
 
     @classmethod
     def empty(cls, num_pages: int, cfg=None, k_scale: float = 1.0, v_scale: float = 1.0, device="cuda", stream=None):
         data = torch.zeros(pkv_q4_pool_bytes(cfg, num_pages), dtype=torch.uint8, device=device)
         return cls(data, cfg, k_scale, v_scale, stream)
 
-    # The methods check what the functions of the same names check, in one place and once: these calls are short
-    # beside a Python function call.
+    # A call whose arguments are as they should be goes through _fast.  What that returns None for, and every call
+    # where the module was not built, is checked here, and a wrong argument raises.
 
     def append(self, k, v, k_norm_w, positions, prow, table, stream=None, rows=None, pages=None) -> None:
         """k normed and roped, then k and v quantised into their slots (prow None: token t is row t)."""
+        raw = _raw_stream(self._index) if stream is None else _stream(stream)
+        if _fast is not None and _fast.append(self._h, self._spec, k, v, k_norm_w, positions, prow, table, rows, pages,
+                                              raw) == 0:
+            return
         n = positions.shape[0]
         shape = (n, self._kv_heads, self._dim)
         if k.shape != shape or v.shape != shape or k_norm_w.numel() != self._dim:
@@ -676,19 +707,21 @@ class Q4KVPool(_Pool):
         tp, rows, pages = _table(table, rows, pages)
         rc = self._lib.pkv_q4_append(
             self.handle, _dev(k, _BF16, "k"), _dev(v, _BF16, "v"), _dev(k_norm_w, _BF16, "k_norm_w"),
-            _dev(positions, _I32, "positions"), None if prow is None else _prow(prow, n), tp, n, rows, pages,
-            _raw_stream(self._index) if stream is None else _stream(stream))
+            _dev(positions, _I32, "positions"), None if prow is None else _prow(prow, n), tp, n, rows, pages, raw)
         if rc:
             raise PkvError(rc, "pkv_q4_append")
 
     def read(self, positions, prow, table, k=None, v=None, stream=None, rows=None, pages=None):
         """(k, v) [tokens][kv_heads][head_dim] that the pool holds at the tokens' positions."""
+        raw = _raw_stream(self._index) if stream is None else _stream(stream)
         n = positions.shape[0]
         shape = (n, self._kv_heads, self._dim)
         if k is None or v is None:
             with _on(stream):
                 new = torch.empty(2, *shape, dtype=torch.bfloat16, device=self.device)
             k, v = new[0] if k is None else k, new[1] if v is None else v
+        if _fast is not None and _fast.read(self._h, self._spec, positions, prow, table, k, v, rows, pages, raw) == 0:
+            return k, v
         strides = k.stride()
         if k.shape != shape or v.shape != shape or v.stride() != strides or strides[2] != 1:
             raise ValueError(f"k and v must be {list(shape)} with contiguous heads and the same strides, got "
@@ -698,8 +731,7 @@ class Q4KVPool(_Pool):
         tp, rows, pages = _table(table, rows, pages)
         rc = self._lib.pkv_q4_read(
             self.handle, _dev(positions, _I32, "positions"), None if prow is None else _prow(prow, n), tp, n, rows, pages,
-            k.data_ptr(), v.data_ptr(), strides[0], strides[1],
-            _raw_stream(self._index) if stream is None else _stream(stream))
+            k.data_ptr(), v.data_ptr(), strides[0], strides[1], raw)
         if rc:
             raise PkvError(rc, "pkv_q4_read")
         return k, v
@@ -712,6 +744,13 @@ class Q4KVPool(_Pool):
         if out is None:
             with _on(stream):
                 out = torch.empty_like(q)
+        raw = _raw_stream(self._index) if stream is None else _stream(stream)
+        ws = self._streams.get(raw)
+        if ws is not None and raw != 0 and _capturing(stream):   # (the default stream is never captured)
+            ws = None
+        if ws is not None and _fast is not None and _fast.decode(
+                self._h, self._spec, q, k, v, q_norm_w, k_norm_w, positions, table, pages, out, ws[0], ws[1], raw) == 0:
+            return out
         rows = positions.shape[0]
         qs, ks = (rows, self._heads, self._dim), (rows, self._kv_heads, self._dim)
         if q.shape != qs or out.shape != qs or k.shape != ks or v.shape != ks:
@@ -722,13 +761,11 @@ class Q4KVPool(_Pool):
         tp, table_rows, pages = _table(table, rows, pages)
         if table_rows != rows:
             raise ValueError(f"table has {table_rows} rows, positions {rows}")
-        raw = _raw_stream(self._index) if stream is None else _stream(stream)
         args = (self.handle, _dev(q, _BF16, "q"), _dev(k, _BF16, "k"), _dev(v, _BF16, "v"),
                 _dev(q_norm_w, _BF16, "q_norm_w"), _dev(k_norm_w, _BF16, "k_norm_w"), _dev(positions, _I32, "positions"),
                 tp, rows, pages, _dev(out, _BF16, "out"))
-        ws = self._streams.get(raw)
         rc = PKV_EWORKSPACE
-        if ws is not None and (raw == 0 or not _capturing(stream)):   # (the default stream is never captured)
+        if ws is not None:
             rc = self._lib.pkv_q4_decode(*args, ws[0], ws[1], raw)
         if rc == PKV_EWORKSPACE:   # a first call, more rows than any call on this stream so far, or a capture
             n = pkv_workspace_bytes(self.handle, rows, pages, 0)

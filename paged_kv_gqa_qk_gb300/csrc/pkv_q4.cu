@@ -24,8 +24,12 @@
 namespace pkv {
 
 // A launch that may start while the kernel before it on the stream drains: every kernel
-// here waits for that one (pdl_wait) before it reads or writes memory, and lets the
-// next start its own launch early.
+// here waits for that one (pdl_wait) before it reads or writes memory.  The short ones let
+// the next one's CTAs come early (pdl_launch_dependents); the append and the split
+// attention, which fill the SMs by themselves, do not: CTAs that wait beside theirs cost
+// more than their early start saves (append and read of 2048 tokens 13.0 -> 9.1 us, steps
+// of 64 rows 43.5 -> 40.9, of 256 rows 210.1 -> 207.8 us without; a trigger at the
+// attention's end 41.4 and 210.7).
 template <class P>
 static cudaError_t launch_dependent(void (*kernel)(P), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
                                     const P& p, bool early = true)
@@ -125,7 +129,6 @@ __global__ void __launch_bounds__(32 * kQ4AppendWarps, !kFullRot ? 4 : kQuads ==
     const int lane = threadIdx.x & 31, j = lane & 7, groups = (p.kv_heads + 4 * kQuads - 1) / (4 * kQuads);
     const int item = blockIdx.x * kQ4AppendWarps + (threadIdx.x >> 5), t = item / groups;
     pdl_wait();
-    pdl_launch_dependents();
     if (t >= p.tokens) return;
     const int g0 = 4 * kQuads * (item - t * groups) + (lane >> 3);  // this lane's heads: g0, g0 + 4, ...
     uint4 kraw[kQuads][2] = {}, vraw[kQuads][2] = {}, wk[2];
@@ -640,7 +643,6 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
         for (int i = 0; i < kQ4Stages; ++i) mbar_init(bars + 8 * i, 1);
         fence_mbar_init();
     }
-    pdl_launch_dependents();
     // chunks per token and their prefix over tokens (one run of tokens a thread; every CTA computes it)
     const int nt = p.ntok, per = (nt + 32 * kQ4Warps - 1) / (32 * kQ4Warps);
     const int t0 = min(nt, tid * per), t1 = min(nt, t0 + per);

@@ -342,7 +342,7 @@ static int create_pool(const pkv_config* cfg, int num_pages, void* k, void* v, b
     ok &= cudaMemsetAsync(p->err, 0, 256, s) == cudaSuccess;
     ok &= cudaStreamSynchronize(s) == cudaSuccess;  // the host vectors die with this call
     if (q4) {
-        ok &= configure_q4() == cudaSuccess;
+        ok &= configure_q4(p) == cudaSuccess;
     } else {
         ok &= make_tmap(&p->tmap_k, p->k, num_slots, cfg->kv_heads);
         ok &= make_tmap(&p->tmap_v, p->v, num_slots, cfg->kv_heads);

@@ -51,6 +51,7 @@ struct pkv_pool {
     float2* rope_hi;       // (cos, sin) [max_seq][head_dim/2]: fp32 nearest to the double values
     float2* rope_lo;       // the double values minus rope_hi, in fp32
     int rope_exp;          // no entry of the tables exceeds 2^rope_exp (0 but for scaled rotations)
+    int q4_cluster;        // largest cluster of q4_unit_kernel
     uint32_t* err;         // sticky device error word (word 0 of a 256-byte allocation)
     uint32_t* claims;      // kClaimSlots chunk counters (bytes 128..255 of the same allocation), zero between calls
     std::atomic<uint64_t> call_seq;  // calls enqueued (from any host thread): call n uses claims[n % kClaimSlots]
@@ -196,7 +197,7 @@ cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& pl
 cudaError_t launch_q4_read(const pkv_pool* pool, const int32_t* positions, const int32_t* prow, const int32_t* table,
                            int tokens, int rows, int pages, void* k, void* v, int64_t token_stride, int64_t head_stride,
                            cudaStream_t s);
-cudaError_t configure_q4();
+cudaError_t configure_q4(pkv_pool* pool);
 
 // ---- pkv_norm_rope (pkv_norm_rope.cu): q and k (index 0 and 1; null: not given) ----
 struct NormRope {

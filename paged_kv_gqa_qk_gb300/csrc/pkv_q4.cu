@@ -9,6 +9,7 @@
 //                     copies and keeps its own softmax state
 //   q4_combine_kernel merge of the pieces of a (token, kv head) that several
 //                     warps shared
+//   q4_unit_kernel    the whole decode call of few short rows in one launch
 //   q4_read_kernel    cached k and v of a list of tokens as bf16
 //
 // Source of the computation (as the bf16 pool's): qwen3-8b Nest files,
@@ -177,8 +178,11 @@ __device__ __forceinline__ float q4_query(const float (&y)[16], float k_scale, u
 }
 
 // In front of the attention: one CTA per row checks every page that the row will read,
-// writes its attended length (and the zeros of a skipped row's output), appends its k and v (items 0 .. quads - 1 of 4 kv heads)
-// and prepares its queries (items from there on, the 4 query heads of a kv head each).
+// writes its attended length (and the zeros of a skipped row's output), appends its k and v
+// (items 0 .. quads - 1 of 4 kv heads) and prepares its queries (items from there on, the 4
+// query heads of a kv head each).  A chain of latencies (position, page ids, k and the
+// tables, sums over a head): 7 us alone for 8 to 64 rows, 11 for 256, all under 4 MB; most
+// of it runs beside the attention's own start (without that overlap 64 rows take 1.9 us more).
 template <bool kFullRot>
 __global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
 {
@@ -304,9 +308,10 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
 // are far apart in that sequence (w = warp * CTAs + CTA): a small call spreads over
 // all SMs.  A unit inside one warp's share is written out; the pieces of the others
 // go to index u + w of the partials (unique: units and warps both increase along the
-// sequence).  A warp counts its pieces in when its share is done; the CTA of the
-// warp that was last at a unit merges its pieces, in an order that depends on the
-// sizes alone.  No warp waits for a warp of another CTA.
+// sequence), and q4_combine_kernel merges them, in an order that depends on the sizes
+// alone.  No warp waits for a warp of another CTA.  (Merging in this kernel, by the warp or
+// the CTA that counts itself last at a unit, took longer than the launch: 8 rows of 36000
+// 74 and 86 us a call, 61 so.)
 //
 // The kernel starts beside q4_prep_kernel (programmatic launch): it splits the work
 // by the positions and starts its first copies at once -- all but a row's last chunk,
@@ -323,6 +328,16 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
 // The codes become fp16 by the conversion instruction and are multiplied by their
 // scales as fp16 pairs, exactly; V's are first regrouped so that one byte holds a
 // dim's codes of two positions.  P is turned between the fragments by movmatrix.
+//
+// What bounds it (alone, cold cache): long rows by memory, 8 rows of 32768-40960 331 MB in
+// 57 us, 5.8 TB/s; 64 rows of 512-4096 182 MB in 37 us, 5.0 TB/s, 5 us of them the start and
+// the last warps' ends; many rows by instructions, 256 rows of 1024-8192 1.04 GB in 200 us,
+// 5.2 TB/s: about 237 warp instructions a block, 111 of them on the integer pipe (the
+// conversions and the scales' products), at 2.5 an SM and cycle.  mma.sync m16n8k16 is used a third of
+// its rate there; an instruction with K = 16 takes the 16 dims of a scale whole.
+// 12 warps of 2 stages of a page: 16 warps of half pages 50 / 69 / 237 us a call on these three
+// workloads against 45 / 64 / 212 then, 8 warps of 3 stages no better, a copying warp
+// beside 11 others 51 / 75 / 257.
 constexpr int kQ4Warps = 12;
 constexpr int kQ4Stages = 2;
 constexpr int kQ4Chunk = 64;                         // positions: a page
@@ -821,8 +836,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
 }
 
 // =====================================================================================
-// q4_combine_kernel: one CTA per (token, kv head) unit; kSub warps share a query head's
-// pieces, a lane holds 4 dims
+// q4_combine_kernel: kHeads query heads of a (token, kv head) unit per CTA, kSub warps each;
+// a lane holds 4 dims
 // =====================================================================================
 struct Q4CombineParams {
     const int32_t* prefix;
@@ -835,13 +850,15 @@ struct Q4CombineParams {
 
 // out = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M).  Each warp takes every kSub-th piece,
 // kBatch of them in flight, and its own maximum; the warps' sums are joined in warp order.
-// Few units mean many pieces each, and few CTAs: they get 4 warps a head.
-template <int kSub, int kBatch>
-__global__ void __launch_bounds__(32 * kGroup * kSub) q4_combine_kernel(Q4CombineParams p)
+// Few units mean many pieces each, and few CTAs: a head's pieces get up to 16 warps, and every
+// head its own CTA.
+template <int kHeads, int kSub>
+__global__ void __launch_bounds__(32 * kHeads * kSub) q4_combine_kernel(Q4CombineParams p)
 {
+    constexpr int kBatch = 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.kv_heads;
-    const int head = warp % kGroup, sub = warp / kGroup;
-    const int u = blockIdx.x, t = u / G, g = u % G;
+    const int mine = warp % kHeads, sub = warp / kHeads, head = blockIdx.x % (kGroup / kHeads) * kHeads + mine;
+    const int u = blockIdx.x / (kGroup / kHeads), t = u / G, g = u % G;
     pdl_wait();
     pdl_launch_dependents();
     const int pre = p.prefix[t], n = p.prefix[t + 1] - pre, total = p.prefix[p.ntok];
@@ -882,20 +899,20 @@ __global__ void __launch_bounds__(32 * kGroup * kSub) q4_combine_kernel(Q4Combin
         }
     }
     if constexpr (kSub > 1) {
-        __shared__ float part[kSub][kGroup][6][32];
-        float(&mine)[6][32] = part[sub][head];
-        mine[0][lane] = acc[0], mine[1][lane] = acc[1], mine[2][lane] = acc[2], mine[3][lane] = acc[3];
-        mine[4][lane] = sum, mine[5][lane] = M;
+        __shared__ float part[kSub][kHeads][6][32];
+        float(&my)[6][32] = part[sub][mine];
+        my[0][lane] = acc[0], my[1][lane] = acc[1], my[2][lane] = acc[2], my[3][lane] = acc[3];
+        my[4][lane] = sum, my[5][lane] = M;
         __syncthreads();
         if (sub != 0) return;
         float all = -CUDART_INF_F;
 #pragma unroll
-        for (int q = 0; q < kSub; ++q) all = fmaxf(all, part[q][head][5][lane]);
+        for (int q = 0; q < kSub; ++q) all = fmaxf(all, part[q][mine][5][lane]);
         sum = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
 #pragma unroll
         for (int q = 0; q < kSub; ++q) {
             if (q >= np) break;  // no piece, no maximum
-            const float(&o)[6][32] = part[q][head];
+            const float(&o)[6][32] = part[q][mine];
             const float f = exp2f(o[5][lane] - all);
             sum += f * o[4][lane];
 #pragma unroll
@@ -915,12 +932,13 @@ __global__ void __launch_bounds__(32 * kGroup * kSub) q4_combine_kernel(Q4Combin
 // turn (chunk j: warp j mod the cluster's warps, spread over its CTAs first).  Every
 // CTA checks the row and prepares the unit's queries; the warp that has the last chunk
 // quantises the row's k and v while that chunk is on its way, and puts them into the
-// pool and into the staged chunk.  The warps' sums meet in the first CTA, which reads
-// the others' through distributed shared memory.
+// pool and into the staged chunk.  A CTA joins its warps' sums, and the first CTA of the
+// cluster the CTAs', through distributed shared memory.
 //
 // A call of few short rows is bound by its chain of latencies, not by bytes: this has
 // one launch and one trip to memory after the table, where preparation, split attention
-// and combine are three launches.  (Measured on one row of 700: 9 us a call instead of 14.)
+// and combine are three launches (one row of 700: 6.1 us a call instead of 9.1; the rule
+// and its other figures are at q4_unit_ctas).
 constexpr int kUnitWarps = 4;
 constexpr int kUnitStages = 2;
 
@@ -1063,7 +1081,8 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
         __syncwarp();
     }
 
-    // ---- the warps' sums into their own ring (nothing in flight there any more), then one warp a head joins them
+    // ---- the warps' sums into their own ring (nothing in flight there any more); one warp a head joins the CTA's,
+    // and the first CTA's those of the cluster
     const float LA = S.o[8][0], LB = S.o[8][1];
     float* part = reinterpret_cast<float*>(ring);
     if (L.c < 2 && first < n) {
@@ -1079,46 +1098,66 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
             sML[warp * kGroup + 2 * L.c + 1] = make_float2(S.mB, LB);
         }
     }
-    if (cs > 1)
-        cluster_sync();
-    else
-        __syncthreads();
-    if (rank == 0) {
-        const int h = warp, parts = min(n, step);  // warp w of CTA r has chunk w cs + r first: parts are 0 .. parts - 1
-        // maxima and sums of the parts, one a lane
-        float2 ml = make_float2(-CUDART_INF_F, 0.f);
-        if (lane < parts) {
-            const uint32_t a = base + Q4UnitSmem::kML + 8 * (lane / cs * kGroup + h);
-            ml = ld_cluster_f32x2(cluster_map(a, lane % cs));
+    __syncthreads();
+    const int h = warp;
+    float M = -CUDART_INF_F, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float4* joined = reinterpret_cast<float4*>(sbase + 4 * (h * kHeadDim + 4 * lane));  // warp 0's part, of this warp's head
+    if (rank < n) {  // (warp w has a part if chunk w cs + rank is there)
+        float2 ml[kUnitWarps];
+#pragma unroll
+        for (int w = 0; w < kUnitWarps; ++w) {
+            ml[w] = w * cs + rank < n ? sML[w * kGroup + h] : make_float2(-CUDART_INF_F, 0.f);
+            M = fmaxf(M, ml[w].x);
         }
-        float M = ml.x;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        const float f = lane < parts ? exp2f(ml.x - M) : 0.f;  // (NaN sums: M is theirs or above; f * NaN or NaN)
-        float sum = f * ml.y;
+        for (int w = 0; w < kUnitWarps; ++w) {
+            if (w * cs + rank >= n) break;
+            const float f = exp2f(ml[w].x - M);  // (NaN sums: M is theirs or above; f * NaN or NaN)
+            const float4 x = joined[w * (kUnitStages * kQ4ChunkBytes / 16)];
+            sum += f * ml[w].y;
+            acc[0] += f * x.x;
+            acc[1] += f * x.y;
+            acc[2] += f * x.z;
+            acc[3] += f * x.w;
+        }
+    }
+    if (cs > 1) {
+        __syncwarp();  // every lane has read the warps' maxima and sums of this head
+        *joined = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (lane == 0) sML[h] = make_float2(M, sum);
+        cluster_sync();
+        if (rank == 0) {
+            const int parts = min(n, cs);  // the CTAs that have one, its maximum and sum a lane
+            float2 ml = make_float2(-CUDART_INF_F, 0.f);
+            if (lane < parts) ml = ld_cluster_f32x2(cluster_map(base + Q4UnitSmem::kML + 8 * h, lane));
+            M = ml.x;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        constexpr int kBatch = 4;
-        for (int k0 = 0; k0 < parts; k0 += kBatch) {
-            float4 x[kBatch];
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+            const float f = lane < parts ? exp2f(ml.x - M) : 0.f;
+            sum = f * ml.y;
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int q = min(k0 + k, parts - 1);
-                const uint32_t a = base + q / cs * (kUnitStages * kQ4ChunkBytes) + 4 * (h * kHeadDim + 4 * lane);
-                x[k] = ld_cluster_f32x4(cluster_map(a, q % cs));
-            }
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+            acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+            constexpr int kBatch = 8;
+            for (int k0 = 0; k0 < parts; k0 += kBatch) {
+                float4 x[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const float fk = __shfl_sync(kFull, f, min(k0 + k, parts - 1));
-                if (k0 + k < parts) {
-                    acc[0] += fk * x[k].x;
-                    acc[1] += fk * x[k].y;
-                    acc[2] += fk * x[k].z;
-                    acc[3] += fk * x[k].w;
+                for (int k = 0; k < kBatch; ++k)
+                    x[k] = ld_cluster_f32x4(cluster_map(base + 4 * (h * kHeadDim + 4 * lane), min(k0 + k, parts - 1)));
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float fk = __shfl_sync(kFull, f, min(k0 + k, parts - 1));
+                    if (k0 + k < parts) {
+                        acc[0] += fk * x[k].x;
+                        acc[1] += fk * x[k].y;
+                        acc[2] += fk * x[k].z;
+                        acc[3] += fk * x[k].w;
+                    }
                 }
             }
         }
+    }
+    if (rank == 0) {
         const float inv = v_scale / sum;
         const float y[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
         *reinterpret_cast<uint2*>(p.out + ((int64_t)t * p.heads + g * kGroup + h) * kHeadDim + 4 * lane) = pack4(y);
@@ -1148,33 +1187,57 @@ Q4Plan make_q4_plan(const pkv_pool* pool, int rows)
 }
 
 // The CTAs that each unit gets in q4_unit_kernel, or 0: the call goes through the split
-// attention.  A unit gets as many CTAs (up to a cluster's 8) as leave about one an SM,
-// and no more than its pages can use.  A CTA's life is about 6 us and 1.25 us more for
-// every further page of its warps; the split attention costs 10 us and the time of its
-// bytes, and more where few units are cut into many pieces.  Measured (us, units
-// against split): 1 row of 700 6.3 / 10.3, 1 of 30000 24 / 38, 4 of 8000 15.3 / 21.4, 16 of
-// 500-1500 11.8 / 16.6, 64 of 1-640 15.5 / 19.6; 32 of 500-1500 18.8 / 18.8, 128 of 1-640
-// 25.4 / 24.7, 256 of 1-64 27.6 / 17.6.  The rows' lengths are not known here: `pages`, the
-// table's width, stands for the longest.  A grid size set by pkv_set_ctas is the split
-// attention's.
+// attention.  A unit gets as many CTAs (a power of two, up to a cluster's 16) as leave about
+// one an SM, and no more than its pages can use.  A CTA's life is about 6 us and 1 to 1.6 us
+// for every further page of its warps; the split attention costs 9 us and the time of its
+// bytes, and more where few units are cut into many pieces.  They meet at 30 to 50 pages an
+// SM in all, and with more than a few short units an SM.  Measured (us, units against split,
+// 8 kv heads): 1 row of 700 6.1 / 9.1, of 16000 12.3 / 18.1, of 36000 20.5 / 22.9, of 64000
+// 33.4 / 27.8; 2 rows of 16000 17.7 / 18.6; 4 of 8000 14.5 / 17.5, of 16000 24.6 / 24.1; 8 of 1000
+// 7.9 / 11.5, of 8000 24.8 / 23.6; 16 of 500-1500 11.1 / 14.6, of 4500 25.8 / 24.6; 64 of 1-640 14.1 /
+// 16.7; 128 of 1-256 16.2 / 15.8; one kv head, 1 row of 32000 14.5 / 21.5.  The rows' lengths are
+// not known here: `pages`, the table's width, stands for the longest.  A grid size set by
+// pkv_set_ctas is the split attention's.
 static int q4_unit_ctas(const pkv_pool* pool, int rows, int pages)
 {
     if (pool->ctas_override > 0) return 0;
     const int64_t units = (int64_t)rows * pool->cfg.kv_heads, sms = pool->num_sms;
+    if (units > 4 * sms || units * pages > 40 * sms) return 0;
     int cs = 1;
-    while (cs < 8 && 3 * units * 2 * cs <= 4 * sms && cs * kUnitWarps < pages) cs *= 2;
-    const int rounds = (pages + cs * kUnitWarps - 1) / (cs * kUnitWarps);
-    if (3 * units * cs <= 4 * sms) return rounds <= 16 ? cs : 0;
-    return units <= 4 * sms && rounds <= 4 ? 1 : 0;
+    while (cs < pool->q4_cluster && 3 * units * 2 * cs <= 4 * sms && cs * kUnitWarps < pages) cs *= 2;
+    return cs;
 }
 
-cudaError_t configure_q4()
+cudaError_t configure_q4(pkv_pool* pool)
 {
     cudaError_t rc;
     if ((rc = cudaFuncSetAttribute(q4_unit_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4UnitSmem::kAlloc)) != cudaSuccess ||
         (rc = cudaFuncSetAttribute(q4_unit_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4UnitSmem::kAlloc)) != cudaSuccess)
         return rc;
-    return cudaFuncSetAttribute(q4_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4Smem::kAlloc);
+    if ((rc = cudaFuncSetAttribute(q4_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4Smem::kAlloc)) != cudaSuccess)
+        return rc;
+    // clusters of 16 are beyond what every device holds: asked for here
+    for (auto kernel : {q4_unit_kernel<true>, q4_unit_kernel<false>}) {
+        if ((rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return rc;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 16;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(32 * kUnitWarps);
+        cfg.dynamicSmemBytes = Q4UnitSmem::kAlloc;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            clusters = 0;
+        }
+        pool->q4_cluster = clusters > 0 ? 16 : 8;
+        if (clusters <= 0) break;
+    }
+    return cudaSuccess;
 }
 
 static cudaError_t launch_q4_units(const pkv_pool* pool, const Q4AppendParams& ap, int cs, cudaStream_t s)
@@ -1261,17 +1324,22 @@ cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& pl
     cp.heads = p.heads;
     cp.kv_heads = p.kv_heads;
     cp.warps = plan.ctas * kQ4Warps;
-    const int64_t units = (int64_t)a.rows * p.kv_heads;
-    return units < 2 * (int64_t)plan.ctas
-               ? launch_dependent(q4_combine_kernel<4, 8>, (unsigned)units, 32 * kGroup * 4, 0, s, cp)
-               : launch_dependent(q4_combine_kernel<1, 8>, (unsigned)units, 32 * kGroup, 0, s, cp);
+    const unsigned units = (unsigned)(a.rows * p.kv_heads), pieces = cp.warps / units;
+    // pieces of a unit, measured with 4 / 8 / 16 warps a head (us a call): 9 (24 rows of 8000) 44.3 / 44.7 / 46.9,
+    // 28 (8 of 36000) 58.8 / 58.2 / 59.3, 114 (2 of 65000) 41.3 / 36.7 / 34.8, 228 (1 of 130000) 50.3 / 41.3 /
+    // 36.9; and less than six (64 rows): one warp a head 41.0, 4 42.6
+    if (units >= 2u * plan.ctas) return launch_dependent(q4_combine_kernel<kGroup, 1>, units, 32 * kGroup, 0, s, cp);
+    return pieces < 20    ? launch_dependent(q4_combine_kernel<1, 4>, kGroup * units, 32 * 4, 0, s, cp)
+           : pieces < 100 ? launch_dependent(q4_combine_kernel<1, 8>, kGroup * units, 32 * 8, 0, s, cp)
+                          : launch_dependent(q4_combine_kernel<1, 16>, kGroup * units, 32 * 16, 0, s, cp);
 }
 
 // =====================================================================================
 // q4_read_kernel: a warp takes kQuads times 4 kv heads of one token, 8 lanes a head, lane j
 // the dims 8j .. 8j + 7 and 64 + 8j .. of k and v (as the append's lanes): 16-byte stores.
-// Bound by its instructions next to memory: 8 heads a warp share a token's address
-// arithmetic.
+// Bound by its stores: 33800 tokens of 8 heads, 39 MB read and 138 MB written, in 31 us, 5.7
+// TB/s, at 0.58 of the issue slots; 8 heads a warp share a token's address arithmetic.  (Several
+// tokens a warp in turn: 33 to 35 us.)  Few tokens are one launch and four trips to memory.
 // =====================================================================================
 struct Q4ReadParams {
     const uint8_t* data;

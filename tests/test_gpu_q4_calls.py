@@ -245,6 +245,21 @@ def test_split_attention_replays_from_graphs_beside_eager_calls():
     pool.close()
 
 
+@pytest.mark.parametrize("rows,length,kv_heads,ctas", [
+    (1, 4096, 8, 0), (1, 4033, 1, 0), (2, 2500, 2, 0), (3, 900, 3, 0),     # clusters of 16, 16, 16 and 4 CTAs a unit
+    (1, 4096, 1, 152), (1, 3500, 8, 152), (5, 1500, 4, 152),               # 16, 16 and 8 warps for a head's pieces
+    (40, 400, 4, 152), (80, 600, 4, 152)])                                 # 4, and one
+def test_few_rows_many_pieces(rows, length, kv_heads, ctas):
+    """Long rows cut among many warps, in either form of the call."""
+    wl, cache = make([length - 7 * b for b in range(rows)], kv_heads, max_seq=4096)
+    pool = pool_of(wl, cache, ctas)
+    ref, bound, after = reference(wl, cache)
+    check(pool.decode(*inputs(wl)), ref, bound)
+    assert pool.check_errors() == 0
+    assert np.array_equal(pool.data.cpu().numpy().reshape(after.data.shape), after.data)
+    pool.close()
+
+
 def test_split_attention_beyond_32_bit_offsets():
     """Rows whose pages lie behind byte 2^32 of a pool, read by many CTAs."""
     n, cfg = 60000, dict(heads=32, kv_heads=8, max_seq=4096)

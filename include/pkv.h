@@ -431,7 +431,7 @@ PKV_API int pkv_q4_pool_data(const pkv_pool* pool, void** data, size_t* bytes);
  *   slot = table[prow[t]][positions[t] / page_size] * page_size + positions[t] % page_size.
  * k is QK-normed and roped first (as pkv_decode does), v is quantised as given.
  *   k, v       device bf16 [tokens][kv_heads][head_dim], 16-byte aligned
- *   k_norm_w   device bf16 [head_dim]
+ *   k_norm_w   device bf16 [head_dim], 8-byte aligned
  *   positions  device int32 [tokens]; -1 = nothing to write
  *   prow       device int32 [tokens], or NULL: token t is row t (rows >= tokens)
  *   table      device int32 [rows][pages], or NULL: contiguous rows

@@ -81,6 +81,16 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* head, int j, uint4 (
     r[0] = *reinterpret_cast<const uint4*>(head + 8 * j);
     r[1] = *reinterpret_cast<const uint4*>(head + 64 + 8 * j);
 }
+// The same of norm weights, which may lie on an 8-byte border.
+__device__ __forceinline__ void load16_weights(const __nv_bfloat16* w, int j, uint4 (&r)[2])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint2 a = *reinterpret_cast<const uint2*>(w + 64 * h + 8 * j);
+        const uint2 b = *reinterpret_cast<const uint2*>(w + 64 * h + 8 * j + 4);
+        r[h] = make_uint4(a.x, a.y, b.x, b.y);
+    }
+}
 
 // What is wrong with a token's position and row, as an error bit; 0: nothing, or no step (-1).
 __device__ __forceinline__ uint32_t q4_fault(const Q4AppendParams& p, int pos, int row)
@@ -140,7 +150,7 @@ __global__ void __launch_bounds__(32 * kQ4AppendWarps, !kFullRot ? 4 : kQuads ==
             load16(p.k + src, j, kraw[q]);
             load16(p.v + src, j, vraw[q]);
         }
-    load16(p.kw, j, wk);
+    load16_weights(p.kw, j, wk);
     const int pos = p.positions[t], row = p.prow ? p.prow[t] : t;
     const bool active = pos != -1;
     uint32_t e = q4_fault(p, pos, row);
@@ -201,10 +211,10 @@ __global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
                 load16(p.k + src, j, a);
                 load16(p.v + src, j, b);
             }
-            load16(p.kw, j, w);
+            load16_weights(p.kw, j, w);
         } else if (item < items) {
             load16(p.q + ((int64_t)t * p.heads + 4 * (item - quads) + sub) * kHeadDim, j, a);
-            load16(p.qw, j, w);
+            load16_weights(p.qw, j, w);
         }
     };
     load();
@@ -983,12 +993,12 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
     uint4 qraw[2], kraw[2], vraw[2], wq[2], wk[2];
     if (warp == 0) {
         load16(p.q + ((int64_t)t * p.heads + g * kGroup + sub) * kHeadDim, lj, qraw);
-        load16(p.qw, lj, wq);
+        load16_weights(p.qw, lj, wq);
     }
     const int64_t kv = ((int64_t)t * G + g) * kHeadDim;
     load16(p.k + kv, lj, kraw);
     load16(p.v + kv, lj, vraw);
-    load16(p.kw, lj, wk);
+    load16_weights(p.kw, lj, wk);
     const int pos = p.positions[t], row = t;
     const bool active = pos != -1;
     uint32_t e = q4_fault(p, pos, row);

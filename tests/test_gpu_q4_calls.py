@@ -151,6 +151,30 @@ def test_norm_rope_refusals(way):
     pool.close()
 
 
+@pytest.mark.parametrize("ctas", [0, 152])
+def test_weights_on_an_8_byte_border(ctas):
+    """Norm weights inside a larger tensor: 8 bytes off a 16-byte border as any others, 4 off refused."""
+    wl, cache = make([100, 30, 70], 8)
+    pool = pool_of(wl, cache, ctas)
+    q, k, v, qw, kw, pos, table = inputs(wl)
+    both = torch.zeros(2, 132, dtype=torch.bfloat16, device=DEV)
+    both[0, 4:], both[1, :128] = qw, kw
+    qw8, kw8 = both[0, 4:], both[1, :128]
+    assert qw8.data_ptr() % 16 == 8 and kw8.data_ptr() % 16 == 8
+    ref, bound, after = reference(wl, cache)
+    check(pool.decode(q, k, v, qw8, kw8, pos, table), ref, bound)
+    pool.append(k, v, kw8, pos, None, table)
+    assert pool.check_errors() == 0
+    assert np.array_equal(pool.data.cpu().numpy().reshape(after.data.shape), after.data)
+    odd = torch.zeros(130, dtype=torch.bfloat16, device=DEV)[2:]
+    for call in (lambda: pool.decode(q, k, v, odd, kw, pos, table), lambda: pool.decode(q, k, v, qw, odd, pos, table),
+                 lambda: pool.append(k, v, odd, pos, None, table), lambda: pool.norm_rope(q, k, odd, kw, pos)):
+        with pytest.raises(pkv.PkvError) as e:
+            call()
+        assert e.value.code == pkv.PKV_EINVAL
+    pool.close()
+
+
 def test_set_rope_refusals():
     wl, cache = make([20], 1)
     pool = pool_of(wl, cache)

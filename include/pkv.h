@@ -510,7 +510,8 @@ PKV_API int pkv_rope_frequencies(const pkv_config* cfg, int scaling, double fact
 
 /* Replace the pool's RoPE tables: pair i turns by position * inv_freq[i] (host, rotary_dim/2 of
  * them, >= 0 and finite) and cos and sin are multiplied by mscale (> 0, at most 1024).  Every entry of this
- * pool uses them from then on; what the pool already holds is not rotated again.  Waits for the
+ * pool uses them from then on, captured calls that are replayed included; what the pool already
+ * holds is not rotated again.  Waits for the
  * device's work and is not for a stream under capture (PKV_EINVAL).  Errors: PKV_EINVAL,
  * PKV_EDEVICE, PKV_ENOMEM, PKV_ECUDA. */
 PKV_API int pkv_pool_set_rope(pkv_pool* pool, const double* inv_freq, double mscale, void* stream);

@@ -878,13 +878,13 @@ int pkv_pool_set_rope(pkv_pool* pool, const double* inv_freq, double mscale, voi
         return PKV_ENOMEM;
     }
     const size_t tab = hi.size() * sizeof(float2);
+    const int rope_exp = std::max(0, (int)std::ceil(std::log2(mscale)));
     if (cudaDeviceSynchronize() != cudaSuccess) return PKV_ECUDA;  // calls in flight read the old tables
     if (cudaMemcpyAsync(pool->rope_hi, hi.data(), tab, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaMemcpyAsync(pool->rope_lo, lo.data(), tab, cudaMemcpyHostToDevice, s) != cudaSuccess)
+        cudaMemcpyAsync(pool->rope_lo, lo.data(), tab, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+        cudaMemcpyAsync(pool->err + 1, &rope_exp, sizeof rope_exp, cudaMemcpyHostToDevice, s) != cudaSuccess)
         return PKV_ECUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return PKV_ECUDA;
-    pool->rope_exp = std::max(0, (int)std::ceil(std::log2(mscale)));
-    return PKV_OK;
+    return cudaStreamSynchronize(s) == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
 int pkv_norm_rope(pkv_pool* pool, const void* q, const void* k, const void* q_norm_w, const void* k_norm_w,

@@ -50,9 +50,9 @@ struct pkv_pool {
     float k_scale, v_scale;  // 4-bit pool: the powers of two on every value
     float2* rope_hi;       // (cos, sin) [max_seq][head_dim/2]: fp32 nearest to the double values
     float2* rope_lo;       // the double values minus rope_hi, in fp32
-    int rope_exp;          // no entry of the tables exceeds 2^rope_exp (0 but for scaled rotations)
     int q4_cluster;        // largest cluster of q4_unit_kernel
-    uint32_t* err;         // sticky device error word (word 0 of a 256-byte allocation)
+    uint32_t* err;         // sticky device error word (word 0 of a 256-byte allocation); word 1: no entry of the
+                           // tables exceeds 2^it (0 but for scaled rotations)
     uint32_t* claims;      // kClaimSlots chunk counters (bytes 128..255 of the same allocation), zero between calls
     std::atomic<uint64_t> call_seq;  // calls enqueued (from any host thread): call n uses claims[n % kClaimSlots]
     CUtensorMap tmap_k;    // 3-D tiled view of K: {head_dim, num_slots, kv_heads}, box {64, 64, 1}, 128B swizzle

@@ -72,7 +72,7 @@ struct Q4AppendParams {
     float eps, k_scale;
     float2 eps2;                // eps as a pair of floats
     float k_inv6, k_inv, v_inv6, v_inv;  // 1 / (6 s) and 1 / s of the pool's scales
-    int rope_exp;               // |cos|, |sin| <= 2^rope_exp
+    const int* rope_exp;        // |cos|, |sin| <= 2^rope_exp (on the device: a captured call follows pkv_pool_set_rope)
 };
 
 // The two 16-byte pieces of a head vector that lane j of 8 holds.
@@ -114,12 +114,13 @@ __device__ __forceinline__ void prefetch_rope(const Q4AppendParams& p, int pos, 
 // pieces; g: its head; live: there is such a head).  All lanes take part.
 template <bool kFullRot>
 __device__ __forceinline__ void q4_append_heads(const Q4AppendParams& p, const uint4 (&kraw)[2], const uint4 (&vraw)[2],
-                                                const uint4 (&wk)[2], int g, bool live, int page, int pos, int lane)
+                                                const uint4 (&wk)[2], int rope_exp, int g, bool live, int page, int pos,
+                                                int lane)
 {
     const int64_t at = (int64_t)pos * kRopeHalf;
     float x[16];
     uint32_t bits[8];
-    norm_rope_k_paired<kFullRot>(kraw, wk, p.rope_hi + at, p.rope_lo + at, p.eps2, p.rope_exp, lane, p.rot, x, bits);
+    norm_rope_k_paired<kFullRot>(kraw, wk, p.rope_hi + at, p.rope_lo + at, p.eps2, rope_exp, lane, p.rot, x, bits);
     // (heads beyond the last quantise zeros and store nothing: the shuffles want every lane)
     uint8_t* block = p.data + q4_block(page, p.kv_heads, live ? g : 0, pos % kPageSize);
     q4_store(block, false, pos % kQ4Block, x, bits, p.k_inv6, p.k_inv, lane & 7, live);
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(32 * kQ4AppendWarps, !kFullRot ? 4 : kQuads ==
             load16(p.v + src, j, vraw[q]);
         }
     load16_weights(p.kw, j, wk);
-    const int pos = p.positions[t], row = p.prow ? p.prow[t] : t;
+    const int pos = p.positions[t], row = p.prow ? p.prow[t] : t, rope_exp = *p.rope_exp;
     const bool active = pos != -1;
     uint32_t e = q4_fault(p, pos, row);
     int page = 0;
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(32 * kQ4AppendWarps, !kFullRot ? 4 : kQuads ==
     if (!active || e) return;
 #pragma unroll
     for (int q = 0; q < kQuads; ++q)
-        q4_append_heads<kFullRot>(p, kraw[q], vraw[q], wk, g0 + 4 * q, g0 + 4 * q < p.kv_heads, page, pos, lane);
+        q4_append_heads<kFullRot>(p, kraw[q], vraw[q], wk, rope_exp, g0 + 4 * q, g0 + 4 * q < p.kv_heads, page, pos, lane);
 }
 
 // A query head over 8 lanes as fp16, times the power of two that brings its largest
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
         }
     };
     load();
-    const int pos = p.positions[t], row = t;
+    const int pos = p.positions[t], row = t, rope_exp = *p.rope_exp;
     const bool active = pos != -1;
     uint32_t e = q4_fault(p, pos, row);
     int page = 0, bad = 0;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
     for (; item < items; item += warps, load()) {
         if (item < quads) {
             const int g = 4 * item + sub;
-            q4_append_heads<kFullRot>(p, a, b, w, g, g < p.kv_heads, page, pos, lane);
+            q4_append_heads<kFullRot>(p, a, b, w, rope_exp, g, g < p.kv_heads, page, pos, lane);
             continue;
         }
         float x[16], y[16];
@@ -274,7 +275,7 @@ static Q4AppendParams append_params(const pkv_pool* pool)
     p.rot = pool->cfg.rotary_dim > 0 ? pool->cfg.rotary_dim : kHeadDim;
     p.eps = (float)pool->cfg.eps;
     p.eps2 = make_float2(p.eps, (float)(pool->cfg.eps - (double)p.eps));
-    p.rope_exp = pool->rope_exp;
+    p.rope_exp = reinterpret_cast<const int*>(pool->err + 1);
     p.k_scale = pool->k_scale;
     p.k_inv6 = (1.f / 6.f) / pool->k_scale;  // (the scales are powers of two)
     p.k_inv = 1.f / pool->k_scale;
@@ -999,7 +1000,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
     load16(p.k + kv, lj, kraw);
     load16(p.v + kv, lj, vraw);
     load16_weights(p.kw, lj, wk);
-    const int pos = p.positions[t], row = t;
+    const int pos = p.positions[t], row = t, rope_exp = *p.rope_exp;
     const bool active = pos != -1;
     uint32_t e = q4_fault(p, pos, row);
     const int n = active && !e ? pos / kPageSize + 1 : 0;  // chunks (pages)
@@ -1046,7 +1047,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
     float xn[16];      // lanes of sub 0 and 1: the new k, of 2 and 3: v
     uint32_t bits[8];  // the same as bf16
     if (owner) {
-        norm_rope_k_paired<kFullRot>(kraw, wk, p.rope_hi + at, p.rope_lo + at, p.eps2, p.rope_exp, lane, p.rot, xn, bits);
+        norm_rope_k_paired<kFullRot>(kraw, wk, p.rope_hi + at, p.rope_lo + at, p.eps2, rope_exp, lane, p.rot, xn, bits);
         if (sub >= 2) {
             unpack16(vraw[0], vraw[1], xn);
             bits[0] = vraw[0].x, bits[1] = vraw[0].y, bits[2] = vraw[0].z, bits[3] = vraw[0].w;

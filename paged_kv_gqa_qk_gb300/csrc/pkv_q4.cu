@@ -1149,7 +1149,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
             acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-            constexpr int kBatch = 8;
+            constexpr int kBatch = 4;
             for (int k0 = 0; k0 < parts; k0 += kBatch) {
                 float4 x[kBatch];
 #pragma unroll

@@ -531,6 +531,13 @@ def pkv_timer_read(pool):
 
 # ------------------------------------------------------------------ convenience (marshalling only)
 
+def _on_device(index: int, **tensors) -> None:
+    """Refuses tensors of another device than the pool's: its kernels would read their pointers there."""
+    for what, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.get_device() != index:
+            raise ValueError(f"{what} lies on {t.device}, the pool on cuda:{index}")
+
+
 class _Pool:
     """What pools of either format share: the workspace, norm + rotation, errors, closing."""
 
@@ -567,6 +574,8 @@ class _Pool:
                                  q_out, k_out, raw)
             if rc == 0:
                 return q_out, k_out
+        _on_device(self._spec[0], q=q, k=k, q_norm_w=q_norm_w, k_norm_w=k_norm_w, positions=positions, q_out=q_out,
+                   k_out=k_out)
         pkv_norm_rope(self.handle, q, k, q_norm_w, k_norm_w, positions, q_out, k_out, layout, stream, self._shape)
         return q_out, k_out
 
@@ -699,6 +708,7 @@ class Q4KVPool(_Pool):
         if _fast is not None and _fast.append(self._h, self._spec, k, v, k_norm_w, positions, prow, table, rows, pages,
                                               raw) == 0:
             return
+        _on_device(self._index, k=k, v=v, k_norm_w=k_norm_w, positions=positions, prow=prow, table=table)
         n = positions.shape[0]
         shape = (n, self._kv_heads, self._dim)
         if k.shape != shape or v.shape != shape or k_norm_w.numel() != self._dim:
@@ -722,6 +732,7 @@ class Q4KVPool(_Pool):
             k, v = new[0] if k is None else k, new[1] if v is None else v
         if _fast is not None and _fast.read(self._h, self._spec, positions, prow, table, k, v, rows, pages, raw) == 0:
             return k, v
+        _on_device(self._index, positions=positions, prow=prow, table=table, k=k, v=v)
         strides = k.stride()
         if k.shape != shape or v.shape != shape or v.stride() != strides or strides[2] != 1:
             raise ValueError(f"k and v must be {list(shape)} with contiguous heads and the same strides, got "
@@ -751,6 +762,8 @@ class Q4KVPool(_Pool):
         if ws is not None and _fast is not None and _fast.decode(
                 self._h, self._spec, q, k, v, q_norm_w, k_norm_w, positions, table, pages, out, ws[0], ws[1], raw) == 0:
             return out
+        _on_device(self._index, q=q, k=k, v=v, q_norm_w=q_norm_w, k_norm_w=k_norm_w, positions=positions, table=table,
+                   out=out)
         rows = positions.shape[0]
         qs, ks = (rows, self._heads, self._dim), (rows, self._kv_heads, self._dim)
         if q.shape != qs or out.shape != qs or k.shape != ks or v.shape != ks:

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
@@ -81,7 +82,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(obj, [src] + headers):
             cmd = [NVCC, *ARCH, *FLAGS, *extra_flags, "-c", src, "-o", obj]
             jobs.append(cmd)
-    fast = force or _stale(FAST, [FAST_SRC])
+    torch = importlib.util.find_spec("torch")  # (another torch installed since: built again)
+    fast = force or _stale(FAST, [FAST_SRC] + ([torch.origin] if torch and torch.origin else []))
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
         if fast:
             fast = ex.submit(_build_fast, verbose)

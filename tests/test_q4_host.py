@@ -112,3 +112,29 @@ def test_unknown_scaling(lib):
         assert lib.pkv_rope_frequencies(ctypes.byref(cfg), kind, 1.0, 1, f, ctypes.byref(m)) == pkv.PKV_EINVAL
     with pytest.raises(KeyError):
         pkv.pkv_rope_frequencies(None, "other")
+
+
+def test_tensors_of_another_device_are_refused():
+    t = torch.zeros(2)
+    pkv._on_device(-1, a=t, b=None)
+    with pytest.raises(ValueError, match="weights lies on cpu, the pool on cuda:1"):
+        pkv._on_device(1, table=None, weights=t)
+
+
+def test_the_short_way_leaves_what_it_does_not_like(lib):
+    """csrc/pkv_torch.cpp's functions return None for wrong arguments of any kind and launch nothing."""
+    if pkv._fast is None:
+        pytest.skip("the module was not built")
+    t, i = torch.zeros(1, 8, 128, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    spec = (0, 32, 8, 128)
+    good = {"decode": (0, spec, t, t, t, t, t, i, i, None, t, 0, 0, 0), "append": (0, spec, t, t, t, i, None, i, 1, 1, 0),
+            "read": (0, spec, i, None, i, t, t, 1, 1, 0), "norm_rope": (0, spec, t, t, t, t, i, 0, t, t, 0)}
+    for name, args in good.items():
+        f = getattr(pkv._fast, name)
+        assert f() is None and f(*args[:-1]) is None and f(*args, 1) is None
+        assert f(*args) is None                     # tensors of the host
+        for k in range(len(args)):
+            for bad in ("x", None, 1.5, -1, 2 ** 70, (), (1, 2, 3, "x"), object()):
+                assert f(*args[:k], bad, *args[k + 1:]) is None
+    with pytest.raises(TypeError):
+        pkv._fast.bind(1, 2)

@@ -50,7 +50,7 @@ struct pkv_pool {
     float k_scale, v_scale;  // 4-bit pool: the powers of two on every value
     float2* rope_hi;       // (cos, sin) [max_seq][head_dim/2]: fp32 nearest to the double values
     float2* rope_lo;       // the double values minus rope_hi, in fp32
-    int q4_cluster;        // largest cluster of q4_unit_kernel
+    int q4_clusters[2][5];  // clusters of 1, 2, 4, 8 and 16 CTAs of q4_unit_kernel's two forms that the device holds at a time
     uint32_t* err;         // sticky device error word (word 0 of a 256-byte allocation); word 1: no entry of the
                            // tables exceeds 2^it (0 but for scaled rotations)
     uint32_t* claims;      // kClaimSlots chunk counters (bytes 128..255 of the same allocation), zero between calls

@@ -535,13 +535,14 @@ struct Q4State {
         mA = mB = -CUDART_INF_F;
     }
 
-    // One chunk in shared memory at sb, of which the unit has `left` positions (as many or more: all).
+    // One chunk of kBlocks blocks in shared memory at sb, of which the unit has `left` positions (as many or more: all).
+    template <int kBlocks>
     __device__ __forceinline__ void chunk(const Q4Lane& L, const uint8_t* sb, int left)
     {
         // ---- S = K q^T
-        float s[kQ4Blocks][4];
+        float s[kBlocks][4];
 #pragma unroll
-        for (int b = 0; b < kQ4Blocks; ++b) {
+        for (int b = 0; b < kBlocks; ++b) {
             s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
             const uint8_t* kb = sb + b * kQ4BlockBytes;
             const uint4 k0 = *reinterpret_cast<const uint4*>(kb + L.koff), k1 = *reinterpret_cast<const uint4*>(kb + L.koff + 512);
@@ -567,12 +568,12 @@ struct Q4State {
         // ---- softmax, base 2: s[b][0], [1]: heads 2c, 2c + 1 at position L.pi_r of block b; [2], [3]: at L.pi_r + 8
         // Positions past the row's end: scores of -inf, and V scales of 0 (the codes are finite
         // whatever lies there), in a row's last chunk only.
-        uint32_t vmask[kQ4Blocks];
+        uint32_t vmask[kBlocks];
 #pragma unroll
-        for (int b = 0; b < kQ4Blocks; ++b) vmask[b] = ~0u;
-        if (left < kQ4Chunk) {
+        for (int b = 0; b < kBlocks; ++b) vmask[b] = ~0u;
+        if (left < kBlocks * kQ4Block) {
 #pragma unroll
-            for (int b = 0; b < kQ4Blocks; ++b) {
+            for (int b = 0; b < kBlocks; ++b) {
                 const int at = left - kQ4Block * b;
                 if (L.pi_r >= at) s[b][0] = s[b][1] = -CUDART_INF_F;
                 if (L.pi_r + 8 >= at) s[b][2] = s[b][3] = -CUDART_INF_F;
@@ -582,7 +583,7 @@ struct Q4State {
         }
         float nA = fmaxf(s[0][0], s[0][2]), nB = fmaxf(s[0][1], s[0][3]);
 #pragma unroll
-        for (int b = 1; b < kQ4Blocks; ++b) {
+        for (int b = 1; b < kBlocks; ++b) {
             nA = fmaxf(nA, fmaxf(s[b][0], s[b][2]));
             nB = fmaxf(nB, fmaxf(s[b][1], s[b][3]));
         }
@@ -610,9 +611,9 @@ struct Q4State {
                 o[k][3] *= aB;
             }
         }
-        uint32_t pb[kQ4Blocks][2];
+        uint32_t pb[kBlocks][2];
 #pragma unroll
-        for (int b = 0; b < kQ4Blocks; ++b) {
+        for (int b = 0; b < kBlocks; ++b) {
             float e[4];
             e[0] = ex2(__fmaf_rn(s[b][0], mulA, -mA));
             e[1] = ex2(__fmaf_rn(s[b][1], mulB, -mB));
@@ -625,7 +626,7 @@ struct Q4State {
 
         // ---- O^T += V^T P
 #pragma unroll
-        for (int b = 0; b < kQ4Blocks; ++b) {
+        for (int b = 0; b < kBlocks; ++b) {
             const uint8_t* vb = sb + b * kQ4BlockBytes;
             const uint2 v0 = *reinterpret_cast<const uint2*>(vb + L.voff0), v1 = *reinterpret_cast<const uint2*>(vb + L.voff1);
             const uint2 v2 = *reinterpret_cast<const uint2*>(vb + L.voff0 + 512), v3 = *reinterpret_cast<const uint2*>(vb + L.voff1 + 512);
@@ -788,7 +789,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
             ok = false;
             break;
         }
-        S.chunk(L, wring + st * kQ4ChunkBytes, len - j * kQ4Chunk);
+        S.chunk<kQ4Blocks>(L, wring + st * kQ4ChunkBytes, len - j * kQ4Chunk);
         __syncwarp();  // every lane has read the stage: it may be filled again
 
         if (++st == kQ4Stages) {
@@ -939,29 +940,39 @@ __global__ void __launch_bounds__(32 * kHeads * kSub) q4_combine_kernel(Q4Combin
 // q4_unit_kernel: a whole decode call in one launch, for small calls
 // =====================================================================================
 //
-// A cluster of CTAs per (token, kv head) unit; its warps take the unit's chunks in
-// turn (chunk j: warp j mod the cluster's warps, spread over its CTAs first).  Every
-// CTA checks the row and prepares the unit's queries; the warp that has the last chunk
-// quantises the row's k and v while that chunk is on its way, and puts them into the
-// pool and into the staged chunk.  A CTA joins its warps' sums, and the first CTA of the
+// A cluster of CTAs per (token, kv head) unit; its warps take the unit's pieces (pages or
+// half pages) in turn (piece j: warp j mod the cluster's warps, spread over its CTAs first).
+// Every CTA checks the row and prepares the unit's queries; the warp that has the last piece
+// quantises the row's k and v while that piece is on its way, and puts them into the
+// pool and into the staged piece.  A CTA joins its warps' sums, and the first CTA of the
 // cluster the CTAs', through distributed shared memory.
 //
 // A call of few short rows is bound by its chain of latencies, not by bytes: this has
 // one launch and one trip to memory after the table, where preparation, split attention
-// and combine are three launches (one row of 700: 6.1 us a call instead of 9.1; the rule
-// and its other figures are at q4_unit_ctas).
-constexpr int kUnitWarps = 4;
+// and combine are three launches (one row of 700: 5.9 us a call instead of 9.1).  Half pages
+// halve the chain of a warp's first piece, 1.3 us, where there are warps for all of them;
+// whole pages carry more a round.  Both have 8 warps, two a scheduler, of which one computes
+// while the other waits (4 warps of pages: 16 rows of 500-1500 10.8 us, 9.4 with 8).  The
+// rule and its other figures are at q4_unit_choice.
 constexpr int kUnitStages = 2;
 
-struct Q4UnitSmem {
-    static constexpr int kBars = kUnitWarps * kUnitStages * kQ4ChunkBytes;
-    static constexpr int kQ = kBars + 8 * kUnitWarps * kUnitStages;  // __half [4][128]
+// The forms of the kernel: a warp takes a piece of kBlocks blocks of 16 positions at a time.
+template <int kBlocks_>
+struct Q4Unit {
+    static constexpr int kWarps = 8, kBlocks = kBlocks_;
+    static constexpr int kPiece = kBlocks * kQ4Block, kPerPage = kPageSize / kPiece;
+    static constexpr int kPieceBytes = kBlocks * kQ4BlockBytes;
+    static constexpr int kRing = kUnitStages * kPieceBytes;          // of a warp; later its sums
+    static constexpr int kBars = kWarps * kRing;
+    static constexpr int kQ = kBars + 8 * kWarps * kUnitStages;      // __half [4][128]
     static constexpr int kMul = kQ + 2 * kGroup * kHeadDim;          // float [4]
     static constexpr int kML = kMul + 4 * kGroup;                    // float2 [warps][4]: maximum and sum
-    static constexpr int kBytes = kML + 8 * kUnitWarps * kGroup;
+    static constexpr int kBytes = kML + 8 * kWarps * kGroup;
     static constexpr int kAlloc = kBytes + 128;
+    static constexpr int kCtas = kBlocks == 4 ? 1 : 2;               // an SM (bounds the registers)
+    static_assert(4 * kGroup * kHeadDim <= kRing, "a warp's sums fit its ring");
+    static_assert(kCtas * kAlloc <= 227 * 1024, "the rings fit");
 };
-static_assert(kUnitWarps == kGroup, "the merge has a warp a query head");
 
 __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr)
 {
@@ -970,19 +981,19 @@ __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr)
     return v;
 }
 
-template <bool kFullRot>
-__global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams p, float v_scale, uint64_t wait_ns, int cs)
+template <class U, bool kFullRot>
+__global__ void __launch_bounds__(32 * U::kWarps, U::kCtas) q4_unit_kernel(Q4AppendParams p, float v_scale, uint64_t wait_ns, int cs)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 127u) & ~127u;
     uint8_t* sbase = smem_raw + (base - raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lj = lane & 7, sub = lane >> 3, G = p.kv_heads;
     const int u = blockIdx.x / cs, t = u / G, g = u % G, rank = (int)cluster_rank();
-    const uint32_t bars = base + Q4UnitSmem::kBars + 8 * kUnitStages * warp;
-    uint8_t* ring = sbase + warp * (kUnitStages * kQ4ChunkBytes);
-    __half* sQ = reinterpret_cast<__half*>(sbase + Q4UnitSmem::kQ);
-    float* sMul = reinterpret_cast<float*>(sbase + Q4UnitSmem::kMul);
-    float2* sML = reinterpret_cast<float2*>(sbase + Q4UnitSmem::kML);
+    const uint32_t bars = base + U::kBars + 8 * kUnitStages * warp;
+    uint8_t* ring = sbase + warp * U::kRing;
+    __half* sQ = reinterpret_cast<__half*>(sbase + U::kQ);
+    float* sMul = reinterpret_cast<float*>(sbase + U::kMul);
+    float2* sML = reinterpret_cast<float2*>(sbase + U::kML);
     if (lane == 0) {
         for (int i = 0; i < kUnitStages; ++i) mbar_init(bars + 8 * i, 1);
         fence_mbar_init();
@@ -1003,10 +1014,10 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
     const int pos = p.positions[t], row = t, rope_exp = *p.rope_exp;
     const bool active = pos != -1;
     uint32_t e = q4_fault(p, pos, row);
-    const int n = active && !e ? pos / kPageSize + 1 : 0;  // chunks (pages)
+    const int n = active && !e ? pos / U::kPiece + 1 : 0;  // pieces
     int bad = 0;
     if (n) prefetch_rope(p, pos, threadIdx.x);
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    for (int i = threadIdx.x; i * U::kPerPage < n; i += blockDim.x) {
         const int id = page_of(p.table, p.pages, row, i);
         bad |= id < 0 || id >= p.num_pages;
     }
@@ -1020,14 +1031,14 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
         return;
     }
 
-    // this warp's chunks first, first + step, ...; the copies of the first stages
-    const int step = cs * kUnitWarps, first = warp * cs + rank;
+    // this warp's pieces first, first + step, ...; the copies of the first stages
+    const int step = cs * U::kWarps, first = warp * cs + rank;
     int issued = first;
     auto issue = [&](int st) {  // (one lane)
-        const int page = page_of(p.table, p.pages, row, issued);
-        const uint32_t bytes = min((pos - issued * kQ4Chunk) / kQ4Block + 1, kQ4Blocks) * kQ4BlockBytes;
+        const int page = page_of(p.table, p.pages, row, issued / U::kPerPage);
+        const uint32_t bytes = min((pos - issued * U::kPiece) / kQ4Block + 1, U::kBlocks) * kQ4BlockBytes;
         mbar_arrive_expect_tx(bars + 8 * st, bytes);
-        bulk_copy_g2s(smem_u32(ring) + st * kQ4ChunkBytes, p.data + q4_block(page, G, g, 0), bytes, bars + 8 * st);
+        bulk_copy_g2s(smem_u32(ring) + st * U::kPieceBytes, p.data + q4_block(page, G, g, issued % U::kPerPage * U::kPiece), bytes, bars + 8 * st);
     };
     for (int st = 0; st < kUnitStages && issued < n; ++st, issued += step)
         if (lane == 0) issue(st);
@@ -1043,7 +1054,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
         *reinterpret_cast<uint4*>(sQ + sub * kHeadDim + 64 + 8 * lj) = make_uint4(h[4], h[5], h[6], h[7]);
         if (lj == 0) sMul[sub] = mul;
     }
-    const bool owner = first < n && (n - 1 - first) % step == 0;  // this warp has the last chunk
+    const bool owner = first < n && (n - 1 - first) % step == 0;  // this warp has the last piece
     float xn[16];      // lanes of sub 0 and 1: the new k, of 2 and 3: v
     uint32_t bits[8];  // the same as bf16
     if (owner) {
@@ -1067,15 +1078,15 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
             ok = false;
             break;
         }
-        uint8_t* sb = ring + st * kQ4ChunkBytes;
-        if (j == n - 1) {  // the new position into the staged chunk (sub 0, 2) and into the pool (1, 3)
+        uint8_t* sb = ring + st * U::kPieceBytes;
+        if (j == n - 1) {  // the new position into the staged piece (sub 0, 2) and into the pool (1, 3)
             const int s = pos % kPageSize;
-            uint8_t* pool = p.data + q4_block(page_of(p.table, p.pages, row, j), G, g, s);
-            q4_store((sub & 1) ? pool : sb + s / kQ4Block * kQ4BlockBytes, sub >= 2, s % kQ4Block, xn, bits,
+            uint8_t* pool = p.data + q4_block(page_of(p.table, p.pages, row, j / U::kPerPage), G, g, s);
+            q4_store((sub & 1) ? pool : sb + s % U::kPiece / kQ4Block * kQ4BlockBytes, sub >= 2, s % kQ4Block, xn, bits,
                      sub < 2 ? p.k_inv6 : p.v_inv6, sub < 2 ? p.k_inv : p.v_inv, lj, true);
             __syncwarp();
         }
-        S.chunk(L, sb, pos + 1 - j * kQ4Chunk);
+        S.chunk<U::kBlocks>(L, sb, pos + 1 - j * U::kPiece);
         __syncwarp();
         if (issued < n) {
             if (lane == 0) issue(st);
@@ -1113,18 +1124,18 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
     const int h = warp;
     float M = -CUDART_INF_F, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     float4* joined = reinterpret_cast<float4*>(sbase + 4 * (h * kHeadDim + 4 * lane));  // warp 0's part, of this warp's head
-    if (rank < n) {  // (warp w has a part if chunk w cs + rank is there)
-        float2 ml[kUnitWarps];
+    if (h < kGroup && rank < n) {  // (warp w has a part if piece w cs + rank is there)
+        float2 ml[U::kWarps];
 #pragma unroll
-        for (int w = 0; w < kUnitWarps; ++w) {
+        for (int w = 0; w < U::kWarps; ++w) {
             ml[w] = w * cs + rank < n ? sML[w * kGroup + h] : make_float2(-CUDART_INF_F, 0.f);
             M = fmaxf(M, ml[w].x);
         }
 #pragma unroll
-        for (int w = 0; w < kUnitWarps; ++w) {
+        for (int w = 0; w < U::kWarps; ++w) {
             if (w * cs + rank >= n) break;
             const float f = exp2f(ml[w].x - M);  // (NaN sums: M is theirs or above; f * NaN or NaN)
-            const float4 x = joined[w * (kUnitStages * kQ4ChunkBytes / 16)];
+            const float4 x = joined[w * (U::kRing / 16)];
             sum += f * ml[w].y;
             acc[0] += f * x.x;
             acc[1] += f * x.y;
@@ -1134,13 +1145,15 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
     }
     if (cs > 1) {
         __syncwarp();  // every lane has read the warps' maxima and sums of this head
-        *joined = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        if (lane == 0) sML[h] = make_float2(M, sum);
+        if (h < kGroup) {
+            *joined = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (lane == 0) sML[h] = make_float2(M, sum);
+        }
         cluster_sync();
-        if (rank == 0) {
+        if (h < kGroup && rank == 0) {
             const int parts = min(n, cs);  // the CTAs that have one, its maximum and sum a lane
             float2 ml = make_float2(-CUDART_INF_F, 0.f);
-            if (lane < parts) ml = ld_cluster_f32x2(cluster_map(base + Q4UnitSmem::kML + 8 * h, lane));
+            if (lane < parts) ml = ld_cluster_f32x2(cluster_map(base + U::kML + 8 * h, lane));
             M = ml.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
@@ -1168,7 +1181,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps) q4_unit_kernel(Q4AppendParams
             }
         }
     }
-    if (rank == 0) {
+    if (h < kGroup && rank == 0) {
         const float inv = v_scale / sum;
         const float y[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
         *reinterpret_cast<uint2*>(p.out + ((int64_t)t * p.heads + g * kGroup + h) * kHeadDim + 4 * lane) = pack4(y);
@@ -1197,77 +1210,108 @@ Q4Plan make_q4_plan(const pkv_pool* pool, int rows)
     return pl;
 }
 
-// The CTAs that each unit gets in q4_unit_kernel, or 0: the call goes through the split
-// attention.  A unit gets as many CTAs (a power of two, up to a cluster's 16) as leave about
-// one an SM, and no more than its pages can use.  A CTA's life is about 6 us and 1 to 1.6 us
-// for every further page of its warps; the split attention costs 9 us and the time of its
-// bytes, and more where few units are cut into many pieces.  They meet at 30 to 50 pages an
-// SM in all, and with more than a few short units an SM.  Measured (us, units against split,
-// 8 kv heads): 1 row of 700 6.1 / 9.1, of 16000 12.3 / 18.1, of 36000 20.5 / 22.9, of 64000
-// 33.4 / 27.8; 2 rows of 16000 17.7 / 18.6; 4 of 8000 14.5 / 17.5, of 16000 24.6 / 24.1; 8 of 1000
-// 7.9 / 11.5, of 8000 24.8 / 23.6; 16 of 500-1500 11.1 / 14.6, of 4500 25.8 / 24.6; 64 of 1-640 14.1 /
-// 16.7; 128 of 1-256 16.2 / 15.8; one kv head, 1 row of 32000 14.5 / 21.5.  The rows' lengths are
-// not known here: `pages`, the table's width, stands for the longest.  A grid size set by
-// pkv_set_ctas is the split attention's.
-static int q4_unit_ctas(const pkv_pool* pool, int rows, int pages)
+using Q4UnitHalf = Q4Unit<2>;
+using Q4UnitPage = Q4Unit<4>;
+
+// f(kernel, threads, shared memory) of a form.
+template <class F>
+static cudaError_t with_unit_kernel(bool whole_pages, bool full, F f)
 {
-    if (pool->ctas_override > 0) return 0;
-    const int64_t units = (int64_t)rows * pool->cfg.kv_heads, sms = pool->num_sms;
-    if (units > 4 * sms || units * pages > 40 * sms) return 0;
-    int cs = 1;
-    while (cs < pool->q4_cluster && 3 * units * 2 * cs <= 4 * sms && cs * kUnitWarps < pages) cs *= 2;
-    return cs;
+    if (whole_pages)
+        return f(full ? q4_unit_kernel<Q4UnitPage, true> : q4_unit_kernel<Q4UnitPage, false>, 32 * Q4UnitPage::kWarps,
+                 Q4UnitPage::kAlloc);
+    return f(full ? q4_unit_kernel<Q4UnitHalf, true> : q4_unit_kernel<Q4UnitHalf, false>, 32 * Q4UnitHalf::kWarps,
+             Q4UnitHalf::kAlloc);
 }
+
+static bool full_rotation(const pkv_pool* pool) { return pool->cfg.rotary_dim <= 0 || pool->cfg.rotary_dim == kHeadDim; }
 
 cudaError_t configure_q4(pkv_pool* pool)
 {
-    cudaError_t rc;
-    if ((rc = cudaFuncSetAttribute(q4_unit_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4UnitSmem::kAlloc)) != cudaSuccess ||
-        (rc = cudaFuncSetAttribute(q4_unit_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4UnitSmem::kAlloc)) != cudaSuccess)
-        return rc;
-    if ((rc = cudaFuncSetAttribute(q4_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4Smem::kAlloc)) != cudaSuccess)
-        return rc;
-    // clusters of 16 are beyond what every device holds: asked for here
-    for (auto kernel : {q4_unit_kernel<true>, q4_unit_kernel<false>}) {
-        if ((rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return rc;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 16;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(16);
-        cfg.blockDim = dim3(32 * kUnitWarps);
-        cfg.dynamicSmemBytes = Q4UnitSmem::kAlloc;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            clusters = 0;
-        }
-        pool->q4_cluster = clusters > 0 ? 16 : 8;
-        if (clusters <= 0) break;
-    }
-    return cudaSuccess;
+    cudaError_t rc = cudaFuncSetAttribute(q4_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4Smem::kAlloc);
+    for (int whole = 0; whole < 2 && rc == cudaSuccess; ++whole)
+        rc = with_unit_kernel(whole, full_rotation(pool), [&](auto kernel, int threads, int smem) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            for (int k = 0; k < 5; ++k) {  // clusters of 2^k CTAs that the device holds at a time
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = 1u << k;
+                attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3(1u << k);
+                cfg.blockDim = dim3(threads);
+                cfg.dynamicSmemBytes = smem;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                if (cudaOccupancyMaxActiveClusters(&pool->q4_clusters[whole][k], kernel, &cfg) != cudaSuccess) {
+                    cudaGetLastError();  // (a size that the device does not have)
+                    pool->q4_clusters[whole][k] = 0;
+                }
+            }
+            return cudaSuccess;
+        });
+    return rc;
 }
 
-static cudaError_t launch_q4_units(const pkv_pool* pool, const Q4AppendParams& ap, int cs, cudaStream_t s)
+// How q4_unit_kernel takes a call: its form and the CTAs (2^k, a cluster) of each unit; cs 0: the call goes through the
+// split attention.
+struct Q4UnitChoice {
+    bool whole_pages;
+    int cs;
+};
+
+// The kernel's life is 4.5 to 5.5 us, 0.6 us more in a cluster, and 1.3 to 1.8 us for every further round of its warps'
+// pieces; the split attention's is 8 to 11 us and the time of its bytes, and more where few units are cut into many
+// pieces.  Measured (us; half pages / whole pages, CTAs a unit in brackets / split; 8 kv heads unless named):
+//   rows that one CTA takes in one round: 8 of 1-128 5.1 / 5.8 / 9.3, 8 of 400 6.2 / 5.6 / 10.9, 16 of 100-300 6.2 / 5.6 / 11.1
+//   in one round of a cluster, about one CTA an SM: 1 of 700 5.9 [4] / 6.6 [2] / 9.1, 24 of 1-640 (2 heads) 6.5 [4] /
+//     6.8 [2], 1 of 1500 (1 head) 5.8 [8] / 6.3 [4] / 9.1; more CTAs than that: 4 of 2000 7.5 [8] / 6.8 [4] / 12.0
+//   longer: 1 of 4000 7.1 [8] / 6.7 [8] / 11.5, of 16000 14.1 [8] / 11.8 [8] / 18.2, of 32000 20.1 [16] / 18.9 [8] / 20.9, 2
+//     of 16000 22.9 [4] / 18.5 [4] / 18.7, 4 of 8000 14.0 [4] / 12.2 [4] / 17.6, 16 of 500-1500 10.7 / 9.4 / 14.6, of 3000
+//     18.5 / 16.4 / 20.5; clusters beyond what the device holds at a time take turns: 4 of 8000 24.1 [8]
+//   more units than SMs: 32 of 500-1500 15.0 / 17.4 / 18.0, 64 of 1-640 15.5 / 21.6 / 16.8
+// The rows' lengths are not known here: `pages`, the table's width, stands for the longest.  A grid size set by
+// pkv_set_ctas is the split attention's.
+static Q4UnitChoice q4_unit_choice(const pkv_pool* pool, int rows, int64_t pages)
 {
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cs;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(ap.tokens * ap.kv_heads * cs));
-    cfg.blockDim = dim3(32 * kUnitWarps);
-    cfg.dynamicSmemBytes = Q4UnitSmem::kAlloc;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, ap.rot == kHeadDim ? q4_unit_kernel<true> : q4_unit_kernel<false>, ap, pool->v_scale,
-                              pool->wait_ns, cs);
+    constexpr int kWarps = Q4UnitPage::kWarps, kRounds = 10, kRoundsInTurn = 6;
+    const int64_t units = (int64_t)rows * pool->cfg.kv_heads, sms = pool->num_sms;
+    const int *half = pool->q4_clusters[0], *whole = pool->q4_clusters[1];
+    if (pool->ctas_override > 0 || units > 4 * sms) return {false, 0};
+    if (units <= whole[0]) {
+        if (2 * pages <= kWarps) return {false, 1};
+        if (pages <= kWarps) return {true, 1};
+        int k = 1;
+        while (k < 3 && (kWarps << k) < 2 * pages) ++k;
+        if ((kWarps << k) >= 2 * pages && units <= half[k] && 3 * (units << k) <= 4 * sms) return {false, 1 << k};
+        k = 0;
+        while (k < 4 && units <= whole[k + 1] && (kWarps << k) < pages) ++k;
+        return {true, pages <= (kRounds * kWarps) << k ? 1 << k : 0};
+    }
+    const int64_t turns = half[0] > 0 ? (units + half[0] - 1) / half[0] : kRoundsInTurn + 1;
+    return {false, turns * ((2 * pages + kWarps - 1) / kWarps) <= kRoundsInTurn ? 1 : 0};
+}
+
+static cudaError_t launch_q4_units(const pkv_pool* pool, const Q4AppendParams& ap, Q4UnitChoice c, cudaStream_t s)
+{
+    return with_unit_kernel(c.whole_pages, full_rotation(pool), [&](auto kernel, int threads, int smem) {
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)c.cs;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(ap.tokens * ap.kv_heads * c.cs));
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, kernel, ap, pool->v_scale, pool->wait_ns, c.cs);
+    });
 }
 
 cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& plan, cudaStream_t s)
@@ -1289,9 +1333,9 @@ cudaError_t launch_q4_decode(pkv_pool* pool, const StepArgs& a, const Q4Plan& pl
     cudaError_t rc;
     const bool timed = pool->timer_on != 0;
     const int slot = timed ? (int)(pool->timer_count.fetch_add(1) % kTimerSlots) : 0;
-    if (const int cs = q4_unit_ctas(pool, a.rows, a.pages)) {
+    if (const Q4UnitChoice c = q4_unit_choice(pool, a.rows, a.pages); c.cs) {
         if (timed && (rc = cudaEventRecord(pool->ev_start[slot], s)) != cudaSuccess) return rc;
-        if ((rc = launch_q4_units(pool, ap, cs, s)) != cudaSuccess) return rc;
+        if ((rc = launch_q4_units(pool, ap, c, s)) != cudaSuccess) return rc;
         return timed ? cudaEventRecord(pool->ev_stop[slot], s) : cudaSuccess;
     }
     const int items = (ap.kv_heads + 3) / 4 + ap.kv_heads;

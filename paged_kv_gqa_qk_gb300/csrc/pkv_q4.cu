@@ -1271,12 +1271,14 @@ struct Q4UnitChoice {
 //   longer: 1 of 4000 7.1 [8] / 6.7 [8] / 11.5, of 16000 14.1 [8] / 11.8 [8] / 18.2, of 32000 20.1 [16] / 18.9 [8] / 20.9, 2
 //     of 16000 22.9 [4] / 18.5 [4] / 18.7, 4 of 8000 14.0 [4] / 12.2 [4] / 17.6, 16 of 500-1500 10.7 / 9.4 / 14.6, of 3000
 //     18.5 / 16.4 / 20.5; clusters beyond what the device holds at a time take turns: 4 of 8000 24.1 [8]
+//   longest: 1 of 40000 23.0 [8] / 23.3, of 60000 32.2 [8] / 26.8, 8 of 10000 24.6 / 26.0, 16 of 200-5000 22.4 / 22.5; in
+//     clusters of 16 (1 head) 1 of 80000 22.3 / 39.6, of 130000 33.2 / 55.9, of 300000 71.3 / 60.1
 //   more units than SMs: 32 of 500-1500 15.0 / 17.4 / 18.0, 64 of 1-640 15.5 / 21.6 / 16.8
 // The rows' lengths are not known here: `pages`, the table's width, stands for the longest.  A grid size set by
 // pkv_set_ctas is the split attention's.
 static Q4UnitChoice q4_unit_choice(const pkv_pool* pool, int rows, int64_t pages)
 {
-    constexpr int kWarps = Q4UnitPage::kWarps, kRounds = 10, kRoundsInTurn = 6;
+    constexpr int kWarps = Q4UnitPage::kWarps, kRounds = 10, kRoundsOf16 = 16, kRoundsInTurn = 6;
     const int64_t units = (int64_t)rows * pool->cfg.kv_heads, sms = pool->num_sms;
     const int *half = pool->q4_clusters[0], *whole = pool->q4_clusters[1];
     if (pool->ctas_override > 0 || units > 4 * sms) return {false, 0};
@@ -1288,7 +1290,7 @@ static Q4UnitChoice q4_unit_choice(const pkv_pool* pool, int rows, int64_t pages
         if ((kWarps << k) >= 2 * pages && units <= half[k] && 3 * (units << k) <= 4 * sms) return {false, 1 << k};
         k = 0;
         while (k < 4 && units <= whole[k + 1] && (kWarps << k) < pages) ++k;
-        return {true, pages <= (kRounds * kWarps) << k ? 1 << k : 0};
+        return {true, pages <= ((k < 4 ? kRounds : kRoundsOf16) * kWarps) << k ? 1 << k : 0};
     }
     const int64_t turns = half[0] > 0 ? (units + half[0] - 1) / half[0] : kRoundsInTurn + 1;
     return {false, turns * ((2 * pages + kWarps - 1) / kWarps) <= kRoundsInTurn ? 1 : 0};

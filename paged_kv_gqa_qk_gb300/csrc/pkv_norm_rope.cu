@@ -34,7 +34,11 @@ struct NormRopeParams {
 //
 // One CTA per token; warp w of W takes the groups w, w + W, ... of 4 heads (q's, then k's),
 // the next group's loads out before one is computed.
-template <bool kInterleaved, bool kF32, bool kFullRot>
+//
+// kRot: the rotated dims in the half layout, whose pairs lie differently for each of the four
+// that a pool can have (one form for all of them took 47 us for 8192 tokens to fp32, and 4.1
+// instead of 2.7 for 300, with its selects).  Interleaved pairs are alike for every p.rot.
+template <bool kInterleaved, bool kF32, int kRot>
 __global__ void __launch_bounds__(512) norm_rope_kernel(NormRopeParams p)
 {
     const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -56,21 +60,19 @@ __global__ void __launch_bounds__(512) norm_rope_kernel(NormRopeParams p)
     const bool ok = pos >= 0 && pos < p.max_seq;
     if (!ok && pos != -1 && threadIdx.x == 0) atomicOr(p.err, PKV_DEVERR_POSITION);
 
-    // (cos, sin) of the lane's dims; part[m]: where their partners are (half layout)
-    float2 cs[4][4];
-    int part[4];
-    float sgn[4];
+    // (cos, sin) of the lane's dims 32 m + 4 j .. + 3, or of those that share their pairs: half layout, the sets are m = 0
+    // (32 and 64 rotated dims), 0 and 1 (128), 0, 1 and 2 (96)
+    constexpr int kSets = kInterleaved ? 4 : kRot == 128 ? 2 : kRot == 96 ? 3 : 1;
+    float2 cs[kSets][4];
+    const bool low = j < 4;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const int d = 4 * j + 32 * m, half = p.rot / 2;
-        const bool rotated = d < p.rot, first = d < half;
-        const int pd = kInterleaved ? d : (first ? d + half : d - half);
-        part[m] = pd >> 5;
-        sgn[m] = first ? -1.f : 1.f;
+    for (int m = 0; m < kSets; ++m) {
+        const int d = 4 * j + 32 * m;
 #pragma unroll
         for (int k = 0; k < 4; ++k) cs[m][k] = make_float2(1.f, 0.f);
-        if (!ok || !rotated || (kFullRot && !kInterleaved && m >= 2)) continue;
-        const float2* row = p.rope + (int64_t)pos * kRopeHalf + (kInterleaved ? d / 2 : (first ? d : pd));
+        if (!ok || (kInterleaved && d >= p.rot)) continue;
+        const bool second = !kInterleaved && kRot % 64 != 0 && d >= kRot / 2;  // of its pair: its partner's term is added
+        const float2* row = p.rope + (int64_t)pos * kRopeHalf + (kInterleaved ? d / 2 : second ? d - kRot / 2 : d);
         const float4 a = *reinterpret_cast<const float4*>(row);
         if constexpr (kInterleaved) {
             cs[m][0] = cs[m][1] = make_float2(a.x, a.y);
@@ -79,9 +81,11 @@ __global__ void __launch_bounds__(512) norm_rope_kernel(NormRopeParams p)
             const float4 b = *reinterpret_cast<const float4*>(row + 2);
             cs[m][0] = make_float2(a.x, a.y), cs[m][1] = make_float2(a.z, a.w);
             cs[m][2] = make_float2(b.x, b.y), cs[m][3] = make_float2(b.z, b.w);
+            if (kRot % 64 != 0 && !second)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) cs[m][k].y = -cs[m][k].y;
         }
     }
-    const bool near = kInterleaved || p.rot % 64 == 0;  // partners in the lane itself
     float w[4][4];
     const __nv_bfloat16* have = nullptr;
     for (int grp = warp; grp < groups; grp += warps) {
@@ -120,25 +124,28 @@ __global__ void __launch_bounds__(512) norm_rope_kernel(NormRopeParams p)
                     y[m][k] = inv * (x[m][k] * cs[m][k].x - x[m][k + 1] * cs[m][k].y);
                     y[m][k + 1] = inv * (x[m][k + 1] * cs[m][k].x + x[m][k] * cs[m][k].y);
                 }
-        } else if constexpr (kFullRot) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    y[m][k] = inv * (x[m][k] * cs[m][k].x - x[m + 2][k] * cs[m][k].y);
-                    y[m + 2][k] = inv * (x[m + 2][k] * cs[m][k].x + x[m][k] * cs[m][k].y);
-                }
         } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float other[4];  // dims + 32m of the lane with the partners (m = 3 is never rotated)
+                if constexpr (kRot % 64 == 0) {  // partners in the lane itself
 #pragma unroll
-                for (int m = 0; m < 3; ++m) other[m] = near ? x[m][k] : __shfl_xor_sync(kFull, x[m][k], 4);
+                    for (int m = 0; m < kSets; ++m) {
+                        constexpr int kTo = kRot / 64;
+                        y[m][k] = inv * (x[m][k] * cs[m][k].x - x[m + kTo][k] * cs[m][k].y);
+                        y[m + kTo][k] = inv * (x[m + kTo][k] * cs[m][k].x + x[m][k] * cs[m][k].y);
+                    }
+                } else {  // in lane j ^ 4: of 96 dims, dims + 48 or - 48
+                    float other[kSets];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const float up = sgn[m] * (part[m] == 0 ? other[0] : part[m] == 1 ? other[1] : other[2]);
-                    y[m][k] = inv * (x[m][k] * cs[m][k].x + up * cs[m][k].y);
+                    for (int m = 0; m < kSets; ++m) other[m] = __shfl_xor_sync(kFull, x[m][k], 4);
+#pragma unroll
+                    for (int m = 0; m < kSets; ++m) {
+                        const float up = kSets == 1 ? other[0] : low ? other[(m + 1) % kSets] : other[(m + 2) % kSets];
+                        y[m][k] = inv * (x[m][k] * cs[m][k].x + up * cs[m][k].y);
+                    }
                 }
+#pragma unroll
+                for (int m = kRot / 32; m < 4; ++m) y[m][k] = inv * x[m][k];
             }
         }
         if (h >= (is_k ? p.heads[1] : p.heads[0])) continue;
@@ -187,13 +194,14 @@ cudaError_t launch_norm_rope(const pkv_pool* pool, const NormRope& a, cudaStream
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const bool full = p.rot == kHeadDim;
-    auto launch = [&](auto kernel_full, auto kernel) { return cudaLaunchKernelEx(&cfg, full ? kernel_full : kernel, p); };
-    if (a.interleaved)
-        return a.f32 ? launch(norm_rope_kernel<true, true, true>, norm_rope_kernel<true, true, true>)
-                     : launch(norm_rope_kernel<true, false, true>, norm_rope_kernel<true, false, true>);
-    return a.f32 ? launch(norm_rope_kernel<false, true, true>, norm_rope_kernel<false, true, false>)
-                 : launch(norm_rope_kernel<false, false, true>, norm_rope_kernel<false, false, false>);
+    auto launch = [&](auto to_f32, auto to_bf16) { return cudaLaunchKernelEx(&cfg, a.f32 ? to_f32 : to_bf16, p); };
+    if (a.interleaved) return launch(norm_rope_kernel<true, true, 128>, norm_rope_kernel<true, false, 128>);
+    switch (p.rot) {
+        case 32: return launch(norm_rope_kernel<false, true, 32>, norm_rope_kernel<false, false, 32>);
+        case 64: return launch(norm_rope_kernel<false, true, 64>, norm_rope_kernel<false, false, 64>);
+        case 96: return launch(norm_rope_kernel<false, true, 96>, norm_rope_kernel<false, false, 96>);
+        default: return launch(norm_rope_kernel<false, true, 128>, norm_rope_kernel<false, false, 128>);
+    }
 }
 
 }  // namespace pkv

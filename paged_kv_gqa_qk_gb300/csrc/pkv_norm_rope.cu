@@ -32,6 +32,9 @@ struct NormRopeParams {
 // heads, and the partner of a dim lies in the lane itself (interleaved pairs, and
 // halves of 128 or 64 rotated dims) or in lane j ^ 4 (32 and 96).
 //
+// Bound by memory: 8192 tokens of 40 heads to fp32, 252 MB, in 40.1 us, 6.3 TB/s; to bf16, 168 MB,
+// in 31.5, 5.3 TB/s.
+//
 // One CTA per token; warp w of W takes the groups w, w + W, ... of 4 heads (q's, then k's),
 // the next group's loads out before one is computed.
 //
@@ -86,7 +89,11 @@ __global__ void __launch_bounds__(512) norm_rope_kernel(NormRopeParams p)
                 for (int k = 0; k < 4; ++k) cs[m][k].y = -cs[m][k].y;
         }
     }
-    float w[4][4];
+    // weights as they are where the pairs take two sets of cos and sin or more: 64 registers instead of 86, and with
+    // them more warps (8192 tokens to fp32 40.8 us, 41.9 as floats); else as floats (to bf16 28.9 us, 31.0)
+    constexpr bool kPacked = kInterleaved || kRot == 128;
+    uint2 packed[kPacked ? 4 : 1];
+    float w[kPacked ? 1 : 4][4];
     const __nv_bfloat16* have = nullptr;
     for (int grp = warp; grp < groups; grp += warps) {
         const bool is_k = grp >= qg;
@@ -100,7 +107,13 @@ __global__ void __launch_bounds__(512) norm_rope_kernel(NormRopeParams p)
         if (wp) {
             if (wp != have) {
 #pragma unroll
-                for (int m = 0; m < 4; ++m) unpack4(*reinterpret_cast<const uint2*>(wp + 4 * j + 32 * m), w[m]);
+                for (int m = 0; m < 4; ++m) {
+                    const uint2 a = *reinterpret_cast<const uint2*>(wp + 4 * j + 32 * m);
+                    if constexpr (kPacked)
+                        packed[m] = a;
+                    else
+                        unpack4(a, w[m]);
+                }
                 have = wp;
             }
             float ss = 0.f;
@@ -112,9 +125,17 @@ __global__ void __launch_bounds__(512) norm_rope_kernel(NormRopeParams p)
             for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
             inv = rsqrtf(__fmaf_rn(ss, 1.0f / kHeadDim, p.eps));
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+            for (int m = 0; m < 4; ++m) {
+                float unpacked[4];
+                if constexpr (kPacked) unpack4(packed[m], unpacked);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[m][k] *= w[m][k];
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (kPacked)
+                        x[m][k] *= unpacked[k];
+                    else
+                        x[m][k] *= w[m][k];
+                }
+            }
         }
         if constexpr (kInterleaved) {
 #pragma unroll
@@ -181,10 +202,12 @@ cudaError_t launch_norm_rope(const pkv_pool* pool, const NormRope& a, cudaStream
     p.rot = pool->cfg.rotary_dim > 0 ? pool->cfg.rotary_dim : kHeadDim;
     p.eps = (float)pool->cfg.eps;
     const int groups = (p.heads[0] + 3) / 4 + (p.heads[1] + 3) / 4;
-    // few tokens: a warp a group of heads, for the latency; many: as few warps a token as leave 32 an SM,
-    // which share the loads of its tables and weights (8192 tokens of 40 heads, interleaved, fp32 out, 252 MB:
-    // 42.3 us with one warp a token, 43.0 with two, 46.5 with four; one token 2.1 us a call with ten)
-    const int warps = std::min(std::min(groups, 16), std::max(1, 32 * pool->num_sms / a.tokens));
+    // up to a token an SM: a warp a group of heads, for the latency; more: half of that, and with more tokens as few as
+    // leave 32 warps an SM, which share the loads of a token's tables and weights, but two (40 heads, 10 groups, to
+    // fp32; us with 1 / 2 / 4 / 5 / 10 warps: 300 tokens 5.2 / 3.6 / 2.9 / 2.7 / 3.2, 1000 9.4 / 6.5 / 6.0 / 6.8 / 7.7,
+    // 4000 22.4 / 20.9 / 21.4 / 22.0, 8192 40.8 / 40.1; one token 2.1 with five, 2.0 with ten)
+    const int most = std::min(groups, 16), fair = std::min((groups + 1) / 2, 32 * pool->num_sms / a.tokens);
+    const int warps = a.tokens <= pool->num_sms ? most : std::min(most, std::max(2, fair));
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -133,7 +133,7 @@ constexpr int kQ4AppendWarps = 4;
 
 // pkv_q4_append: a warp takes kQuads times 4 kv heads of one token.  Bound by its
 // instructions: about 860 a quad, half of them k's norm and rotation in pairs of floats
-// (16384 tokens of 8 heads, 86 MB: 33.9 us, 2.5 TB/s, 0.67 of the issue slots).  Resident
+// (16384 tokens of 8 heads, 86 MB: 33.9 us, 2.5 TB/s, 0.71 of the issue slots).  Resident
 // CTAs by measurement: 6 an SM of the two-quad form (5: 35.8, 8: 36.9 us), 7 of the other.
 template <bool kFullRot, int kQuads>
 __global__ void __launch_bounds__(32 * kQ4AppendWarps, !kFullRot ? 4 : kQuads == 1 ? 7 : 6) q4_append_kernel(Q4AppendParams p)
@@ -298,9 +298,9 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
     p.tokens = tokens;
     p.rows = rows;
     p.pages = pages;
-    // few tokens: 4 heads a warp, for the shorter chain (2048 tokens of 8 heads 6.7 us, 7.4 with 8 heads a warp);
-    // many: 8, which share the token's address arithmetic (16384 tokens 37.4 us with 4, 33.9 with 8)
-    const int quads = (p.kv_heads + 3) / 4, per = quads > 1 && (int64_t)tokens * quads >= 64 * (int64_t)pool->num_sms ? 2 : 1;
+    // few tokens: 4 heads a warp, for the shorter chain; many: 8, which share the token's address arithmetic (8 heads, us
+    // with 4 / 8: 77 tokens 2.5 / 3.5, 2048 5.8 / 6.2, 3000 8.1 / 7.3, 16384 38.8 / 34.2)
+    const int quads = (p.kv_heads + 3) / 4, per = quads > 1 && (int64_t)tokens * quads >= 32 * (int64_t)pool->num_sms ? 2 : 1;
     const int64_t items = (int64_t)tokens * ((quads + per - 1) / per);
     const unsigned grid = (unsigned)((items + kQ4AppendWarps - 1) / kQ4AppendWarps);
     const bool full = p.rot == kHeadDim;
@@ -1505,8 +1505,9 @@ cudaError_t launch_q4_read(const pkv_pool* pool, const int32_t* positions, const
     p.kv_heads = pool->cfg.kv_heads;
     p.k_scale = pool->k_scale;
     p.v_scale = pool->v_scale;
-    // few tokens: 4 heads a warp, for the shorter chain; from about two warps a scheduler on, 8
-    const int quads = (p.kv_heads + 3) / 4, per = quads > 1 && (int64_t)tokens * quads >= 16 * (int64_t)pool->num_sms ? 2 : 1;
+    // few tokens: 4 heads a warp, for the shorter chain; many: 8 (8 heads, us with 4 / 8: 77 tokens 1.7 / 2.0, 2048
+    // 2.9 / 3.0, 4096 4.7 / 4.3, 16384 17.2 / 16.3)
+    const int quads = (p.kv_heads + 3) / 4, per = quads > 1 && (int64_t)tokens * quads >= 32 * (int64_t)pool->num_sms ? 2 : 1;
     const int64_t items = (int64_t)tokens * ((quads + per - 1) / per);
     const unsigned grid = (unsigned)((items + kQ4ReadWarps - 1) / kQ4ReadWarps);
     return launch_dependent(per == 1 ? q4_read_kernel<1> : q4_read_kernel<2>, grid, 32 * kQ4ReadWarps, 0, s, p);

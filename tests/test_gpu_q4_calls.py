@@ -1,6 +1,7 @@
 """Calls over a 4-bit pool and of norm + rotation: both ways of the binding, what they refuse, the split attention
 in graphs and behind 32-bit offsets, and the entries of the other pool format."""
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -327,6 +328,36 @@ def test_split_attention_beyond_32_bit_offsets():
     ref, bound, after = reference(wl, cache)
     check(out, ref, bound)
     assert np.array_equal(data[n - P:].cpu().numpy(), after.data) and not data[:8].any()
+    pool.close()
+
+
+@pytest.mark.parametrize("ctas", [0, 152])
+def test_host_threads_on_their_own_streams(ctas):
+    """Four threads of the host, a stream each, over one pool: every call of each gives the same bits."""
+    wl, cache = make([400, 90, 1, 777], 2)
+    pool = pool_of(wl, cache, ctas)
+    args = inputs(wl)
+    ref = pool.decode(*args)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                outs = [pool.decode(*args) for _ in range(25)]
+                kv = [pool.read(args[5], None, args[6])[0] for _ in range(5)]
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(o, ref) for o in outs) or not all(torch.equal(x, kv[0]) for x in kv):
+                    bad.append("different")
+        except Exception as e:
+            bad.append(e)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and pool.check_errors() == 0
     pool.close()
 
 

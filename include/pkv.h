@@ -457,7 +457,8 @@ PKV_API int pkv_q4_read(pkv_pool* pool, const int32_t* positions, const int32_t*
 /* decode_paged over a 4-bit pool: pkv_decode's steps, with k and v quantised as they are
  * appended and the attention over the values the pool holds (the new position's own
  * quantised values included).  Arguments, skipped rows and error bits as pkv_decode, out
- * 16-byte aligned; as there, slots must be distinct and a row's new slot must not be read by
+ * 16-byte aligned; queries and softmax weights are kept to 22 bits, sums are fp32, the output is rounded once
+ * to bf16.  As there, slots must be distinct and a row's new slot must not be read by
  * another row of the call (PKV_CHECK=1 checks both).  Results are the same from run to run.
  * Small calls run in one launch, larger ones in three (their results differ by rounding
  * only); a grid size set by pkv_set_ctas, up to 4096 CTAs, always takes the latter. */

@@ -63,7 +63,7 @@ struct Q4AppendParams {
     const float2* rope_hi;
     const float2* rope_lo;
     uint8_t* data;
-    __half* q_hat;              // decode: [tokens][heads][128], each head times a power of two
+    __half* q_hat;              // decode: [tokens][kv_heads][8][128]: 4 heads, each times a power of two, and their remainders
     float* q_mul;               // decode: [tokens][heads], what a score of it is multiplied with
     __nv_bfloat16* out;         // decode: [tokens][heads][128], zeroed for skipped tokens
     int32_t* tok_len;           // decode: [tokens], 0: skip
@@ -167,11 +167,21 @@ __global__ void __launch_bounds__(32 * kQ4AppendWarps, !kFullRot ? 4 : kQuads ==
         q4_append_heads<kFullRot>(p, kraw[q], vraw[q], wk, rope_exp, g0 + 4 * q, g0 + 4 * q < p.kv_heads, page, pos, lane);
 }
 
-// A query head over 8 lanes as fp16, times the power of two that brings its largest
-// value into [1, 2), so that fp16 keeps 11 bits of it whatever its size.  Returns what
-// a score of it is multiplied with: never 0, which would make a masked score NaN (below
-// 1e-30 the scores are 0 either way).
-__device__ __forceinline__ float q4_query(const float (&y)[16], float k_scale, uint32_t (&r)[8])
+// Two floats as fp16, and the fp16 of what that leaves of them (lo).
+__device__ __forceinline__ __half2 split_half2(float x, float y, uint32_t& lo)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(__fsub_rn(x, f.x), __fsub_rn(y, f.y));
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+    return h;
+}
+
+// A query head over 8 lanes as an fp16 head (r) and the fp16 of its remainder (rl), times the
+// power of two that brings its largest value into [1, 2): 22 bits of it, or 2^-25 of the
+// largest value, whatever its size.  Returns what a score of it is multiplied with: never
+// 0, which would make a masked score NaN (below 1e-30 the scores are 0 either way).
+__device__ __forceinline__ float q4_query(const float (&y)[16], float k_scale, uint32_t (&r)[8], uint32_t (&rl)[8])
 {
     float top = 0.f;
 #pragma unroll
@@ -182,10 +192,22 @@ __device__ __forceinline__ float q4_query(const float (&y)[16], float k_scale, u
     const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const __half2 h = __floats2half2_rn(y[2 * k] * down, y[2 * k + 1] * down);
+        const __half2 h = split_half2(y[2 * k] * down, y[2 * k + 1] * down, rl[k]);
         r[k] = *reinterpret_cast<const uint32_t*>(&h);
     }
     return fmaxf(__uint_as_float((uint32_t)ex << 23) * kQScale * k_scale, 1e-30f);
+}
+
+// The 8 columns of a (token, kv head) in the score product: its 4 query heads and, 4 columns
+// on, their remainders.  head: of this lane's head; lane j of 8.
+constexpr int kQ4Columns = 2 * kGroup;
+__device__ __forceinline__ void store_query(__half* head, int j, const uint32_t (&r)[8], const uint32_t (&rl)[8])
+{
+    __half* rest = head + kGroup * kHeadDim;
+    *reinterpret_cast<uint4*>(head + 8 * j) = make_uint4(r[0], r[1], r[2], r[3]);
+    *reinterpret_cast<uint4*>(head + 64 + 8 * j) = make_uint4(r[4], r[5], r[6], r[7]);
+    *reinterpret_cast<uint4*>(rest + 8 * j) = make_uint4(rl[0], rl[1], rl[2], rl[3]);
+    *reinterpret_cast<uint4*>(rest + 64 + 8 * j) = make_uint4(rl[4], rl[5], rl[6], rl[7]);
 }
 
 // In front of the attention: one CTA per row checks every page that the row will read,
@@ -250,14 +272,13 @@ __global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
             continue;
         }
         float x[16], y[16];
-        uint32_t r[8];
+        uint32_t r[8], rl[8];
         unpack16(a[0], a[1], x);
         norm_rope_q16<kFullRot>(x, w, p.rope_hi + (int64_t)pos * kRopeHalf, p.eps, lane, p.rot, y);
-        const float mul = q4_query(y, p.k_scale, r);
-        const int64_t head = (int64_t)t * p.heads + 4 * (item - quads) + sub;
-        *reinterpret_cast<uint4*>(p.q_hat + head * kHeadDim + 8 * j) = make_uint4(r[0], r[1], r[2], r[3]);
-        *reinterpret_cast<uint4*>(p.q_hat + head * kHeadDim + 64 + 8 * j) = make_uint4(r[4], r[5], r[6], r[7]);
-        if (j == 0) p.q_mul[head] = mul;
+        const float mul = q4_query(y, p.k_scale, r, rl);
+        const int64_t u = (int64_t)t * p.kv_heads + (item - quads);
+        store_query(p.q_hat + (u * kQ4Columns + sub) * kHeadDim, j, r, rl);
+        if (j == 0) p.q_mul[u * kGroup + sub] = mul;
     }
 }
 
@@ -331,11 +352,13 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
 //
 // Per 16 positions (a block), with lane = 4 r + c:
 //   S[16 pos][8] = K[16][128] q[128][8], m16n8k16 fp16: column h = query head h of the
-//     group (columns 4-7 are zero), row i = position pi(i), row i + 8 = pi(i) + 8,
-//     pi(2c + b) = (c ^ b) + 4b.  Lane (r, c) holds dims 32c..32c+31 of rows r and r + 8:
+//     group in fp16, column h + 4 = the fp16 of its remainder (S = column h + column h + 4: 22
+//     bits of q), row i = position pi(i), row i + 8 = pi(i) + 8, pi(2c + b) = (c ^ b) + 4b.  Lane (r, c) holds dims 32c..32c+31 of rows r and r + 8:
 //     one 16-byte read of codes each, two scales each.
 //   O^T[128][8] += V^T[128][16 pos] P[16][8]: lane (r, c) holds dims 16r..16r+15 (one
 //     group) of positions pi(2c), pi(2c + 1) and the same + 8: four 8-byte reads, four scales.
+//     P as S: columns h its head's fp16, h + 4 the remainders', added at the segment's end; a weight is kept to
+//     2^-22 of itself or 2^-32 of the largest, as good as the fp32 it was computed in.
 // The codes become fp16 by the conversion instruction and are multiplied by their
 // scales as fp16 pairs, exactly; V's are first regrouped so that one byte holds a
 // dim's codes of two positions.  P is turned between the fragments by movmatrix.
@@ -354,7 +377,8 @@ constexpr int kQ4Stages = 2;
 constexpr int kQ4Chunk = 64;                         // positions: a page
 constexpr int kQ4Blocks = kQ4Chunk / kQ4Block;
 constexpr int kQ4ChunkBytes = kQ4Blocks * kQ4BlockBytes;
-constexpr float kQ4Slack = 8.f;                      // base-2 exponent that a weight may reach (q4_attn_kernel)
+constexpr float kQ4Lift = 7.f;                       // base-2 exponent of the largest weight when it is set (Q4State)
+constexpr float kQ4Most = 15.f;                      // that a weight may reach: 2^15 is within fp16
 
 struct Q4AttnParams {
     const __half* q_hat;
@@ -484,6 +508,7 @@ __device__ __forceinline__ float ex2(float x)
 // What a lane keeps of its place in the fragments (lane = 4 r + c).
 struct Q4Lane {
     int r, c;
+    bool up;          // c >= 2: the lane has the remainders' columns, and the softmax of rows r + 8 (else of rows r)
     int pi_r;         // position of row r
     int pi_0, pi_1;   // positions of k = 2c, 2c + 1
     uint32_t koff, voff0, voff1, soff;
@@ -491,6 +516,7 @@ struct Q4Lane {
     {
         r = lane >> 2;
         c = lane & 3;
+        up = c >= 2;
         pi_r = ((r >> 1) ^ (r & 1)) | ((r & 1) << 2);
         pi_0 = c;
         pi_1 = (c ^ 1) | 4;
@@ -501,22 +527,22 @@ struct Q4Lane {
     }
 };
 
-// A warp's attention of one (token, kv head) over some of its chunks.
+// A warp's attention of one (token, kv head) over some of its chunks.  Lanes c and c + 2 hold the heads
+// 2 (c & 1) and 2 (c & 1) + 1, A and B: lane c the products with the fp16 heads of the queries or weights,
+// lane c + 2 those with the remainders.
 struct Q4State {
     uint32_t bq[8][2];   // the queries' fragments
-    float mulA, mulB;    // what scores of heads 2c and 2c + 1 are multiplied with (c < 2)
-    float o[9][4];       // o[k][0], [2]: dims 16r + 2k, + 1 of head 2c; [1], [3] of head 2c + 1; not normalised;
+    float mulA, mulB;    // what scores of heads A and B are multiplied with
+    float o[9][4];       // o[k][0], [2]: dims 16r + 2k, + 1 of head A; [1], [3] of head B; not normalised;
                          // o[8]: the weights' sums (the product with ones), in every row
-    float mA, mB;        // running maximum
+    float mA, mB;        // weights are 2^(score - m)
 
-    // q_hat: 4 heads of 128 fp16; q_mul: their multipliers
+    // q_hat: 8 columns of 128 fp16; q_mul: the 4 heads' multipliers
     __device__ __forceinline__ void open(const Q4Lane& L, const __half* q_hat, const float* q_mul)
     {
-        uint4 x[4] = {};
-        if (L.r < kGroup) {
+        uint4 x[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = reinterpret_cast<const uint4*>(q_hat + L.r * kHeadDim + 32 * L.c)[k];
-        }
+        for (int k = 0; k < 4; ++k) x[k] = reinterpret_cast<const uint4*>(q_hat + L.r * kHeadDim + 32 * L.c)[k];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             bq[2 * k][0] = x[k].x;
@@ -524,15 +550,28 @@ struct Q4State {
             bq[2 * k + 1][0] = x[k].z;
             bq[2 * k + 1][1] = x[k].w;
         }
-        mulA = mulB = 1.f;
-        if (L.c < 2) {
-            const float2 mul = *reinterpret_cast<const float2*>(q_mul + 2 * L.c);
-            mulA = mul.x;
-            mulB = mul.y;
-        }
+        const float2 mul = *reinterpret_cast<const float2*>(q_mul + 2 * (L.c & 1));
+        mulA = mul.x;
+        mulB = mul.y;
 #pragma unroll
         for (int k = 0; k < 9; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
         mA = mB = -CUDART_INF_F;
+    }
+
+    // The end of a segment: the products with heads and remainders added.  y[k][0], [1]: dims d + 2k, + 1 of head A;
+    // [2], [3] of head B, with d = 16r, + 8 in the lanes c >= 2; LA, LB: the weights' sums.
+    __device__ __forceinline__ void close(const Q4Lane& L, float (&y)[4][4], float& LA, float& LB) const
+    {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int f = 2 * (e & 1) + (e >> 1);
+                const float mine = L.up ? o[4 + k][f] : o[k][f], other = L.up ? o[k][f] : o[4 + k][f];
+                y[k][e] = __fadd_rn(mine, __shfl_xor_sync(kFull, other, 2));
+            }
+        LA = __fadd_rn(o[8][0], __shfl_xor_sync(kFull, o[8][0], 2));
+        LB = __fadd_rn(o[8][1], __shfl_xor_sync(kFull, o[8][1], 2));
     }
 
     // One chunk of kBlocks blocks in shared memory at sb, of which the unit has `left` positions (as many or more: all).
@@ -565,7 +604,16 @@ struct Q4State {
             }
         }
 
-        // ---- softmax, base 2: s[b][0], [1]: heads 2c, 2c + 1 at position L.pi_r of block b; [2], [3]: at L.pi_r + 8
+        // ---- softmax, base 2.  s[b][0], [1]: heads A and B at position L.pi_r of block b, [2], [3]: at L.pi_r + 8; lanes
+        // c >= 2 have the remainders' share of the same.  The two lanes of a pair add up, one row each: t[b][0], [1].
+        float t[kBlocks][2];
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float mine = L.up ? s[b][2 + e] : s[b][e], other = L.up ? s[b][e] : s[b][2 + e];
+                t[b][e] = __fadd_rn(mine, __shfl_xor_sync(kFull, other, 2));
+            }
         // Positions past the row's end: scores of -inf, and V scales of 0 (the codes are finite
         // whatever lies there), in a row's last chunk only.
         uint32_t vmask[kBlocks];
@@ -575,30 +623,30 @@ struct Q4State {
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
                 const int at = left - kQ4Block * b;
-                if (L.pi_r >= at) s[b][0] = s[b][1] = -CUDART_INF_F;
-                if (L.pi_r + 8 >= at) s[b][2] = s[b][3] = -CUDART_INF_F;
+                if (L.pi_r + (L.up ? 8 : 0) >= at) t[b][0] = t[b][1] = -CUDART_INF_F;
                 vmask[b] = (L.pi_0 < at ? 0xffu : 0u) | (L.pi_1 < at ? 0xff00u : 0u) | (L.pi_0 + 8 < at ? 0xff0000u : 0u) |
                            (L.pi_1 + 8 < at ? 0xff000000u : 0u);
             }
         }
-        float nA = fmaxf(s[0][0], s[0][2]), nB = fmaxf(s[0][1], s[0][3]);
+        float nA = t[0][0], nB = t[0][1];
 #pragma unroll
         for (int b = 1; b < kBlocks; ++b) {
-            nA = fmaxf(nA, fmaxf(s[b][0], s[b][2]));
-            nB = fmaxf(nB, fmaxf(s[b][1], s[b][3]));
+            nA = fmaxf(nA, t[b][0]);
+            nB = fmaxf(nB, t[b][1]);
         }
         nA *= mulA;
         nB *= mulB;
-        // the running maximum follows only when a lane's passes it by more than kQ4Slack: weights stay below
-        // 2^kQ4Slack, well inside fp16, and most chunks need no maximum over the lanes and rescale nothing
-        if (__any_sync(kFull, nA > mA + kQ4Slack || nB > mB + kQ4Slack)) {
+        // m lies kQ4Lift below the largest score it was set at, and follows only when a lane's passes it by more than
+        // kQ4Most: weights stay below 2^kQ4Most, inside fp16, and most chunks need no maximum over the lanes and
+        // rescale nothing
+        if (__any_sync(kFull, nA > mA + kQ4Most || nB > mB + kQ4Most)) {
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
+            for (int d = 2; d < 32; d <<= 1) {
                 nA = fmaxf(nA, __shfl_xor_sync(kFull, nA, d));
                 nB = fmaxf(nB, __shfl_xor_sync(kFull, nB, d));
             }
-            nA = fmaxf(nA, mA);
-            nB = fmaxf(nB, mB);
+            nA = fmaxf(nA - kQ4Lift, mA);
+            nB = fmaxf(nB - kQ4Lift, mB);
             // (a maximum still at -inf -- scores that are all NaN -- leaves nothing to rescale)
             const float aA = nA == -CUDART_INF_F ? 1.f : ex2(mA - nA), aB = nB == -CUDART_INF_F ? 1.f : ex2(mB - nB);
             mA = nA;
@@ -611,17 +659,16 @@ struct Q4State {
                 o[k][3] *= aB;
             }
         }
+        // weights as an fp16 head and the fp16 of its remainder, of the lane's row; rows r of all columns make the
+        // first fragment, rows r + 8 the second
         uint32_t pb[kBlocks][2];
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-            float e[4];
-            e[0] = ex2(__fmaf_rn(s[b][0], mulA, -mA));
-            e[1] = ex2(__fmaf_rn(s[b][1], mulB, -mB));
-            e[2] = ex2(__fmaf_rn(s[b][2], mulA, -mA));
-            e[3] = ex2(__fmaf_rn(s[b][3], mulB, -mB));
-            const __half2 lo = __floats2half2_rn(e[0], e[1]), hi = __floats2half2_rn(e[2], e[3]);
-            pb[b][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&lo));
-            pb[b][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&hi));
+            uint32_t lo;
+            const __half2 h = split_half2(ex2(__fmaf_rn(t[b][0], mulA, -mA)), ex2(__fmaf_rn(t[b][1], mulB, -mB)), lo);
+            const uint32_t hi = as_u32(h), got = __shfl_xor_sync(kFull, L.up ? hi : lo, 2);
+            pb[b][0] = movmatrix_trans(L.up ? got : hi);
+            pb[b][1] = movmatrix_trans(L.up ? lo : got);
         }
 
         // ---- O^T += V^T P
@@ -780,7 +827,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
     for (int i = 0; i < count; ++i) {
         if (issued < count) issue();
         if (fresh) {
-            S.open(L, p.q_hat + ((int64_t)t * H + g * kGroup) * kHeadDim, p.q_mul + (int64_t)t * H + g * kGroup);
+            const int64_t u = (int64_t)t * G + g;
+            S.open(L, p.q_hat + u * kQ4Columns * kHeadDim, p.q_mul + u * kGroup);
             live = p.tok_len[t] > 0;
             whole = j == 0;
             fresh = false;
@@ -798,40 +846,33 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
         }
         const bool last = j == n - 1;
         if ((last || i == count - 1) && live) {  // end of the segment
-            const float LA = S.o[8][0], LB = S.o[8][1];
-            const int r = L.r, c = L.c;
-            const float(&o)[9][4] = S.o;
+            float y[4][4], LA, LB;
+            S.close(L, y, LA, LB);
             const int64_t u = (int64_t)t * G + g;
-            if (c < 2) {
-                const float iA = p.v_scale / LA, iB = p.v_scale / LB;
-                const int hA = g * kGroup + 2 * c;
-                // o[j][0], [2]: dims 16r + 2j, + 1 of head A; [1], [3] of head B
-                if (whole && last) {
-                    __nv_bfloat16* dst = p.out + ((int64_t)t * H + hA) * kHeadDim + 16 * r;
+            const int hA = 2 * (L.c & 1), d = 16 * L.r + (L.up ? 8 : 0);
+            const float iA = p.v_scale / LA, iB = p.v_scale / LB;
+            if (whole && last) {
+                __nv_bfloat16* dst = p.out + ((int64_t)t * H + g * kGroup + hA) * kHeadDim + d;
+                uint32_t a[4], b[4];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t x[4], y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[e] = pack_bf16(__float2bfloat16_rn(o[4 * k + e][0] * iA), __float2bfloat16_rn(o[4 * k + e][2] * iA));
-                            y[e] = pack_bf16(__float2bfloat16_rn(o[4 * k + e][1] * iB), __float2bfloat16_rn(o[4 * k + e][3] * iB));
-                        }
-                        *reinterpret_cast<uint4*>(dst + 8 * k) = make_uint4(x[0], x[1], x[2], x[3]);
-                        *reinterpret_cast<uint4*>(dst + kHeadDim + 8 * k) = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
-                } else {
-                    float* po = p.part_o + ((u + w) * kGroup + 2 * c) * kHeadDim + 16 * r;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        *reinterpret_cast<float4*>(po + 4 * k) = make_float4(o[2 * k][0] * iA, o[2 * k][2] * iA,
-                                                                              o[2 * k + 1][0] * iA, o[2 * k + 1][2] * iA);
-                        *reinterpret_cast<float4*>(po + kHeadDim + 4 * k) = make_float4(
-                            o[2 * k][1] * iB, o[2 * k][3] * iB, o[2 * k + 1][1] * iB, o[2 * k + 1][3] * iB);
-                    }
-                    if (r == 0)
-                        *reinterpret_cast<float2*>(p.part_lse + (u + w) * kGroup + 2 * c) =
-                            make_float2(S.mA + log2f(LA), S.mB + log2f(LB));
+                for (int k = 0; k < 4; ++k) {
+                    a[k] = pack_bf16(__float2bfloat16_rn(y[k][0] * iA), __float2bfloat16_rn(y[k][1] * iA));
+                    b[k] = pack_bf16(__float2bfloat16_rn(y[k][2] * iB), __float2bfloat16_rn(y[k][3] * iB));
                 }
+                *reinterpret_cast<uint4*>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
+                *reinterpret_cast<uint4*>(dst + kHeadDim) = make_uint4(b[0], b[1], b[2], b[3]);
+            } else {
+                float* po = p.part_o + ((u + w) * kGroup + hA) * kHeadDim + d;
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    *reinterpret_cast<float4*>(po + 2 * k) =
+                        make_float4(y[k][0] * iA, y[k][1] * iA, y[k + 1][0] * iA, y[k + 1][1] * iA);
+                    *reinterpret_cast<float4*>(po + kHeadDim + 2 * k) =
+                        make_float4(y[k][2] * iB, y[k][3] * iB, y[k + 1][2] * iB, y[k + 1][3] * iB);
+                }
+                if (L.r == 0 && !L.up)
+                    *reinterpret_cast<float2*>(p.part_lse + (u + w) * kGroup + hA) =
+                        make_float2(S.mA + log2f(LA), S.mB + log2f(LB));
             }
         }
         fresh |= last;
@@ -964,8 +1005,8 @@ struct Q4Unit {
     static constexpr int kPieceBytes = kBlocks * kQ4BlockBytes;
     static constexpr int kRing = kUnitStages * kPieceBytes;          // of a warp; later its sums
     static constexpr int kBars = kWarps * kRing;
-    static constexpr int kQ = kBars + 8 * kWarps * kUnitStages;      // __half [4][128]
-    static constexpr int kMul = kQ + 2 * kGroup * kHeadDim;          // float [4]
+    static constexpr int kQ = kBars + 8 * kWarps * kUnitStages;      // __half [8][128]
+    static constexpr int kMul = kQ + 2 * kQ4Columns * kHeadDim;      // float [4]
     static constexpr int kML = kMul + 4 * kGroup;                    // float2 [warps][4]: maximum and sum
     static constexpr int kBytes = kML + 8 * kWarps * kGroup;
     static constexpr int kAlloc = kBytes + 128;
@@ -1046,12 +1087,11 @@ __global__ void __launch_bounds__(32 * U::kWarps, U::kCtas) q4_unit_kernel(Q4App
     const int64_t at = (int64_t)pos * kRopeHalf;
     if (warp == 0) {
         float x[16], y[16];
-        uint32_t h[8];
+        uint32_t h[8], hl[8];
         unpack16(qraw[0], qraw[1], x);
         norm_rope_q16<kFullRot>(x, wq, p.rope_hi + at, p.eps, lane, p.rot, y);
-        const float mul = q4_query(y, p.k_scale, h);
-        *reinterpret_cast<uint4*>(sQ + sub * kHeadDim + 8 * lj) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(sQ + sub * kHeadDim + 64 + 8 * lj) = make_uint4(h[4], h[5], h[6], h[7]);
+        const float mul = q4_query(y, p.k_scale, h, hl);
+        store_query(sQ + sub * kHeadDim, lj, h, hl);
         if (lj == 0) sMul[sub] = mul;
     }
     const bool owner = first < n && (n - 1 - first) % step == 0;  // this warp has the last piece
@@ -1105,19 +1145,20 @@ __global__ void __launch_bounds__(32 * U::kWarps, U::kCtas) q4_unit_kernel(Q4App
 
     // ---- the warps' sums into their own ring (nothing in flight there any more); one warp a head joins the CTA's,
     // and the first CTA's those of the cluster
-    const float LA = S.o[8][0], LB = S.o[8][1];
     float* part = reinterpret_cast<float*>(ring);
-    if (L.c < 2 && first < n) {
-        float* pa = part + 2 * L.c * kHeadDim + 16 * L.r;
+    if (first < n) {  // (the same for the whole warp)
+        float y[4][4], LA, LB;
+        S.close(L, y, LA, LB);
+        const int hA = 2 * (L.c & 1);
+        float* pa = part + hA * kHeadDim + 16 * L.r + (L.up ? 8 : 0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            *reinterpret_cast<float4*>(pa + 4 * k) = make_float4(S.o[2 * k][0], S.o[2 * k][2], S.o[2 * k + 1][0], S.o[2 * k + 1][2]);
-            *reinterpret_cast<float4*>(pa + kHeadDim + 4 * k) =
-                make_float4(S.o[2 * k][1], S.o[2 * k][3], S.o[2 * k + 1][1], S.o[2 * k + 1][3]);
+        for (int k = 0; k < 4; k += 2) {
+            *reinterpret_cast<float4*>(pa + 2 * k) = make_float4(y[k][0], y[k][1], y[k + 1][0], y[k + 1][1]);
+            *reinterpret_cast<float4*>(pa + kHeadDim + 2 * k) = make_float4(y[k][2], y[k][3], y[k + 1][2], y[k + 1][3]);
         }
-        if (L.r == 0) {
-            sML[warp * kGroup + 2 * L.c] = make_float2(S.mA, LA);
-            sML[warp * kGroup + 2 * L.c + 1] = make_float2(S.mB, LB);
+        if (L.r == 0 && !L.up) {
+            sML[warp * kGroup + hA] = make_float2(S.mA, LA);
+            sML[warp * kGroup + hA + 1] = make_float2(S.mB, LB);
         }
     }
     __syncthreads();
@@ -1202,7 +1243,7 @@ Q4Plan make_q4_plan(const pkv_pool* pool, int rows)
     size_t off = 0;
     pl.off_len = off, off = up(off + sizeof(int32_t) * rows);
     pl.off_prefix = off, off = up(off + sizeof(int32_t) * (rows + 1));
-    pl.off_qhat = off, off = up(off + sizeof(__half) * heads * kHeadDim);
+    pl.off_qhat = off, off = up(off + sizeof(__half) * 2 * heads * kHeadDim);  // (and the remainders)
     pl.off_qmul = off, off = up(off + sizeof(float) * heads);
     pl.off_po = off, off = up(off + sizeof(float) * slots * kGroup * kHeadDim);
     pl.off_plse = off, off = up(off + sizeof(float) * slots * kGroup);

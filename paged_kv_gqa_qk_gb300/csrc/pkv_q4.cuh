@@ -128,7 +128,8 @@ __device__ __forceinline__ void q4_store(uint8_t* block, bool is_v, int i, const
         }
         float y[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = __fmaf_rn(x[8 * h + k], r, x[8 * h + k] * rl);
+        for (int k = 0; k < 8; ++k)  // (rounded towards 0, the correction cannot overflow: far beyond the scale x r decides)
+            y[k] = __fmaf_rn(x[8 * h + k], r, __fmul_rz(x[8 * h + k], rl));
         asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
             "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
             "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"

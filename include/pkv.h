@@ -52,6 +52,11 @@
  *     they write different slots.  Each pkv_decode / pkv_step call takes one
  *     of the pool's 32 work counters in turn (zero between calls), so at most
  *     32 such calls may be in flight at once.
+ *   - A workspace belongs to one call at a time.  Calls that pass the same one
+ *     are made on one stream and by one host thread at a time: an entry
+ *     enqueues several kernels, and another call's between them would read and
+ *     overwrite what they hand on.  Every captured call needs its own, unless
+ *     its graph is ordered with all others that use it.
  *   - Every `table` argument may be NULL: the contiguous-row layout of the
  *     pages' non-paged entries (src/attention.linnet decode_rows,
  *     prefill_packed, step_packed), where row b owns the `pages` pool pages

@@ -14,6 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -595,7 +596,8 @@ class _Pool:
 
 
 class PagedKVPool(_Pool):
-    """A pool over caller-owned K/V torch tensors [kv_heads][num_pages*page_size][head_dim] (bf16)."""
+    """A pool over caller-owned K/V torch tensors [kv_heads][num_pages*page_size][head_dim] (bf16).  Its calls share one
+    workspace: on one stream and from one host thread at a time."""
 
     def __init__(self, K: torch.Tensor, V: torch.Tensor, cfg=None, stream=None):
         c = _cfg(cfg)
@@ -689,7 +691,7 @@ class Q4KVPool(_Pool):
             raise ValueError(f"data must be uint8, a multiple of {per_page} bytes, got {data.dtype} x {data.numel()}")
         self.data, self.cfg, self.device, self._streams = data, c, data.device, {}
         self._shape = self._heads, self._kv_heads, self._dim = c.heads, c.kv_heads, c.head_dim
-        self._lib, self._index = load_library(), data.get_device()
+        self._lib, self._index, self._lock = load_library(), data.get_device(), threading.Lock()
         self.num_pages = data.numel() // per_page
         self.handle = pkv_q4_pool_wrap(c, self.num_pages, data, k_scale, v_scale, stream)
         self._h, self._spec = self.handle.value, (self._index, *self._shape)
@@ -751,17 +753,24 @@ class Q4KVPool(_Pool):
         """One step of every row: append its k and v, attend over its cached positions.
 
         The workspace is the class's own: one kept per stream, and each captured call's in its graph, so that graphs
-        and calls on other streams may run at the same time."""
+        and calls on other streams may run at the same time.  Host threads may share a stream: a call's launches go
+        out together (the library runs without the interpreter's lock, and another thread's launches between them
+        would find the same workspace)."""
         if out is None:
             with _on(stream):
                 out = torch.empty_like(q)
         raw = _raw_stream(self._index) if stream is None else _stream(stream)
+        with self._lock:
+            self._decode(q, k, v, q_norm_w, k_norm_w, positions, table, out, stream, raw, pages)
+        return out
+
+    def _decode(self, q, k, v, q_norm_w, k_norm_w, positions, table, out, stream, raw, pages) -> None:
         ws = self._streams.get(raw)
         if ws is not None and raw != 0 and _capturing(stream):   # (the default stream is never captured)
             ws = None
         if ws is not None and _fast is not None and _fast.decode(
                 self._h, self._spec, q, k, v, q_norm_w, k_norm_w, positions, table, pages, out, ws[0], ws[1], raw) == 0:
-            return out
+            return
         _on_device(self._index, q=q, k=k, v=v, q_norm_w=q_norm_w, k_norm_w=k_norm_w, positions=positions, table=table,
                    out=out)
         rows = positions.shape[0]
@@ -789,4 +798,3 @@ class Q4KVPool(_Pool):
             rc = self._lib.pkv_q4_decode(*args, buf.data_ptr(), n, raw)
         if rc:
             raise PkvError(rc, "pkv_q4_decode")
-        return out

@@ -573,7 +573,8 @@ class _Pool:
             raw = _raw_stream(self._spec[0]) if stream is None else _stream(stream)
             rc = _fast.norm_rope(self._h, self._spec, q, k, q_norm_w, k_norm_w, positions, ROPE_LAYOUTS[layout],
                                  q_out, k_out, raw)
-            if rc == 0:
+            if rc is not None:
+                _check(rc, "pkv_norm_rope")
                 return q_out, k_out
         _on_device(self._spec[0], q=q, k=k, q_norm_w=q_norm_w, k_norm_w=k_norm_w, positions=positions, q_out=q_out,
                    k_out=k_out)
@@ -701,15 +702,17 @@ class Q4KVPool(_Pool):
         data = torch.zeros(pkv_q4_pool_bytes(cfg, num_pages), dtype=torch.uint8, device=device)
         return cls(data, cfg, k_scale, v_scale, stream)
 
-    # A call whose arguments are as they should be goes through _fast.  What that returns None for, and every call
-    # where the module was not built, is checked here, and a wrong argument raises.
+    # A call whose arguments are as they should be goes through _fast, and a code that the library returns is raised.
+    # What _fast returns None for, and every call where the module was not built, is checked here, and a wrong
+    # argument raises.
 
     def append(self, k, v, k_norm_w, positions, prow, table, stream=None, rows=None, pages=None) -> None:
         """k normed and roped, then k and v quantised into their slots (prow None: token t is row t)."""
         raw = _raw_stream(self._index) if stream is None else _stream(stream)
-        if _fast is not None and _fast.append(self._h, self._spec, k, v, k_norm_w, positions, prow, table, rows, pages,
-                                              raw) == 0:
-            return
+        if _fast is not None:
+            rc = _fast.append(self._h, self._spec, k, v, k_norm_w, positions, prow, table, rows, pages, raw)
+            if rc is not None:
+                return _check(rc, "pkv_q4_append")
         _on_device(self._index, k=k, v=v, k_norm_w=k_norm_w, positions=positions, prow=prow, table=table)
         n = positions.shape[0]
         shape = (n, self._kv_heads, self._dim)
@@ -732,8 +735,11 @@ class Q4KVPool(_Pool):
             with _on(stream):
                 new = torch.empty(2, *shape, dtype=torch.bfloat16, device=self.device)
             k, v = new[0] if k is None else k, new[1] if v is None else v
-        if _fast is not None and _fast.read(self._h, self._spec, positions, prow, table, k, v, rows, pages, raw) == 0:
-            return k, v
+        if _fast is not None:
+            rc = _fast.read(self._h, self._spec, positions, prow, table, k, v, rows, pages, raw)
+            if rc is not None:
+                _check(rc, "pkv_q4_read")
+                return k, v
         _on_device(self._index, positions=positions, prow=prow, table=table, k=k, v=v)
         strides = k.stride()
         if k.shape != shape or v.shape != shape or v.stride() != strides or strides[2] != 1:
@@ -768,9 +774,11 @@ class Q4KVPool(_Pool):
         ws = self._streams.get(raw)
         if ws is not None and raw != 0 and _capturing(stream):   # (the default stream is never captured)
             ws = None
-        if ws is not None and _fast is not None and _fast.decode(
-                self._h, self._spec, q, k, v, q_norm_w, k_norm_w, positions, table, pages, out, ws[0], ws[1], raw) == 0:
-            return
+        if ws is not None and _fast is not None:
+            rc = _fast.decode(self._h, self._spec, q, k, v, q_norm_w, k_norm_w, positions, table, pages, out, ws[0], ws[1],
+                              raw)
+            if rc is not None and rc != PKV_EWORKSPACE:
+                return _check(rc, "pkv_q4_decode")
         _on_device(self._index, q=q, k=k, v=v, q_norm_w=q_norm_w, k_norm_w=k_norm_w, positions=positions, table=table,
                    out=out)
         rows = positions.shape[0]

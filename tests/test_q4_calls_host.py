@@ -55,3 +55,51 @@ def test_threads_on_one_stream_enqueue_one_call_at_a_time(pool, monkeypatch, mod
     for t in threads:
         t.join()
     assert len(most) == 20 and max(most) == 1
+
+
+@pytest.mark.parametrize("call", ["decode", "append", "read", "norm_rope"])
+def test_a_code_of_the_library_is_raised_at_once(pool, monkeypatch, call):
+    """What the library refused or could not enqueue is not tried a second time another way."""
+    tried = []
+
+    def entry(*args):
+        tried.append(args)
+        return pkv.PKV_ECUDA
+
+    class Entries:
+        def __getattr__(self, name):
+            return entry
+    monkeypatch.setattr(pkv, "_fast", Entries())
+    pool._lib = Entries()
+    monkeypatch.setattr(pkv, "pkv_norm_rope", lambda *a, **kw: pkv._check(entry(), "pkv_norm_rope"))
+    a = arguments()
+    calls = {
+        "decode": lambda: pool.decode(**a),
+        "append": lambda: pool.append(a["k"], a["v"], a["k_norm_w"], a["positions"], None, a["table"]),
+        "read": lambda: pool.read(a["positions"], None, a["table"], a["k"], a["v"]),
+        "norm_rope": lambda: pool.norm_rope(a["q"], a["k"], None, None, a["positions"]),
+    }
+    with pytest.raises(pkv.PkvError) as e:
+        calls[call]()
+    assert e.value.code == pkv.PKV_ECUDA and len(tried) == 1
+
+
+def test_a_workspace_that_has_become_too_small_is_replaced(pool, monkeypatch):
+    """PKV_EWORKSPACE is not an error of the call: it is made again with a larger one, which is kept."""
+    seen = []
+
+    class Entries:
+        @staticmethod
+        def decode(*args):
+            return pkv.PKV_EWORKSPACE
+
+        @staticmethod
+        def pkv_q4_decode(*args):
+            seen.append(args[-2])
+            return pkv.PKV_OK if args[-2] >= 1 << 21 else pkv.PKV_EWORKSPACE
+    monkeypatch.setattr(pkv, "_fast", Entries)
+    monkeypatch.setattr(pkv, "pkv_workspace_bytes", lambda *a: 1 << 21)
+    monkeypatch.setattr(pkv, "_capturing", lambda stream: False)
+    pool._lib = Entries
+    pool.decode(**arguments())
+    assert seen == [1 << 20, 1 << 21] and pool._streams[0][1] == 1 << 21

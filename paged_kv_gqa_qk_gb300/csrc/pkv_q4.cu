@@ -373,6 +373,7 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
 // workloads against 45 / 64 / 212 then, 8 warps of 3 stages no better, a copying warp
 // beside 11 others 51 / 75 / 257.
 constexpr int kQ4Warps = 12;
+constexpr int kQ4MostCtas = 4096;                    // of a grid that pkv_set_ctas asks for
 constexpr int kQ4Stages = 2;
 constexpr int kQ4Chunk = 64;                         // positions: a page
 constexpr int kQ4Blocks = kQ4Chunk / kQ4Block;
@@ -419,7 +420,8 @@ __device__ __forceinline__ int q4_len(const Q4AttnParams& p, int t)
 __device__ __forceinline__ int q4_chunks(int len) { return (len + kQ4Chunk - 1) / kQ4Chunk; }
 
 // The split of T chunks over W <= T warps: warp w has chunks [floor(w T / W), floor((w + 1) T / W)),
-// in 32-bit arithmetic (W is a few thousand: w rem < 2^31).
+// in unsigned 32-bit arithmetic: rem < W and w <= W, so w rem < W^2.
+static_assert((uint64_t)kQ4MostCtas * kQ4Warps * kQ4MostCtas * kQ4Warps < (uint64_t(1) << 32), "w rem fits 32 bits");
 struct Q4Split {
     int T, W, q, rem;
     __device__ __forceinline__ Q4Split(int T_, int W_) : T(T_), W(W_), q(W_ ? T_ / W_ : 0), rem(W_ ? T_ - q * W_ : 0) {}
@@ -1237,7 +1239,7 @@ Q4Plan make_q4_plan(const pkv_pool* pool, int rows)
 {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     Q4Plan pl;
-    pl.ctas = std::min(pool->ctas_override > 0 ? pool->ctas_override : pool->num_sms, 4096);  // (Q4Split's 32 bits)
+    pl.ctas = std::min(pool->ctas_override > 0 ? pool->ctas_override : pool->num_sms, kQ4MostCtas);  // (Q4Split's 32 bits)
     const size_t units = (size_t)rows * pool->cfg.kv_heads, slots = units + (size_t)pl.ctas * kQ4Warps;
     const size_t heads = (size_t)rows * pool->cfg.heads;
     size_t off = 0;

@@ -67,12 +67,6 @@ __device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t two)
     asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two));
     return r;
 }
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 
 // ---- a head vector over 8 lanes ---------------------------------------------------------
 // Lane j of 8 holds dims 8j .. 8j + 7 (elements 0-7) and 64 + 8j .. 64 + 8j + 7 (8-15): two

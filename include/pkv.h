@@ -396,7 +396,8 @@ PKV_API int pkv_decode_static(pkv_pool* pool, const void* q, const void* k, cons
  * hold: k after QK-norm and RoPE in fp32 (correctly rounded), rounded to bf16, v as given --
  *   scale = e4m3(max |x| / (6 s)),   code = e2m1(x / (scale s)),
  * each rounded to nearest, ties to even, scale at most 448; a group whose scale rounds to
- * 0 is 0.  A group holding an Inf or a NaN is stored as NaN.  k_scale and v_scale are
+ * 0 is 0.  A group holding an Inf or a NaN is stored as NaN, and so is the whole of a k head that
+ * comes with one, or whose squares add up beyond fp32's range (values of 2^60 and more).  k_scale and v_scale are
  * powers of two from 2^-60 to 2^60 (they move the range of the scales, 2^-9 .. 448, to
  * that of the data; 1 suits values of order 0.01 to 1000).
  *

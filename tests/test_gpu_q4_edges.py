@@ -38,3 +38,30 @@ def test_values_beyond_the_largest_scale(e):
     ref = _q4.values(*_q4.quantise(f64(v), s), s)
     assert np.array_equal(f64(got), ref), f"{(f64(got) != ref).sum()} of {ref.size} differ"
     pool.close()
+
+
+@pytest.mark.parametrize("kv_heads", [2, 8])
+def test_a_key_with_an_infinity_is_nan_as_a_whole(kv_heads):
+    """k with an Inf or a NaN: that head's position is NaN in all its dims; the other heads, the other positions and all
+    of v are as ever.  Large keys are normed like others."""
+    n = 64
+    rng = np.random.RandomState(2)
+    x = rng.randn(n, kv_heads, 128) * 2.0 ** rng.randint(-20, 58, (n, kv_heads, 1))
+    x[3, 1, 7], x[9, 0, 100], x[10, 1, 64] = np.inf, np.nan, -np.inf
+    k = torch.from_numpy(x).to(torch.bfloat16)
+    v = torch.from_numpy(rng.randn(n, kv_heads, 128)).to(torch.bfloat16)
+    w = torch.from_numpy(rng.rand(128) + 0.5).to(torch.bfloat16)
+    pool = pkv.Q4KVPool.empty(1, dict(heads=4 * kv_heads, kv_heads=kv_heads, max_seq=64))
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    pool.append(k.to(DEV), v.to(DEV), w.to(DEV), pos, pos * 0, table)
+    kk, vv = (f64(t) for t in pool.read(pos, pos * 0, table))
+    assert pool.check_errors() == 0
+    bad = np.zeros((n, kv_heads), bool)
+    bad[3, 1] = bad[9, 0] = bad[10, 1] = True
+    assert np.isnan(kk[bad]).all() and np.isfinite(kk[~bad]).all()
+    with np.errstate(invalid="ignore"):
+        want = _q4.bf16(np.where(bad[..., None], 0.0, _q4.norm_rope(f64(k), f64(w), np.arange(n))))
+    assert np.array_equal(kk[~bad], _q4.values(*_q4.quantise(want, 1.0), 1.0)[~bad])
+    assert np.array_equal(vv, _q4.values(*_q4.quantise(f64(v), 1.0), 1.0))
+    pool.close()

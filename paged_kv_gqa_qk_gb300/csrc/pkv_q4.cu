@@ -63,7 +63,7 @@ struct Q4AppendParams {
     const float2* rope_hi;
     const float2* rope_lo;
     uint8_t* data;
-    __half* q_hat;              // decode: [tokens][kv_heads][8][128]: 4 heads, each times a power of two, and their remainders
+    __half* q_hat;              // decode: [tokens][kv_heads][4][2][128]: each head times a power of two, and its remainder
     float* q_mul;               // decode: [tokens][heads], what a score of it is multiplied with
     __nv_bfloat16* out;         // decode: [tokens][heads][128], zeroed for skipped tokens
     int32_t* tok_len;           // decode: [tokens], 0: skip
@@ -198,14 +198,14 @@ __device__ __forceinline__ float q4_query(const float (&y)[16], float k_scale, u
     return fmaxf(__uint_as_float((uint32_t)ex << 23) * kQScale * k_scale, 1e-30f);
 }
 
-// The 8 columns of a (token, kv head) in the score product: its 4 query heads and, 4 columns
-// on, their remainders.  head: of this lane's head; lane j of 8.
+// The 8 columns of a (token, kv head) in the score product: column 2h its query head h, column 2h + 1 the remainder.
+// `to`: of this lane's head; lane j of 8.
 constexpr int kQ4Columns = 2 * kGroup;
-__device__ __forceinline__ void store_query(__half* head, int j, const uint32_t (&r)[8], const uint32_t (&rl)[8])
+__device__ __forceinline__ void store_query(__half* to, int j, const uint32_t (&r)[8], const uint32_t (&rl)[8])
 {
-    __half* rest = head + kGroup * kHeadDim;
-    *reinterpret_cast<uint4*>(head + 8 * j) = make_uint4(r[0], r[1], r[2], r[3]);
-    *reinterpret_cast<uint4*>(head + 64 + 8 * j) = make_uint4(r[4], r[5], r[6], r[7]);
+    __half* rest = to + kHeadDim;
+    *reinterpret_cast<uint4*>(to + 8 * j) = make_uint4(r[0], r[1], r[2], r[3]);
+    *reinterpret_cast<uint4*>(to + 64 + 8 * j) = make_uint4(r[4], r[5], r[6], r[7]);
     *reinterpret_cast<uint4*>(rest + 8 * j) = make_uint4(rl[0], rl[1], rl[2], rl[3]);
     *reinterpret_cast<uint4*>(rest + 64 + 8 * j) = make_uint4(rl[4], rl[5], rl[6], rl[7]);
 }
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(512) q4_prep_kernel(Q4AppendParams p)
         norm_rope_q16<kFullRot>(x, w, p.rope_hi + (int64_t)pos * kRopeHalf, p.eps, lane, p.rot, y);
         const float mul = q4_query(y, p.k_scale, r, rl);
         const int64_t u = (int64_t)t * p.kv_heads + (item - quads);
-        store_query(p.q_hat + (u * kQ4Columns + sub) * kHeadDim, j, r, rl);
+        store_query(p.q_hat + (u * kQ4Columns + 2 * sub) * kHeadDim, j, r, rl);
         if (j == 0) p.q_mul[u * kGroup + sub] = mul;
     }
 }
@@ -351,14 +351,14 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
 // preparation before it needs the queries.
 //
 // Per 16 positions (a block), with lane = 4 r + c:
-//   S[16 pos][8] = K[16][128] q[128][8], m16n8k16 fp16: column h = query head h of the
-//     group in fp16, column h + 4 = the fp16 of its remainder (S = column h + column h + 4: 22
-//     bits of q), row i = position pi(i), row i + 8 = pi(i) + 8, pi(2c + b) = (c ^ b) + 4b.  Lane (r, c) holds dims 32c..32c+31 of rows r and r + 8:
+//   S[16 pos][8] = K[16][128] q[128][8], m16n8k16 fp16: column 2h = query head h of the
+//     group in fp16, column 2h + 1 = the fp16 of its remainder (S = the two columns' sum, in one
+//     lane: 22 bits of q), row i = position pi(i), row i + 8 = pi(i) + 8, pi(2c + b) = (c ^ b) + 4b.  Lane (r, c) holds dims 32c..32c+31 of rows r and r + 8:
 //     one 16-byte read of codes each, two scales each.
 //   O^T[128][8] += V^T[128][16 pos] P[16][8]: lane (r, c) holds dims 16r..16r+15 (one
 //     group) of positions pi(2c), pi(2c + 1) and the same + 8: four 8-byte reads, four scales.
-//     P as S: columns h its head's fp16, h + 4 the remainders', added at the segment's end; a weight is kept to
-//     2^-22 of itself or 2^-32 of the largest, as good as the fp32 it was computed in.
+//     P's columns as q's, added at the segment's end; a weight is kept to 2^-21 of itself or 2^-32 of
+//     the largest, nearly the fp32 it was computed in.
 // The codes become fp16 by the conversion instruction and are multiplied by their
 // scales as fp16 pairs, exactly; V's are first regrouped so that one byte holds a
 // dim's codes of two positions.  P is turned between the fragments by movmatrix.
@@ -378,7 +378,7 @@ constexpr int kQ4Stages = 2;
 constexpr int kQ4Chunk = 64;                         // positions: a page
 constexpr int kQ4Blocks = kQ4Chunk / kQ4Block;
 constexpr int kQ4ChunkBytes = kQ4Blocks * kQ4BlockBytes;
-constexpr float kQ4Lift = 7.f;                       // base-2 exponent of the largest weight when it is set (Q4State)
+constexpr float kQ4Lift = 8.f;                       // base-2 exponent of the largest weight when it is set (Q4State)
 constexpr float kQ4Most = 15.f;                      // that a weight may reach: 2^15 is within fp16
 
 struct Q4AttnParams {
@@ -510,7 +510,6 @@ __device__ __forceinline__ float ex2(float x)
 // What a lane keeps of its place in the fragments (lane = 4 r + c).
 struct Q4Lane {
     int r, c;
-    bool up;          // c >= 2: the lane has the remainders' columns, and the softmax of rows r + 8 (else of rows r)
     int pi_r;         // position of row r
     int pi_0, pi_1;   // positions of k = 2c, 2c + 1
     uint32_t koff, voff0, voff1, soff;
@@ -518,7 +517,6 @@ struct Q4Lane {
     {
         r = lane >> 2;
         c = lane & 3;
-        up = c >= 2;
         pi_r = ((r >> 1) ^ (r & 1)) | ((r & 1) << 2);
         pi_0 = c;
         pi_1 = (c ^ 1) | 4;
@@ -529,15 +527,14 @@ struct Q4Lane {
     }
 };
 
-// A warp's attention of one (token, kv head) over some of its chunks.  Lanes c and c + 2 hold the heads
-// 2 (c & 1) and 2 (c & 1) + 1, A and B: lane c the products with the fp16 heads of the queries or weights,
-// lane c + 2 those with the remainders.
+// A warp's attention of one (token, kv head) over some of its chunks.  Lanes c hold head c: of a product's two
+// columns, the one with the fp16 heads of the queries or weights and the one with their remainders.
 struct Q4State {
     uint32_t bq[8][2];   // the queries' fragments
-    float mulA, mulB;    // what scores of heads A and B are multiplied with
-    float o[9][4];       // o[k][0], [2]: dims 16r + 2k, + 1 of head A; [1], [3] of head B; not normalised;
-                         // o[8]: the weights' sums (the product with ones), in every row
-    float mA, mB;        // weights are 2^(score - m)
+    float mul;           // what scores are multiplied with
+    float o[9][4];       // o[k][0] + [1]: dim 16r + 2k, [2] + [3]: dim 16r + 2k + 1; not normalised; o[8]: the weights'
+                         // sum (the product with ones), [0] + [1] as [2] + [3], in every row
+    float m;             // weights are 2^(score - m)
 
     // q_hat: 8 columns of 128 fp16; q_mul: the 4 heads' multipliers
     __device__ __forceinline__ void open(const Q4Lane& L, const __half* q_hat, const float* q_mul)
@@ -552,29 +549,15 @@ struct Q4State {
             bq[2 * k + 1][0] = x[k].z;
             bq[2 * k + 1][1] = x[k].w;
         }
-        const float2 mul = *reinterpret_cast<const float2*>(q_mul + 2 * (L.c & 1));
-        mulA = mul.x;
-        mulB = mul.y;
+        mul = q_mul[L.c];
 #pragma unroll
         for (int k = 0; k < 9; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
-        mA = mB = -CUDART_INF_F;
+        m = -CUDART_INF_F;
     }
 
-    // The end of a segment: the products with heads and remainders added.  y[k][0], [1]: dims d + 2k, + 1 of head A;
-    // [2], [3] of head B, with d = 16r, + 8 in the lanes c >= 2; LA, LB: the weights' sums.
-    __device__ __forceinline__ void close(const Q4Lane& L, float (&y)[4][4], float& LA, float& LB) const
-    {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int f = 2 * (e & 1) + (e >> 1);
-                const float mine = L.up ? o[4 + k][f] : o[k][f], other = L.up ? o[k][f] : o[4 + k][f];
-                y[k][e] = __fadd_rn(mine, __shfl_xor_sync(kFull, other, 2));
-            }
-        LA = __fadd_rn(o[8][0], __shfl_xor_sync(kFull, o[8][0], 2));
-        LB = __fadd_rn(o[8][1], __shfl_xor_sync(kFull, o[8][1], 2));
-    }
+    // Heads and remainders added: dims 16r + 2k and + 1 of the lane's head, and the weights' sum.
+    __device__ __forceinline__ float2 pair(int k) const { return make_float2(o[k][0] + o[k][1], o[k][2] + o[k][3]); }
+    __device__ __forceinline__ float sum() const { return o[8][0] + o[8][1]; }
 
     // One chunk of kBlocks blocks in shared memory at sb, of which the unit has `left` positions (as many or more: all).
     template <int kBlocks>
@@ -606,16 +589,13 @@ struct Q4State {
             }
         }
 
-        // ---- softmax, base 2.  s[b][0], [1]: heads A and B at position L.pi_r of block b, [2], [3]: at L.pi_r + 8; lanes
-        // c >= 2 have the remainders' share of the same.  The two lanes of a pair add up, one row each: t[b][0], [1].
+        // ---- softmax, base 2, of the lane's head: s[b][0] + [1] at position L.pi_r of block b, [2] + [3] at L.pi_r + 8
         float t[kBlocks][2];
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float mine = L.up ? s[b][2 + e] : s[b][e], other = L.up ? s[b][e] : s[b][2 + e];
-                t[b][e] = __fadd_rn(mine, __shfl_xor_sync(kFull, other, 2));
-            }
+        for (int b = 0; b < kBlocks; ++b) {
+            t[b][0] = s[b][0] + s[b][1];
+            t[b][1] = s[b][2] + s[b][3];
+        }
         // Positions past the row's end: scores of -inf, and V scales of 0 (the codes are finite
         // whatever lies there), in a row's last chunk only.
         uint32_t vmask[kBlocks];
@@ -625,53 +605,43 @@ struct Q4State {
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
                 const int at = left - kQ4Block * b;
-                if (L.pi_r + (L.up ? 8 : 0) >= at) t[b][0] = t[b][1] = -CUDART_INF_F;
+                if (L.pi_r >= at) t[b][0] = -CUDART_INF_F;
+                if (L.pi_r + 8 >= at) t[b][1] = -CUDART_INF_F;
                 vmask[b] = (L.pi_0 < at ? 0xffu : 0u) | (L.pi_1 < at ? 0xff00u : 0u) | (L.pi_0 + 8 < at ? 0xff0000u : 0u) |
                            (L.pi_1 + 8 < at ? 0xff000000u : 0u);
             }
         }
-        float nA = t[0][0], nB = t[0][1];
+        float top = fmaxf(t[0][0], t[0][1]);
 #pragma unroll
-        for (int b = 1; b < kBlocks; ++b) {
-            nA = fmaxf(nA, t[b][0]);
-            nB = fmaxf(nB, t[b][1]);
-        }
-        nA *= mulA;
-        nB *= mulB;
+        for (int b = 1; b < kBlocks; ++b) top = fmaxf(top, fmaxf(t[b][0], t[b][1]));
+        top *= mul;
         // m lies kQ4Lift below the largest score it was set at, and follows only when a lane's passes it by more than
         // kQ4Most: weights stay below 2^kQ4Most, inside fp16, and most chunks need no maximum over the lanes and
         // rescale nothing
-        if (__any_sync(kFull, nA > mA + kQ4Most || nB > mB + kQ4Most)) {
+        if (__any_sync(kFull, top > m + kQ4Most)) {
 #pragma unroll
-            for (int d = 2; d < 32; d <<= 1) {
-                nA = fmaxf(nA, __shfl_xor_sync(kFull, nA, d));
-                nB = fmaxf(nB, __shfl_xor_sync(kFull, nB, d));
-            }
-            nA = fmaxf(nA - kQ4Lift, mA);
-            nB = fmaxf(nB - kQ4Lift, mB);
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+            top = fmaxf(top - kQ4Lift, m);
             // (a maximum still at -inf -- scores that are all NaN -- leaves nothing to rescale)
-            const float aA = nA == -CUDART_INF_F ? 1.f : ex2(mA - nA), aB = nB == -CUDART_INF_F ? 1.f : ex2(mB - nB);
-            mA = nA;
-            mB = nB;
+            const float f = top == -CUDART_INF_F ? 1.f : ex2(m - top);
+            m = top;
 #pragma unroll
             for (int k = 0; k < 9; ++k) {
-                o[k][0] *= aA;
-                o[k][1] *= aB;
-                o[k][2] *= aA;
-                o[k][3] *= aB;
+                o[k][0] *= f;
+                o[k][1] *= f;
+                o[k][2] *= f;
+                o[k][3] *= f;
             }
         }
-        // weights as an fp16 head and the fp16 of its remainder, of the lane's row; rows r of all columns make the
-        // first fragment, rows r + 8 the second
+        // the weights of both rows, each as its upper 11 bits and the fp16 of what they leave, side by side
         uint32_t pb[kBlocks][2];
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            uint32_t lo;
-            const __half2 h = split_half2(ex2(__fmaf_rn(t[b][0], mulA, -mA)), ex2(__fmaf_rn(t[b][1], mulB, -mB)), lo);
-            const uint32_t hi = as_u32(h), got = __shfl_xor_sync(kFull, L.up ? hi : lo, 2);
-            pb[b][0] = movmatrix_trans(L.up ? got : hi);
-            pb[b][1] = movmatrix_trans(L.up ? lo : got);
-        }
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float w = ex2(__fmaf_rn(t[b][e], mul, -m)), head = __uint_as_float(__float_as_uint(w) & ~0x1fffu);
+                pb[b][e] = movmatrix_trans(as_u32(__floats2half2_rn(head, __fsub_rn(w, head))));
+            }
 
         // ---- O^T += V^T P
 #pragma unroll
@@ -848,33 +818,26 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attn_kernel(Q4AttnParams 
         }
         const bool last = j == n - 1;
         if ((last || i == count - 1) && live) {  // end of the segment
-            float y[4][4], LA, LB;
-            S.close(L, y, LA, LB);
+            const float sum = S.sum(), inv = p.v_scale / sum;
             const int64_t u = (int64_t)t * G + g;
-            const int hA = 2 * (L.c & 1), d = 16 * L.r + (L.up ? 8 : 0);
-            const float iA = p.v_scale / LA, iB = p.v_scale / LB;
             if (whole && last) {
-                __nv_bfloat16* dst = p.out + ((int64_t)t * H + g * kGroup + hA) * kHeadDim + d;
-                uint32_t a[4], b[4];
+                __nv_bfloat16* dst = p.out + ((int64_t)t * H + g * kGroup + L.c) * kHeadDim + 16 * L.r;
+                uint32_t x[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    a[k] = pack_bf16(__float2bfloat16_rn(y[k][0] * iA), __float2bfloat16_rn(y[k][1] * iA));
-                    b[k] = pack_bf16(__float2bfloat16_rn(y[k][2] * iB), __float2bfloat16_rn(y[k][3] * iB));
+                for (int k = 0; k < 8; ++k) {
+                    const float2 y = S.pair(k);
+                    x[k] = pack_bf16(__float2bfloat16_rn(y.x * inv), __float2bfloat16_rn(y.y * inv));
                 }
-                *reinterpret_cast<uint4*>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
-                *reinterpret_cast<uint4*>(dst + kHeadDim) = make_uint4(b[0], b[1], b[2], b[3]);
+                *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4*>(dst + 8) = make_uint4(x[4], x[5], x[6], x[7]);
             } else {
-                float* po = p.part_o + ((u + w) * kGroup + hA) * kHeadDim + d;
+                float* po = p.part_o + ((u + w) * kGroup + L.c) * kHeadDim + 16 * L.r;
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                    *reinterpret_cast<float4*>(po + 2 * k) =
-                        make_float4(y[k][0] * iA, y[k][1] * iA, y[k + 1][0] * iA, y[k + 1][1] * iA);
-                    *reinterpret_cast<float4*>(po + kHeadDim + 2 * k) =
-                        make_float4(y[k][2] * iB, y[k][3] * iB, y[k + 1][2] * iB, y[k + 1][3] * iB);
+                for (int k = 0; k < 8; k += 2) {
+                    const float2 y = S.pair(k), z = S.pair(k + 1);
+                    *reinterpret_cast<float4*>(po + 2 * k) = make_float4(y.x * inv, y.y * inv, z.x * inv, z.y * inv);
                 }
-                if (L.r == 0 && !L.up)
-                    *reinterpret_cast<float2*>(p.part_lse + (u + w) * kGroup + hA) =
-                        make_float2(S.mA + log2f(LA), S.mB + log2f(LB));
+                if (L.r == 0) p.part_lse[(u + w) * kGroup + L.c] = S.m + log2f(sum);
             }
         }
         fresh |= last;
@@ -1007,7 +970,7 @@ struct Q4Unit {
     static constexpr int kPieceBytes = kBlocks * kQ4BlockBytes;
     static constexpr int kRing = kUnitStages * kPieceBytes;          // of a warp; later its sums
     static constexpr int kBars = kWarps * kRing;
-    static constexpr int kQ = kBars + 8 * kWarps * kUnitStages;      // __half [8][128]
+    static constexpr int kQ = kBars + 8 * kWarps * kUnitStages;      // __half [4][2][128]
     static constexpr int kMul = kQ + 2 * kQ4Columns * kHeadDim;      // float [4]
     static constexpr int kML = kMul + 4 * kGroup;                    // float2 [warps][4]: maximum and sum
     static constexpr int kBytes = kML + 8 * kWarps * kGroup;
@@ -1093,7 +1056,7 @@ __global__ void __launch_bounds__(32 * U::kWarps, U::kCtas) q4_unit_kernel(Q4App
         unpack16(qraw[0], qraw[1], x);
         norm_rope_q16<kFullRot>(x, wq, p.rope_hi + at, p.eps, lane, p.rot, y);
         const float mul = q4_query(y, p.k_scale, h, hl);
-        store_query(sQ + sub * kHeadDim, lj, h, hl);
+        store_query(sQ + 2 * sub * kHeadDim, lj, h, hl);
         if (lj == 0) sMul[sub] = mul;
     }
     const bool owner = first < n && (n - 1 - first) % step == 0;  // this warp has the last piece
@@ -1148,20 +1111,14 @@ __global__ void __launch_bounds__(32 * U::kWarps, U::kCtas) q4_unit_kernel(Q4App
     // ---- the warps' sums into their own ring (nothing in flight there any more); one warp a head joins the CTA's,
     // and the first CTA's those of the cluster
     float* part = reinterpret_cast<float*>(ring);
-    if (first < n) {  // (the same for the whole warp)
-        float y[4][4], LA, LB;
-        S.close(L, y, LA, LB);
-        const int hA = 2 * (L.c & 1);
-        float* pa = part + hA * kHeadDim + 16 * L.r + (L.up ? 8 : 0);
+    if (first < n) {
+        float* pa = part + L.c * kHeadDim + 16 * L.r;
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-            *reinterpret_cast<float4*>(pa + 2 * k) = make_float4(y[k][0], y[k][1], y[k + 1][0], y[k + 1][1]);
-            *reinterpret_cast<float4*>(pa + kHeadDim + 2 * k) = make_float4(y[k][2], y[k][3], y[k + 1][2], y[k + 1][3]);
+        for (int k = 0; k < 8; k += 2) {
+            const float2 y = S.pair(k), z = S.pair(k + 1);
+            *reinterpret_cast<float4*>(pa + 2 * k) = make_float4(y.x, y.y, z.x, z.y);
         }
-        if (L.r == 0 && !L.up) {
-            sML[warp * kGroup + hA] = make_float2(S.mA, LA);
-            sML[warp * kGroup + hA + 1] = make_float2(S.mB, LB);
-        }
+        if (L.r == 0) sML[warp * kGroup + L.c] = make_float2(S.m, S.sum());
     }
     __syncthreads();
     const int h = warp;

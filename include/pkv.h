@@ -467,7 +467,9 @@ PKV_API int pkv_q4_read(pkv_pool* pool, const int32_t* positions, const int32_t*
  * to bf16.  As there, slots must be distinct and a row's new slot must not be read by
  * another row of the call (PKV_CHECK=1 checks both).  Results are the same from run to run.
  * Small calls run in one launch, larger ones in three (their results differ by rounding
- * only); a grid size set by pkv_set_ctas, up to 4096 CTAs, always takes the latter. */
+ * only); a grid size set by pkv_set_ctas, up to 4096 CTAs, always takes the latter.  `pages`
+ * counts as the longest row's in that choice: short rows are fastest under a table that is no
+ * wider than they need. */
 PKV_API int pkv_q4_decode(pkv_pool* pool, const void* q, const void* k, const void* v, const void* q_norm_w,
                           const void* k_norm_w, const int32_t* positions, const int32_t* table, int rows, int pages,
                           void* out, void* workspace, size_t workspace_bytes, void* stream);
@@ -501,11 +503,13 @@ PKV_API int pkv_norm_rope(pkv_pool* pool, const void* q, const void* k, const vo
 /* Frequencies for contexts `factor` (>= 1) times the trained one.  Host only: fills
  * inv_freq[R/2] (R = rotary_dim) and the factor on cos and sin.  f_i = theta^(-2i/R):
  *   PKV_ROPE_NONE    f_i
- *   PKV_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   PKV_ROPE_LINEAR  f_i / factor (position interpolation: Chen et al., arXiv 2306.15595)
  *   PKV_ROPE_BASE    theta * factor^(R/(R-2)) in theta's place: the slowest pair is divided by factor
+ *                    ("NTK-aware" interpolation: Peng et al., YaRN, arXiv 2309.00071, section 3.1)
  *   PKV_ROPE_RAMP    f_i where the pair turns 32 times or more over the `trained` positions,
  *                    f_i / factor where it turns once or less, a linear ramp over the pair's index
  *                    between (its ends rounded outwards); *mscale = 0.1 ln(factor) + 1
+ *                    (the method of the same paper, sections 3.2 to 3.4, with its bounds 32 and 1)
  * *mscale = 1 but for the ramp.  Errors: PKV_EINVAL (null, unknown scaling, factor < 1 or not
  * finite, trained <= 0 for the ramp), and pkv_pool_alloc's for the config. */
 #define PKV_ROPE_NONE 0

@@ -25,7 +25,8 @@
 namespace pkv {
 
 // A launch that may start while the kernel before it on the stream drains: every kernel
-// here waits for that one (pdl_wait) before it reads or writes memory.  The short ones let
+// here waits for that one (pdl_wait) before it reads or writes memory (the split attention
+// reads and writes what the preparation does not touch before).  The short ones let
 // the next one's CTAs come early (pdl_launch_dependents); the append and the split
 // attention, which fill the SMs by themselves, do not: CTAs that wait beside theirs cost
 // more than their early start saves (append and read of 2048 tokens 13.0 -> 9.1 us, steps
@@ -364,14 +365,17 @@ cudaError_t launch_q4_append(const pkv_pool* pool, const void* k, const void* v,
 // dim's codes of two positions.  P is turned between the fragments by movmatrix.
 //
 // What bounds it (alone, cold cache): long rows by memory, 8 rows of 32768-40960 331 MB in
-// 57 us, 5.8 TB/s; 64 rows of 512-4096 182 MB in 37 us, 5.0 TB/s, 5 us of them the start and
-// the last warps' ends; many rows by instructions, 256 rows of 1024-8192 1.04 GB in 200 us,
-// 5.2 TB/s: about 237 warp instructions a block, 111 of them on the integer pipe (the
-// conversions and the scales' products), at 2.5 an SM and cycle.  mma.sync m16n8k16 is used a third of
+// 58.6 us, 5.6 TB/s; 64 rows of 512-4096 182 MB in 37.5 us, 4.9 TB/s, 5 us of them the start and
+// the last warps' ends; many rows by instructions, 256 rows of 1024-8192 1.04 GB in 206 us,
+// 5.1 TB/s: about 237 warp instructions a block, 111 of them on the integer pipe (the
+// conversions and the scales' products), at 2.4 an SM and cycle.  mma.sync m16n8k16 is used a third of
 // its rate there; an instruction with K = 16 takes the 16 dims of a scale whole.
+// The remainders of q and P cost 5 us of the 256 rows (the longer chain from score to weight) and nothing
+// where memory bounds; with heads in columns 0-3 and remainders in 4-7, whose halves meet by
+// shuffles, they cost 10, and the 64 rows 1.
 // 12 warps of 2 stages of a page: 16 warps of half pages 50 / 69 / 237 us a call on these three
 // workloads against 45 / 64 / 212 then, 8 warps of 3 stages no better, a copying warp
-// beside 11 others 51 / 75 / 257.
+// beside 11 others 51 / 75 / 257 (all without remainders).
 constexpr int kQ4Warps = 12;
 constexpr int kQ4MostCtas = 4096;                    // of a grid that pkv_set_ctas asks for
 constexpr int kQ4Stages = 2;
@@ -955,7 +959,7 @@ __global__ void __launch_bounds__(32 * kHeads * kSub) q4_combine_kernel(Q4Combin
 //
 // A call of few short rows is bound by its chain of latencies, not by bytes: this has
 // one launch and one trip to memory after the table, where preparation, split attention
-// and combine are three launches (one row of 700: 5.9 us a call instead of 9.1).  Half pages
+// and combine are three launches (one row of 700: 5.7 us a call instead of 8.9).  Half pages
 // halve the chain of a warp's first piece, 1.3 us, where there are warps for all of them;
 // whole pages carry more a round.  Both have 8 warps, two a scheduler, of which one computes
 // while the other waits (4 warps of pages: 16 rows of 500-1500 10.8 us, 9.4 with 8).  The
@@ -1265,17 +1269,18 @@ struct Q4UnitChoice {
 // The kernel's life is 4.5 to 5.5 us, 0.6 us more in a cluster, and 1.3 to 1.8 us for every further round of its warps'
 // pieces; the split attention's is 8 to 11 us and the time of its bytes, and more where few units are cut into many
 // pieces.  Measured (us; half pages / whole pages, CTAs a unit in brackets / split; 8 kv heads unless named):
-//   rows that one CTA takes in one round: 8 of 1-128 5.1 / 5.8 / 9.3, 8 of 400 6.2 / 5.6 / 10.9, 16 of 100-300 6.2 / 5.6 / 11.1
-//   in one round of a cluster, about one CTA an SM: 1 of 700 5.9 [4] / 6.6 [2] / 9.1, 24 of 1-640 (2 heads) 6.5 [4] /
-//     6.8 [2], 1 of 1500 (1 head) 5.8 [8] / 6.3 [4] / 9.1; more CTAs than that: 4 of 2000 7.5 [8] / 6.8 [4] / 12.0
-//   longer: 1 of 4000 7.1 [8] / 6.7 [8] / 11.5, of 16000 14.1 [8] / 11.8 [8] / 18.2, of 32000 20.1 [16] / 18.9 [8] / 20.9, 2
-//     of 16000 22.9 [4] / 18.5 [4] / 18.7, 4 of 8000 14.0 [4] / 12.2 [4] / 17.6, 16 of 500-1500 10.7 / 9.4 / 14.6, of 3000
-//     18.5 / 16.4 / 20.5; clusters beyond what the device holds at a time take turns: 4 of 8000 24.1 [8]
-//   longest: 1 of 40000 23.0 [8] / 23.3, of 60000 32.2 [8] / 26.8, 8 of 10000 24.6 / 26.0, 16 of 200-5000 22.4 / 22.5; in
-//     clusters of 16 (1 head) 1 of 80000 22.3 / 39.6, of 130000 33.2 / 55.9, of 300000 71.3 / 60.1
-//   more units than SMs: 32 of 500-1500 15.0 / 17.4 / 18.0, 64 of 1-640 15.5 / 21.6 / 16.8
-// The rows' lengths are not known here: `pages`, the table's width, stands for the longest.  A grid size set by
-// pkv_set_ctas is the split attention's.
+//   rows that one CTA takes in one round: 8 of 1-128 5.0 / 5.8 / 9.1, 8 of 400 6.1 / 5.5 / 10.4, 16 of 100-300 6.1 / 5.6 / 10.7
+//   in one round of a cluster, about one CTA an SM: 1 of 700 5.7 [4] / 6.4 [2] / 8.9, 24 of 1-640 (2 heads) 6.4 [4] /
+//     6.8 [2], 1 of 1500 (1 head) 5.7 [8] / 6.2 [4] / 8.7; more CTAs than that: 4 of 2000 7.6 [8] / 6.8 [4] / 11.6
+//   longer: 1 of 4000 7.1 [8] / 6.7 [8] / 11.2, of 16000 13.9 [8] / 11.8 [8] / 18.0, of 32000 20.2 [16] / 18.7 [8] / 20.4, 2
+//     of 16000 22.8 [4] / 18.5 [4] / 18.2, 4 of 8000 14.0 [4] / 12.2 [4] / 17.5, 16 of 500-1500 10.6 / 9.4 / 14.5, of 3000
+//     18.1 / 16.0 / 20.5; clusters beyond what the device holds at a time take turns: 4 of 8000 24.2 [8]
+//   longest: 1 of 40000 22.7 [8] / 23.4, of 60000 32.5 [8] / 26.9, 8 of 10000 24.5 [2] / 25.7, 16 of 200-5000 22.1 / 22.0; in
+//     clusters of 16 (1 head) 1 of 80000 22.4 / 38.8, of 130000 33.1 / 53.2, of 300000 70.8 / 57.7
+//   more units than SMs: 32 of 500-1500 15.1 / 17.4 / 17.7, 64 of 1-640 15.6 / 21.4 / 16.9
+// The rows' lengths are not known here: `pages`, the table's width, stands for the longest, so that short rows under a
+// wide table go through the split attention (8 rows of 1-128 under 640 pages 9.3 us instead of 5.0, 16 of 500-1500 14.6
+// instead of 9.4; one row of 700 5.9).  A grid size set by pkv_set_ctas is the split attention's.
 static Q4UnitChoice q4_unit_choice(const pkv_pool* pool, int rows, int64_t pages)
 {
     constexpr int kWarps = Q4UnitPage::kWarps, kRounds = 10, kRoundsOf16 = 16, kRoundsInTurn = 6;

@@ -18,7 +18,8 @@ def attend(q, K, V):
     10 2^-24, rsqrt 2^-22, two products).  Split into an fp16 and the fp16 of the rest it keeps 2^-22 of itself or
     2^-25 of the head's largest.  A score is 8 products of 16 in fp32, each within 2^-22 of its terms' sizes (2^-19 in
     all), times a multiplier (3 2^-24): 2^-18 of sum |q k| covers these.  The exponent's rounding (2^-20, arguments up
-    to 32) and ex2 (2^-22) are 2^-19 of a weight.  A weight's own split keeps 2^-22 of it or 2^-32 of the largest.  The
+    to 32), ex2 (2^-22) and a weight's own split (2^-21) are under 2^-19 + 2^-22 of it, and the split loses 2^-32 of the
+    largest where it ends in fp16's subnormals.  The
     weighted sums add 2^-22 of their sizes per 16 positions, and a few more where pieces are joined."""
     n, G = K.shape[0], K.shape[1]
     out, bound = np.zeros_like(q), np.zeros_like(q)

@@ -527,6 +527,76 @@ PKV_API int pkv_rope_frequencies(const pkv_config* cfg, int scaling, double fact
  * PKV_EDEVICE, PKV_ENOMEM, PKV_ECUDA. */
 PKV_API int pkv_pool_set_rope(pkv_pool* pool, const double* inv_freq, double mscale, void* stream);
 
+/* ---- a layer's norms and projections in microscaled form ------------------------------------------
+ * The norms and linear maps around the attention (qwen3-8b Nest files, src/norm.linnet RmsNorm;
+ * DecoderLayer.decode_paged: attention_norm, the attention, the residual's addition, mlp_norm)
+ * with both operands of every product in 8 or 4 bits: half or a quarter of the weights' bytes,
+ * on the tensor cores' 8- and 4-bit rates.  One step of a layer is
+ *   pkv_add_norm -> pkv_mx_qkv_proj -> pkv_decode / pkv_q4_decode / ... -> pkv_mx_quantize of the
+ *   attention's output -> pkv_mx_linear (o_proj) -> pkv_add_norm.
+ * Any pool names the device (and, for pkv_add_norm, gives eps).
+ *
+ * A microscaled tensor [rows][cols] (OCP Microscaling Formats (MX) Specification v1.0) holds every
+ * group of 32 consecutive values of a row as code * 2^e, with e the least whole number >= -127
+ * with which no value of the group exceeds the largest code, and code the value / 2^e rounded to
+ * nearest, ties to even:
+ *   PKV_MX8  codes e4m3 (largest 448), uint8 [rows][cols]
+ *   PKV_MX4  codes e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), uint8 [rows][cols / 2], the even column
+ *            in the low half of its byte
+ *   scales   uint8 e + 127, in tiles of 128 rows by 4 groups: tile (row / 128) * (cols / 128) + group / 4
+ *            of 512 bytes, byte 16 (row % 32) + 4 (row % 128 / 32) + group % 4 of it
+ * A group holding an Inf or a NaN has scale byte 255 (NaN) and codes 0.  cols % 128 == 0
+ * (PKV_ENOTIMPL otherwise).  Rows behind the last one of its last tile are neither written nor
+ * used: their scale bytes may hold anything.
+ *
+ * pkv_mx_bytes: bytes of the codes and of the scales.  Either output may be NULL.
+ * In all entries here codes and scales are device pointers, 16-byte aligned; rows <= 2^24, cols <= 2^20
+ * (PKV_ERANGE beyond); sizes <= 0 and type other than PKV_MX8 and PKV_MX4 are PKV_EINVAL. */
+#define PKV_MX8 2
+#define PKV_MX4 3
+PKV_API int pkv_mx_bytes(int type, int rows, int cols, size_t* codes, size_t* scales);
+
+/* bf16 [rows][cols], x_stride elements between rows (>= cols, a multiple of 8; x 16-byte aligned), to a
+ * microscaled tensor: activations before a product, or weights once at load. */
+PKV_API int pkv_mx_quantize(pkv_pool* pool, const void* x, int64_t x_stride, int rows, int cols, int type, void* codes,
+                            void* scales, void* stream);
+
+/* The values of a microscaled tensor as bf16 (exact in bf16's range), y_stride elements between rows
+ * (>= cols, a multiple of 8; y 16-byte aligned).  A scale byte of 255 gives NaN. */
+PKV_API int pkv_mx_read(pkv_pool* pool, int type, const void* codes, const void* scales, int rows, int cols, void* y,
+                        int64_t y_stride, void* stream);
+
+/* The residual's addition and a layer's RMS norm in one pass:
+ *   h = bf16(x + residual),  y = h / sqrt(mean(h^2) + eps) * w
+ * h is rounded once, to bf16, and the norm is that of the rounded h; the sum of squares, the root and
+ * the products are carried in pairs of floats (about 2^-44), so that y's one rounding, to out_type, is
+ * that of the exact value.  A row with an Inf or a NaN, or whose squares add up beyond fp32's range
+ * (values of 2^60 and more), is NaN throughout.
+ *   x             device bf16 [tokens][hidden], x_stride elements between rows (>= hidden, a multiple of 8)
+ *   residual      device bf16 [tokens][hidden], or NULL: h = x
+ *   residual_out  device bf16 [tokens][hidden]: h (NULL if and only if residual is)
+ *   w             device bf16 [hidden]
+ *   out_type      PKV_BF16: out is bf16 [tokens][hidden], scales NULL, hidden % 8 == 0;
+ *                 PKV_MX8 or PKV_MX4: out and scales are a microscaled tensor's, hidden % 128 == 0
+ *                 (PKV_ENOTIMPL otherwise)
+ * All 16-byte aligned; hidden <= 32768, tokens <= 2^24 (PKV_ERANGE).  residual_out or a bf16 out may be
+ * residual or, with x_stride == hidden, x; outputs must not overlap inputs in another way, nor
+ * each other. */
+PKV_API int pkv_add_norm(pkv_pool* pool, const void* x, int64_t x_stride, const void* residual, void* residual_out,
+                         const void* w, int tokens, int hidden, int out_type, void* out, void* scales, void* stream);
+
+/* y[t][o] = sum_k x[t][k] w[o][k] of two microscaled tensors of one type, x [tokens][in_features] and
+ * w [out_features][in_features]; products exact, fp32 accumulation, bf16 output (pkv_linear's, over the
+ * values the tensors hold).  out_features % 128 == 0 (PKV_ENOTIMPL otherwise).  A NaN scale makes its row
+ * of x (or its feature of w) NaN in y.  y: device bf16 [tokens][out_features], 16-byte aligned.
+ * The same from run to run; rows of x do not affect each other. */
+PKV_API int pkv_mx_linear(pkv_pool* pool, int type, const void* x_codes, const void* x_scales, const void* w_codes,
+                          const void* w_scales, void* y, int tokens, int in_features, int out_features, void* stream);
+
+/* pkv_qkv_proj of microscaled x [tokens][hidden] and w_qkv [(heads + 2 kv_heads) * head_dim][hidden]. */
+PKV_API int pkv_mx_qkv_proj(pkv_pool* pool, int type, const void* x_codes, const void* x_scales, const void* w_codes,
+                            const void* w_scales, int tokens, int hidden, void* q, void* k, void* v, void* stream);
+
 /* ---- errors ------------------------------------------------------------------------------
  * Synchronise `stream`, then read and clear the pool's sticky device error
  * word (PKV_DEVERR_* bits of every call since the last read) into *flags.

@@ -32,10 +32,12 @@ ABI_SYMBOLS = ("pkv_config_default", "pkv_strerror", "pkv_pool_alloc", "pkv_pool
                "pkv_linear_workspace_bytes", "pkv_linear", "pkv_qkv_proj", "pkv_qkv_proj_append",
                "pkv_decode_appended", "pkv_output_gate", "pkv_q4_pool_bytes", "pkv_q4_pool_alloc", "pkv_q4_pool_wrap",
                "pkv_q4_pool_data", "pkv_q4_append", "pkv_q4_read", "pkv_q4_decode", "pkv_norm_rope",
-               "pkv_rope_frequencies", "pkv_pool_set_rope")
+               "pkv_rope_frequencies", "pkv_pool_set_rope", "pkv_mx_bytes", "pkv_mx_quantize", "pkv_mx_read",
+               "pkv_add_norm", "pkv_mx_linear", "pkv_mx_qkv_proj")
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}                  # PKV_ROPE_HALF, PKV_ROPE_INTERLEAVED
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}  # PKV_ROPE_NONE ...
+MX_KINDS = {"mx8": 2, "mx4": 3}                               # PKV_MX8, PKV_MX4
 
 # Size of the scratch array pkv_decode_static uses in place of a workspace.
 PKV_STATIC_SCRATCH_BYTES = 32 << 20
@@ -111,6 +113,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "pkv_rope_frequencies": ([cfgp, i32, ctypes.c_double, i32, ctypes.POINTER(ctypes.c_double),
                                   ctypes.POINTER(ctypes.c_double)], i32),
         "pkv_pool_set_rope": ([vp, ctypes.POINTER(ctypes.c_double), ctypes.c_double, vp], i32),
+        "pkv_mx_bytes": ([i32, i32, i32, ctypes.POINTER(sz), ctypes.POINTER(sz)], i32),
+        "pkv_mx_quantize": ([vp, vp, i64, i32, i32, i32, vp, vp, vp], i32),
+        "pkv_mx_read": ([vp, i32, vp, vp, i32, i32, vp, i64, vp], i32),
+        "pkv_add_norm": ([vp, vp, i64, vp, vp, vp, i32, i32, i32, vp, vp, vp], i32),
+        "pkv_mx_linear": ([vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp], i32),
+        "pkv_mx_qkv_proj": ([vp, i32, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -505,6 +513,134 @@ def pkv_pool_set_rope(pool, inv_freq, mscale: float = 1.0, stream=None) -> None:
                                             _stream(stream)), "pkv_pool_set_rope")
 
 
+# ---- microscaled tensors
+
+def pkv_mx_bytes(kind: str, rows: int, cols: int):
+    """(bytes of the codes, bytes of the scales) of a microscaled tensor."""
+    codes, scales = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load_library().pkv_mx_bytes(MX_KINDS[kind], int(rows), int(cols), ctypes.byref(codes), ctypes.byref(scales)),
+           "pkv_mx_bytes")
+    return codes.value, scales.value
+
+
+class MxTensor:
+    """A microscaled tensor [rows][cols] over caller-owned uint8 tensors: ``codes`` [rows][cols] (kind mx8) or
+    [rows][cols / 2] (mx4), and ``scales``, whose order include/pkv.h gives.  cols is a multiple of 128."""
+
+    def __init__(self, kind: str, rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor):
+        if kind not in MX_KINDS:
+            raise ValueError(f"kind must be one of {sorted(MX_KINDS)}, got {kind!r}")
+        need = pkv_mx_bytes(kind, rows, cols)
+        for what, t, n in (("codes", codes, need[0]), ("scales", scales, need[1])):
+            if t.dtype is not torch.uint8:
+                raise TypeError(f"{what} must be torch.uint8, got {t.dtype}")
+            if t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"{what} of {kind} [{rows}][{cols}] must be {n} contiguous bytes, got {t.numel()}")
+        if codes.device != scales.device:
+            raise ValueError(f"codes lie on {codes.device}, scales on {scales.device}")
+        self.kind, self.rows, self.cols, self.codes, self.scales = kind, int(rows), int(cols), codes, scales
+        self.shape, self.device = (self.rows, self.cols), codes.device
+        self._spec = (MX_KINDS[kind], self.rows, self.cols)
+
+    @classmethod
+    def empty(cls, kind: str, rows: int, cols: int, device="cuda"):
+        if kind not in MX_KINDS:
+            raise ValueError(f"kind must be one of {sorted(MX_KINDS)}, got {kind!r}")
+        codes, scales = pkv_mx_bytes(kind, rows, cols)
+        return cls(kind, rows, cols, torch.empty(rows, codes // rows, dtype=torch.uint8, device=device),
+                   torch.empty(scales, dtype=torch.uint8, device=device))
+
+
+def _rows(x, what, shape=None):
+    """(pointer, row stride) of a bf16 CUDA matrix with contiguous rows."""
+    if not isinstance(x, torch.Tensor) or x.dtype is not _BF16 or not x.is_cuda:
+        raise TypeError(f"{what} must be a bf16 CUDA tensor")
+    if x.dim() != 2 or (shape is not None and tuple(x.shape) != tuple(shape)):
+        raise ValueError(f"{what} must be {'a matrix' if shape is None else list(shape)}, got {tuple(x.shape)}")
+    if x.stride(1) != 1 and x.shape[1] > 1:
+        raise ValueError(f"{what} must have contiguous rows, got strides {x.stride()}")
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _matrix(x, what, shape):
+    """Pointer of a contiguous bf16 CUDA matrix of that shape."""
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {list(shape)}, got {tuple(x.shape)}")
+    return _dev(x, _BF16, what)
+
+
+def _mx(t, what):
+    """(code of the kind, pointers of codes and scales) of a microscaled tensor."""
+    if not isinstance(t, MxTensor):
+        raise TypeError(f"{what} must be an MxTensor")
+    return MX_KINDS[t.kind], _dev(t.codes, torch.uint8, what), _dev(t.scales, torch.uint8, what)
+
+
+def pkv_mx_quantize(pool, x, out: MxTensor, stream=None) -> None:
+    """bf16 x [rows][cols] (contiguous rows, any row stride) into a microscaled tensor of its shape."""
+    kind, codes, scales = _mx(out, "out")
+    ptr, stride = _rows(x, "x", out.shape)
+    _check(load_library().pkv_mx_quantize(pool, ptr, stride, out.rows, out.cols, kind, codes, scales, _stream(stream)),
+           "pkv_mx_quantize")
+
+
+def pkv_mx_read(pool, x: MxTensor, y, stream=None) -> None:
+    """The values of a microscaled tensor into bf16 y of its shape (contiguous rows, any row stride)."""
+    kind, codes, scales = _mx(x, "x")
+    ptr, stride = _rows(y, "y", x.shape)
+    _check(load_library().pkv_mx_read(pool, kind, codes, scales, x.rows, x.cols, ptr, stride, _stream(stream)),
+           "pkv_mx_read")
+
+
+def pkv_add_norm(pool, x, residual, w, out, residual_out=None, stream=None) -> None:
+    """residual_out = x + residual and out = its RMS norm by w; out is a bf16 tensor or an MxTensor.  Without a
+    residual (None, with residual_out None) it is the norm of x."""
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out are given together")
+    ptr, stride = _rows(x, "x")
+    tokens, hidden = x.shape
+    if w.numel() != hidden:
+        raise ValueError(f"w must be [{hidden}], got {tuple(w.shape)}")
+    if isinstance(out, MxTensor):
+        if out.shape != (tokens, hidden):
+            raise ValueError(f"out must be {[tokens, hidden]}, got {list(out.shape)}")
+        kind, codes, scales = _mx(out, "out")
+    else:
+        kind, codes, scales = 0, _matrix(out, "out", x.shape), None
+    res = None if residual is None else _matrix(residual, "residual", x.shape)
+    res_out = None if residual_out is None else _matrix(residual_out, "residual_out", x.shape)
+    _check(load_library().pkv_add_norm(pool, ptr, stride, res, res_out, _dev(w, _BF16, "w"), tokens, hidden, kind, codes,
+                                       scales, _stream(stream)), "pkv_add_norm")
+
+
+def _pair_of_kind(x, w):
+    """Pointers of the two operands of a product."""
+    kind, xc, xs = _mx(x, "x")
+    wkind, wc, ws = _mx(w, "w")
+    if kind != wkind or x.cols != w.cols:
+        raise ValueError(f"x is {x.kind} {list(x.shape)}, w {w.kind} {list(w.shape)}: kinds and columns must match")
+    return kind, xc, xs, wc, ws
+
+
+def pkv_mx_linear(pool, x: MxTensor, w: MxTensor, y, stream=None) -> None:
+    """y = x w^T of microscaled x [tokens][in] and w [out][in] of one kind, y bf16 [tokens][out]."""
+    operands = _pair_of_kind(x, w)
+    _check(load_library().pkv_mx_linear(pool, *operands, _matrix(y, "y", (x.rows, w.rows)), x.rows, x.cols, w.rows,
+                                        _stream(stream)), "pkv_mx_linear")
+
+
+def pkv_mx_qkv_proj(pool, x: MxTensor, w_qkv: MxTensor, q, k, v, stream=None) -> None:
+    """pkv_qkv_proj of microscaled tensors of one kind."""
+    operands = _pair_of_kind(x, w_qkv)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.shape[0] != x.rows:
+            raise ValueError(f"{name} has {t.shape[0]} tokens, x has {x.rows}")
+    if w_qkv.rows != q[0].numel() + k[0].numel() + v[0].numel():
+        raise ValueError(f"w_qkv {list(w_qkv.shape)} does not stack the q, k, v projections of x {list(x.shape)}")
+    _check(load_library().pkv_mx_qkv_proj(pool, *operands, x.rows, x.cols, _dev(q, _BF16, "q"), _dev(k, _BF16, "k"),
+                                          _dev(v, _BF16, "v"), _stream(stream)), "pkv_mx_qkv_proj")
+
+
 def pkv_check_errors(pool, stream=None) -> int:
     f = ctypes.c_uint32()
     _check(load_library().pkv_check_errors(pool, _stream(stream), ctypes.byref(f)), "pkv_check_errors")
@@ -580,6 +716,67 @@ class _Pool:
                    k_out=k_out)
         pkv_norm_rope(self.handle, q, k, q_norm_w, k_norm_w, positions, q_out, k_out, layout, stream, self._shape)
         return q_out, k_out
+
+    def add_norm(self, x, residual, w, out="mx8", residual_out=None, stream=None):
+        """The residual's addition and a layer's RMS norm: (out, residual_out) with residual_out = x + residual and out its
+        norm.  out: a bf16 tensor or an MxTensor, or the kind of a new one ("bf16", "mx8", "mx4").  residual None: the
+        norm of x, and no residual_out.  residual_out may be residual itself."""
+        with _on(stream):
+            if isinstance(out, str):
+                out = torch.empty(x.shape, dtype=_BF16, device=x.device) if out == "bf16" else \
+                    MxTensor.empty(out, *x.shape, device=x.device)
+            if residual is not None and residual_out is None:
+                residual_out = torch.empty_like(residual)
+        codes, scales = (out.codes, out.scales) if isinstance(out, MxTensor) else (out, None)
+        _on_device(self._spec[0], x=x, residual=residual, w=w, out=codes, scales=scales, residual_out=residual_out)
+        pkv_add_norm(self.handle, x, residual, w, out, residual_out, stream)
+        return out, residual_out
+
+    def mx_quantize(self, x, kind="mx8", out=None, stream=None) -> MxTensor:
+        """bf16 x [rows][cols] as a microscaled tensor of that kind."""
+        if out is None:
+            with _on(stream):
+                out = MxTensor.empty(kind, *x.shape, device=x.device)
+        elif out.kind != kind:
+            raise ValueError(f"out is {out.kind}, kind {kind}")
+        _on_device(self._spec[0], x=x, codes=out.codes, scales=out.scales)
+        pkv_mx_quantize(self.handle, x, out, stream)
+        return out
+
+    def mx_read(self, x: MxTensor, out=None, stream=None) -> torch.Tensor:
+        """The values that a microscaled tensor holds, as bf16 [rows][cols]."""
+        if out is None:
+            with _on(stream):
+                out = torch.empty(x.shape, dtype=_BF16, device=x.device)
+        _on_device(self._spec[0], codes=x.codes, scales=x.scales, out=out)
+        pkv_mx_read(self.handle, x, out, stream)
+        return out
+
+    def mx_linear(self, x, w: MxTensor, y=None, stream=None) -> torch.Tensor:
+        """y = x w^T of microscaled x [tokens][in] and w [out][in], y bf16; a bf16 x is quantised to w's kind first."""
+        if not isinstance(x, MxTensor):
+            x = self.mx_quantize(x, w.kind, stream=stream)
+        if y is None:
+            with _on(stream):
+                y = torch.empty(x.rows, w.rows, dtype=_BF16, device=x.device)
+        _on_device(self._spec[0], x=x.codes, x_scales=x.scales, w=w.codes, w_scales=w.scales, y=y)
+        pkv_mx_linear(self.handle, x, w, y, stream)
+        return y
+
+    def mx_qkv_proj(self, x, w_qkv: MxTensor, q=None, k=None, v=None, stream=None):
+        """qkv_proj of microscaled weights (and x, or a bf16 x, quantised to their kind first)."""
+        if not isinstance(x, MxTensor):
+            x = self.mx_quantize(x, w_qkv.kind, stream=stream)
+        heads, kv_heads, dim = self._shape
+        with _on(stream):
+            q, k, v = (torch.empty(x.rows, n, dim, dtype=_BF16, device=x.device) if t is None else t
+                       for t, n in ((q, heads), (k, kv_heads), (v, kv_heads)))
+        for name, t, n in (("q", q, heads), ("k", k, kv_heads), ("v", v, kv_heads)):
+            if tuple(t.shape) != (x.rows, n, dim):
+                raise ValueError(f"{name} must be {[x.rows, n, dim]}, got {list(t.shape)}")
+        _on_device(self._spec[0], x=x.codes, x_scales=x.scales, w_qkv=w_qkv.codes, w_scales=w_qkv.scales, q=q, k=k, v=v)
+        pkv_mx_qkv_proj(self.handle, x, w_qkv, q, k, v, stream)
+        return q, k, v
 
     def check_errors(self, stream=None) -> int:
         return pkv_check_errors(self.handle, stream)

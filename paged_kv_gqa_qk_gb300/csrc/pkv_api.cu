@@ -157,6 +157,20 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t o
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_bytes(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_heads(CUtensorMap* map, const void* base, int heads, int tokens)
 {
     auto fn = encode_fn();
@@ -349,6 +363,7 @@ static int create_pool(const pkv_config* cfg, int num_pages, void* k, void* v, b
     }
     ok &= configure_kernels() == cudaSuccess;
     ok &= configure_prefill() == cudaSuccess;
+    ok &= configure_mx_linear() == cudaSuccess;
     p->ctas_per_sm = attn_ctas_per_sm();
     ok &= p->ctas_per_sm > 0;
     if (!ok) {
@@ -917,6 +932,115 @@ int pkv_norm_rope(pkv_pool* pool, const void* q, const void* k, const void* q_no
     a.interleaved = layout == PKV_ROPE_INTERLEAVED;
     a.f32 = out_type == PKV_F32;
     return launch_norm_rope(pool, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+// ---- microscaled tensors --------------------------------------------------------------------
+static int mx_checks(int type, int rows, int cols)
+{
+    if ((type != PKV_MX8 && type != PKV_MX4) || rows <= 0 || cols <= 0) return PKV_EINVAL;
+    if (cols % 128) return PKV_ENOTIMPL;
+    return rows > (1 << 24) || cols > (1 << 20) ? PKV_ERANGE : PKV_OK;
+}
+
+static int on_device(const pkv_pool* pool)
+{
+    int dev = -1;
+    return cudaGetDevice(&dev) != cudaSuccess || dev != pool->device ? PKV_EDEVICE : PKV_OK;
+}
+
+int pkv_mx_bytes(int type, int rows, int cols, size_t* codes, size_t* scales)
+{
+    const int rc = mx_checks(type, rows, cols);
+    if (rc != PKV_OK) return rc;
+    if (codes) *codes = (size_t)rows * (type == PKV_MX8 ? cols : cols / 2);
+    if (scales) *scales = ((size_t)rows + 127) / 128 * (cols / 128) * 512;
+    return PKV_OK;
+}
+
+int pkv_mx_quantize(pkv_pool* pool, const void* x, int64_t x_stride, int rows, int cols, int type, void* codes,
+                    void* scales, void* stream)
+{
+    NvtxRange range("pkv_mx_quantize");
+    if (!pool || !x || !codes || !scales) return PKV_EINVAL;
+    int rc = mx_checks(type, rows, cols);
+    if (rc != PKV_OK) return rc;
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16) || x_stride < cols || x_stride % 8) return PKV_EINVAL;
+    if ((rc = on_device(pool)) != PKV_OK) return rc;
+    return launch_mx_quantize(pool, x, x_stride, rows, cols, type, codes, scales, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? PKV_OK
+               : PKV_ECUDA;
+}
+
+int pkv_mx_read(pkv_pool* pool, int type, const void* codes, const void* scales, int rows, int cols, void* y,
+                int64_t y_stride, void* stream)
+{
+    NvtxRange range("pkv_mx_read");
+    if (!pool || !codes || !scales || !y) return PKV_EINVAL;
+    int rc = mx_checks(type, rows, cols);
+    if (rc != PKV_OK) return rc;
+    if (!aligned(y, 16) || !aligned(codes, 16) || !aligned(scales, 16) || y_stride < cols || y_stride % 8) return PKV_EINVAL;
+    if ((rc = on_device(pool)) != PKV_OK) return rc;
+    return launch_mx_read(pool, type, codes, scales, rows, cols, y, y_stride, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? PKV_OK
+               : PKV_ECUDA;
+}
+
+int pkv_add_norm(pkv_pool* pool, const void* x, int64_t x_stride, const void* residual, void* residual_out,
+                 const void* w, int tokens, int hidden, int out_type, void* out, void* scales, void* stream)
+{
+    NvtxRange range("pkv_add_norm");
+    if (!pool || !x || !w || !out || !residual != !residual_out || tokens <= 0 || hidden <= 0) return PKV_EINVAL;
+    if (out_type != PKV_BF16 && out_type != PKV_MX8 && out_type != PKV_MX4) return PKV_EINVAL;
+    if (!scales != (out_type == PKV_BF16)) return PKV_EINVAL;
+    if (hidden % (out_type == PKV_BF16 ? 8 : 128)) return PKV_ENOTIMPL;
+    if (tokens > (1 << 24) || hidden > 32768) return PKV_ERANGE;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(residual_out, 16) || !aligned(w, 16) || !aligned(out, 16) ||
+        !aligned(scales, 16) || x_stride < hidden || x_stride % 8)
+        return PKV_EINVAL;
+    const int rc = on_device(pool);
+    if (rc != PKV_OK) return rc;
+    const AddNorm a = {x, residual, residual_out, w, out, scales, x_stride, tokens, hidden, out_type};
+    return launch_add_norm(pool, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+static int run_mx_linear(pkv_pool* pool, const MxLinear& a, void* stream)
+{
+    if (!pool || !a.x_codes || !a.x_scales || !a.w_codes || !a.w_scales) return PKV_EINVAL;
+    int out = 0;
+    for (int i = 0; i < a.segments; ++i) {
+        if (!a.y[i] || a.widths[i] <= 0) return PKV_EINVAL;
+        if (a.widths[i] % 128) return PKV_ENOTIMPL;
+        if (a.widths[i] > (1 << 20)) return PKV_ERANGE;
+        out += a.widths[i];
+    }
+    int rc = mx_checks(a.type, a.tokens, a.in);
+    if (rc != PKV_OK || (rc = mx_checks(a.type, out, a.in)) != PKV_OK) return rc;
+    for (const void* ptr : {a.x_codes, a.x_scales, a.w_codes, a.w_scales})
+        if (!aligned(ptr, 16)) return PKV_EINVAL;
+    for (int i = 0; i < a.segments; ++i)
+        if (!aligned(a.y[i], 16)) return PKV_EINVAL;
+    if ((rc = on_device(pool)) != PKV_OK) return rc;
+    return launch_mx_linear(pool, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+int pkv_mx_linear(pkv_pool* pool, int type, const void* x_codes, const void* x_scales, const void* w_codes,
+                  const void* w_scales, void* y, int tokens, int in_features, int out_features, void* stream)
+{
+    NvtxRange range("pkv_mx_linear");
+    const MxLinear a = {x_codes, x_scales, w_codes, w_scales, {y}, {out_features}, 1, tokens, in_features, type};
+    return run_mx_linear(pool, a, stream);
+}
+
+int pkv_mx_qkv_proj(pkv_pool* pool, int type, const void* x_codes, const void* x_scales, const void* w_codes,
+                    const void* w_scales, int tokens, int hidden, void* q, void* k, void* v, void* stream)
+{
+    NvtxRange range("pkv_mx_qkv_proj");
+    if (!pool) return PKV_EINVAL;
+    const int qw = pool->cfg.heads * pool->cfg.head_dim, kw = pool->cfg.kv_heads * pool->cfg.head_dim;
+    const MxLinear a = {x_codes, x_scales, w_codes, w_scales, {q, k, v}, {qw, kw, kw}, 3, tokens, hidden, type};
+    return run_mx_linear(pool, a, stream);
 }
 
 int pkv_check_errors(pkv_pool* pool, void* stream, uint32_t* flags)

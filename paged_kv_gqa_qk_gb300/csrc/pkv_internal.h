@@ -211,6 +211,34 @@ struct NormRope {
 };
 cudaError_t launch_norm_rope(const pkv_pool* pool, const NormRope& a, cudaStream_t s);
 
+// ---- microscaled tensors (pkv_mx.cu), the product of two (pkv_mx_linear.cu) ----
+cudaError_t launch_mx_quantize(const pkv_pool* pool, const void* x, int64_t x_stride, int rows, int cols, int type,
+                               void* codes, void* scales, cudaStream_t s);
+cudaError_t launch_mx_read(const pkv_pool* pool, int type, const void* codes, const void* scales, int rows, int cols,
+                           void* y, int64_t y_stride, cudaStream_t s);
+struct AddNorm {
+    const void* x;
+    const void* residual;
+    void* residual_out;
+    const void* w;
+    void* out;
+    void* scales;
+    int64_t x_stride;
+    int tokens, hidden, type;
+};
+cudaError_t launch_add_norm(const pkv_pool* pool, const AddNorm& a, cudaStream_t s);
+struct MxLinear {
+    const void *x_codes, *x_scales, *w_codes, *w_scales;
+    void* y[3];       // consecutive output features, a tensor [tokens][width] each
+    int widths[3];
+    int segments, tokens, in, type;
+};
+cudaError_t launch_mx_linear(const pkv_pool* pool, const MxLinear& a, cudaStream_t s);
+cudaError_t configure_mx_linear();
+// 2-D tiled tensor map of a row-major byte matrix (128-byte swizzle, zero fill past the
+// edges), boxes of 128 bytes by `box_rows`; false if the driver refuses it.
+bool make_tmap_bytes(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
+
 // Per-device kernel attributes (dynamic shared memory); called with the
 // pool's device current when a pool is created.
 cudaError_t configure_kernels();

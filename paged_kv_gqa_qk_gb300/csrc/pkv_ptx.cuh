@@ -229,6 +229,51 @@ __device__ __forceinline__ void umma_bf16_ts_acc(uint32_t tmem_d, uint32_t tmem_
         "r"(tmem_a), "l"(b), "r"(idesc));
 }
 
+// ---- block-scaled products: 8-bit (e4m3) or 4-bit (e2m1) operands, a power of two (e8m0) on
+// every 32 values along K.  K is 32 values (8-bit) or 64 (4-bit) an instruction, 32 bytes of
+// either operand's rows.  The scales lie in tensor memory: row 32 j + i's in lane i of column j,
+// 4 bytes for 4 consecutive groups, copied from shared memory by umma_copy_scales.
+//
+// Instruction descriptor: M x N; sf = which byte of a column's 4 holds this instruction's
+// first group (8-bit: 0..3, 4-bit: 0 or 2), the same for both operands.
+__host__ __device__ constexpr uint32_t umma_idesc_mx(bool four_bits, int M, int N, int sf)
+{
+    const uint32_t format = four_bits ? 1u : 0u;  // e2m1 of kind mxf4, e4m3 of kind mxf8f6f4
+    return ((uint32_t)sf << 4) | (format << 7) | (format << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(M >> 7) << 27) | ((uint32_t)sf << 29);
+}
+
+// D(tmem) (+)= (A scaled by sfa)(smem) * (B scaled by sfb)(smem); issued by one thread.
+template <bool kFourBits>
+__device__ __forceinline__ void umma_mx(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, bool accumulate)
+{
+    if constexpr (kFourBits)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                tmem_d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(sfa), "r"(sfb)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                tmem_d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(sfa), "r"(sfb)
+            : "memory");
+}
+
+// Copies one tile of scales (512 bytes: 32 rows of 16) from shared memory to 4 columns of tensor
+// memory, the same for the lanes of all four warps.  Products that the same thread issues
+// afterwards find it, and those issued before are done with the columns.
+__device__ __forceinline__ void umma_copy_scales(uint32_t taddr, uint32_t saddr)
+{
+    // no swizzle, descriptor version 1; 128 bytes between groups of 8 rows
+    const uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
 // Arrive once on `bar` when every tcgen05 operation this thread issued so far has completed.
 __device__ __forceinline__ void umma_commit(uint32_t bar)
 {

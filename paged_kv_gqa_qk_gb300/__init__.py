@@ -138,7 +138,8 @@ def _load_fast(lib) -> None:
         return
     if fast.torch_version == torch.__version__:
         fast.bind(*(ctypes.cast(getattr(lib, "pkv_" + name), ctypes.c_void_p).value
-                    for name in ("q4_decode", "q4_append", "q4_read", "norm_rope")))
+                    for name in ("q4_decode", "q4_append", "q4_read", "norm_rope", "mx_quantize", "mx_read", "add_norm",
+                                 "mx_linear", "mx_qkv_proj")))
         _fast = fast
 
 
@@ -721,24 +722,37 @@ class _Pool:
         """The residual's addition and a layer's RMS norm: (out, residual_out) with residual_out = x + residual and out its
         norm.  out: a bf16 tensor or an MxTensor, or the kind of a new one ("bf16", "mx8", "mx4").  residual None: the
         norm of x, and no residual_out.  residual_out may be residual itself."""
-        with _on(stream):
-            if isinstance(out, str):
+        if isinstance(out, str):
+            with _on(stream):
                 out = torch.empty(x.shape, dtype=_BF16, device=x.device) if out == "bf16" else \
                     MxTensor.empty(out, *x.shape, device=x.device)
-            if residual is not None and residual_out is None:
+        if residual is not None and residual_out is None:
+            with _on(stream):
                 residual_out = torch.empty_like(residual)
-        codes, scales = (out.codes, out.scales) if isinstance(out, MxTensor) else (out, None)
+        mx, codes, scales = (out._spec, out.codes, out.scales) if isinstance(out, MxTensor) else (None, out, None)
+        if _fast is not None:
+            raw = _raw_stream(self._spec[0]) if stream is None else _stream(stream)
+            rc = _fast.add_norm(self._h, self._spec, x, residual, w, mx, codes, scales, residual_out, raw)
+            if rc is not None:
+                _check(rc, "pkv_add_norm")
+                return out, residual_out
         _on_device(self._spec[0], x=x, residual=residual, w=w, out=codes, scales=scales, residual_out=residual_out)
         pkv_add_norm(self.handle, x, residual, w, out, residual_out, stream)
         return out, residual_out
 
-    def mx_quantize(self, x, kind="mx8", out=None, stream=None) -> MxTensor:
-        """bf16 x [rows][cols] as a microscaled tensor of that kind."""
+    def mx_quantize(self, x, kind=None, out=None, stream=None) -> MxTensor:
+        """bf16 x [rows][cols] as a microscaled tensor of that kind ("mx8" if neither it nor out is given)."""
         if out is None:
             with _on(stream):
-                out = MxTensor.empty(kind, *x.shape, device=x.device)
-        elif out.kind != kind:
+                out = MxTensor.empty(kind or "mx8", *x.shape, device=x.device)
+        elif kind is not None and out.kind != kind:
             raise ValueError(f"out is {out.kind}, kind {kind}")
+        if _fast is not None:
+            raw = _raw_stream(self._spec[0]) if stream is None else _stream(stream)
+            rc = _fast.mx_quantize(self._h, self._spec, x, out._spec, out.codes, out.scales, raw)
+            if rc is not None:
+                _check(rc, "pkv_mx_quantize")
+                return out
         _on_device(self._spec[0], x=x, codes=out.codes, scales=out.scales)
         pkv_mx_quantize(self.handle, x, out, stream)
         return out
@@ -748,6 +762,12 @@ class _Pool:
         if out is None:
             with _on(stream):
                 out = torch.empty(x.shape, dtype=_BF16, device=x.device)
+        if _fast is not None:
+            raw = _raw_stream(self._spec[0]) if stream is None else _stream(stream)
+            rc = _fast.mx_read(self._h, self._spec, x._spec, x.codes, x.scales, out, raw)
+            if rc is not None:
+                _check(rc, "pkv_mx_read")
+                return out
         _on_device(self._spec[0], codes=x.codes, scales=x.scales, out=out)
         pkv_mx_read(self.handle, x, out, stream)
         return out
@@ -759,6 +779,12 @@ class _Pool:
         if y is None:
             with _on(stream):
                 y = torch.empty(x.rows, w.rows, dtype=_BF16, device=x.device)
+        if _fast is not None:
+            raw = _raw_stream(self._spec[0]) if stream is None else _stream(stream)
+            rc = _fast.mx_linear(self._h, self._spec, x._spec, x.codes, x.scales, w._spec, w.codes, w.scales, y, raw)
+            if rc is not None:
+                _check(rc, "pkv_mx_linear")
+                return y
         _on_device(self._spec[0], x=x.codes, x_scales=x.scales, w=w.codes, w_scales=w.scales, y=y)
         pkv_mx_linear(self.handle, x, w, y, stream)
         return y
@@ -768,9 +794,17 @@ class _Pool:
         if not isinstance(x, MxTensor):
             x = self.mx_quantize(x, w_qkv.kind, stream=stream)
         heads, kv_heads, dim = self._shape
-        with _on(stream):
-            q, k, v = (torch.empty(x.rows, n, dim, dtype=_BF16, device=x.device) if t is None else t
-                       for t, n in ((q, heads), (k, kv_heads), (v, kv_heads)))
+        if q is None or k is None or v is None:
+            with _on(stream):
+                q, k, v = (torch.empty(x.rows, n, dim, dtype=_BF16, device=x.device) if t is None else t
+                           for t, n in ((q, heads), (k, kv_heads), (v, kv_heads)))
+        if _fast is not None:
+            raw = _raw_stream(self._spec[0]) if stream is None else _stream(stream)
+            rc = _fast.mx_qkv_proj(self._h, self._spec, x._spec, x.codes, x.scales, w_qkv._spec, w_qkv.codes, w_qkv.scales,
+                                   q, k, v, raw)
+            if rc is not None:
+                _check(rc, "pkv_mx_qkv_proj")
+                return q, k, v
         for name, t, n in (("q", q, heads), ("k", k, kv_heads), ("v", v, kv_heads)):
             if tuple(t.shape) != (x.rows, n, dim):
                 raise ValueError(f"{name} must be {[x.rows, n, dim]}, got {list(t.shape)}")

@@ -1,4 +1,4 @@
-// The short way from Python to four calls of libpkv: a CPython module that checks
+// The short way from Python to nine calls of libpkv: a CPython module that checks
 // the torch tensors of a call and passes their pointers on, as the ctypes functions
 // of the binding do, in a tenth of the time (a decode step of a few rows runs for 6 us
 // on the GPU; its checks take 4 us in Python and 0.4 us here).
@@ -25,10 +25,20 @@ using Read = int (*)(void*, const int32_t*, const int32_t*, const int32_t*, int,
                      void*);
 using NormRope = int (*)(void*, const void*, const void*, const void*, const void*, const int32_t*, int, int, int,
                          int64_t, int64_t, void*, void*, int64_t, int64_t, void*);
+using Quantize = int (*)(void*, const void*, int64_t, int, int, int, void*, void*, void*);
+using MxRead = int (*)(void*, int, const void*, const void*, int, int, void*, int64_t, void*);
+using AddNorm = int (*)(void*, const void*, int64_t, const void*, void*, const void*, int, int, int, void*, void*, void*);
+using MxLinear = int (*)(void*, int, const void*, const void*, const void*, const void*, void*, int, int, int, void*);
+using MxQkv = int (*)(void*, int, const void*, const void*, const void*, const void*, int, int, void*, void*, void*, void*);
 Decode g_decode;
 Append g_append;
 Read g_read;
 NormRope g_norm_rope;
+Quantize g_quantize;
+MxRead g_mx_read;
+AddNorm g_add_norm;
+MxLinear g_mx_linear;
+MxQkv g_mx_qkv;
 
 struct Bad {};  // an argument that the binding's own checks shall see
 
@@ -95,6 +105,14 @@ struct Pool {
         need(t.dim() == 3 && t.size(0) == tokens && t.size(1) == h && t.size(2) == dim && t.stride(2) == 1 &&
              (h == 1 || t.stride(1) == dim));
         *stride = tokens > 1 ? t.stride(0) : h * dim;
+        return t.data_ptr();
+    }
+    // [rows][cols] bf16, contiguous rows, any row stride (stride null: contiguous)
+    void* matrix(PyObject* o, int64_t rows, int64_t cols, int64_t* stride) const
+    {
+        const at::Tensor& t = tensor(o, at::kBFloat16);
+        need(t.dim() == 2 && t.size(0) == rows && t.size(1) == cols && (stride ? t.stride(1) == 1 : t.is_contiguous()));
+        if (stride) *stride = rows > 1 ? t.stride(0) : cols;
         return t.data_ptr();
     }
     const void* weight(PyObject* o) const
@@ -254,18 +272,143 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
-// bind(decode, append, read, norm_rope): the addresses of libpkv's entries
+// A microscaled tensor: (kind, rows, cols), its codes and its scales.
+struct Mx {
+    int kind;
+    int64_t rows, cols;
+    void *codes, *scales;
+    Mx(const Pool& p, PyObject* spec, PyObject* c, PyObject* s)
+    {
+        need(PyTuple_Check(spec) && PyTuple_GET_SIZE(spec) == 3);
+        kind = (int)number(PyTuple_GET_ITEM(spec, 0));
+        rows = number(PyTuple_GET_ITEM(spec, 1));
+        cols = number(PyTuple_GET_ITEM(spec, 2));
+        need((kind == 2 || kind == 3) && rows > 0 && rows <= INT32_MAX && cols > 0 && cols <= INT32_MAX && cols % 128 == 0);
+        codes = bytes(p, c, kind == 2 ? rows * cols : rows * (cols / 2));
+        scales = bytes(p, s, (rows + 127) / 128 * (cols / 128) * 512);
+    }
+    static void* bytes(const Pool& p, PyObject* o, int64_t n)
+    {
+        const at::Tensor& t = p.tensor(o, at::kByte);
+        need(t.numel() == n && t.is_contiguous());
+        return t.data_ptr();
+    }
+};
+
+// mx_quantize(handle, spec, x, mx, codes, scales, stream)
+PyObject* mx_quantize(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return checked([&] {
+        need(n == 7 && g_quantize);
+        const Pool p(a[0], a[1]);
+        const Mx m(p, a[3], a[4], a[5]);
+        int64_t stride;
+        void *x = p.matrix(a[2], m.rows, m.cols, &stride), *stream = address(a[6]);
+        return without_gil([&] {
+            return g_quantize(p.handle, x, stride, (int)m.rows, (int)m.cols, m.kind, m.codes, m.scales, stream);
+        });
+    });
+}
+
+// mx_read(handle, spec, mx, codes, scales, y, stream)
+PyObject* mx_read(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return checked([&] {
+        need(n == 7 && g_mx_read);
+        const Pool p(a[0], a[1]);
+        const Mx m(p, a[2], a[3], a[4]);
+        int64_t stride;
+        void *y = p.matrix(a[5], m.rows, m.cols, &stride), *stream = address(a[6]);
+        return without_gil([&] {
+            return g_mx_read(p.handle, m.kind, m.codes, m.scales, (int)m.rows, (int)m.cols, y, stride, stream);
+        });
+    });
+}
+
+// add_norm(handle, spec, x, residual, w, mx, out, scales, residual_out, stream); mx None: out is bf16
+PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return checked([&] {
+        need(n == 10 && g_add_norm);
+        const Pool p(a[0], a[1]);
+        const at::Tensor& t = p.tensor(a[2], at::kBFloat16);
+        need(t.dim() == 2 && t.size(0) <= INT32_MAX && t.size(1) <= INT32_MAX);
+        const int64_t tokens = t.size(0), hidden = t.size(1);
+        int64_t stride;
+        const void* x = p.matrix(a[2], tokens, hidden, &stride);
+        need((a[3] == Py_None) == (a[8] == Py_None));
+        const void* residual = a[3] == Py_None ? nullptr : p.matrix(a[3], tokens, hidden, nullptr);
+        void* residual_out = a[8] == Py_None ? nullptr : p.matrix(a[8], tokens, hidden, nullptr);
+        const at::Tensor& w = p.tensor(a[4], at::kBFloat16);
+        need(w.numel() == hidden && w.is_contiguous());
+        int kind = 0;
+        void *out, *scales = nullptr;
+        if (a[5] == Py_None) {
+            out = p.matrix(a[6], tokens, hidden, nullptr);
+        } else {
+            const Mx m(p, a[5], a[6], a[7]);
+            need(m.rows == tokens && m.cols == hidden);
+            kind = m.kind, out = m.codes, scales = m.scales;
+        }
+        const void* wp = w.data_ptr();
+        void* stream = address(a[9]);
+        return without_gil([&] {
+            return g_add_norm(p.handle, x, stride, residual, residual_out, wp, (int)tokens, (int)hidden, kind, out, scales,
+                              stream);
+        });
+    });
+}
+
+// mx_linear(handle, spec, x's mx, codes, scales, w's mx, codes, scales, y, stream)
+PyObject* mx_linear(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return checked([&] {
+        need(n == 10 && g_mx_linear);
+        const Pool p(a[0], a[1]);
+        const Mx x(p, a[2], a[3], a[4]), w(p, a[5], a[6], a[7]);
+        need(x.kind == w.kind && x.cols == w.cols);
+        void *y = p.matrix(a[8], x.rows, w.rows, nullptr), *stream = address(a[9]);
+        return without_gil([&] {
+            return g_mx_linear(p.handle, x.kind, x.codes, x.scales, w.codes, w.scales, y, (int)x.rows, (int)x.cols,
+                               (int)w.rows, stream);
+        });
+    });
+}
+
+// mx_qkv_proj(handle, spec, x's mx, codes, scales, w's mx, codes, scales, q, k, v, stream)
+PyObject* mx_qkv_proj(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return checked([&] {
+        need(n == 12 && g_mx_qkv);
+        const Pool p(a[0], a[1]);
+        const Mx x(p, a[2], a[3], a[4]), w(p, a[5], a[6], a[7]);
+        need(x.kind == w.kind && x.cols == w.cols && w.rows == (p.heads + 2 * p.kv_heads) * p.dim);
+        void *q = p.heads_of(a[8], x.rows, p.heads), *k = p.heads_of(a[9], x.rows, p.kv_heads),
+             *v = p.heads_of(a[10], x.rows, p.kv_heads), *stream = address(a[11]);
+        return without_gil([&] {
+            return g_mx_qkv(p.handle, x.kind, x.codes, x.scales, w.codes, w.scales, (int)x.rows, (int)x.cols, q, k, v, stream);
+        });
+    });
+}
+
+// bind(decode, append, read, norm_rope, mx_quantize, mx_read, add_norm, mx_linear, mx_qkv_proj): the addresses of
+// libpkv's entries
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     try {
-        need(n == 4);
+        need(n == 9);
         g_decode = reinterpret_cast<Decode>(address(a[0]));
         g_append = reinterpret_cast<Append>(address(a[1]));
         g_read = reinterpret_cast<Read>(address(a[2]));
         g_norm_rope = reinterpret_cast<NormRope>(address(a[3]));
+        g_quantize = reinterpret_cast<Quantize>(address(a[4]));
+        g_mx_read = reinterpret_cast<MxRead>(address(a[5]));
+        g_add_norm = reinterpret_cast<AddNorm>(address(a[6]));
+        g_mx_linear = reinterpret_cast<MxLinear>(address(a[7]));
+        g_mx_qkv = reinterpret_cast<MxQkv>(address(a[8]));
     } catch (const Bad&) {
         PyErr_Clear();
-        PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+        PyErr_SetString(PyExc_TypeError, "bind takes nine addresses");
         return nullptr;
     }
     Py_RETURN_NONE;
@@ -278,7 +421,9 @@ PyMethodDef method(const char* name)
 }
 
 PyMethodDef g_methods[] = {method<decode>("decode"), method<append>("append"),       method<read>("read"),
-                           method<norm_rope>("norm_rope"), method<bind>("bind"), {nullptr, nullptr, 0, nullptr}};
+                           method<norm_rope>("norm_rope"), method<mx_quantize>("mx_quantize"), method<mx_read>("mx_read"),
+                           method<add_norm>("add_norm"), method<mx_linear>("mx_linear"), method<mx_qkv_proj>("mx_qkv_proj"),
+                           method<bind>("bind"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_pkv_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

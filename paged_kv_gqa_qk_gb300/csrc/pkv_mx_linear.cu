@@ -282,6 +282,7 @@ cudaError_t launch_mx_linear(const pkv_pool* pool, const MxLinear& a, cudaStream
     p.in = a.in;
     p.out = p.seg_end[2];
     p.row_blocks = (a.tokens + 127) / 128;
+    if (a.tokens > 256) return launch_mx_pair(pool, a, s);
     return a.type == PKV_MX8 ? launch_type<PKV_MX8>(pool, a, p, s) : launch_type<PKV_MX4>(pool, a, p, s);
 }
 

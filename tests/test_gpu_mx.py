@@ -216,6 +216,10 @@ def check_product(y, x, w):
     (200, 4096, 512),
     (333, 896, 1280),
     (700, 2048, 1536),      # more tiles than one a SM
+    (257, 128, 128),        # one token beyond a tile, half a tile of features, less than a stage in 4 bits
+    (1025, 1152, 640),      # a 4-bit row of a stage and a half, features of two tiles and a half
+    (5000, 256, 1280),      # many tiles of few stages
+    (384, 8192, 256),       # a long row
 ])
 def test_linear(pool, kind, tokens, n_in, n_out):
     x, w = operands(tokens, n_in, n_out, kind, seed=tokens + n_in + n_out)
@@ -225,3 +229,23 @@ def test_linear(pool, kind, tokens, n_in, n_out):
     check_product(y, _mx.stored(xm), _mx.stored(wm))
     assert torch.equal(pool.mx_linear(x, wm), y)        # bf16 x: quantised to the weights' kind first
     assert torch.equal(pool.mx_linear(xm, wm), y)       # the same from run to run
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kv_heads", [1, 2, 3])
+@pytest.mark.parametrize("tokens", [1, 70, 300])
+def test_qkv_proj(kind, kv_heads, tokens):
+    """q, k and v are the columns of the one product (tiles that span them included)."""
+    z = torch.zeros(2, kv_heads, 64, 128, dtype=torch.bfloat16, device=DEV)
+    p = pkv.PagedKVPool(z[0], z[1], cfg=dict(heads=4 * kv_heads, kv_heads=kv_heads, max_seq=64))
+    x, w = operands(tokens, 640, 6 * kv_heads * 128, kind, seed=tokens)
+    xm, wm = p.mx_quantize(x, kind), p.mx_quantize(w, kind)
+    q, k, v = p.mx_qkv_proj(xm, wm)
+    assert q.shape == (tokens, 4 * kv_heads, 128) and k.shape == v.shape == (tokens, kv_heads, 128)
+    y = p.mx_linear(xm, wm)
+    check_product(y, _mx.stored(xm), _mx.stored(wm))
+    assert torch.equal(torch.cat([q.flatten(1), k.flatten(1), v.flatten(1)], 1), y)
+    for got, ref in zip(p.mx_qkv_proj(x, wm), (q, k, v)):
+        assert torch.equal(got, ref)
+    assert p.check_errors() == 0
+    p.close()

@@ -19,7 +19,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 // 16 lanes take 128 columns of a row, 8 each; a group of 32 is 4 lanes.
 template <int kType, int kPasses>
 __global__ void __launch_bounds__(256)
-    mx_quantize_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride, int rows, int cols, uint8_t* codes,
+    mx_quantize_kernel(const __nv_bfloat16* x, int64_t x_stride, int rows, int cols, uint8_t* codes,
                        uint8_t* scales)
 {
     const int tiles = cols / kMxTileCols, tile = blockIdx.x % tiles;
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256)
 // ---- microscaled -> bf16 ----
 template <int kType, int kPasses>
 __global__ void __launch_bounds__(256)
-    mx_read_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int rows, int cols,
+    mx_read_kernel(const uint8_t* codes, const uint8_t* scales, int rows, int cols,
                    __nv_bfloat16* y, int64_t y_stride)
 {
     const int tiles = cols / kMxTileCols, tile = blockIdx.x % tiles;

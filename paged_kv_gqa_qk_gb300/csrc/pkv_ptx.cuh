@@ -276,8 +276,8 @@ __device__ __forceinline__ void umma_copy_scales(uint32_t taddr, uint32_t saddr)
 
 // ---- the same over a CTA pair (cta_group::2) ---------------------------------------------
 // One thread of the even CTA issues for both: A is 128 rows of each CTA's shared memory, B half of N
-// in each, the accumulator 128 rows in each CTA's tensor memory.  Scales: A's own rows and all of
-// B's in each CTA, copied at both by one instruction from the same shared-memory offsets.
+// in each, the accumulator 128 rows in each CTA's tensor memory.  Scales: those of A's own rows
+// and all of B's in each CTA's.
 template <bool kFourBits>
 __device__ __forceinline__ void umma_mx_pair(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                              uint32_t sfb, bool accumulate)
@@ -296,12 +296,6 @@ __device__ __forceinline__ void umma_mx_pair(uint32_t tmem_d, uint64_t a, uint64
                 tmem_d),
             "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(sfa), "r"(sfb)
             : "memory");
-}
-
-__device__ __forceinline__ void umma_copy_scales_pair(uint32_t taddr, uint32_t saddr)
-{
-    const uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
 // Arrive on the barrier at `bar`'s offset of both CTAs when this thread's operations have completed.
@@ -340,6 +334,14 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The same without ordering this thread's memory operations before it: for what is handed over in
+// tensor memory alone, after tcgen05.wait (a release at cluster scope waits for the thread's loads
+// in flight).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Bring a box of global memory into L2.
@@ -429,6 +431,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+// 4 consecutive columns.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint4 r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r.x), "r"(r.y), "r"(r.z),
+                 "r"(r.w)
+                 : "memory");
 }
 
 // 32 consecutive columns; complete with tmem_wait_ld().

@@ -13,6 +13,17 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// One lane of a converged warp.  Code that issues tensor-core products or bulk copies runs its loop
+// with the whole warp and issues under this: in a branch that one thread alone has taken, every such
+// instruction costs some 120 cycles, since its operands, which the instruction takes from the warp's
+// common registers, are no longer known to be the same in all lanes.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // ---- mbarrier ---------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
@@ -243,6 +254,9 @@ __host__ __device__ constexpr uint32_t umma_idesc_mx(bool four_bits, int M, int 
            ((uint32_t)(M >> 7) << 27) | ((uint32_t)sf << 29);
 }
 
+// The descriptor's bits of another sf, to be added to one of sf 0.
+__host__ __device__ constexpr uint32_t umma_idesc_sf(int sf) { return ((uint32_t)sf << 4) | ((uint32_t)sf << 29); }
+
 // D(tmem) (+)= (A scaled by sfa)(smem) * (B scaled by sfb)(smem); issued by one thread.
 template <bool kFourBits>
 __device__ __forceinline__ void umma_mx(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
@@ -361,7 +375,7 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int 
                  : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Barrier `id` (1..15) among `threads` threads of the CTA.

@@ -171,6 +171,20 @@ bool make_tmap_bytes(CUtensorMap* map, const void* base, uint64_t row_bytes, uin
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_scales(CUtensorMap* map, const void* base, int tiles, int row_blocks, int box_tiles, int box_blocks)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)tiles * 128, (cuuint64_t)row_blocks};
+    cuuint64_t strides[1] = {(cuuint64_t)tiles * 512};
+    cuuint32_t box[2] = {(cuuint32_t)box_tiles * 128, (cuuint32_t)box_blocks};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_heads(CUtensorMap* map, const void* base, int heads, int tokens)
 {
     auto fn = encode_fn();

@@ -241,6 +241,9 @@ cudaError_t configure_mx_pair(pkv_pool* pool);
 // 2-D tiled tensor map of a row-major byte matrix (128-byte swizzle, zero fill past the
 // edges), boxes of 128 bytes by `box_rows`; false if the driver refuses it.
 bool make_tmap_bytes(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
+// The scales of a microscaled tensor as a matrix of 512-byte tiles, boxes of box_tiles by
+// box_blocks of them, one row of tiles behind the other (zero fill past the edges).
+bool make_tmap_scales(CUtensorMap* map, const void* base, int tiles, int row_blocks, int box_tiles, int box_blocks);
 
 // Per-device kernel attributes (dynamic shared memory); called with the
 // pool's device current when a pool is created.

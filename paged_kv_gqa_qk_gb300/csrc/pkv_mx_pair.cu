@@ -20,7 +20,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 448;                 // 4 warps of scales, 2 x 4 of the epilogue, the producer's, the products'
+constexpr int kThreads = 480;                 // 4 warps of scales, 2 x 4 of the epilogue, products, operands' and scales' loads
 constexpr int kSpan = 128;                    // bytes of a row a stage
 constexpr int kTileM = 256, kTileN = 192;     // tokens, output features at most
 constexpr int kUnit = 64;                     // features that the pairs share out
@@ -44,12 +44,11 @@ struct Shape {
 };
 
 struct Maps {
-    CUtensorMap x, w, y[3];
+    CUtensorMap x, w, sfx, sfw, y[3];
 };
 
 struct Params {
     uint32_t* err;
-    const uint8_t *x_scales, *w_scales;
     int seg_end[3];
     int tokens, in, out, units;  // units: of 64 features in a row of tiles
 };
@@ -75,6 +74,16 @@ struct Walk {
         n = (left + tiles - 1) / tiles;
         at += n;
         return true;
+    }
+};
+
+// Stages of the ring in turn, with the parity of the barriers' present phase.
+struct Ring {
+    int st = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++st == kStages) st = 0, parity ^= 1;
     }
 };
 
@@ -107,6 +116,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         tma_prefetch_desc(&maps.x);
         tma_prefetch_desc(&maps.w);
+        tma_prefetch_desc(&maps.sfx);
+        tma_prefetch_desc(&maps.sfw);
     }
     if (warp == 13) tmem_alloc_pair(base + S::kTmemSlot, S::kCols);
     tc_fence_before();
@@ -119,19 +130,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         // ---- scales: row 32 j + lane of a block to column j, the same in each warp's quarter of the lanes
         const uint32_t to = tmem + ((uint32_t)(32 * warp) << 16) + S::kSfCol, bar0 = cluster_map(bar_ready, 0);
-        int it = 0;
+        Ring ring;
         bool ok = true;
-        while (ok && walk.next())
-            for (int k = 0; k < nk; ++k, ++it) {
-                const int st = it % kStages;
-                ok = __all_sync(0xffffffffu, mbar_wait_spin(bar_landed + 8 * st, (it / kStages) & 1));
-                if (!ok) {
-                    if (lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
-                    break;
-                }
+        while (walk.next())
+            for (int k = 0; k < nk; ++k, ring.next()) {
+                ok &= mbar_wait_spin(bar_landed + 8 * ring.st, ring.parity, ok ? kWaitLimitNs : 0);
                 tc_fence_after();  // (the stage's columns: its last products were done before it was loaded again)
-                const uint4* from = reinterpret_cast<const uint4*>(sbase + S::kSf + st * 3 * S::kSfBlock) + lane;
-                const uint32_t at = to + st * S::kSfCols;
+                const uint4* from = reinterpret_cast<const uint4*>(sbase + S::kSf + ring.st * 3 * S::kSfBlock) + lane;
+                const uint32_t at = to + ring.st * S::kSfCols;
 #pragma unroll
                 for (int s = 0; s < S::kSfTiles; ++s) {
                     tmem_st4(at + 4 * s, from[32 * s]);
@@ -141,58 +147,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(bar0 + 8 * st);
+                if (lane == 0) mbar_arrive_cluster_relaxed(bar0 + 8 * ring.st);
             }
+        if (!ok && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 12) {
-        // ---- producer: operands complete on the even CTA's barrier, scales on this CTA's
-        const uint64_t keep = l2_policy_evict_last();  // both operands are read again by other pairs
-        int it = 0;
-        bool ok = true;
+        // ---- operands: they complete on the even CTA's barrier
+        const uint64_t keep = l2_policy_evict_last();  // both are read again by other pairs
+        Ring ring;
+        bool ok = true, again = false;
         while (walk.next()) {
-            const int m0 = walk.m * kTileM + (int)rank * 128, f0 = walk.f * kUnit;
-            const int n0 = f0 + (int)rank * (walk.n * kUnit / 2);  // (rows beyond half of the tile are not used)
-            const uint8_t* sx = p.x_scales + (int64_t)(m0 / 128) * sf_tiles * kMxTileBytes;
-            const uint8_t* sw = p.w_scales + (int64_t)(f0 / 128) * sf_tiles * kMxTileBytes;
-            const bool has_x = m0 < p.tokens, has_w = f0 / 128 * 128 + 128 < p.out;  // (else unused: nothing to load)
-            for (int k = 0; k < nk; ++k, ++it) {
-                const int st = it % kStages;
-                if (it >= kStages) ok &= mbar_wait_spin(bar_empty + 8 * st, ((it / kStages) - 1) & 1, ok ? kWaitLimitNs : 0);
+            const int m0 = walk.m * kTileM + (int)rank * 128;
+            const int n0 = walk.f * kUnit + (int)rank * (walk.n * kUnit / 2);  // (rows beyond half of the tile are not used)
+            for (int k = 0; k < nk; ++k, ring.next()) {
+                if (again) ok &= mbar_wait_spin(bar_empty + 8 * ring.st, ring.parity ^ 1, ok ? kWaitLimitNs : 0);
                 if (elect_one() && ok) {
-                    const uint32_t a = base + st * S::kStageBytes, sf = base + S::kSf + st * 3 * S::kSfBlock;
-                    const uint32_t bar = bar_landed + 8 * st, ready = bar_ready + 8 * st;
-                    const uint32_t bytes = min(S::kSfTiles, sf_tiles - k * S::kSfTiles) * kMxTileBytes;
-                    const int64_t at = (int64_t)k * S::kSfBlock;
-                    if (rank == 0) mbar_arrive_expect_tx(ready, 2 * S::kStageBytes);
-                    tma_load_2d_pair(a, &maps.x, k * kSpan, m0, ready, keep);
-                    tma_load_2d_pair(a + S::kA, &maps.w, k * kSpan, n0, ready, keep);
-                    mbar_arrive_expect_tx(bar, (1 + has_x + has_w) * bytes);
-                    if (has_x) bulk_copy_g2s(sf, sx + at, bytes, bar);
-                    bulk_copy_g2s(sf + S::kSfBlock, sw + at, bytes, bar);
-                    if (has_w) bulk_copy_g2s(sf + 2 * S::kSfBlock, sw + (int64_t)sf_tiles * kMxTileBytes + at, bytes, bar);
+                    const uint32_t a = base + ring.st * S::kStageBytes, bar = bar_ready + 8 * ring.st;
+                    if (rank == 0) mbar_arrive_expect_tx(bar, 2 * S::kStageBytes);
+                    tma_load_2d_pair(a, &maps.x, k * kSpan, m0, bar, keep);
+                    tma_load_2d_pair(a + S::kA, &maps.w, k * kSpan, n0, bar, keep);
                 }
                 __syncwarp();
+                again |= ring.st == kStages - 1;
             }
         }
         // the last stages' products are done with this CTA's ring and barriers before it leaves
-        for (int i = it > kStages ? it - kStages : 0; i < it; ++i)
-            ok &= mbar_wait_spin(bar_empty + 8 * (i % kStages), (i / kStages) & 1, ok ? kWaitLimitNs : 0);
+        for (int i = 0; i < kStages; ++i, ring.next())
+            if (again || ring.parity) ok &= mbar_wait_spin(bar_empty + 8 * ring.st, ring.parity ^ 1, ok ? kWaitLimitNs : 0);
+        if (!ok && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+    } else if (warp == 14) {
+        // ---- scales: x's block of 128 tokens and W's two of features, on this CTA's barrier
+        const uint64_t keep = l2_policy_evict_last();
+        Ring ring;
+        bool ok = true, again = false;
+        while (walk.next()) {
+            const int mb = walk.m * 2 + (int)rank, nb = walk.f / 2;
+            for (int k = 0; k < nk; ++k, ring.next()) {
+                if (again) ok &= mbar_wait_spin(bar_empty + 8 * ring.st, ring.parity ^ 1, ok ? kWaitLimitNs : 0);
+                if (elect_one() && ok) {
+                    const uint32_t to = base + S::kSf + ring.st * 3 * S::kSfBlock, bar = bar_landed + 8 * ring.st;
+                    mbar_arrive_expect_tx(bar, 3 * S::kSfBlock);
+                    tma_load_2d(to, &maps.sfx, k * S::kSfTiles * 128, mb, bar, keep);
+                    tma_load_2d(to + S::kSfBlock, &maps.sfw, k * S::kSfTiles * 128, nb, bar, keep);
+                }
+                __syncwarp();
+                again |= ring.st == kStages - 1;
+            }
+        }
         if (!ok && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 13) {
         if (rank == 0) {
             // ---- products of the pair (a wait that ran out does not end the loop, which would make its
             // counters differ between lanes: the later waits are single looks, the results are void)
-            int it = 0;
+            Ring ring;
             bool ok = true;
             for (int done = 0; walk.next(); ++done) {
                 const uint32_t half = done & 1, acc = tmem + half * kTileN;
                 if (done >= 2) ok &= mbar_wait_spin(bar_free + 8 * half, (done / 2 - 1) & 1, ok ? kWaitLimitNs : 0);
                 const uint32_t shape = umma_idesc_mx(kType == PKV_MX4, kTileM, 0, 0) | ((uint32_t)(walk.n * kUnit / 8) << 17);
                 const uint32_t odd = walk.f & 1 ? 2 : 0;  // columns: the tile starts in the middle of a block of 128
-                for (int k = 0; k < nk; ++k, ++it) {
-                    const int st = it % kStages;
-                    ok &= mbar_wait_spin(bar_ready + 8 * st, (it / kStages) & 1, ok ? kWaitLimitNs : 0);
+                for (int k = 0; k < nk; ++k, ring.next()) {
+                    ok &= mbar_wait_spin(bar_ready + 8 * ring.st, ring.parity, ok ? kWaitLimitNs : 0);
                     tc_fence_after();
-                    const uint32_t a = base + st * S::kStageBytes, sfc = tmem + S::kSfCol + st * S::kSfCols;
+                    const uint32_t a = base + ring.st * S::kStageBytes, sfc = tmem + S::kSfCol + ring.st * S::kSfCols;
                     const int have = min(S::kSfTiles, sf_tiles - k * S::kSfTiles);
                     const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(a + S::kA, 16, 1024);
                     constexpr int kPer = 4 / S::kSfTiles;  // products a tile of scales
@@ -205,7 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                                shape | umma_idesc_sf(kk % kPer * (4 / kPer)), sfc + 4 * s,
                                                                sfc + 4 * S::kSfTiles + 8 * s + odd, k > 0 || kk > 0);
                         }
-                        umma_commit_pair(bar_empty + 8 * st);
+                        umma_commit_pair(bar_empty + 8 * ring.st);
                         if (k == nk - 1) umma_commit_pair(bar_acc + 8 * half);
                     }
                     __syncwarp();
@@ -289,11 +305,11 @@ cudaError_t launch(const pkv_pool* pool, const MxLinear& a, cudaStream_t s)
         else if (!make_tmap_2d(&m.y[i], a.y[i], a.widths[i], a.tokens, (uint64_t)a.widths[i] * 2, 64, 128))
             return cudaErrorInvalidValue;
     }
-    const int row = mx_row_bytes(kType, a.in);
-    if (!make_tmap_bytes(&m.x, a.x_codes, row, a.tokens, 128) || !make_tmap_bytes(&m.w, a.w_codes, row, end, kTileN / 2))
+    const int row = mx_row_bytes(kType, a.in), sf_tiles = a.in / kMxTileCols;
+    if (!make_tmap_bytes(&m.x, a.x_codes, row, a.tokens, 128) || !make_tmap_bytes(&m.w, a.w_codes, row, end, kTileN / 2) ||
+        !make_tmap_scales(&m.sfx, a.x_scales, sf_tiles, (a.tokens + 127) / 128, S::kSfTiles, 1) ||
+        !make_tmap_scales(&m.sfw, a.w_scales, sf_tiles, end / 128, S::kSfTiles, 2))
         return cudaErrorInvalidValue;
-    p.x_scales = static_cast<const uint8_t*>(a.x_scales);
-    p.w_scales = static_cast<const uint8_t*>(a.w_scales);
     p.err = pool->err;
     p.tokens = a.tokens;
     p.in = a.in;

@@ -5,12 +5,13 @@
 // v_proj, o_proj), with both operands held as codes of 8 or 4 bits and a power of two on every
 // 32 of them: y[t][o] = sum_g 2^(ex + ew) sum_{k in g} x[t][k] w[o][k].
 //
-// A CTA computes 128 output features x BN tokens, D = W_tile x_tile^T, in tensor memory
-// (lane = feature, column = token).  A stage of its ring holds 128 bytes of every row (128
-// or 256 values) and their scales' tiles; one thread copies the scales to tensor memory
-// and issues the four products of a stage.  Where the tiles alone would leave SMs idle,
-// the input features are split over the CTAs of a cluster, which sum their tiles over
-// distributed shared memory in a fixed order.
+// The kernel here is for few tokens, where reading W bounds the product; pkv_mx_pair.cu has the
+// one for many.  A CTA computes 128 output features x BN tokens, D = W_tile x_tile^T, in tensor
+// memory (lane = feature, column = token).  A stage of its ring holds 128 bytes of every row
+// (128 or 256 values) and their scales' tiles; one warp copies the scales to tensor memory and
+// issues the four products of a stage.  The input features are split over the CTAs of a cluster,
+// so that every SM has a part of W to read; each CTA sends its sums of a part of the tokens to
+// each other, which adds those of its tokens in the CTAs' order.
 #include <type_traits>
 
 #include "pkv_mx.cuh"
@@ -27,20 +28,16 @@ constexpr int kMaxSplits = 8;   // a portable cluster
 template <int kType, int BN>
 struct Shape {
     static constexpr int kSfTiles = kType == PKV_MX4 ? 2 : 1;       // tiles of scales a stage and 128 rows
-    static constexpr int kRowBlocks = (BN + 127) / 128;
-    static constexpr int kABytes = kBM * kSpan, kBBytes = BN * kSpan;
-    static constexpr int kSfA = kSfTiles * kMxTileBytes, kSfB = kRowBlocks * kSfA;
-    static constexpr int kStageBytes = (kABytes + kBBytes + kSfA + kSfB + 1023) / 1024 * 1024;
-    static constexpr int kStages = BN == 64 ? 4 : (200 * 1024) / kStageBytes;
-    static_assert(kStages * kStageBytes >= kBM * BN * 4, "the ring holds the fp32 partial tile");
-    static constexpr int kBars = kStages * kStageBytes;  // full[S], empty[S], done
-    static constexpr int kTmemSlot = kBars + 8 * (2 * kStages + 1);
-    static constexpr int kAlloc = kTmemSlot + 16 + 1024;
+    static constexpr int kABytes = kBM * kSpan, kBBytes = BN * kSpan, kSf = kSfTiles * kMxTileBytes;
+    static constexpr int kStageBytes = kABytes + kBBytes + 2 * kSf;
+    static_assert(kStageBytes % 1024 == 0, "operands on 1024-byte borders");
+    static constexpr int kSums = kBM * BN * 4;                      // the cluster's sums of this CTA's tokens
+    static constexpr int kMost = (BN <= 32 ? 112 : 220) * 1024;     // shared memory: two CTAs an SM, or one
+    static constexpr int kMaxStages = (kMost - kSums - 2048) / kStageBytes;
     // tensor memory: the accumulator, then the scales of W and of x, 4 columns a tile
-    static constexpr int kSfaCol = BN, kSfbCol = BN + 4 * kSfTiles;
-    static constexpr int kCols = BN == 64 ? 128 : BN == 128 ? 256 : 512;
-    static_assert(kSfbCol + 4 * kSfTiles * kRowBlocks <= kCols, "columns");
-    static_assert(kAlloc <= 227 * 1024, "shared memory");
+    static constexpr int kSfaCol = BN, kSfbCol = BN + 4 * kSfTiles, kUsed = kSfbCol + 4 * kSfTiles;
+    static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : 128;
+    static constexpr int alloc(int stages) { return stages * kStageBytes + kSums + 8 * (2 * stages + 1) + 16 + 1024; }
 };
 
 struct Params {
@@ -48,7 +45,7 @@ struct Params {
     __nv_bfloat16* y[3];
     int seg_end[3];     // cumulative widths; seg_end[2] == out
     uint32_t* err;
-    int tokens, in, out, splits, row_blocks;  // row_blocks: of 128 tokens, in x's scales
+    int tokens, in, out, stages;
 };
 
 // The segment holding output features from m0: its tensor, its width and the tile's column in it.
@@ -61,211 +58,263 @@ __device__ __forceinline__ __nv_bfloat16* segment(const Params& p, int m0, int& 
     return p.y[s];
 }
 
-template <int kType, int BN>
-__global__ void __launch_bounds__(kThreads, BN == 64 ? 2 : 1)
+template <int kType, int BN, int NS>
+__global__ void __launch_bounds__(kThreads)
     mx_linear_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, Params p)
 {
     using S = Shape<kType, BN>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
-    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    const uint32_t base = (raw_base + 1023u) & ~1023u;  // (the same offset in the cluster's CTAs)
     uint8_t* sbase = smem_raw + (base - raw_base);
-    const uint32_t bar_full = base + S::kBars, bar_empty = bar_full + 8 * S::kStages, bar_done = bar_empty + 8 * S::kStages;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int m_tiles = p.out / kBM, split = blockIdx.z;
-    const int m0 = (blockIdx.x % m_tiles) * kBM, n0 = (blockIdx.x / m_tiles) * BN;
+    const uint32_t sums = base + p.stages * S::kStageBytes, bar_full = sums + S::kSums, bar_empty = bar_full + 8 * p.stages,
+                   bar_done = bar_empty + 8 * p.stages, slot = bar_done + 8;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int m_tiles = p.out / kBM, rank = blockIdx.x % NS, tile = blockIdx.x / NS;
+    const int m0 = (tile % m_tiles) * kBM, n0 = (tile / m_tiles) * BN;
     // this CTA's share of the input features, in stages; the last one of a 4-bit row may be half
     const int sf_tiles = p.in / kMxTileCols, nk = (sf_tiles + S::kSfTiles - 1) / S::kSfTiles;
-    const int k0 = (int)((int64_t)nk * split / p.splits), k1 = (int)((int64_t)nk * (split + 1) / p.splits);
+    const int k0 = nk * rank / NS, k1 = nk * (rank + 1) / NS;
 
-    if (tid == 0) {
-        for (int i = 0; i < 2 * S::kStages + 1; ++i) mbar_init(bar_full + 8 * i, 1);
-        fence_mbar_init();
-    }
-    if (warp == 1) tmem_alloc(base + S::kTmemSlot, S::kCols);
-    if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&tmW);
-        tma_prefetch_desc(&tmX);
+    // ---- operands and scales of one stage (warp 0)
+    const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
+    const uint8_t* sfw = p.w_scales + (int64_t)(m0 / 128) * sf_tiles * kMxTileBytes;
+    const uint8_t* sfx = p.x_scales + (int64_t)(n0 / 128) * sf_tiles * kMxTileBytes;
+    auto load = [&](int k, int st) {
+        const uint32_t a = base + st * S::kStageBytes, b = a + S::kABytes, sf = b + S::kBBytes, bar = bar_full + 8 * st;
+        const uint32_t sf_bytes = min(S::kSfTiles, sf_tiles - k * S::kSfTiles) * kMxTileBytes;
+        mbar_arrive_expect_tx_warp(bar, S::kABytes + S::kBBytes + 2 * sf_bytes);
+        tma_load_2d_warp(a, &tmW, k * kSpan, m0, bar, pol_w);
+        tma_load_2d_warp(b, &tmX, k * kSpan, n0, bar, pol_x);
+        bulk_copy_g2s_warp(sf, sfw + k * S::kSf, sf_bytes, bar);
+        bulk_copy_g2s_warp(sf + S::kSf, sfx + k * S::kSf, sf_bytes, bar);
+    };
+
+    if (NS > 1) cluster_arrive();  // (waited for before the first store to another CTA: it has started then)
+    const int early = min(k1 - k0, p.stages);
+    if (warp == 0) {
+        if (elect_one()) {
+            for (int i = 0; i < 2 * p.stages + 1; ++i) mbar_init(bar_full + 8 * i, 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+        // W on its way to L2 before the wait for the kernel before this one (which may have written it:
+        // what is read comes after the wait)
+        for (int k = k0; k < k0 + early; ++k) tma_prefetch_2d_warp(&tmW, k * kSpan, m0);
+        pdl_wait();
+        for (int k = 0; k < early; ++k) load(k0 + k, k);
+    } else if (warp == 1) {
+        tmem_alloc(slot, S::kCols);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sbase + S::kTmemSlot);
-
-    pdl_wait();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(sbase + (slot - base)), 0);
     pdl_launch_dependents();
-    if (warp == 0 && lane == 0) {
-        // ---- producer
-        const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
-        const uint8_t* sfw = p.w_scales + (int64_t)(m0 / 128) * sf_tiles * kMxTileBytes;
-        const uint8_t* sfx = p.x_scales + (int64_t)(n0 / 128) * sf_tiles * kMxTileBytes;
-        const int blocks = min(S::kRowBlocks, p.row_blocks - n0 / 128);
-        for (int k = k0; k < k1; ++k) {
-            const int i = k - k0, st = i % S::kStages;
-            if (i >= S::kStages && !mbar_wait(bar_empty + 8 * st, ((i / S::kStages) - 1) & 1)) {
-                atomicOr(p.err, PKV_DEVERR_TIMEOUT);
-                break;
-            }
-            const uint32_t a = base + st * S::kStageBytes, b = a + S::kABytes, sa = b + S::kBBytes, sb = sa + S::kSfA;
-            const uint32_t fb = bar_full + 8 * st;
-            const int tiles = min(S::kSfTiles, sf_tiles - k * S::kSfTiles);
-            const uint32_t sf_bytes = tiles * kMxTileBytes;
-            mbar_arrive_expect_tx(fb, S::kABytes + S::kBBytes + (1 + blocks) * sf_bytes);
-            tma_load_2d(a, &tmW, k * kSpan, m0, fb, pol_w);
-            tma_load_2d(b, &tmX, k * kSpan, n0, fb, pol_x);
-            const int64_t at = (int64_t)k * S::kSfTiles * kMxTileBytes;
-            bulk_copy_g2s(sa, sfw + at, sf_bytes, fb);
-            for (int r = 0; r < blocks; ++r)
-                bulk_copy_g2s(sb + r * S::kSfA, sfx + (int64_t)r * sf_tiles * kMxTileBytes + at, sf_bytes, fb);
+
+    if (warp == 0) {
+        bool ok = true;
+        int st = 0;
+        uint32_t parity = 0;
+        for (int k = k0 + early; k < k1; ++k) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait_spin(bar_empty + 8 * st, parity)))) break;
+            load(k, st);
+            if (++st == p.stages) st = 0, parity ^= 1;
         }
-    } else if (warp == 1 && lane == 0) {
-        // ---- MMA issuer
+        if (!ok && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+    } else if (warp == 1) {
+        // ---- products (a wait that ran out does not end the loop, which would make its counters differ between
+        // lanes: the later waits are single looks, the results are void).  A stage is looked for before the
+        // products of the one before it are issued, which takes as long as the look.
+        bool ok = true, there = mbar_try_wait(bar_full, 0);
+        int st = 0;
+        uint32_t parity = 0;
         for (int k = k0; k < k1; ++k) {
-            const int i = k - k0, st = i % S::kStages;
-            if (!mbar_wait_spin(bar_full + 8 * st, (i / S::kStages) & 1)) {
-                atomicOr(p.err, PKV_DEVERR_TIMEOUT);
-                break;
-            }
+            if (!there) ok &= mbar_wait_spin(bar_full + 8 * st, parity, ok ? kWaitLimitNs : 0);
+            __syncwarp();
+            const int cur = st;
+            if (++st == p.stages) st = 0, parity ^= 1;
+            there = k + 1 < k1 && mbar_test_wait(bar_full + 8 * st, parity);
             tc_fence_after();
-            const uint32_t a = base + st * S::kStageBytes, b = a + S::kABytes, sa = b + S::kBBytes, sb = sa + S::kSfA;
-            const int tiles = min(S::kSfTiles, sf_tiles - k * S::kSfTiles);
-            for (int t = 0; t < tiles; ++t) {  // columns: [tile][row block], 4 each
-                umma_copy_scales(tmem + S::kSfaCol + 4 * t, sa + t * kMxTileBytes);
-                for (int r = 0; r < S::kRowBlocks; ++r)
-                    umma_copy_scales(tmem + S::kSfbCol + 4 * (t * S::kRowBlocks + r), sb + r * S::kSfA + t * kMxTileBytes);
-            }
+            const uint32_t a = base + cur * S::kStageBytes, b = a + S::kABytes, sf = b + S::kBBytes;
+            const int have = min(S::kSfTiles, sf_tiles - k * S::kSfTiles);
+            const uint32_t sfb = tmem + S::kSfbCol + (BN == 64 ? n0 % 128 / 32 : 0);  // (the second half of a block)
             const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(b, 16, 1024);
             constexpr int kPer = 4 / S::kSfTiles;  // products a tile of scales
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const int t = kk / kPer;
-                if (t < tiles)
-                    umma_mx<kType == PKV_MX4>(tmem, da + 2 * kk, db + 2 * kk,
-                                              umma_idesc_mx(kType == PKV_MX4, kBM, BN, kk % kPer * (4 / kPer)),
-                                              tmem + S::kSfaCol + 4 * t, tmem + S::kSfbCol + 4 * t * S::kRowBlocks,
-                                              i > 0 || kk > 0);
+            for (int s = 0; s < S::kSfTiles; ++s) {
+                umma_copy_scales_warp(tmem + S::kSfaCol + 4 * s, sf + s * kMxTileBytes);
+                umma_copy_scales_warp(tmem + S::kSfbCol + 4 * s, sf + S::kSf + s * kMxTileBytes);
             }
-            umma_commit(bar_empty + 8 * st);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const int s = kk / kPer;
+                if (s < have)
+                    umma_mx_warp<kType == PKV_MX4>(tmem, da + 2 * kk, db + 2 * kk,
+                                                   umma_idesc_mx(kType == PKV_MX4, kBM, BN, kk % kPer * (4 / kPer)),
+                                                   tmem + S::kSfaCol + 4 * s, sfb + 4 * s, k > k0 || kk > 0);
+            }
+            if (k1 - k0 > p.stages) umma_commit_warp(bar_empty + 8 * cur);  // (else no stage is loaded again)
         }
-        umma_commit(bar_done);  // also on a timeout: the epilogue and the release wait for it
+        umma_commit_warp(bar_done);
+        if (!ok && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     }
     __syncwarp();
 
-    // ---- epilogue: thread (warp w, lane l) holds output feature m0 + 32 w + l for BN tokens
-    const bool ok = mbar_wait(bar_done, 0);
+    // ---- each thread's feature of every token to the token's CTA: [CTA it comes from][its tokens / 4][features][4]
+    constexpr int kOwn = BN / NS, kVec = kOwn < 4 ? kOwn : 4, kStep = BN < 32 ? 16 : 32;
+    static_assert(kVec >= 2, "two tokens a CTA at least");
+    const bool ok = mbar_wait_spin(bar_done, 0);
     tc_fence_after();
-    int yw, yc;
-    __nv_bfloat16* const y = segment(p, m0, yw, yc);
-    if (p.splits == 1) {
-        const int o = yc + 32 * warp + lane;
-        if (ok) {
+    if (NS > 1) cluster_wait();
+    const int tokens = min(BN, p.tokens - n0), feature = 32 * warp + lane;
 #pragma unroll 1
-            for (int c0 = 0; c0 < BN; c0 += 32) {
-                uint32_t v[32];
-                tmem_ld32(tmem + ((uint32_t)(32 * warp) << 16) + c0, v);
-                tmem_wait_ld_regs(v);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int t = n0 + c0 + j;
-                    if (t < p.tokens) y[(int64_t)t * yw + o] = __float2bfloat16_rn(__uint_as_float(v[j]));
-                }
-            }
+    for (int c0 = 0; c0 < tokens; c0 += kStep) {
+        uint32_t v[kStep];
+        if constexpr (kStep == 16) {
+            tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + c0, v);
+            tmem_wait_ld();
+        } else {
+            tmem_ld32(tmem + ((uint32_t)(32 * warp) << 16) + c0, v);
+            tmem_wait_ld_regs(v);
         }
-        tc_fence_before();
-        __syncthreads();
-        if (warp == 1) {
-            tc_fence_after();
-            tmem_dealloc(tmem, S::kCols);
-        }
-        return;
-    }
-    // ---- split over the cluster: the partial tile, [token][feature] fp32, in this CTA's idle ring
-    float* part = reinterpret_cast<float*>(sbase);
-#pragma unroll 1
-    for (int c0 = 0; c0 < BN; c0 += 32) {
-        uint32_t v[32];
-        tmem_ld32(tmem + ((uint32_t)(32 * warp) << 16) + c0, v);
-        tmem_wait_ld_regs(v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) part[(c0 + j) * kBM + 32 * warp + lane] = ok ? __uint_as_float(v[j]) : 0.f;
+        for (int j = 0; j < kStep; j += kVec) {
+            const int t = c0 + j, owner = t / kOwn;
+            if (t >= tokens) break;
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) f[i] = ok ? __uint_as_float(v[j + i]) : 0.f;
+            uint32_t to = sums + (uint32_t)((rank * (kOwn / kVec) + t % kOwn / kVec) * kBM + feature) * (4 * kVec);
+            if (NS > 1) to = cluster_map(to, owner);  // (without a cluster, shared::cluster is this CTA's)
+            if constexpr (kVec == 4)
+                st_cluster_f32x4(to, f[0], f[1], f[2], f[3]);
+            else
+                st_cluster_f32x2(to, f[0], f[1]);
+        }
     }
     tc_fence_before();
-    cluster_sync();  // every partial tile of the cluster is in place
+    if (NS > 1)
+        cluster_sync();
+    else
+        __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, S::kCols);
     }
-    // CTA r sums features [r 128 / splits, (r + 1) 128 / splits), four a thread, in rank order
-    const int r = (int)cluster_rank(), per = kBM / 4 / p.splits;
-    const uint32_t local = smem_u32(part);
-    for (int i = tid; i < BN * per; i += kThreads) {
-        const int t = i / per, f = 4 * (r * per + i % per);
-        if (n0 + t >= p.tokens) break;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int q = 0; q < p.splits; ++q) {
-            const float4 v = ld_cluster_f32x4(cluster_map(local, q) + (uint32_t)(t * kBM + f) * 4);
-            acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    // ---- this CTA's tokens: a thread adds up its feature of kVec of them; two lanes then share theirs out, so
+    // that each writes two features of a token at a time
+    int yw, yc;
+    __nv_bfloat16* const y = segment(p, m0, yw, yc) + (int64_t)n0 * yw;
+    const bool odd = lane & 1;
+    for (int i = 0; i < kOwn / kVec; ++i) {
+        const int t0 = rank * kOwn + i * kVec;
+        if (t0 >= tokens) break;
+        float acc[kVec];
+#pragma unroll
+        for (int q = 0; q < NS; ++q) {
+            const float* from = reinterpret_cast<const float*>(sbase + (sums - base)) + (size_t)((q * (kOwn / kVec) + i) * kBM + feature) * kVec;
+            float v[kVec];
+            if constexpr (kVec == 4) {
+                const float4 u = *reinterpret_cast<const float4*>(from);
+                v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+            } else {
+                const float2 u = *reinterpret_cast<const float2*>(from);
+                v[0] = u.x, v[1] = u.y;
+            }
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) acc[j] = q ? acc[j] + v[j] : v[j];
         }
-        uint2 o2;
-        o2.x = pack_bf16(__float2bfloat16_rn(acc.x), __float2bfloat16_rn(acc.y));
-        o2.y = pack_bf16(__float2bfloat16_rn(acc.z), __float2bfloat16_rn(acc.w));
-        *reinterpret_cast<uint2*>(y + (int64_t)(n0 + t) * yw + yc + f) = o2;
+        // the even lane takes the first half of the tokens for both features, the odd lane the second
+#pragma unroll
+        for (int j = 0; j < kVec / 2; ++j) {
+            const float lo = acc[j], hi = acc[j + kVec / 2];
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+            const int t = t0 + j + (odd ? kVec / 2 : 0);
+            const float a = odd ? other : lo, b = odd ? hi : other;
+            if (t < tokens)
+                *reinterpret_cast<uint32_t*>(y + (int64_t)t * yw + yc + (feature & ~1)) =
+                    pack_bf16(__float2bfloat16_rn(a), __float2bfloat16_rn(b));
+        }
     }
-    cluster_sync();  // no CTA leaves while another reads its shared memory
+}
+
+template <int kType, int BN, int NS>
+cudaError_t launch(const MxLinear& a, Params& p, const CUtensorMap& tmW, const CUtensorMap& tmX, cudaStream_t s)
+{
+    using S = Shape<kType, BN>;
+    const int nk = (mx_row_bytes(kType, a.in) + kSpan - 1) / kSpan, share = (nk + NS - 1) / NS;
+    p.stages = share < S::kMaxStages ? share : S::kMaxStages;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = NS;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.out / kBM) * ((a.tokens + BN - 1) / BN) * NS));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::alloc(p.stages);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, mx_linear_kernel<kType, BN, NS>, tmW, tmX, p);
 }
 
 template <int kType, int BN>
-cudaError_t launch(const pkv_pool* pool, const MxLinear& a, Params& p, cudaStream_t s)
+cudaError_t launch_bn(const pkv_pool* pool, const MxLinear& a, Params& p, cudaStream_t s)
 {
-    using S = Shape<kType, BN>;
     CUtensorMap tmW, tmX;
-    const int row = mx_row_bytes(kType, a.in);
+    const int row = mx_row_bytes(kType, a.in), nk = (row + kSpan - 1) / kSpan;
     if (!make_tmap_bytes(&tmW, a.w_codes, row, p.out, kBM) || !make_tmap_bytes(&tmX, a.x_codes, row, a.tokens, BN))
         return cudaErrorInvalidValue;
-    const int tiles = (p.out / kBM) * ((a.tokens + BN - 1) / BN), steps = row / kSpan;
-    const int slots = pool->num_sms * (BN == 64 ? 2 : 1);
-    p.splits = 1;
-    while (p.splits < kMaxSplits && tiles * p.splits * 2 <= slots && steps / (p.splits * 2) >= 2) p.splits *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles, 1, p.splits);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kAlloc;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = p.splits;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, mx_linear_kernel<kType, BN>, tmW, tmX, p);
+    // Splits of the input features: while the CTAs run at the same time (two an SM up to 32 tokens), two stages a
+    // CTA are left, and clusters of 8 while they find an SM each (us with 1 / 2 / 4 / 8: one token, 4096 x 6144 in 4
+    // bits 5.8 / 5.4 / 4.7 / 7.1, 4096 x 1024 in 8 bits 7.7 / 5.4 / 4.0 / 3.1, 16 tokens, 4096 x 4096 in 4 bits 5.4 / 4.3 /
+    // 3.5 / 5.1; 64 tokens, 4096 x 4096 in 8 bits 9.4 / 7.2 / 6.9 / 15, 4096 x 6144 10.2 / 8.1 / 11.6)
+    const int64_t tiles = (int64_t)(p.out / kBM) * ((a.tokens + BN - 1) / BN);
+    int splits = 1;
+    while (splits < kMaxSplits && nk / (splits * 2) >= 2 &&
+           tiles * splits * 2 <= (BN <= 32 && splits < 4 ? 2 : 1) * (int64_t)pool->num_sms)
+        splits *= 2;
+    switch (splits) {
+        case 1: return launch<kType, BN, 1>(a, p, tmW, tmX, s);
+        case 2: return launch<kType, BN, 2>(a, p, tmW, tmX, s);
+        case 4: return launch<kType, BN, 4>(a, p, tmW, tmX, s);
+        default: return launch<kType, BN, 8>(a, p, tmW, tmX, s);
+    }
 }
 
 template <int kType>
 cudaError_t launch_type(const pkv_pool* pool, const MxLinear& a, Params& p, cudaStream_t s)
 {
-    if (a.tokens <= 64) return launch<kType, 64>(pool, a, p, s);
-    if (a.tokens <= 128) return launch<kType, 128>(pool, a, p, s);
-    return launch<kType, 256>(pool, a, p, s);
+    if (a.tokens <= 16) return launch_bn<kType, 16>(pool, a, p, s);
+    if (a.tokens <= 32) return launch_bn<kType, 32>(pool, a, p, s);
+    return launch_bn<kType, 64>(pool, a, p, s);
 }
 
+template <int kType, int BN, int NS>
+bool configure_one()
+{
+    return cudaFuncSetAttribute(mx_linear_kernel<kType, BN, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Shape<kType, BN>::alloc(Shape<kType, BN>::kMaxStages)) == cudaSuccess;
+}
 template <int kType, int BN>
+bool configure_bn()
+{
+    return configure_one<kType, BN, 1>() && configure_one<kType, BN, 2>() && configure_one<kType, BN, 4>() &&
+           configure_one<kType, BN, 8>();
+}
+template <int kType>
 bool configure()
 {
-    return cudaFuncSetAttribute(mx_linear_kernel<kType, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Shape<kType, BN>::kAlloc) == cudaSuccess;
+    return configure_bn<kType, 16>() && configure_bn<kType, 32>() && configure_bn<kType, 64>();
 }
 
 }  // namespace
 
-cudaError_t configure_mx_linear()
-{
-    const bool ok = configure<PKV_MX8, 64>() && configure<PKV_MX8, 128>() && configure<PKV_MX8, 256>() &&
-                    configure<PKV_MX4, 64>() && configure<PKV_MX4, 128>() && configure<PKV_MX4, 256>();
-    return ok ? cudaSuccess : cudaErrorInvalidValue;
-}
+cudaError_t configure_mx_linear() { return configure<PKV_MX8>() && configure<PKV_MX4>() ? cudaSuccess : cudaErrorInvalidValue; }
 
 cudaError_t launch_mx_linear(const pkv_pool* pool, const MxLinear& a, cudaStream_t s)
 {
@@ -281,8 +330,12 @@ cudaError_t launch_mx_linear(const pkv_pool* pool, const MxLinear& a, cudaStream
     p.tokens = a.tokens;
     p.in = a.in;
     p.out = p.seg_end[2];
-    p.row_blocks = (a.tokens + 127) / 128;
-    if (a.tokens > 256) return launch_mx_pair(pool, a, s);
+    // Tiles of up to 64 tokens while each finds an SM, and in more turns than one for up to 48 tokens, where the work
+    // is W's bytes (us here / over pairs, in 4 and in 8 bits: 128 tokens, 4096 x 6144 7.9 / 8.4 and 10.7 / 11.9; 333
+    // tokens, 4096 x 1024 5.7 / 6.4 and 7.0 / 9.6, 4096 x 4096 15 / 8.3 and 22 / 11.7; 64 tokens, 4096 x 65536 38 / 31 and
+    // 56 / 55, 32 tokens, 4096 x 16384 8.4 / 14.5 and 12.7 / 20.7)
+    const int64_t tiles = (int64_t)(p.out / kBM) * ((a.tokens + 63) / 64);
+    if (a.tokens > 48 && tiles > pool->num_sms) return launch_mx_pair(pool, a, s);
     return a.type == PKV_MX8 ? launch_type<PKV_MX8>(pool, a, p, s) : launch_type<PKV_MX4>(pool, a, p, s);
 }
 

@@ -155,18 +155,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t keep = l2_policy_evict_last();  // both are read again by other pairs
         Ring ring;
         bool ok = true, again = false;
-        while (walk.next()) {
+        while (ok && walk.next()) {
             const int m0 = walk.m * kTileM + (int)rank * 128;
             const int n0 = walk.f * kUnit + (int)rank * (walk.n * kUnit / 2);  // (rows beyond half of the tile are not used)
             for (int k = 0; k < nk; ++k, ring.next()) {
                 if (again) ok &= mbar_wait_spin(bar_empty + 8 * ring.st, ring.parity ^ 1, ok ? kWaitLimitNs : 0);
-                if (elect_one() && ok) {
-                    const uint32_t a = base + ring.st * S::kStageBytes, bar = bar_ready + 8 * ring.st;
-                    if (rank == 0) mbar_arrive_expect_tx(bar, 2 * S::kStageBytes);
-                    tma_load_2d_pair(a, &maps.x, k * kSpan, m0, bar, keep);
-                    tma_load_2d_pair(a + S::kA, &maps.w, k * kSpan, n0, bar, keep);
-                }
-                __syncwarp();
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                const uint32_t a = base + ring.st * S::kStageBytes, bar = bar_ready + 8 * ring.st;
+                if (rank == 0) mbar_arrive_expect_tx_warp(bar, 2 * S::kStageBytes);
+                tma_load_2d_pair_warp(a, &maps.x, k * kSpan, m0, bar, keep);
+                tma_load_2d_pair_warp(a + S::kA, &maps.w, k * kSpan, n0, bar, keep);
                 again |= ring.st == kStages - 1;
             }
         }
@@ -179,17 +177,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t keep = l2_policy_evict_last();
         Ring ring;
         bool ok = true, again = false;
-        while (walk.next()) {
+        while (ok && walk.next()) {
             const int mb = walk.m * 2 + (int)rank, nb = walk.f / 2;
             for (int k = 0; k < nk; ++k, ring.next()) {
                 if (again) ok &= mbar_wait_spin(bar_empty + 8 * ring.st, ring.parity ^ 1, ok ? kWaitLimitNs : 0);
-                if (elect_one() && ok) {
-                    const uint32_t to = base + S::kSf + ring.st * 3 * S::kSfBlock, bar = bar_landed + 8 * ring.st;
-                    mbar_arrive_expect_tx(bar, 3 * S::kSfBlock);
-                    tma_load_2d(to, &maps.sfx, k * S::kSfTiles * 128, mb, bar, keep);
-                    tma_load_2d(to + S::kSfBlock, &maps.sfw, k * S::kSfTiles * 128, nb, bar, keep);
-                }
-                __syncwarp();
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                const uint32_t to = base + S::kSf + ring.st * 3 * S::kSfBlock, bar = bar_landed + 8 * ring.st;
+                mbar_arrive_expect_tx_warp(bar, 3 * S::kSfBlock);
+                tma_load_2d_warp(to, &maps.sfx, k * S::kSfTiles * 128, mb, bar, keep);
+                tma_load_2d_warp(to + S::kSfBlock, &maps.sfw, k * S::kSfTiles * 128, nb, bar, keep);
                 again |= ring.st == kStages - 1;
             }
         }
@@ -199,33 +195,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // ---- products of the pair (a wait that ran out does not end the loop, which would make its
             // counters differ between lanes: the later waits are single looks, the results are void)
             Ring ring;
-            bool ok = true;
+            bool ok = true, there = false;
             for (int done = 0; walk.next(); ++done) {
                 const uint32_t half = done & 1, acc = tmem + half * kTileN;
                 if (done >= 2) ok &= mbar_wait_spin(bar_free + 8 * half, (done / 2 - 1) & 1, ok ? kWaitLimitNs : 0);
                 const uint32_t shape = umma_idesc_mx(kType == PKV_MX4, kTileM, 0, 0) | ((uint32_t)(walk.n * kUnit / 8) << 17);
                 const uint32_t odd = walk.f & 1 ? 2 : 0;  // columns: the tile starts in the middle of a block of 128
-                for (int k = 0; k < nk; ++k, ring.next()) {
-                    ok &= mbar_wait_spin(bar_ready + 8 * ring.st, ring.parity, ok ? kWaitLimitNs : 0);
+                for (int k = 0; k < nk; ++k) {
+                    // (the next stage is looked for before this one's products are issued)
+                    if (!there) ok &= mbar_wait_spin(bar_ready + 8 * ring.st, ring.parity, ok ? kWaitLimitNs : 0);
+                    __syncwarp();
+                    const int st = ring.st;
+                    ring.next();
+                    there = mbar_test_wait(bar_ready + 8 * ring.st, ring.parity);
                     tc_fence_after();
-                    const uint32_t a = base + ring.st * S::kStageBytes, sfc = tmem + S::kSfCol + ring.st * S::kSfCols;
+                    const uint32_t a = base + st * S::kStageBytes, sfc = tmem + S::kSfCol + st * S::kSfCols;
                     const int have = min(S::kSfTiles, sf_tiles - k * S::kSfTiles);
                     const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(a + S::kA, 16, 1024);
                     constexpr int kPer = 4 / S::kSfTiles;  // products a tile of scales
-                    if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const int s = kk / kPer;
-                            if (s < have)
-                                umma_mx_pair<kType == PKV_MX4>(acc, da + 2 * kk, db + 2 * kk,
-                                                               shape | umma_idesc_sf(kk % kPer * (4 / kPer)), sfc + 4 * s,
-                                                               sfc + 4 * S::kSfTiles + 8 * s + odd, k > 0 || kk > 0);
-                        }
-                        umma_commit_pair(bar_empty + 8 * ring.st);
-                        if (k == nk - 1) umma_commit_pair(bar_acc + 8 * half);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const int s = kk / kPer;
+                        if (s < have)
+                            umma_mx_pair_warp<kType == PKV_MX4>(acc, da + 2 * kk, db + 2 * kk,
+                                                                shape | umma_idesc_sf(kk % kPer * (4 / kPer)), sfc + 4 * s,
+                                                                sfc + 4 * S::kSfTiles + 8 * s + odd, k > 0 || kk > 0);
                     }
-                    __syncwarp();
+                    umma_commit_pair_warp(bar_empty + 8 * st);
                 }
+                umma_commit_pair_warp(bar_acc + 8 * half);
             }
             if (!ok && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
         }

@@ -13,16 +13,20 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// One lane of a converged warp.  Code that issues tensor-core products or bulk copies runs its loop
-// with the whole warp and issues under this: in a branch that one thread alone has taken, every such
-// instruction costs some 120 cycles, since its operands, which the instruction takes from the warp's
-// common registers, are no longer known to be the same in all lanes.
+// One lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0;
 }
+
+// Functions named ..._warp are executed by a converged warp, one lane of which issues the instruction.
+// Products, commits and bulk copies take their operands from registers common to the warp.  In a
+// branch that one thread has taken alone, the operands are carried there one by one for every
+// instruction (a product 70 to 120 cycles, measured by 8000 of them in a row); issued like this
+// they are computed there (50, or the product's own 45 to 128).
+#define PKV_ELECT "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t@q "
 
 // ---- mbarrier ---------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
@@ -78,6 +82,11 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
+}
+
+__device__ __forceinline__ void mbar_arrive_expect_tx_warp(uint32_t bar, uint32_t bytes)
+{
+    asm volatile(PKV_ELECT "mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // default limit of every wait: one second
@@ -257,68 +266,55 @@ __host__ __device__ constexpr uint32_t umma_idesc_mx(bool four_bits, int M, int 
 // The descriptor's bits of another sf, to be added to one of sf 0.
 __host__ __device__ constexpr uint32_t umma_idesc_sf(int sf) { return ((uint32_t)sf << 4) | ((uint32_t)sf << 29); }
 
-// D(tmem) (+)= (A scaled by sfa)(smem) * (B scaled by sfb)(smem); issued by one thread.
+#define PKV_MX_PRODUCT(INSTR)                                                                                       \
+    asm volatile("{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t@q " INSTR     \
+                 " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(tmem_d),                                             \
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(sfa), "r"(sfb)                           \
+                 : "memory")
+
+// D(tmem) (+)= (A scaled by sfa)(smem) * (B scaled by sfb)(smem).
 template <bool kFourBits>
-__device__ __forceinline__ void umma_mx(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                        uint32_t sfb, bool accumulate)
+__device__ __forceinline__ void umma_mx_warp(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, bool accumulate)
 {
     if constexpr (kFourBits)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-                tmem_d),
-            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(sfa), "r"(sfb)
-            : "memory");
+        PKV_MX_PRODUCT("tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X");
     else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-                tmem_d),
-            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(sfa), "r"(sfb)
-            : "memory");
+        PKV_MX_PRODUCT("tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X");
 }
 
 // Copies one tile of scales (512 bytes: 32 rows of 16) from shared memory to 4 columns of tensor
 // memory, the same for the lanes of all four warps.  Products that the same thread issues
 // afterwards find it, and those issued before are done with the columns.
-__device__ __forceinline__ void umma_copy_scales(uint32_t taddr, uint32_t saddr)
+__device__ __forceinline__ void umma_copy_scales_warp(uint32_t taddr, uint32_t saddr)
 {
     // no swizzle, descriptor version 1; 128 bytes between groups of 8 rows
     const uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    asm volatile(PKV_ELECT "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(d) : "memory");
 }
 
 // ---- the same over a CTA pair (cta_group::2) ---------------------------------------------
-// One thread of the even CTA issues for both: A is 128 rows of each CTA's shared memory, B half of N
+// A warp of the even CTA issues for both: A is 128 rows of each CTA's shared memory, B half of N
 // in each, the accumulator 128 rows in each CTA's tensor memory.  Scales: those of A's own rows
 // and all of B's in each CTA's.
 template <bool kFourBits>
-__device__ __forceinline__ void umma_mx_pair(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                             uint32_t sfb, bool accumulate)
+__device__ __forceinline__ void umma_mx_pair_warp(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                                  uint32_t sfb, bool accumulate)
 {
     if constexpr (kFourBits)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-                tmem_d),
-            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(sfa), "r"(sfb)
-            : "memory");
+        PKV_MX_PRODUCT("tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X");
     else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-                tmem_d),
-            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(sfa), "r"(sfb)
-            : "memory");
+        PKV_MX_PRODUCT("tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X");
 }
 
 // Arrive on the barrier at `bar`'s offset of both CTAs when this thread's operations have completed.
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar)
+__device__ __forceinline__ void umma_commit_pair_warp(uint32_t bar)
 {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
+    asm volatile(PKV_ELECT
+                 "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+                     bar),
+                 "h"((uint16_t)3)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t slot, uint32_t ncols)
@@ -334,12 +330,13 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 
 // A box into this CTA's shared memory whose bytes complete on the even CTA's barrier at `bar`'s
 // offset (bit 24 of a shared::cluster address tells the CTAs of a pair apart).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
-                                                 uint64_t policy)
+__device__ __forceinline__ void tma_load_2d_pair_warp(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                                      uint64_t policy)
 {
     asm volatile(
+        PKV_ELECT
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        " [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar & 0xFEFFFFFFu), "l"(policy)
         : "memory");
 }
@@ -359,9 +356,9 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar)
 }
 
 // Bring a box of global memory into L2.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y)
+__device__ __forceinline__ void tma_prefetch_2d_warp(const CUtensorMap* map, int x, int y)
 {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+    asm volatile(PKV_ELECT "cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n\t}" ::"l"(reinterpret_cast<uint64_t>(map)),
                  "r"(x), "r"(y)
                  : "memory");
 }
@@ -397,10 +394,41 @@ __device__ __forceinline__ bool named_all(int id, int threads, bool ok)
     return r != 0;
 }
 
-// A float into the shared memory of a CTA of the cluster (an address from cluster_map).
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
+__device__ __forceinline__ void tma_load_2d_warp(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                                 uint64_t policy)
 {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+    asm volatile(
+        PKV_ELECT
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_copy_g2s_warp(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile(PKV_ELECT
+                 "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void umma_commit_warp(uint32_t bar)
+{
+    asm volatile(PKV_ELECT "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+                 : "memory");
+}
+
+// The two halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Floats into the shared memory of a CTA of the cluster (an address from cluster_map).
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32x2(uint32_t addr, float a, float b)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
 // Arrive once on `bar` when every tcgen05 operation this thread issued so far has completed.

@@ -6,6 +6,7 @@
 // qwen3-8b Nest files, src/norm.linnet (RmsNorm) and DecoderLayer.decode_paged, which runs
 // attention_norm before the attention and the residual's addition with mlp_norm after it.
 #include <algorithm>
+#include <type_traits>
 
 #include "pkv_mx.cuh"
 
@@ -38,27 +39,25 @@ __global__ void __launch_bounds__(256)
         const int64_t r = row0 + 16 * i + sub;
         float v[8];
         unpack8(raw[i], v);
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
-        top = max(top, __shfl_xor_sync(kAll, top, 1));
-        top = max(top, __shfl_xor_sync(kAll, top, 2));
+        // the largest magnitude of the group, as 16-bit integers (a NaN above an Inf above all numbers)
+        uint32_t two = __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                                __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
+        two = __vmaxu2(two, __shfl_xor_sync(kAll, two, 1));
+        two = __vmaxu2(two, __shfl_xor_sync(kAll, two, 2));
+        const uint32_t top = max(two << 16, two & 0xffff0000u);
         const uint32_t byte = mx_scale_byte<kType>(top);
         const float inv = mx_inverse(byte);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] *= inv;
         uint2 c = mx_codes8<kType>(v);
         if (byte == 255u) c = make_uint2(0, 0);
-        uint32_t word = byte << (8 * (j >> 2));   // the row's four bytes of the tile
-        word |= __shfl_xor_sync(kAll, word, 4);
-        word |= __shfl_xor_sync(kAll, word, 8);
         if (r >= rows) continue;
         uint8_t* dst = codes + r * mx_row_bytes(kType, cols) + mx_row_bytes(kType, col);
         if constexpr (kType == PKV_MX8)
             *reinterpret_cast<uint2*>(dst) = c;
         else
             *reinterpret_cast<uint32_t*>(dst) = c.x;
-        if (j == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_at(r, 4 * tile, tiles)) = word;
+        if ((j & 3) == 0) scales[mx_scale_at(r, 4 * tile + (j >> 2), tiles)] = (uint8_t)byte;
     }
 }
 
@@ -138,109 +137,187 @@ __device__ __forceinline__ Pair inv_rms_pair(Pair ss, Pair inv_n, Pair eps)
 
 struct AddNormParams {
     const __nv_bfloat16* x;
-    const __nv_bfloat16* residual;  // null: nothing to add
+    const __nv_bfloat16* residual;
     __nv_bfloat16* residual_out;
     const __nv_bfloat16* w;
     void* out;
     uint8_t* scales;
     int64_t x_stride;
-    int tokens, hidden;
+    int tokens, hidden, warps;
     Pair inv_n, eps;
 };
 
-// h * w * r as a float and the rest of it, rounded to odd: what a rounding of it to
-// fewer bits gives is then the rounding of the exact value (but for 2^-44 of it).
-__device__ __forceinline__ float scaled_odd(float hw, Pair r)
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
 {
-    const float q = __fmul_rn(hw, r.l), p = __fmaf_rn(hw, r.h, q);
-    const float e = __fadd_rn(__fmaf_rn(hw, r.h, -p), q);
-    const uint32_t b = __float_as_uint(p);
-    const uint32_t odd = (b - ((b ^ __float_as_uint(e)) >> 31)) | 1u;
-    return e != 0.f && (b << 1) != 0 && (b << 1) < 0xff000000u ? __uint_as_float(odd) : p;
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_fma_rz(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// two bf16 as two floats
+__device__ __forceinline__ uint64_t f2_of_bf16(uint32_t two)
+{
+    return f2_pack(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+}
+// two sums of bf16, each rounded once
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// the larger magnitude, a NaN if either is one
+__device__ __forceinline__ float max_abs(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
 }
 
-// One CTA per token; thread i holds chunks i, i + T, ... of 8 columns.
-template <int kType, int kChunks>
+// hw * r for two elements, truncated, the last bit set where something was cut off: what a rounding
+// of it to fewer bits gives is then the rounding of the exact value (but for 2^-44 of it).  Nothing
+// is cut off only where r is a float (kExact: r.l = 0, looked at for a row) and the product fits
+// one; with the rest of r at least the products are never floats.
+template <bool kExact>
+__device__ __forceinline__ void scaled_odd(uint64_t hw, uint64_t rh, uint64_t rl, float& a, float& b)
+{
+    const uint64_t p = f2_fma_rz(hw, rh, f2_mul(hw, rl));
+    f2_unpack(p, a, b);
+    uint32_t cut_a = 1u, cut_b = 1u;
+    if constexpr (kExact) {
+        float ea, eb;
+        const uint64_t minus = f2_pack(-a, -b);
+        f2_unpack(f2_fma(hw, rh, minus), ea, eb);
+        cut_a = ea != 0.f, cut_b = eb != 0.f;
+    }
+    a = __uint_as_float(__float_as_uint(a) | cut_a);
+    b = __uint_as_float(__float_as_uint(b) | cut_b);
+}
+
+// A CTA takes tokens blockIdx.x, + gridDim.x, ...; its thread i holds chunks i, i + T, ... of 8 columns of each.
+// Every warp forms the sum of the warps' sums and the root by itself, with one barrier a token.
+//
+// Bound by memory where a residual is added: 8192 x 4096 to 8 bits, 236 MB, in 37.7 us, 6.3 TB/s, to bf16, 268 MB, in
+// 42; without one by instructions, some 29 an element with a token's share of the sums (to 4 bits, 85 MB, in 33 us).
+template <int kType, bool kAdd, int kChunks>
 __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
 {
-    __shared__ Pair part[32];
-    const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x;
+    __shared__ Pair part[2][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, warps = T >> 5;
     const int chunks = p.hidden / 8;
     pdl_wait();
-    uint4 raw[kChunks];
-    Pair ss = {0.f, 0.f};
+    // What waits for its predecessor before it reads microscaled operands may start early.  (A product of bf16 loads
+    // its weights without that wait: no early start behind a bf16 output, which could be such weights.)
+    if (kType != PKV_BF16) pdl_launch_dependents();
+    uint4 x[kChunks], more[kChunks], w[kChunks];
+    auto load = [&](int64_t t) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const int at = tid + c * T;
-        raw[c] = make_uint4(0, 0, 0, 0);
-        if (at >= chunks) continue;
-        raw[c] = *reinterpret_cast<const uint4*>(p.x + t * p.x_stride + 8 * at);
-        if (p.residual) {
-            const uint4 more = *reinterpret_cast<const uint4*>(p.residual + t * p.hidden + 8 * at);
-            float a[8], b[8];
-            unpack8(raw[c], a);
-            unpack8(more, b);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) a[k] += b[k];
-            raw[c] = pack8(a);
-            *reinterpret_cast<uint4*>(p.residual_out + t * p.hidden + 8 * at) = raw[c];
-        }
-        float h[8];
-        unpack8(raw[c], h);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const Pair s = two_sum(ss.h, __fmul_rn(h[k], h[k]));
-            ss.h = s.h;
-            ss.l = __fadd_rn(ss.l, s.l);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss = add(ss, {__shfl_xor_sync(kAll, ss.h, o), __shfl_xor_sync(kAll, ss.l, o)});
-    if (lane == 0) part[warp] = ss;
-    __syncthreads();
-    ss = part[0];
-    for (int i = 1; i < T / 32; ++i) ss = add(ss, part[i]);
-    const Pair r = inv_rms_pair(ss, p.inv_n, p.eps);
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const int at = tid + c * T;
-        float v[8], w[8];
-        unpack8(raw[c], v);
-        if (at < chunks) {
-            unpack8(*reinterpret_cast<const uint4*>(p.w + 8 * at), w);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = 0.f;
-        }
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            v[k] = scaled_odd(__fmul_rn(v[k], w[k]), r);
-            top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
-        }
-        if constexpr (kType == PKV_BF16) {
-            if (at < chunks) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + t * p.hidden + 8 * at) = pack8(v);
-        } else {
-            top = max(top, __shfl_xor_sync(kAll, top, 1));
-            top = max(top, __shfl_xor_sync(kAll, top, 2));
-            const uint32_t byte = mx_scale_byte<kType>(top);
-            const float inv = mx_inverse(byte);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= inv;
-            uint2 code = mx_codes8<kType>(v);
-            if (byte == 255u) code = make_uint2(0, 0);
-            uint32_t word = byte << (8 * ((at & 15) >> 2));
-            word |= __shfl_xor_sync(kAll, word, 4);
-            word |= __shfl_xor_sync(kAll, word, 8);
+        for (int c = 0; c < kChunks; ++c) {
+            const int at = tid + c * T;
             if (at >= chunks) continue;
-            uint8_t* dst = static_cast<uint8_t*>(p.out) + t * mx_row_bytes(kType, p.hidden) + mx_row_bytes(kType, 8 * at);
-            if constexpr (kType == PKV_MX8)
-                *reinterpret_cast<uint2*>(dst) = code;
-            else
-                *reinterpret_cast<uint32_t*>(dst) = code.x;
-            if ((at & 15) == 0)
-                *reinterpret_cast<uint32_t*>(p.scales + mx_scale_at(t, at / 4, p.hidden / kMxTileCols)) = word;
+            x[c] = *reinterpret_cast<const uint4*>(p.x + t * p.x_stride + 8 * at);
+            if (kAdd) more[c] = *reinterpret_cast<const uint4*>(p.residual + t * p.hidden + 8 * at);
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) x[c] = more[c] = w[c] = make_uint4(0, 0, 0, 0);
+    load(blockIdx.x);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+        if (tid + c * T < chunks) w[c] = *reinterpret_cast<const uint4*>(p.w + 8 * (tid + c * T));
+    int turn = 0;
+    for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x, turn ^= 1) {
+        uint32_t h[kChunks][4];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            h[c][0] = x[c].x, h[c][1] = x[c].y, h[c][2] = x[c].z, h[c][3] = x[c].w;
+            if constexpr (kAdd) {
+                h[c][0] = add_bf16x2(h[c][0], more[c].x), h[c][1] = add_bf16x2(h[c][1], more[c].y);
+                h[c][2] = add_bf16x2(h[c][2], more[c].z), h[c][3] = add_bf16x2(h[c][3], more[c].w);
+                if (tid + c * T < chunks)
+                    *reinterpret_cast<uint4*>(p.residual_out + t * p.hidden + 8 * (tid + c * T)) =
+                        make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
+            }
+        }
+        if (t + gridDim.x < p.tokens) load(t + gridDim.x);
+        // squares (exact) added up with what each addition loses
+        const uint64_t minus_one = f2_pack(-1.f, -1.f);
+        uint64_t s2 = 0, l2 = 0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t v = f2_of_bf16(h[c][k]);
+                const uint64_t sum = f2_fma(v, v, s2);
+                const uint64_t back = f2_fma(sum, minus_one, s2);             // minus the part of v^2 that went in
+                const uint64_t lost = f2_add(f2_fma(f2_add(sum, back), minus_one, s2), f2_fma(v, v, back));
+                l2 = f2_add(l2, lost);
+                s2 = sum;
+            }
+        Pair ss, other;
+        f2_unpack(s2, ss.h, other.h);
+        f2_unpack(l2, ss.l, other.l);
+        ss = add(ss, other);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss = add(ss, {__shfl_xor_sync(kAll, ss.h, o), __shfl_xor_sync(kAll, ss.l, o)});
+        if (warps > 1) {
+            if (lane == 0) part[turn][warp] = ss;
+            __syncthreads();
+            ss = lane < warps ? part[turn][lane] : Pair{0.f, 0.f};
+            for (int o = 1; o < warps; o <<= 1) ss = add(ss, {__shfl_xor_sync(kAll, ss.h, o), __shfl_xor_sync(kAll, ss.l, o)});
+            ss = {__shfl_sync(kAll, ss.h, 0), __shfl_sync(kAll, ss.l, 0)};
+        }
+        const Pair r = inv_rms_pair(ss, p.inv_n, p.eps);
+        const uint64_t rh = f2_pack(r.h, r.h), rl = f2_pack(r.l, r.l);
+        const bool exact = r.l == 0.f;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int at = tid + c * T;
+            const uint32_t wc[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+            uint64_t hw[4];
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) hw[k] = f2_mul(f2_of_bf16(h[c][k]), f2_of_bf16(wc[k]));
+            if (exact) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) scaled_odd<true>(hw[k], rh, rl, v[2 * k], v[2 * k + 1]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) scaled_odd<false>(hw[k], rh, rl, v[2 * k], v[2 * k + 1]);
+            }
+            if constexpr (kType == PKV_BF16) {
+                if (at < chunks) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + t * p.hidden + 8 * at) = pack8(v);
+            } else {
+                uint32_t top = __float_as_uint(max_abs(max_abs(max_abs(v[0], v[1]), max_abs(v[2], v[3])),
+                                                       max_abs(max_abs(v[4], v[5]), max_abs(v[6], v[7])))) & 0x7fffffffu;
+                top = max(top, __shfl_xor_sync(kAll, top, 1));
+                top = max(top, __shfl_xor_sync(kAll, top, 2));
+                const uint32_t byte = mx_scale_byte<kType>(top);
+                const float inv = mx_inverse(byte);
+                const uint64_t inv2 = f2_pack(inv, inv);
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) f2_unpack(f2_mul(f2_pack(v[k], v[k + 1]), inv2), v[k], v[k + 1]);
+                uint2 code = mx_codes8<kType>(v);
+                if (byte == 255u) code = make_uint2(0, 0);
+                if (at >= chunks) continue;
+                uint8_t* dst = static_cast<uint8_t*>(p.out) + t * mx_row_bytes(kType, p.hidden) + mx_row_bytes(kType, 8 * at);
+                if constexpr (kType == PKV_MX8)
+                    *reinterpret_cast<uint2*>(dst) = code;
+                else
+                    *reinterpret_cast<uint32_t*>(dst) = code.x;
+                if ((lane & 3) == 0) p.scales[mx_scale_at(t, at / 4, p.hidden / kMxTileCols)] = (uint8_t)byte;
+            }
         }
     }
 }
@@ -271,15 +348,15 @@ cudaError_t launch_mx_quantize(const pkv_pool* pool, const void* x, int64_t x_st
 {
     const int tiles = cols / kMxTileCols;
     const bool many = (int64_t)(rows + 127) / 128 * tiles >= 2 * pool->num_sms;
-    const int step = many ? 128 : 16;
+    const int step = many ? 64 : 16;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config((unsigned)((rows + step - 1) / step * tiles), 256, attr, s);
     auto launch = [&](auto kernel) {
         return cudaLaunchKernelEx(&cfg, kernel, static_cast<const __nv_bfloat16*>(x), x_stride, rows, cols,
                                   static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
     };
-    if (type == PKV_MX8) return many ? launch(mx_quantize_kernel<PKV_MX8, 8>) : launch(mx_quantize_kernel<PKV_MX8, 1>);
-    return many ? launch(mx_quantize_kernel<PKV_MX4, 8>) : launch(mx_quantize_kernel<PKV_MX4, 1>);
+    if (type == PKV_MX8) return many ? launch(mx_quantize_kernel<PKV_MX8, 4>) : launch(mx_quantize_kernel<PKV_MX8, 1>);
+    return many ? launch(mx_quantize_kernel<PKV_MX4, 4>) : launch(mx_quantize_kernel<PKV_MX4, 1>);
 }
 
 cudaError_t launch_mx_read(const pkv_pool* pool, int type, const void* codes, const void* scales, int rows, int cols,
@@ -287,15 +364,15 @@ cudaError_t launch_mx_read(const pkv_pool* pool, int type, const void* codes, co
 {
     const int tiles = cols / kMxTileCols;
     const bool many = (int64_t)(rows + 127) / 128 * tiles >= 2 * pool->num_sms;
-    const int step = many ? 128 : 16;
+    const int step = many ? 64 : 16;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config((unsigned)((rows + step - 1) / step * tiles), 256, attr, s);
     auto launch = [&](auto kernel) {
         return cudaLaunchKernelEx(&cfg, kernel, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),
                                   rows, cols, static_cast<__nv_bfloat16*>(y), y_stride);
     };
-    if (type == PKV_MX8) return many ? launch(mx_read_kernel<PKV_MX8, 8>) : launch(mx_read_kernel<PKV_MX8, 1>);
-    return many ? launch(mx_read_kernel<PKV_MX4, 8>) : launch(mx_read_kernel<PKV_MX4, 1>);
+    if (type == PKV_MX8) return many ? launch(mx_read_kernel<PKV_MX8, 4>) : launch(mx_read_kernel<PKV_MX8, 1>);
+    return many ? launch(mx_read_kernel<PKV_MX4, 4>) : launch(mx_read_kernel<PKV_MX4, 1>);
 }
 
 cudaError_t launch_add_norm(const pkv_pool* pool, const AddNorm& a, cudaStream_t s)
@@ -313,17 +390,28 @@ cudaError_t launch_add_norm(const pkv_pool* pool, const AddNorm& a, cudaStream_t
     p.inv_n = pair_of(1.0 / a.hidden);
     p.eps = pair_of(pool->cfg.eps);
     const int chunks = a.hidden / 8;
-    const int per = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : 4;
+    // chunks a thread: two (8192 x 4096 to 8 bits us with 1 / 2 / 4: 50 / 37.8 / 59), four where 1024 threads need it,
+    // one for a few short rows (300 x 2048 2.4 / 2.6)
+    const int per = chunks > 2048 ? 4 : chunks <= 256 && a.tokens <= 2 * pool->num_sms ? 1 : 2;
     const unsigned threads = (unsigned)((chunks + 32 * per - 1) / (32 * per) * 32);
+    // as many CTAs as can be resident, each loading its next token while it works on one (a CTA a token 42 us)
+    const unsigned grid = std::min((unsigned)a.tokens, (unsigned)pool->num_sms * std::max(1u, std::min(32u, 2048 / threads)));
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = config((unsigned)a.tokens, threads, attr, s);
-    auto launch = [&](auto one, auto two, auto four) {
-        return cudaLaunchKernelEx(&cfg, per == 1 ? one : per == 2 ? two : four, p);
+    cudaLaunchConfig_t cfg = config(grid, threads, attr, s);
+    auto with = [&](auto type, auto add) {
+        constexpr int kType = decltype(type)::value;
+        constexpr bool kAdd = decltype(add)::value;
+        switch (per) {
+            case 1: return cudaLaunchKernelEx(&cfg, add_norm_kernel<kType, kAdd, 1>, p);
+            case 2: return cudaLaunchKernelEx(&cfg, add_norm_kernel<kType, kAdd, 2>, p);
+            default: return cudaLaunchKernelEx(&cfg, add_norm_kernel<kType, kAdd, 4>, p);
+        }
     };
+    auto of = [&](auto type) { return a.residual ? with(type, std::true_type{}) : with(type, std::false_type{}); };
     switch (a.type) {
-        case PKV_MX8: return launch(add_norm_kernel<PKV_MX8, 1>, add_norm_kernel<PKV_MX8, 2>, add_norm_kernel<PKV_MX8, 4>);
-        case PKV_MX4: return launch(add_norm_kernel<PKV_MX4, 1>, add_norm_kernel<PKV_MX4, 2>, add_norm_kernel<PKV_MX4, 4>);
-        default: return launch(add_norm_kernel<PKV_BF16, 1>, add_norm_kernel<PKV_BF16, 2>, add_norm_kernel<PKV_BF16, 4>);
+        case PKV_MX8: return of(std::integral_constant<int, PKV_MX8>{});
+        case PKV_MX4: return of(std::integral_constant<int, PKV_MX4>{});
+        default: return of(std::integral_constant<int, PKV_BF16>{});
     }
 }
 

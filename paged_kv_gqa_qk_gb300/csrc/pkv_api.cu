@@ -377,7 +377,6 @@ static int create_pool(const pkv_config* cfg, int num_pages, void* k, void* v, b
     }
     ok &= configure_kernels() == cudaSuccess;
     ok &= configure_prefill() == cudaSuccess;
-    ok &= configure_mx_linear() == cudaSuccess && configure_mx_pair(p) == cudaSuccess;
     p->ctas_per_sm = attn_ctas_per_sm();
     ok &= p->ctas_per_sm > 0;
     if (!ok) {

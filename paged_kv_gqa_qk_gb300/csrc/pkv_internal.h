@@ -51,7 +51,6 @@ struct pkv_pool {
     float2* rope_hi;       // (cos, sin) [max_seq][head_dim/2]: fp32 nearest to the double values
     float2* rope_lo;       // the double values minus rope_hi, in fp32
     int q4_clusters[2][5];  // clusters of 1, 2, 4, 8 and 16 CTAs of q4_unit_kernel's two forms that the device holds at a time
-    int mx_pairs;          // CTA pairs of mx_pair_kernel that the device holds at a time
     uint32_t* err;         // sticky device error word (word 0 of a 256-byte allocation); word 1: no entry of the
                            // tables exceeds 2^it (0 but for scaled rotations)
     uint32_t* claims;      // kClaimSlots chunk counters (bytes 128..255 of the same allocation), zero between calls
@@ -235,9 +234,7 @@ struct MxLinear {
     int segments, tokens, in, type;
 };
 cudaError_t launch_mx_linear(const pkv_pool* pool, const MxLinear& a, cudaStream_t s);
-cudaError_t configure_mx_linear();
 cudaError_t launch_mx_pair(const pkv_pool* pool, const MxLinear& a, cudaStream_t s);  // many tokens (pkv_mx_pair.cu)
-cudaError_t configure_mx_pair(pkv_pool* pool);
 // 2-D tiled tensor map of a row-major byte matrix (128-byte swizzle, zero fill past the
 // edges), boxes of 128 bytes by `box_rows`; false if the driver refuses it.
 bool make_tmap_bytes(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);

@@ -12,6 +12,7 @@
 // issues the four products of a stage.  The input features are split over the CTAs of a cluster,
 // so that every SM has a part of W to read; each CTA sends its sums of a part of the tokens to
 // each other, which adds those of its tokens in the CTAs' order.
+#include <atomic>
 #include <type_traits>
 
 #include "pkv_mx.cuh"
@@ -239,10 +240,25 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// Allows the kernel its shared memory on a device, once.
 template <int kType, int BN, int NS>
-cudaError_t launch(const MxLinear& a, Params& p, const CUtensorMap& tmW, const CUtensorMap& tmX, cudaStream_t s)
+bool allowed(int device)
+{
+    static std::atomic<uint64_t> known{0};
+    const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
+    if (known.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(mx_linear_kernel<kType, BN, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shape<kType, BN>::alloc(Shape<kType, BN>::kMaxStages)) != cudaSuccess)
+        return false;
+    known.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
+template <int kType, int BN, int NS>
+cudaError_t launch(int device, const MxLinear& a, Params& p, const CUtensorMap& tmW, const CUtensorMap& tmX, cudaStream_t s)
 {
     using S = Shape<kType, BN>;
+    if (!allowed<kType, BN, NS>(device)) return cudaErrorInvalidConfiguration;
     const int nk = (mx_row_bytes(kType, a.in) + kSpan - 1) / kSpan, share = (nk + NS - 1) / NS;
     p.stages = share < S::kMaxStages ? share : S::kMaxStages;
     cudaLaunchAttribute attr[2];
@@ -279,10 +295,10 @@ cudaError_t launch_bn(const pkv_pool* pool, const MxLinear& a, Params& p, cudaSt
            tiles * splits * 2 <= (BN <= 32 && splits < 4 ? 2 : 1) * (int64_t)pool->num_sms)
         splits *= 2;
     switch (splits) {
-        case 1: return launch<kType, BN, 1>(a, p, tmW, tmX, s);
-        case 2: return launch<kType, BN, 2>(a, p, tmW, tmX, s);
-        case 4: return launch<kType, BN, 4>(a, p, tmW, tmX, s);
-        default: return launch<kType, BN, 8>(a, p, tmW, tmX, s);
+        case 1: return launch<kType, BN, 1>(pool->device, a, p, tmW, tmX, s);
+        case 2: return launch<kType, BN, 2>(pool->device, a, p, tmW, tmX, s);
+        case 4: return launch<kType, BN, 4>(pool->device, a, p, tmW, tmX, s);
+        default: return launch<kType, BN, 8>(pool->device, a, p, tmW, tmX, s);
     }
 }
 
@@ -294,27 +310,7 @@ cudaError_t launch_type(const pkv_pool* pool, const MxLinear& a, Params& p, cuda
     return launch_bn<kType, 64>(pool, a, p, s);
 }
 
-template <int kType, int BN, int NS>
-bool configure_one()
-{
-    return cudaFuncSetAttribute(mx_linear_kernel<kType, BN, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Shape<kType, BN>::alloc(Shape<kType, BN>::kMaxStages)) == cudaSuccess;
-}
-template <int kType, int BN>
-bool configure_bn()
-{
-    return configure_one<kType, BN, 1>() && configure_one<kType, BN, 2>() && configure_one<kType, BN, 4>() &&
-           configure_one<kType, BN, 8>();
-}
-template <int kType>
-bool configure()
-{
-    return configure_bn<kType, 16>() && configure_bn<kType, 32>() && configure_bn<kType, 64>();
-}
-
 }  // namespace
-
-cudaError_t configure_mx_linear() { return configure<PKV_MX8>() && configure<PKV_MX4>() ? cudaSuccess : cudaErrorInvalidValue; }
 
 cudaError_t launch_mx_linear(const pkv_pool* pool, const MxLinear& a, cudaStream_t s)
 {

@@ -303,22 +303,24 @@ __global__ void __launch_bounds__(kLinThreads, BN == 64 ? 2 : 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sbase + S::kTmemSlot);
 
-    pdl_launch_dependents();  // the next projection may start streaming its weights
+    pdl_launch_dependents();  // the next projection may bring its weights to L2
     if (warp == 0 && lane == 0) {
         // ---- producer: the W box (128 features x 64 inputs) and the x box (BN tokens x 64 inputs).
-        // The first stages' weights are requested before waiting for the kernel before this one
-        // (which may still be writing x); nothing this kernel writes is touched before the wait.
+        // The first stages' weights are on their way to L2 before the wait for the kernel before this
+        // one, which may still be writing x, or w itself: what is read comes after the wait.
         const uint64_t pol_w = l2_policy_evict_first();  // each weight tile is read by one CTA per token tile
         const uint64_t pol_x = l2_policy_evict_last();   // x is read by every output tile
         const int early = min(k1 - k0, S::kStages);
         for (int i = 0; i < early; ++i) {
-            const uint32_t a = base + i * S::kStageBytes, fb = bar_full + 8 * i;
-            mbar_arrive_expect_tx(fb, S::kStageBytes);
-            tma_load_2d(a, &tmW, (k0 + i) * kBK, m0, fb, pol_w);
+            mbar_arrive_expect_tx(bar_full + 8 * i, S::kStageBytes);
+            tma_prefetch_2d(&tmW, (k0 + i) * kBK, m0);
         }
         pdl_wait();
-        for (int i = 0; i < early; ++i)
-            tma_load_2d(base + i * S::kStageBytes + S::kABytes, &tmX, (k0 + i) * kBK, n0, bar_full + 8 * i, pol_x);
+        for (int i = 0; i < early; ++i) {
+            const uint32_t a = base + i * S::kStageBytes, fb = bar_full + 8 * i;
+            tma_load_2d(a, &tmW, (k0 + i) * kBK, m0, fb, pol_w);
+            tma_load_2d(a + S::kABytes, &tmX, (k0 + i) * kBK, n0, fb, pol_x);
+        }
         for (int k = k0 + early; k < k1; ++k) {
             const int i = k - k0, st = i % S::kStages;
             if (!mbar_wait(bar_empty + 8 * st, ((i / S::kStages) - 1) & 1)) {

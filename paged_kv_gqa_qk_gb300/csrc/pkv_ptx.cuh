@@ -356,6 +356,12 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar)
 }
 
 // Bring a box of global memory into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x),
+                 "r"(y)
+                 : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_2d_warp(const CUtensorMap* map, int x, int y)
 {
     asm volatile(PKV_ELECT "cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n\t}" ::"l"(reinterpret_cast<uint64_t>(map)),

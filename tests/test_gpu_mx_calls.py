@@ -248,6 +248,41 @@ def test_each_call_waits_for_the_one_before(pool, kind, tokens):
     assert float(wrong) == 0 and pool.check_errors() == 0
 
 
+@pytest.mark.parametrize("tokens", [1, 400])
+def test_output_of_a_call_as_the_next_products_weights(pool, tokens):
+    """A product of bf16 brings its weights' first boxes to L2 before the call before it has ended, and reads them after:
+    weights that a product, a norm or a read wrote just before are the ones multiplied."""
+    ones = torch.ones(512, dtype=torch.bfloat16, device=DEV)
+    kind, sets = "mx8", []
+    for seed in range(4):
+        a, b = operands(384, 640, 512, kind, seed=seed)
+        am, bm = pool.mx_quantize(a, kind), pool.mx_quantize(b, kind)
+        x = operands(tokens, 512, 128, kind, seed=9)[0]
+        y = pool.mx_linear(am, bm)
+        norm, read = pool.add_norm(y, None, ones, out="bf16")[0], torch.empty_like(y)
+        ym = pool.mx_quantize(y, kind)
+        pool.mx_read(ym, out=read)
+        torch.cuda.synchronize()
+        refs = []
+        for w in (y, norm, read):
+            refs.append(pool.linear(x, w))
+            torch.cuda.synchronize()
+        sets.append((x, am, bm, ym, y, refs))
+    w, z = torch.empty(384, 512, dtype=torch.bfloat16, device=DEV), torch.empty(tokens, 384, dtype=torch.bfloat16, device=DEV)
+    wrong = torch.zeros(3, device=DEV)
+    for i in range(210):
+        x, am, bm, ym, y, refs = sets[i * 7 % 4]
+        if i % 3 == 0:
+            pool.mx_linear(am, bm, y=w)
+        elif i % 3 == 1:
+            pool.add_norm(y, None, ones, out=w)
+        else:
+            pool.mx_read(ym, out=w)
+        pool.linear(x, w, y=z)
+        wrong[i % 3] += (z != refs[i % 3]).any()
+    assert wrong.tolist() == [0, 0, 0] and pool.check_errors() == 0
+
+
 def test_another_stream(pool):
     s = torch.cuda.Stream()
     x, w = operands(300, 1024, 640, "mx8", seed=2)

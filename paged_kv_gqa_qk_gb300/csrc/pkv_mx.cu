@@ -217,9 +217,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, warps = T >> 5;
     const int chunks = p.hidden / 8;
     pdl_wait();
-    // What waits for its predecessor before it reads microscaled operands may start early.  (A product of bf16 loads
-    // its weights without that wait: no early start behind a bf16 output, which could be such weights.)
-    if (kType != PKV_BF16) pdl_launch_dependents();
+    pdl_launch_dependents();
     uint4 x[kChunks], more[kChunks], w[kChunks];
     auto load = [&](int64_t t) {
 #pragma unroll

@@ -152,16 +152,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Ring before;  // the stage whose products used the slot last
         SfRing sf;
         SlotRing slot;
-        bool ok = true;
+        Waits wait;
         while (walk.next())
             for (int k = 0; k < nk; ++k, slot.next(), sf.next()) {
-                ok &= mbar_wait_spin(bar_landed + 8 * sf.st, sf.parity, ok ? kWaitLimitNs : 0);
+                wait.on(bar_landed + 8 * sf.st, sf.parity);
                 const uint4* from = reinterpret_cast<const uint4*>(sbase + S::kSf + sf.st * 3 * S::kSfBlock) + lane;
                 uint4 v[3 * S::kSfTiles];
 #pragma unroll
                 for (int i = 0; i < 3 * S::kSfTiles; ++i) v[i] = from[32 * i];
                 if (slot.again) {
-                    ok &= mbar_wait_spin(bar_empty + 8 * before.st, before.parity, ok ? kWaitLimitNs : 0);
+                    wait.on(bar_empty + 8 * before.st, before.parity);
                     before.next();
                 }
                 tc_fence_after();
@@ -179,18 +179,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(bar0 + 8 * slot.st);
             }
-        if (!ok && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+        if (!wait.ok() && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 12) {
         // ---- operands: they complete on the even CTA's barrier
         const uint64_t keep = l2_policy_evict_last();  // both are read again by other pairs
         Ring ring;
+        Waits wait;
         bool ok = true;
         while (ok && walk.next()) {
             const int m0 = walk.m * kTileM + (int)rank * 128;
             const int n0 = walk.f * kUnit + (int)rank * (walk.n * kUnit / 2);  // (rows beyond half of the tile are not used)
             for (int k = 0; k < nk; ++k, ring.next()) {
-                if (ring.again) ok &= mbar_wait_spin(bar_empty + 8 * ring.st, ring.parity ^ 1, ok ? kWaitLimitNs : 0);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (ring.again) wait.on(bar_empty + 8 * ring.st, ring.parity ^ 1);
+                if (!(ok = __all_sync(0xffffffffu, wait.ok()))) break;
                 const uint32_t a = base + ring.st * S::kStageBytes, bar = bar_full + 8 * ring.st;
                 if (rank == 0) mbar_arrive_expect_tx_warp(bar, 2 * S::kStageBytes);
                 tma_load_2d_pair_warp(a, &maps.x, k * kSpan, m0, bar, keep);
@@ -199,8 +200,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // the last stages' products are done with this CTA's ring and barriers before it leaves
         for (int i = 0; i < kStages; ++i, ring.next())
-            if (ring.again) ok &= mbar_wait_spin(bar_empty + 8 * ring.st, ring.parity ^ 1, ok ? kWaitLimitNs : 0);
-        if (!ok && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+            if (ring.again) wait.on(bar_empty + 8 * ring.st, ring.parity ^ 1);
+        if (!wait.ok() && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 14) {
         // ---- scales: x's block of 128 tokens and W's two of features, on this CTA's barrier; ahead of the operands
         const uint64_t keep = l2_policy_evict_last();
@@ -209,7 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (ok && walk.next()) {
             const int mb = walk.m * 2 + (int)rank, nb = walk.f / 2;
             for (int k = 0; k < nk; ++k, sf.next()) {
-                if (sf.again) ok &= mbar_wait_spin(bar_taken + 8 * sf.st, sf.parity ^ 1, ok ? kWaitLimitNs : 0);
+                if (sf.again) ok = mbar_wait_spin(bar_taken + 8 * sf.st, sf.parity ^ 1);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const uint32_t to = base + S::kSf + sf.st * 3 * S::kSfBlock, bar = bar_landed + 8 * sf.st;
                 mbar_arrive_expect_tx_warp(bar, 3 * S::kSfBlock);
@@ -221,19 +222,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 13) {
         if (rank == 0) {
             // ---- products of the pair (a wait that ran out does not end the loop, which would make its
-            // counters differ between lanes: the later waits are single looks, the results are void)
+            // counters differ between lanes)
             Ring ring;
             SlotRing slot;
-            bool ok = true, there = false, scaled = false;
+            Waits wait;
+            bool there = false, scaled = false;
             for (int done = 0; walk.next(); ++done) {
                 const uint32_t half = done & 1, acc = tmem + half * kTileN;
-                if (done >= 2) ok &= mbar_wait_spin(bar_free + 8 * half, (done / 2 - 1) & 1, ok ? kWaitLimitNs : 0);
+                if (done >= 2) wait.on(bar_free + 8 * half, (done / 2 - 1) & 1);
                 const uint32_t shape = umma_idesc_mx(kType == PKV_MX4, kTileM, 0, 0) | ((uint32_t)(walk.n * kUnit / 8) << 17);
                 const uint32_t odd = walk.f & 1 ? 2 : 0;  // columns: the tile starts in the middle of a block of 128
                 for (int k = 0; k < nk; ++k) {
                     // (the next stage is looked for before this one's products are issued)
-                    if (!there) ok &= mbar_wait_spin(bar_full + 8 * ring.st, ring.parity, ok ? kWaitLimitNs : 0);
-                    if (!scaled) ok &= mbar_wait_spin(bar_sf + 8 * slot.st, slot.parity, ok ? kWaitLimitNs : 0);
+                    if (!there) wait.on(bar_full + 8 * ring.st, ring.parity);
+                    if (!scaled) wait.on(bar_sf + 8 * slot.st, slot.parity);
                     __syncwarp();
                     const int st = ring.st;
                     const uint32_t a = base + st * S::kStageBytes, sfc = tmem + S::kSfCol + slot.st * S::kSfCols;
@@ -257,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 umma_commit_pair_warp(bar_acc + 8 * half);
             }
-            if (!ok && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+            if (!wait.ok() && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
         }
     } else {
         // ---- epilogue: group h writes every other tile; its warp q holds tokens 32 q .. + 31 of this CTA

@@ -119,6 +119,26 @@ __device__ __forceinline__ Pair add(Pair a, Pair b)
     return {s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l))};
 }
 
+// The sum over a warp of pairs >= 0, in every lane, through integers: each lane's value in units of 2^-24 of what makes
+// the warp's largest one 2^24 to 2^25, as two integers that add up without loss.  Beyond fp32's range or NaN: NaN.
+// (A butterfly of pairs takes twice the instructions and five dependent exchanges.)
+__device__ __forceinline__ Pair warp_sum(Pair a)
+{
+    const float h = __fadd_rn(a.h, a.l), l = __fadd_rn(a.l, __fsub_rn(a.h, h));
+    const uint32_t top = __reduce_max_sync(kAll, __float_as_uint(h));
+    if (top >= 0x7f800000u) return {__uint_as_float(0x7fc00000u), 0.f};
+    const uint32_t e = max(top >> 23, 26u);                               // (units below fp32's least number do no harm)
+    const float up = __uint_as_float((278u - e) << 23), down = __uint_as_float((e - 24u) << 23);  // 2^(24 - E), 2^(E - 24)
+    const float x = __fmul_rn(h, up);
+    const int whole = __float2int_rz(x);
+    const int part = __float2int_rn(__fmul_rn(__fsub_rn(x, __int2float_rn(whole)), 0x1p24f)) +
+                     __float2int_rn(__fmul_rn(__fmul_rn(l, up), 0x1p24f));
+    const int w = __reduce_add_sync(kAll, whole), p = __reduce_add_sync(kAll, part);
+    const float wf = __int2float_rn(w);
+    const float rest = __fmaf_rn(__int2float_rn(p), 0x1p-24f, __int2float_rn(w - __float2int_rn(wf)));
+    return {__fmul_rn(wf, down), __fmul_rn(rest, down)};
+}
+
 // 1 / sqrt(ss * inv_n + eps) to about 2^-44: a fp32 root and one step of Newton's
 // iteration, whose residual 1 - v r^2 is formed without loss.
 __device__ __forceinline__ Pair inv_rms_pair(Pair ss, Pair inv_n, Pair eps)
@@ -165,10 +185,16 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// two bf16 as two floats
-__device__ __forceinline__ uint64_t f2_of_bf16(uint32_t two)
+// a * b + c for two bf16 each of a and b (as fast as two of fp32, without their conversions)
+__device__ __forceinline__ uint64_t f2_fma_bf16(uint32_t a, uint32_t b, uint64_t c)
 {
-    return f2_pack(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+    float c0, c1, d0, d1;
+    f2_unpack(c, c0, c1);
+    asm("{\n\t.reg .b16 a0, a1, b0, b1;\n\tmov.b32 {a0, a1}, %2;\n\tmov.b32 {b0, b1}, %3;\n\t"
+        "fma.rn.f32.bf16 %0, a0, b0, %4;\n\tfma.rn.f32.bf16 %1, a1, b1, %5;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "r"(a), "r"(b), "f"(c0), "f"(c1));
+    return f2_pack(d0, d1);
 }
 // two sums of bf16, each rounded once
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b)
@@ -208,47 +234,49 @@ __device__ __forceinline__ void scaled_odd(uint64_t hw, uint64_t rh, uint64_t rl
 // A CTA takes tokens blockIdx.x, + gridDim.x, ...; its thread i holds chunks i, i + T, ... of 8 columns of each.
 // Every warp forms the sum of the warps' sums and the root by itself, with one barrier a token.
 //
-// Bound by memory where a residual is added: 8192 x 4096 to 8 bits, 236 MB, in 37.7 us, 6.3 TB/s, to bf16, 268 MB, in
-// 42; without one by instructions, some 29 an element with a token's share of the sums (to 4 bits, 85 MB, in 33 us).
+// Bound by memory where a residual is added: 8192 x 4096 to 8 bits, 236 MB, in 37.0 us, 6.4 TB/s, to bf16, 268 MB, in
+// 42; without one by instructions, some 25 an element with a token's share of the sums (to 4 bits, 85 MB, in 30 us; 1001
+// x 5120 in 7.4, in three turns of the CTAs that fit).
 template <int kType, bool kAdd, int kChunks>
 __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
 {
     __shared__ Pair part[2][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, warps = T >> 5;
     const int chunks = p.hidden / 8;
+    constexpr int kCodes = kType == PKV_BF16 ? 16 : mx_row_bytes(kType, 8);  // bytes of a chunk in out
     pdl_wait();
     pdl_launch_dependents();
     uint4 x[kChunks], more[kChunks], w[kChunks];
-    auto load = [&](int64_t t) {
+    auto load = [&](int t) {
+        const uint4* const from = reinterpret_cast<const uint4*>(p.x + t * p.x_stride) + tid;
+        const uint4* const add = reinterpret_cast<const uint4*>(p.residual + (int64_t)t * p.hidden) + tid;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            const int at = tid + c * T;
-            if (at >= chunks) continue;
-            x[c] = *reinterpret_cast<const uint4*>(p.x + t * p.x_stride + 8 * at);
-            if (kAdd) more[c] = *reinterpret_cast<const uint4*>(p.residual + t * p.hidden + 8 * at);
+            if (tid + c * T >= chunks) continue;
+            x[c] = from[c * T];
+            if (kAdd) more[c] = add[c * T];
         }
     };
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) x[c] = more[c] = w[c] = make_uint4(0, 0, 0, 0);
-    load(blockIdx.x);
+    load((int)blockIdx.x);
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
         if (tid + c * T < chunks) w[c] = *reinterpret_cast<const uint4*>(p.w + 8 * (tid + c * T));
     int turn = 0;
-    for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x, turn ^= 1) {
+    for (int t = blockIdx.x; t < p.tokens; t += gridDim.x, turn ^= 1) {
         uint32_t h[kChunks][4];
+        uint4* const h_out = reinterpret_cast<uint4*>(p.residual_out + (int64_t)t * p.hidden) + tid;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
             h[c][0] = x[c].x, h[c][1] = x[c].y, h[c][2] = x[c].z, h[c][3] = x[c].w;
             if constexpr (kAdd) {
                 h[c][0] = add_bf16x2(h[c][0], more[c].x), h[c][1] = add_bf16x2(h[c][1], more[c].y);
                 h[c][2] = add_bf16x2(h[c][2], more[c].z), h[c][3] = add_bf16x2(h[c][3], more[c].w);
-                if (tid + c * T < chunks)
-                    *reinterpret_cast<uint4*>(p.residual_out + t * p.hidden + 8 * (tid + c * T)) =
-                        make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
+                if (tid + c * T < chunks) h_out[c * T] = make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
             }
         }
-        if (t + gridDim.x < p.tokens) load(t + gridDim.x);
+        if (t + (int)gridDim.x < p.tokens) load(t + (int)gridDim.x);
         // squares (exact) added up with what each addition loses
         const uint64_t minus_one = f2_pack(-1.f, -1.f);
         uint64_t s2 = 0, l2 = 0;
@@ -256,10 +284,9 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
         for (int c = 0; c < kChunks; ++c)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint64_t v = f2_of_bf16(h[c][k]);
-                const uint64_t sum = f2_fma(v, v, s2);
-                const uint64_t back = f2_fma(sum, minus_one, s2);             // minus the part of v^2 that went in
-                const uint64_t lost = f2_add(f2_fma(f2_add(sum, back), minus_one, s2), f2_fma(v, v, back));
+                const uint64_t sum = f2_fma_bf16(h[c][k], h[c][k], s2);
+                const uint64_t back = f2_fma(sum, minus_one, s2);             // minus the part of h^2 that went in
+                const uint64_t lost = f2_add(f2_fma(f2_add(sum, back), minus_one, s2), f2_fma_bf16(h[c][k], h[c][k], back));
                 l2 = f2_add(l2, lost);
                 s2 = sum;
             }
@@ -267,18 +294,18 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
         f2_unpack(s2, ss.h, other.h);
         f2_unpack(l2, ss.l, other.l);
         ss = add(ss, other);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss = add(ss, {__shfl_xor_sync(kAll, ss.h, o), __shfl_xor_sync(kAll, ss.l, o)});
+        ss = warp_sum(ss);
         if (warps > 1) {
             if (lane == 0) part[turn][warp] = ss;
             __syncthreads();
-            ss = lane < warps ? part[turn][lane] : Pair{0.f, 0.f};
-            for (int o = 1; o < warps; o <<= 1) ss = add(ss, {__shfl_xor_sync(kAll, ss.h, o), __shfl_xor_sync(kAll, ss.l, o)});
-            ss = {__shfl_sync(kAll, ss.h, 0), __shfl_sync(kAll, ss.l, 0)};
+            ss = warp_sum(lane < warps ? part[turn][lane] : Pair{0.f, 0.f});
         }
         const Pair r = inv_rms_pair(ss, p.inv_n, p.eps);
         const uint64_t rh = f2_pack(r.h, r.h), rl = f2_pack(r.l, r.l);
         const bool exact = r.l == 0.f;
+        // (chunk c lies c T chunks, or T / 16 tiles of scales, further along)
+        uint8_t* const dst = static_cast<uint8_t*>(p.out) + t * (int64_t)(chunks * kCodes) + tid * kCodes;
+        uint8_t* const scale = p.scales + mx_scale_at(t, tid / 4, p.hidden / kMxTileCols);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
             const int at = tid + c * T;
@@ -286,7 +313,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
             uint64_t hw[4];
             float v[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) hw[k] = f2_mul(f2_of_bf16(h[c][k]), f2_of_bf16(wc[k]));
+            for (int k = 0; k < 4; ++k) hw[k] = f2_fma_bf16(h[c][k], wc[k], f2_pack(-0.f, -0.f));  // (exact)
             if (exact) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) scaled_odd<true>(hw[k], rh, rl, v[2 * k], v[2 * k + 1]);
@@ -295,7 +322,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
                 for (int k = 0; k < 4; ++k) scaled_odd<false>(hw[k], rh, rl, v[2 * k], v[2 * k + 1]);
             }
             if constexpr (kType == PKV_BF16) {
-                if (at < chunks) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + t * p.hidden + 8 * at) = pack8(v);
+                if (at < chunks) *reinterpret_cast<uint4*>(dst + c * T * kCodes) = pack8(v);
             } else {
                 uint32_t top = __float_as_uint(max_abs(max_abs(max_abs(v[0], v[1]), max_abs(v[2], v[3])),
                                                        max_abs(max_abs(v[4], v[5]), max_abs(v[6], v[7])))) & 0x7fffffffu;
@@ -309,12 +336,11 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
                 uint2 code = mx_codes8<kType>(v);
                 if (byte == 255u) code = make_uint2(0, 0);
                 if (at >= chunks) continue;
-                uint8_t* dst = static_cast<uint8_t*>(p.out) + t * mx_row_bytes(kType, p.hidden) + mx_row_bytes(kType, 8 * at);
                 if constexpr (kType == PKV_MX8)
-                    *reinterpret_cast<uint2*>(dst) = code;
+                    *reinterpret_cast<uint2*>(dst + c * T * kCodes) = code;
                 else
-                    *reinterpret_cast<uint32_t*>(dst) = code.x;
-                if ((lane & 3) == 0) p.scales[mx_scale_at(t, at / 4, p.hidden / kMxTileCols)] = (uint8_t)byte;
+                    *reinterpret_cast<uint32_t*>(dst + c * T * kCodes) = code.x;
+                if ((lane & 3) == 0) scale[c * (T / 16) * kMxTileBytes] = (uint8_t)byte;
             }
         }
     }
@@ -392,7 +418,7 @@ cudaError_t launch_add_norm(const pkv_pool* pool, const AddNorm& a, cudaStream_t
     // one for a few short rows (300 x 2048 2.4 / 2.6)
     const int per = chunks > 2048 ? 4 : chunks <= 256 && a.tokens <= 2 * pool->num_sms ? 1 : 2;
     const unsigned threads = (unsigned)((chunks + 32 * per - 1) / (32 * per) * 32);
-    // as many CTAs as can be resident, each loading its next token while it works on one (a CTA a token 42 us)
+    // CTAs for twice the threads that registers let be resident, each loading its next token while it works on one (a CTA a token 42 us)
     const unsigned grid = std::min((unsigned)a.tokens, (unsigned)pool->num_sms * std::max(1u, std::min(32u, 2048 / threads)));
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config(grid, threads, attr, s);

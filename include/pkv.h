@@ -569,9 +569,10 @@ PKV_API int pkv_mx_read(pkv_pool* pool, int type, const void* codes, const void*
 /* The residual's addition and a layer's RMS norm in one pass:
  *   h = bf16(x + residual),  y = h / sqrt(mean(h^2) + eps) * w
  * h is rounded once, to bf16, and the norm is that of the rounded h; the sum of squares, the root and
- * the products are carried in pairs of floats (about 2^-44), so that y's one rounding, to out_type, is
- * that of the exact value.  A row with an Inf or a NaN, or whose squares add up beyond fp32's range
- * (values of 2^60 and more), is NaN throughout.
+ * the products are carried in pairs of floats (about 2^-44, 2^-40 at least), so that y's one rounding, to
+ * out_type, is that of the exact value.  A row with an Inf or a NaN, or whose squares add up beyond fp32's range
+ * (values of 2^60 and more), is NaN throughout.  Of an h * w below 2^-126, and of a sum of squares below
+ * 2^-80, fp32's subnormals keep less: with the default eps that shows only in a y below 2^-116.
  *   x             device bf16 [tokens][hidden], x_stride elements between rows (>= hidden, a multiple of 8)
  *   residual      device bf16 [tokens][hidden], or NULL: h = x
  *   residual_out  device bf16 [tokens][hidden]: h (NULL if and only if residual is)

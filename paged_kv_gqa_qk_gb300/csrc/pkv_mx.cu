@@ -213,8 +213,8 @@ __device__ __forceinline__ float max_abs(float a, float b)
 
 // hw * r for two elements, truncated, the last bit set where something was cut off: what a rounding
 // of it to fewer bits gives is then the rounding of the exact value (but for 2^-44 of it).  Nothing
-// is cut off only where r is a float (kExact: r.l = 0, looked at for a row) and the product fits
-// one; with the rest of r at least the products are never floats.
+// is cut off only where r is a float (kExact: its rest beyond 2^-70 of it, looked at for a row) and the product
+// fits one; with the rest of r at least the products are never floats.
 template <bool kExact>
 __device__ __forceinline__ void scaled_odd(uint64_t hw, uint64_t rh, uint64_t rl, float& a, float& b)
 {
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
         }
         const Pair r = inv_rms_pair(ss, p.inv_n, p.eps);
         const uint64_t rh = f2_pack(r.h, r.h), rl = f2_pack(r.l, r.l);
-        const bool exact = r.l == 0.f;
+        const bool exact = fabsf(r.l) <= r.h * 0x1p-70f;
         // (chunk c lies c T chunks, or T / 16 tiles of scales, further along)
         uint8_t* const dst = static_cast<uint8_t*>(p.out) + t * (int64_t)(chunks * kCodes) + tid * kCodes;
         uint8_t* const scale = p.scales + mx_scale_at(t, tid / 4, p.hidden / kMxTileCols);

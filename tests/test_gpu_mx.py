@@ -152,6 +152,42 @@ def test_add_norm_sizes_of_values(pool, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", *KINDS])
+@pytest.mark.parametrize("hidden", [128, 2048, 4096, 16384])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+def test_add_norm_uneven_rows(kind, hidden, eps):
+    """Squares that span fp32's range within a thread's columns, a warp's and a row's: the sum is theirs, whatever the order."""
+    gen = torch.Generator().manual_seed(hidden)
+    x = torch.randn(9, hidden, generator=gen)
+    size = torch.randint(-55, 55, (9, hidden), generator=gen).float()
+    x[0] *= 2.0 ** size[0]
+    x[1] *= 2.0 ** (size[1] / 8)
+    x[2, :] = 1.0 + 2.0 ** -7                              # equal ones, whose sum is none of fp32's
+    x[3] *= 2.0 ** -12
+    x[3, hidden - 1] = 2.0 ** 50                           # one that dominates, in the last column
+    x[4] *= 2.0 ** (torch.arange(hidden) % 8 * 6 - 20.0)   # by column of a thread
+    x[5] *= 2.0 ** (torch.arange(hidden) // 8 % 32 - 16.0)  # by lane
+    x[6] *= 2.0 ** (torch.arange(hidden) * 60.0 / hidden - 30)  # by warp
+    x[7] = 0
+    x[7, hidden // 2] = 3.0                                # one alone
+    x = x.to(torch.bfloat16)
+    w = torch.randn(hidden, generator=gen).to(torch.bfloat16)
+    z = torch.zeros(2, 1, 64, 128, dtype=torch.bfloat16, device=DEV)
+    p = pkv.PagedKVPool(z[0], z[1], cfg=dict(heads=4, kv_heads=1, max_seq=64, eps=eps))
+    out, _ = p.add_norm(x.to(DEV), None, w.to(DEV), out=kind)
+    # Rows of equal values and of one that dominates have y on the very borders between two outputs, where the side is open
+    # within 2^-40 of y.  That is what the pairs keep: a lane adds 16 squares to each of two sums; each addition loses 2^-24 of
+    # the sum at most, which is kept, and the up to 16 * 2^-24 of the sum kept are themselves rounded 16 times, by 2^-24: 2^-40
+    # of the sum.  A sum over a warp is off by one unit of 2^-24 a lane, of 2^24 units at least (2^-43), and a rounding of the
+    # 2^7 units behind its first 24 bits (2^-42), twice.  The root halves these, 0.75 * 2^-40; its own error is 2^-45 and the
+    # product's 2^-48.
+    y, d = _mx.norm(_mx.f64(x), _mx.f64(w), eps), 2.0 ** -40
+    form = _mx.bf16 if kind == "bf16" else lambda v: _mx.held(v, kind)
+    got = _mx.f64(out) if kind == "bf16" else _mx.stored(out)
+    assert ((got == form(y * (1 - d))) | (got == form(y * (1 + d)))).all() and p.check_errors() == 0
+    p.close()
+
+
+@pytest.mark.parametrize("kind", ["bf16", *KINDS])
 def test_add_norm_rows_without_a_norm(pool, kind):
     """An Inf, a NaN and squares beyond fp32's range make their row NaN, and no other."""
     x = _mx.activations(5, 256, seed=3)

@@ -17,9 +17,9 @@
 // of the even CTA issues a stage's four products.  Two groups of four warps write y in bf16
 // through shared memory with TMA, an accumulator each.
 //
-// Measured (of four and two times the measured bf16 rate): 8192 x 4096 x 6144 in 4 bits 66 us, 6.2
-// PFLOP/s (0.82), in 8 bits 123 us, 3.35 (0.89); 2048 tokens 21.5 and 34.7 us; 4096 x 8192 x 8192 82
-// and 175.  A call's start and end take some 7 us in all of them.
+// Measured (of four and two times the measured bf16 rate): 8192 x 4096 x 6144 in 4 bits 62 us, 6.6
+// PFLOP/s (0.88), in 8 bits 122 us, 3.4 (0.9); 2048 tokens 20.8 and 34.3 us; 4096 x 8192 x 8192 79
+// and 173.  A call's start and end take some 7 us in all of them.
 #include <atomic>
 
 #include "pkv_mx.cuh"
@@ -143,6 +143,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(sbase + S::kTmemSlot), 0);
+    if (warp == 12) {
+        // the first stages of W on their way to L2 before the wait for the kernel before this one, which may still be
+        // writing it: what is read comes after (8192 x 4096 x 6144 in 4 bits 65 -> 62 us)
+        Walk first = walk;
+        if (first.next())
+            for (int k = 0; k < min(nk, kStages); ++k)
+                tma_prefetch_2d_warp(&maps.w, k * kSpan, first.f * kUnit + (int)rank * (first.n * kUnit / 2));
+    }
     pdl_wait();
     pdl_launch_dependents();
 

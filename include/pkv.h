@@ -588,8 +588,9 @@ PKV_API int pkv_add_norm(pkv_pool* pool, const void* x, int64_t x_stride, const 
 
 /* y[t][o] = sum_k x[t][k] w[o][k] of two microscaled tensors of one type, x [tokens][in_features] and
  * w [out_features][in_features]; products exact, fp32 accumulation, bf16 output (pkv_linear's, over the
- * values the tensors hold).  out_features % 128 == 0 (PKV_ENOTIMPL otherwise).  A NaN scale makes its row
- * of x (or its feature of w) NaN in y.  y: device bf16 [tokens][out_features], 16-byte aligned.
+ * values the tensors hold).  out_features % 128 == 0 (PKV_ENOTIMPL otherwise), <= 2^20 (PKV_ERANGE).
+ * A NaN scale makes its row of x (or its feature of w) NaN in y.  y: device bf16 [tokens][out_features],
+ * 16-byte aligned.
  * The same from run to run; rows of x do not affect each other. */
 PKV_API int pkv_mx_linear(pkv_pool* pool, int type, const void* x_codes, const void* x_scales, const void* w_codes,
                           const void* w_scales, void* y, int tokens, int in_features, int out_features, void* stream);

@@ -18,8 +18,6 @@
 // L2 with 64 tokens (4096 x 4096 in 8 bits: 26 MB into 128 SMs, W's and x's part for every tile of W, 1.8 of 6.9 us);
 // by memory beyond (16 tokens, 4096 x 65536 in 8 bits, 277 MB, 41 us, 6.8 TB/s).  Scales by four warps and sums by
 // st.async in place of the cluster's barrier took as long here.
-#include <atomic>
-
 #include "pkv_mx.cuh"
 
 namespace pkv {
@@ -247,25 +245,13 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// Allows the kernel its shared memory on a device, once.
 template <int kType, int BN, int NS>
-bool allowed(int device)
-{
-    static std::atomic<uint64_t> known{0};
-    const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
-    if (known.load(std::memory_order_relaxed) & bit) return true;
-    if (cudaFuncSetAttribute(mx_linear_kernel<kType, BN, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Shape<kType, BN>::alloc(Shape<kType, BN>::kMaxStages)) != cudaSuccess)
-        return false;
-    known.fetch_or(bit, std::memory_order_relaxed);
-    return true;
-}
-
-template <int kType, int BN, int NS>
-cudaError_t launch(int device, const MxLinear& a, Params& p, const CUtensorMap& tmW, const CUtensorMap& tmX, cudaStream_t s)
+cudaError_t launch(const MxLinear& a, Params& p, const CUtensorMap& tmW, const CUtensorMap& tmX, cudaStream_t s)
 {
     using S = Shape<kType, BN>;
-    if (!allowed<kType, BN, NS>(device)) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = cudaFuncSetAttribute(mx_linear_kernel<kType, BN, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               S::alloc(S::kMaxStages));
+    if (e != cudaSuccess) return e;
     const int nk = (mx_row_bytes(kType, a.in) + kSpan - 1) / kSpan, share = (nk + NS - 1) / NS;
     p.stages = share < S::kMaxStages ? share : S::kMaxStages;
     cudaLaunchAttribute attr[2];
@@ -302,10 +288,10 @@ cudaError_t launch_bn(const pkv_pool* pool, const MxLinear& a, Params& p, cudaSt
            tiles * splits * 2 <= (BN <= 32 && splits < 4 ? 2 : 1) * (int64_t)pool->num_sms)
         splits *= 2;
     switch (splits) {
-        case 1: return launch<kType, BN, 1>(pool->device, a, p, tmW, tmX, s);
-        case 2: return launch<kType, BN, 2>(pool->device, a, p, tmW, tmX, s);
-        case 4: return launch<kType, BN, 4>(pool->device, a, p, tmW, tmX, s);
-        default: return launch<kType, BN, 8>(pool->device, a, p, tmW, tmX, s);
+        case 1: return launch<kType, BN, 1>(a, p, tmW, tmX, s);
+        case 2: return launch<kType, BN, 2>(a, p, tmW, tmX, s);
+        case 4: return launch<kType, BN, 4>(a, p, tmW, tmX, s);
+        default: return launch<kType, BN, 8>(a, p, tmW, tmX, s);
     }
 }
 

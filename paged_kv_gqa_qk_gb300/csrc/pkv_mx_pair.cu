@@ -336,15 +336,15 @@ int resident_pairs(int device)
     static std::atomic<int> known[64];
     const bool keep = device >= 0 && device < 64;
     int pairs = keep ? known[device].load(std::memory_order_relaxed) : 0;
+    if (cudaFuncSetAttribute(mx_pair_kernel<kType>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<kType>::kAlloc) !=
+        cudaSuccess)
+        return 0;
     if (pairs) return pairs;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Shape<kType>::kAlloc;
-    if (cudaFuncSetAttribute(mx_pair_kernel<kType>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<kType>::kAlloc) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&pairs, mx_pair_kernel<kType>, &cfg) != cudaSuccess)
-        return 0;
+    if (cudaOccupancyMaxActiveClusters(&pairs, mx_pair_kernel<kType>, &cfg) != cudaSuccess) return 0;
     if (keep) known[device].store(pairs, std::memory_order_relaxed);
     return pairs;
 }

@@ -252,7 +252,7 @@ __device__ __forceinline__ void umma_bf16_ts_acc(uint32_t tmem_d, uint32_t tmem_
 // ---- block-scaled products: 8-bit (e4m3) or 4-bit (e2m1) operands, a power of two (e8m0) on
 // every 32 values along K.  K is 32 values (8-bit) or 64 (4-bit) an instruction, 32 bytes of
 // either operand's rows.  The scales lie in tensor memory: row 32 j + i's in lane i of column j,
-// 4 bytes for 4 consecutive groups, copied from shared memory by umma_copy_scales.
+// 4 bytes for 4 consecutive groups, copied from shared memory by umma_copy_scales_warp or stored there.
 //
 // Instruction descriptor: M x N; sf = which byte of a column's 4 holds this instruction's
 // first group (8-bit: 0..3, 4-bit: 0 or 2), the same for both operands.
@@ -341,15 +341,9 @@ __device__ __forceinline__ void tma_load_2d_pair_warp(uint32_t dst, const CUtens
         : "memory");
 }
 
-// Arrive once on a barrier of another CTA of the cluster (an address from cluster_map).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// The same without ordering this thread's memory operations before it: for what is handed over in
-// tensor memory alone, after tcgen05.wait (a release at cluster scope waits for the thread's loads
-// in flight).
+// Arrive once on a barrier of another CTA of the cluster (an address from cluster_map) without
+// ordering this thread's memory operations before it: for what is handed over in tensor memory
+// alone, after tcgen05.wait (a release at cluster scope waits for the thread's loads in flight).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");

@@ -29,17 +29,18 @@ constexpr int kBM = 128;        // output features a tile
 constexpr int kSpan = 128;      // bytes of a row a stage
 constexpr int kMaxSplits = 8;   // a portable cluster
 
-template <int kType, int BN>
+template <int kType, int BN, int NS>
 struct Shape {
     static constexpr int kSfTiles = kType == PKV_MX4 ? 2 : 1;       // tiles of scales a stage and 128 rows
     static constexpr int kABytes = kBM * kSpan, kBBytes = BN * kSpan, kSf = kSfTiles * kMxTileBytes;
     static constexpr int kStageBytes = kABytes + kBBytes + 2 * kSf;
     static_assert(kStageBytes % 1024 == 0, "operands on 1024-byte borders");
-    static constexpr int kSums = kBM * BN * 4;                      // the cluster's sums of this CTA's tokens
+    static constexpr int kSums = NS > 1 ? kBM * BN * 4 : 0;         // the cluster's sums of this CTA's tokens
     static constexpr int kMost = (BN <= 32 ? 112 : 220) * 1024;     // shared memory: two CTAs an SM, or one
     static constexpr int kMaxStages = (kMost - kSums - 2048) / kStageBytes;
     // tensor memory: the accumulator, then the scales of W and of x, 4 columns a tile.  As many CTAs as an SM's
-    // shared memory holds (7, 5 and 3 of them) never have to wait for columns, which a CTA keeps until its cluster is done.
+    // shared memory holds (7, 5 and 3 of them) never have to wait for columns, which a CTA keeps until its cluster is done.  (More CTAs
+    // without a cluster may have to, for others that wait for none.)
     static constexpr int kSfaCol = BN, kSfbCol = BN + 4 * kSfTiles, kUsed = kSfbCol + 4 * kSfTiles;
     static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : 128;
     static constexpr int alloc(int stages) { return stages * kStageBytes + kSums + 8 * (2 * stages + 1) + 16 + 1024; }
@@ -67,7 +68,7 @@ template <int kType, int BN, int NS>
 __global__ void __launch_bounds__(kThreads)
     mx_linear_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, Params p)
 {
-    using S = Shape<kType, BN>;
+    using S = Shape<kType, BN, NS>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
     const uint32_t base = (raw_base + 1023u) & ~1023u;  // (the same offset in the cluster's CTAs)
@@ -167,69 +168,89 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncwarp();
 
-    // ---- each thread's feature of every token to the token's CTA: [CTA it comes from][its tokens / 4][features][4]
-    constexpr int kOwn = BN / NS, kVec = kOwn < 4 ? kOwn : 4, kStep = BN < 32 ? 16 : 32;
+    // ---- each thread has a feature of every token
+    constexpr int kOwn = BN / NS, kVec = kOwn < 4 ? kOwn : 4, kRounds = kOwn / kVec;
     static_assert(kVec >= 2, "two tokens a CTA at least");
     const bool ok = mbar_wait_spin(bar_done, 0);
     tc_fence_after();
     if (NS > 1) cluster_wait();
     const int tokens = min(BN, p.tokens - n0), feature = 32 * warp + lane;
-#pragma unroll 1
-    for (int c0 = 0; c0 < tokens; c0 += kStep) {
-        uint32_t v[kStep];
-        if constexpr (kStep == 16) {
-            tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + c0, v);
-            tmem_wait_ld();
-        } else {
-            tmem_ld32(tmem + ((uint32_t)(32 * warp) << 16) + c0, v);
-            tmem_wait_ld_regs(v);
-        }
+    constexpr int kCols = BN < 32 ? BN : 32;  // of a load
+    uint32_t v[BN / kCols][kCols];
 #pragma unroll
-        for (int j = 0; j < kStep; j += kVec) {
-            const int t = c0 + j, owner = t / kOwn;
-            if (t >= tokens) break;
-            float f[4];
+    for (int c = 0; c < BN / kCols; ++c) {
+        const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16) + kCols * c;
+        if constexpr (kCols == 16)
+            tmem_ld16(at, v[c]);
+        else
+            tmem_ld32(at, v[c]);
+    }
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) f[i] = ok ? __uint_as_float(v[j + i]) : 0.f;
-            uint32_t to = sums + (uint32_t)((rank * (kOwn / kVec) + t % kOwn / kVec) * kBM + feature) * (4 * kVec);
-            if (NS > 1) to = cluster_map(to, owner);  // (without a cluster, shared::cluster is this CTA's)
-            if constexpr (kVec == 4)
-                st_cluster_f32x4(to, f[0], f[1], f[2], f[3]);
-            else
-                st_cluster_f32x2(to, f[0], f[1]);
+    for (int c = 0; c < BN / kCols; ++c) tmem_wait_ld_regs(v[c]);
+    if constexpr (NS == 1) {
+        // no cluster: two lanes share their tokens out, so that each writes two features of a token at a time (128 tokens,
+        // 4096 x 6144 in 4 bits 7.2 us, through shared memory as below 7.9)
+        int yw, yc;
+        __nv_bfloat16* const y = segment(p, m0, yw, yc) + (int64_t)n0 * yw + yc + (feature & ~1);
+        const bool odd = lane & 1;
+#pragma unroll
+        for (int t = 0; t < BN; t += 2) {
+            const float lo = __uint_as_float(v[t / kCols][t % kCols]), hi = __uint_as_float(v[t / kCols][t % kCols + 1]);
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+            const float a = odd ? other : lo, b = odd ? hi : other;
+            if (t + odd < tokens)
+                *reinterpret_cast<uint32_t*>(y + (int64_t)(t + odd) * yw) =
+                    ok ? pack_bf16(__float2bfloat16_rn(a), __float2bfloat16_rn(b)) : 0u;
         }
+        tc_fence_before();
+        __syncthreads();
+        if (warp == 1) {
+            tc_fence_after();
+            tmem_dealloc(tmem, S::kCols);
+        }
+        return;
+    }
+    // ---- to the token's CTA: [CTA it comes from][its tokens / 4][features][4]
+#pragma unroll
+    for (int t = 0; t < BN; t += kVec) {
+        if (t >= tokens) break;
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) f[i] = ok ? __uint_as_float(v[t / kCols][t % kCols + i]) : 0.f;
+        const uint32_t at = sums + (uint32_t)((rank * kRounds + t % kOwn / kVec) * kBM + feature) * (4 * kVec);
+        const uint32_t to = cluster_map(at, t / kOwn);
+        if constexpr (kVec == 4)
+            st_cluster_f32x4(to, f[0], f[1], f[2], f[3]);
+        else
+            st_cluster_f32x2(to, f[0], f[1]);
     }
     tc_fence_before();
-    if (NS > 1)
-        cluster_sync();
-    else
-        __syncthreads();
+    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, S::kCols);
     }
-    // ---- this CTA's tokens: a thread adds up its feature of kVec of them; two lanes then share theirs out, so
-    // that each writes two features of a token at a time
+    // ---- this CTA's tokens: a thread adds up its feature of kVec of them; two lanes then share theirs out
     int yw, yc;
     __nv_bfloat16* const y = segment(p, m0, yw, yc) + (int64_t)n0 * yw;
     const bool odd = lane & 1;
-    for (int i = 0; i < kOwn / kVec; ++i) {
+    for (int i = 0; i < kRounds; ++i) {
         const int t0 = rank * kOwn + i * kVec;
         if (t0 >= tokens) break;
         float acc[kVec];
 #pragma unroll
         for (int q = 0; q < NS; ++q) {
-            const float* from = reinterpret_cast<const float*>(sbase + (sums - base)) + (size_t)((q * (kOwn / kVec) + i) * kBM + feature) * kVec;
-            float v[kVec];
+            const float* from = reinterpret_cast<const float*>(sbase + (sums - base)) + (size_t)((q * kRounds + i) * kBM + feature) * kVec;
+            float part[kVec];
             if constexpr (kVec == 4) {
                 const float4 u = *reinterpret_cast<const float4*>(from);
-                v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+                part[0] = u.x, part[1] = u.y, part[2] = u.z, part[3] = u.w;
             } else {
                 const float2 u = *reinterpret_cast<const float2*>(from);
-                v[0] = u.x, v[1] = u.y;
+                part[0] = u.x, part[1] = u.y;
             }
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) acc[j] = q ? acc[j] + v[j] : v[j];
+            for (int j = 0; j < kVec; ++j) acc[j] = q ? acc[j] + part[j] : part[j];
         }
         // the even lane takes the first half of the tokens for both features, the odd lane the second
 #pragma unroll
@@ -248,7 +269,7 @@ __global__ void __launch_bounds__(kThreads)
 template <int kType, int BN, int NS>
 cudaError_t launch(const MxLinear& a, Params& p, const CUtensorMap& tmW, const CUtensorMap& tmX, cudaStream_t s)
 {
-    using S = Shape<kType, BN>;
+    using S = Shape<kType, BN, NS>;
     const cudaError_t e = cudaFuncSetAttribute(mx_linear_kernel<kType, BN, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                S::alloc(S::kMaxStages));
     if (e != cudaSuccess) return e;
@@ -320,7 +341,7 @@ cudaError_t launch_mx_linear(const pkv_pool* pool, const MxLinear& a, cudaStream
     p.in = a.in;
     p.out = p.seg_end[2];
     // Tiles of up to 64 tokens while each finds an SM, and in more turns than one for up to 48 tokens, where the work
-    // is W's bytes (us here / over pairs, in 4 and in 8 bits: 128 tokens, 4096 x 6144 7.9 / 8.4 and 10.7 / 11.9; 333
+    // is W's bytes (us here / over pairs, in 4 and in 8 bits: 128 tokens, 4096 x 6144 6.9 / 8.4 and 9.8 / 11.9; 333
     // tokens, 4096 x 1024 5.7 / 6.4 and 7.0 / 9.6, 4096 x 4096 15 / 8.3 and 22 / 11.7; 64 tokens, 4096 x 65536 38 / 31 and
     // 56 / 55, 32 tokens, 4096 x 16384 8.4 / 14.5 and 12.7 / 20.7)
     const int64_t tiles = (int64_t)(p.out / kBM) * ((a.tokens + 63) / 64);

@@ -38,9 +38,9 @@ struct Shape {
     static constexpr int kSums = NS > 1 ? kBM * BN * 4 : 0;         // the cluster's sums of this CTA's tokens
     static constexpr int kMost = (BN <= 32 ? 112 : 220) * 1024;     // shared memory: two CTAs an SM, or one
     static constexpr int kMaxStages = (kMost - kSums - 2048) / kStageBytes;
-    // tensor memory: the accumulator, then the scales of W and of x, 4 columns a tile.  As many CTAs as an SM's
-    // shared memory holds (7, 5 and 3 of them) never have to wait for columns, which a CTA keeps until its cluster is done.  (More CTAs
-    // without a cluster may have to, for others that wait for none.)
+    // tensor memory: the accumulator, then the scales of W and of x, 4 columns a tile.  As many CTAs with a cluster as an
+    // SM's shared memory holds (7, 5 and 3 of them) never have to wait for columns, which a CTA keeps until its cluster
+    // is done.  (More CTAs without one may have to, for others that wait for none.)
     static constexpr int kSfaCol = BN, kSfbCol = BN + 4 * kSfTiles, kUsed = kSfbCol + 4 * kSfTiles;
     static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : 128;
     static constexpr int alloc(int stages) { return stages * kStageBytes + kSums + 8 * (2 * stages + 1) + 16 + 1024; }

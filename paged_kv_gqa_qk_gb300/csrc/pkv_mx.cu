@@ -17,47 +17,55 @@ namespace {
 constexpr uint32_t kAll = 0xffffffffu;
 
 // ---- bf16 -> microscaled ----
-// 16 lanes take 128 columns of a row, 8 each; a group of 32 is 4 lanes.
+// 8 lanes take 128 columns of a row, 16 each; a group of 32 is 2 lanes.
 template <int kType, int kPasses>
 __global__ void __launch_bounds__(256)
     mx_quantize_kernel(const __nv_bfloat16* x, int64_t x_stride, int rows, int cols, uint8_t* codes,
                        uint8_t* scales)
 {
-    const int tiles = cols / kMxTileCols, tile = blockIdx.x % tiles;
-    const int64_t row0 = (int64_t)(blockIdx.x / tiles) * (16 * kPasses);
-    const int sub = threadIdx.x >> 4, j = threadIdx.x & 15;
-    const int col = tile * kMxTileCols + 8 * j;
+    const int tiles = cols / kMxTileCols, tile = blockIdx.x % tiles, step = blockDim.x >> 3;
+    const int64_t row0 = (int64_t)(blockIdx.x / tiles) * (step * kPasses);
+    const int sub = threadIdx.x >> 3, j = threadIdx.x & 7;
+    const int col = tile * kMxTileCols + 16 * j;
     pdl_wait();
-    uint4 raw[kPasses];
+    uint4 raw[kPasses][2];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-        const int64_t r = row0 + 16 * i + sub;
-        raw[i] = r < rows ? *reinterpret_cast<const uint4*>(x + r * x_stride + col) : make_uint4(0, 0, 0, 0);
+        const int64_t r = row0 + step * i + sub;
+        const uint4* const from = reinterpret_cast<const uint4*>(x + r * x_stride + col);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) raw[i][k] = r < rows ? from[k] : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-        const int64_t r = row0 + 16 * i + sub;
-        float v[8];
-        unpack8(raw[i], v);
+        const int64_t r = row0 + step * i + sub;
         // the largest magnitude of the group, as 16-bit integers (a NaN above an Inf above all numbers)
-        uint32_t two = __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
-                                __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
+        uint32_t two = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            two = __vmaxu2(two, __vmaxu2(__vmaxu2(raw[i][k].x & 0x7fff7fffu, raw[i][k].y & 0x7fff7fffu),
+                                         __vmaxu2(raw[i][k].z & 0x7fff7fffu, raw[i][k].w & 0x7fff7fffu)));
         two = __vmaxu2(two, __shfl_xor_sync(kAll, two, 1));
-        two = __vmaxu2(two, __shfl_xor_sync(kAll, two, 2));
         const uint32_t top = max(two << 16, two & 0xffff0000u);
         const uint32_t byte = mx_scale_byte<kType>(top);
         const float inv = mx_inverse(byte);
+        uint2 c[2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= inv;
-        uint2 c = mx_codes8<kType>(v);
-        if (byte == 255u) c = make_uint2(0, 0);
+        for (int k = 0; k < 2; ++k) {
+            float v[8];
+            unpack8(raw[i][k], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= inv;
+            c[k] = mx_codes8<kType>(v);
+            if (byte == 255u) c[k] = make_uint2(0, 0);
+        }
         if (r >= rows) continue;
         uint8_t* dst = codes + r * mx_row_bytes(kType, cols) + mx_row_bytes(kType, col);
         if constexpr (kType == PKV_MX8)
-            *reinterpret_cast<uint2*>(dst) = c;
+            *reinterpret_cast<uint4*>(dst) = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
         else
-            *reinterpret_cast<uint32_t*>(dst) = c.x;
-        if ((j & 3) == 0) scales[mx_scale_at(r, 4 * tile + (j >> 2), tiles)] = (uint8_t)byte;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(c[0].x, c[1].x);
+        if ((j & 1) == 0) scales[mx_scale_at(r, 4 * tile + (j >> 1), tiles)] = (uint8_t)byte;
     }
 }
 
@@ -372,15 +380,15 @@ cudaError_t launch_mx_quantize(const pkv_pool* pool, const void* x, int64_t x_st
 {
     const int tiles = cols / kMxTileCols;
     const bool many = (int64_t)(rows + 127) / 128 * tiles >= 2 * pool->num_sms;
-    const int step = many ? 64 : 16;
+    const int step = many ? 64 : 16, threads = many ? 256 : 128;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = config((unsigned)((rows + step - 1) / step * tiles), 256, attr, s);
+    cudaLaunchConfig_t cfg = config((unsigned)((rows + step - 1) / step * tiles), threads, attr, s);
     auto launch = [&](auto kernel) {
         return cudaLaunchKernelEx(&cfg, kernel, static_cast<const __nv_bfloat16*>(x), x_stride, rows, cols,
                                   static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
     };
-    if (type == PKV_MX8) return many ? launch(mx_quantize_kernel<PKV_MX8, 4>) : launch(mx_quantize_kernel<PKV_MX8, 1>);
-    return many ? launch(mx_quantize_kernel<PKV_MX4, 4>) : launch(mx_quantize_kernel<PKV_MX4, 1>);
+    if (type == PKV_MX8) return many ? launch(mx_quantize_kernel<PKV_MX8, 2>) : launch(mx_quantize_kernel<PKV_MX8, 1>);
+    return many ? launch(mx_quantize_kernel<PKV_MX4, 2>) : launch(mx_quantize_kernel<PKV_MX4, 1>);
 }
 
 cudaError_t launch_mx_read(const pkv_pool* pool, int type, const void* codes, const void* scales, int rows, int cols,

@@ -243,25 +243,29 @@ __device__ __forceinline__ void scaled_odd(uint64_t hw, uint64_t rh, uint64_t rl
 // Every warp forms the sum of the warps' sums and the root by itself, with one barrier a token.
 //
 // Bound by memory where a residual is added: 8192 x 4096 to 8 bits, 236 MB, in 37.0 us, 6.4 TB/s, to bf16, 268 MB, in
-// 42; without one by instructions, some 25 an element with a token's share of the sums (to 4 bits, 85 MB, in 30 us; 1001
-// x 5120 in 7.4, in three turns of the CTAs that fit).
+// 42; without one by instructions, some 23 an element with a token's share of the sums (to 4 bits, 85 MB, in 28 us; 1001
+// x 5120 in 7.1, in three turns of the CTAs that fit).
 template <int kType, bool kAdd, int kChunks>
 __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
 {
     __shared__ Pair part[2][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, warps = T >> 5;
     const int chunks = p.hidden / 8;
+    // Pairs of chunks beside each other where none of bf16 is written: a group of 32 is two lanes then, not four (8192 x
+    // 4096 to 4 bits 30 -> 28 us).  Stores of 16 bytes 32 apart would cost more than that.
+    constexpr bool kNear = !kAdd && kType != PKV_BF16 && kChunks > 1;
+    auto chunk = [&](int c) { return kNear ? 2 * (tid + c / 2 * T) + c % 2 : tid + c * T; };
     constexpr int kCodes = kType == PKV_BF16 ? 16 : mx_row_bytes(kType, 8);  // bytes of a chunk in out
     pdl_wait();
     pdl_launch_dependents();
     uint4 x[kChunks], more[kChunks], w[kChunks];
     auto load = [&](int t) {
-        const uint4* const from = reinterpret_cast<const uint4*>(p.x + t * p.x_stride) + tid;
-        const uint4* const add = reinterpret_cast<const uint4*>(p.residual + (int64_t)t * p.hidden) + tid;
+        const uint4* const from = reinterpret_cast<const uint4*>(p.x + t * p.x_stride) + chunk(0);
+        const uint4* const add = reinterpret_cast<const uint4*>(p.residual + (int64_t)t * p.hidden) + chunk(0);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            if (tid + c * T >= chunks) continue;
-            x[c] = from[c * T];
+            if (chunk(c) >= chunks) continue;
+            x[c] = from[chunk(c) - chunk(0)];
             if (kAdd) more[c] = add[c * T];
         }
     };
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
     load((int)blockIdx.x);
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
-        if (tid + c * T < chunks) w[c] = *reinterpret_cast<const uint4*>(p.w + 8 * (tid + c * T));
+        if (chunk(c) < chunks) w[c] = *reinterpret_cast<const uint4*>(p.w + 8 * chunk(c));
     int turn = 0;
     for (int t = blockIdx.x; t < p.tokens; t += gridDim.x, turn ^= 1) {
         uint32_t h[kChunks][4];
@@ -311,15 +315,11 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
         const Pair r = inv_rms_pair(ss, p.inv_n, p.eps);
         const uint64_t rh = f2_pack(r.h, r.h), rl = f2_pack(r.l, r.l);
         const bool exact = fabsf(r.l) <= r.h * 0x1p-70f;
-        // (chunk c lies c T chunks, or T / 16 tiles of scales, further along)
-        uint8_t* const dst = static_cast<uint8_t*>(p.out) + t * (int64_t)(chunks * kCodes) + tid * kCodes;
-        uint8_t* const scale = p.scales + mx_scale_at(t, tid / 4, p.hidden / kMxTileCols);
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int at = tid + c * T;
+        uint8_t* const dst = static_cast<uint8_t*>(p.out) + t * (int64_t)(chunks * kCodes) + chunk(0) * kCodes;
+        uint8_t* const scale = p.scales + mx_scale_at(t, chunk(0) / 4, p.hidden / kMxTileCols);
+        auto scaled = [&](int c, float (&v)[8]) {
             const uint32_t wc[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
             uint64_t hw[4];
-            float v[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) hw[k] = f2_fma_bf16(h[c][k], wc[k], f2_pack(-0.f, -0.f));  // (exact)
             if (exact) {
@@ -329,26 +329,52 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) scaled_odd<false>(hw[k], rh, rl, v[2 * k], v[2 * k + 1]);
             }
-            if constexpr (kType == PKV_BF16) {
-                if (at < chunks) *reinterpret_cast<uint4*>(dst + c * T * kCodes) = pack8(v);
-            } else {
-                uint32_t top = __float_as_uint(max_abs(max_abs(max_abs(v[0], v[1]), max_abs(v[2], v[3])),
-                                                       max_abs(max_abs(v[4], v[5]), max_abs(v[6], v[7])))) & 0x7fffffffu;
+        };
+        // (chunk c lies c T chunks, or T / 16 tiles of scales, further along)
+        if constexpr (kType == PKV_BF16) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                float v[8];
+                scaled(c, v);
+                if (chunk(c) < chunks) *reinterpret_cast<uint4*>(dst + c * T * kCodes) = pack8(v);
+            }
+        } else {
+            constexpr int kSet = kNear ? 2 : 1;  // chunks of a set, 16 or 8 columns that lie together
+#pragma unroll
+            for (int c = 0; c < kChunks; c += kSet) {
+                float v[kSet][8];
+                uint32_t top = 0;
+#pragma unroll
+                for (int s = 0; s < kSet; ++s) {
+                    scaled(c + s, v[s]);
+                    top = max(top, __float_as_uint(max_abs(max_abs(max_abs(v[s][0], v[s][1]), max_abs(v[s][2], v[s][3])),
+                                                           max_abs(max_abs(v[s][4], v[s][5]), max_abs(v[s][6], v[s][7])))) &
+                                       0x7fffffffu);
+                }
                 top = max(top, __shfl_xor_sync(kAll, top, 1));
-                top = max(top, __shfl_xor_sync(kAll, top, 2));
+                if (kSet == 1) top = max(top, __shfl_xor_sync(kAll, top, 2));
                 const uint32_t byte = mx_scale_byte<kType>(top);
                 const float inv = mx_inverse(byte);
                 const uint64_t inv2 = f2_pack(inv, inv);
+                uint2 code[kSet];
 #pragma unroll
-                for (int k = 0; k < 8; k += 2) f2_unpack(f2_mul(f2_pack(v[k], v[k + 1]), inv2), v[k], v[k + 1]);
-                uint2 code = mx_codes8<kType>(v);
-                if (byte == 255u) code = make_uint2(0, 0);
-                if (at >= chunks) continue;
-                if constexpr (kType == PKV_MX8)
-                    *reinterpret_cast<uint2*>(dst + c * T * kCodes) = code;
+                for (int s = 0; s < kSet; ++s) {
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) f2_unpack(f2_mul(f2_pack(v[s][k], v[s][k + 1]), inv2), v[s][k], v[s][k + 1]);
+                    code[s] = mx_codes8<kType>(v[s]);
+                    if (byte == 255u) code[s] = make_uint2(0, 0);
+                }
+                if (chunk(c) >= chunks) continue;
+                uint8_t* const to = dst + (chunk(c) - chunk(0)) * kCodes;
+                if constexpr (kNear && kType == PKV_MX8)
+                    *reinterpret_cast<uint4*>(to) = make_uint4(code[0].x, code[0].y, code[kSet - 1].x, code[kSet - 1].y);
+                else if constexpr (kNear)
+                    *reinterpret_cast<uint2*>(to) = make_uint2(code[0].x, code[kSet - 1].x);
+                else if constexpr (kType == PKV_MX8)
+                    *reinterpret_cast<uint2*>(to) = code[0];
                 else
-                    *reinterpret_cast<uint32_t*>(dst + c * T * kCodes) = code.x;
-                if ((lane & 3) == 0) scale[c * (T / 16) * kMxTileBytes] = (uint8_t)byte;
+                    *reinterpret_cast<uint32_t*>(to) = code[0].x;
+                if ((lane & (4 / kSet - 1)) == 0) scale[(chunk(c) - chunk(0)) / 16 * kMxTileBytes] = (uint8_t)byte;
             }
         }
     }

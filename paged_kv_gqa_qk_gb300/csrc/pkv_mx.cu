@@ -151,6 +151,22 @@ __device__ __forceinline__ Pair warp_sum(Pair a)
 // iteration, whose residual 1 - v r^2 is formed without loss.
 __device__ __forceinline__ Pair inv_rms_pair(Pair ss, Pair inv_n, Pair eps)
 {
+    // With the larger of ss and eps from 2^-80 to 2^100 every term here is a normal number (r^2's error is some 2^-48 of
+    // 1 / v, which would be subnormal from 2^102 on, and r^2 itself infinite below 2^-128).  Others take an even power of
+    // two, whose root goes back into r.
+    constexpr uint32_t kLeast = (127 - 80) << 23, kMost = (127 + 100) << 23;
+    uint32_t top = max(__float_as_uint(ss.h), __float_as_uint(eps.h));
+    float back = 1.f;
+    if (top - kLeast > kMost - kLeast) {
+        const float h = __fadd_rn(ss.h, ss.l);  // (a sum of subnormal squares may come with all of it in l)
+        ss = {h, __fadd_rn(ss.l, __fsub_rn(ss.h, h))};
+        top = max(__float_as_uint(h), __float_as_uint(eps.h));
+        const int a = min(max(-(((int)(top >> 23) - 127) & ~1), -126), 126);
+        const float up = __uint_as_float((uint32_t)(a + 127) << 23);
+        back = __uint_as_float((uint32_t)(a / 2 + 127) << 23);
+        ss = {__fmul_rn(ss.h, up), __fmul_rn(ss.l, up)};
+        eps = {__fmul_rn(eps.h, up), __fmul_rn(eps.l, up)};
+    }
     const float t = __fmul_rn(ss.h, inv_n.h);
     const float te = __fmaf_rn(ss.h, inv_n.l, __fmaf_rn(ss.l, inv_n.h, __fmaf_rn(ss.h, inv_n.h, -t)));
     Pair v = two_sum(t, eps.h);
@@ -160,7 +176,7 @@ __device__ __forceinline__ Pair inv_rms_pair(Pair ss, Pair inv_n, Pair eps)
     const float q = __fmul_rn(v.h, p);
     const float qe = __fmaf_rn(v.l, p, __fmaf_rn(v.h, pe, __fmaf_rn(v.h, p, -q)));
     const float e = __fsub_rn(__fsub_rn(1.0f, q), qe);
-    return {r, __fmul_rn(__fmul_rn(r, 0.5f), e)};
+    return {__fmul_rn(r, back), __fmul_rn(__fmul_rn(__fmul_rn(r, 0.5f), e), back)};
 }
 
 struct AddNormParams {

@@ -1,0 +1,73 @@
+"""pkv_add_norm at the ends of the ranges that include/pkv.h gives: sums of squares near fp32's largest and smallest numbers,
+weights of any size."""
+import numpy as np
+import pytest
+import torch
+
+import _mx
+import paged_kv_gqa_qk_gb300 as pkv
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+OUTS = ["bf16", "mx8", "mx4"]
+
+
+def norm_of(x, w, kind, eps):
+    """The norm's values as the output holds them."""
+    z = torch.zeros(2, 1, 64, 128, dtype=torch.bfloat16, device=DEV)
+    p = pkv.PagedKVPool(z[0], z[1], cfg=dict(heads=4, kv_heads=1, max_seq=64, eps=eps))
+    out, _ = p.add_norm(x.to(DEV), None, w.to(DEV), out=kind)
+    assert p.check_errors() == 0
+    p.close()
+    return _mx.f64(out) if kind == "bf16" else _mx.stored(out)
+
+
+def held(y, kind):
+    """Values beyond fp32's (and bf16's) range are infinite; in microscaled form their group is NaN."""
+    y = np.where(np.abs(y) >= 2.0 ** 128, np.copysign(np.inf, y), y)
+    if kind != "bf16":
+        return _mx.held(y, kind)
+    with np.errstate(invalid="ignore"):
+        b = np.where(np.isfinite(y), _mx.bf16(np.where(np.isfinite(y), y, 0)), y)
+    return np.where(np.abs(b) >= 2.0 ** 128, np.copysign(np.inf, b), b)
+
+
+def check(got, y, kind, d):
+    """Each value is the rounding of y or of what lies within d of it."""
+    ok = np.zeros(got.shape, bool)
+    for e in (-d, d):
+        want = held(y * (1 + e), kind)
+        ok |= (got == want) | (np.isnan(got) & np.isnan(want))
+    assert ok.all(), (np.argwhere(~ok)[:4], got[~ok][:4], y[~ok][:4])
+
+
+def uneven(rows, cols, seed, size):
+    """Values of size * [1, 2) with all of bf16's bits and both signs."""
+    gen = torch.Generator().manual_seed(seed)
+    m = 1.0 + torch.randint(0, 128, (rows, cols), generator=gen).double() / 128
+    m *= torch.randint(0, 2, (rows, cols), generator=gen) * 2 - 1
+    return (m * size).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind", OUTS)
+@pytest.mark.parametrize("hidden,size", [(128, 2.0 ** 59), (256, 2.0 ** 59), (4096, 2.0 ** 57), (8192, 2.0 ** 56),
+                                         (256, 2.0 ** 51), (256, 2.0 ** 46), (1024, 2.0 ** -40), (1024, 2.0 ** -45)])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+def test_sums_near_the_largest_number(kind, hidden, size, eps):
+    """A mean square of up to 2^120 (the sum stays below 2^128), and of 2^-90: as exact as any other, to 2^-40."""
+    x = uneven(4, hidden, hidden, size)
+    x[1] = float(np.float32(size * 1.53125))         # equal values: the root of one square, on every border
+    assert float(x.double().square().sum(-1).max()) < 2.0 ** 127.9
+    w = uneven(1, hidden, 1, 0.75)[0]
+    check(norm_of(x, w, kind, eps), _mx.norm(_mx.f64(x), _mx.f64(w), eps), kind, 2.0 ** -40)
+
+
+@pytest.mark.parametrize("kind", OUTS)
+@pytest.mark.parametrize("hidden", [128, 1024, 4096, 16384])
+@pytest.mark.parametrize("size", [2.0 ** -66, 2.0 ** -60])
+def test_rows_of_tiny_values_without_eps(kind, hidden, size):
+    """Squares from 2^-132 on are whole multiples of 2^-146, which fp32's subnormals hold: the sum keeps them but for the
+    roundings of a warp's parts, 16 units of 2^-149 twice, of at least 128 * 2^-132: 2^-19, which the root halves."""
+    x = uneven(3, hidden, hidden, size)
+    w = uneven(1, hidden, 2, 0.75)[0]
+    check(norm_of(x, w, kind, 0.0), _mx.norm(_mx.f64(x), _mx.f64(w), 0.0), kind, 2.0 ** -19)

@@ -71,3 +71,16 @@ def test_rows_of_tiny_values_without_eps(kind, hidden, size):
     x = uneven(3, hidden, hidden, size)
     w = uneven(1, hidden, 2, 0.75)[0]
     check(norm_of(x, w, kind, 0.0), _mx.norm(_mx.f64(x), _mx.f64(w), 0.0), kind, 2.0 ** -19)
+
+
+@pytest.mark.parametrize("size", [2.0 ** 60, 2.0 ** 52, 1.0, 2.0 ** -30])
+def test_digits_of_the_root(size):
+    """Rows whose root is off a whole one by 2^-35: 64 of 256 values are c, one is c / 2^14, so y = 2 w (1 - 2^-35), and in 4
+    bits 3.5 (1 - 2^-35) is 3, where 3.5 itself would be 4.  All mantissas of c."""
+    c = (1.0 + torch.arange(128).double() / 128) * size
+    x = torch.zeros(128, 256, dtype=torch.float64)
+    x[:, :64], x[:, 100] = c[:, None], c / 2 ** 14
+    w = torch.full((256,), 1.75, dtype=torch.bfloat16)
+    w[:64:4] = 3.0
+    got = norm_of(x.to(torch.bfloat16), w, "mx4", 0.0)
+    assert np.array_equal(got[:, :64], np.broadcast_to(np.where(np.arange(64) % 4 == 0, 6.0, 3.0), (128, 64)))

@@ -147,36 +147,44 @@ __device__ __forceinline__ Pair warp_sum(Pair a)
     return {__fmul_rn(wf, down), __fmul_rn(rest, down)};
 }
 
-// 1 / sqrt(ss * inv_n + eps) to about 2^-44: a fp32 root and one step of Newton's
-// iteration, whose residual 1 - v r^2 is formed without loss.
-__device__ __forceinline__ Pair inv_rms_pair(Pair ss, Pair inv_n, Pair eps)
+// ss * inv_n + eps.
+__device__ __forceinline__ Pair mean_pair(Pair ss, Pair inv_n, Pair eps)
 {
-    // With the larger of ss and eps from 2^-80 to 2^100 every term here is a normal number (r^2's error is some 2^-48 of
-    // 1 / v, which would be subnormal from 2^102 on, and r^2 itself infinite below 2^-128).  Others take an even power of
-    // two, whose root goes back into r.
-    constexpr uint32_t kLeast = (127 - 80) << 23, kMost = (127 + 100) << 23;
-    uint32_t top = max(__float_as_uint(ss.h), __float_as_uint(eps.h));
-    float back = 1.f;
-    if (top - kLeast > kMost - kLeast) {
-        const float h = __fadd_rn(ss.h, ss.l);  // (a sum of subnormal squares may come with all of it in l)
-        ss = {h, __fadd_rn(ss.l, __fsub_rn(ss.h, h))};
-        top = max(__float_as_uint(h), __float_as_uint(eps.h));
-        const int a = min(max(-(((int)(top >> 23) - 127) & ~1), -126), 126);
-        const float up = __uint_as_float((uint32_t)(a + 127) << 23);
-        back = __uint_as_float((uint32_t)(a / 2 + 127) << 23);
-        ss = {__fmul_rn(ss.h, up), __fmul_rn(ss.l, up)};
-        eps = {__fmul_rn(eps.h, up), __fmul_rn(eps.l, up)};
-    }
     const float t = __fmul_rn(ss.h, inv_n.h);
     const float te = __fmaf_rn(ss.h, inv_n.l, __fmaf_rn(ss.l, inv_n.h, __fmaf_rn(ss.h, inv_n.h, -t)));
     Pair v = two_sum(t, eps.h);
     v.l = __fadd_rn(v.l, __fadd_rn(te, eps.l));
+    return v;
+}
+
+// 1 / sqrt(v) to about 2^-44: a fp32 root and one step of Newton's iteration, whose residual
+// 1 - v r^2 is formed without loss.
+__device__ __forceinline__ Pair inv_root_pair(Pair v)
+{
     const float r = rsqrtf(v.h);
     const float p = __fmul_rn(r, r), pe = __fmaf_rn(r, r, -p);
     const float q = __fmul_rn(v.h, p);
     const float qe = __fmaf_rn(v.l, p, __fmaf_rn(v.h, pe, __fmaf_rn(v.h, p, -q)));
     const float e = __fsub_rn(__fsub_rn(1.0f, q), qe);
-    return {__fmul_rn(r, back), __fmul_rn(__fmul_rn(__fmul_rn(r, 0.5f), e), back)};
+    return {r, __fmul_rn(__fmul_rn(r, 0.5f), e)};
+}
+
+// 1 / sqrt(ss * inv_n + eps).
+__device__ __forceinline__ Pair inv_rms_pair(Pair ss, Pair inv_n, Pair eps)
+{
+    // With v from 2^-80 to 2^100 every term is a normal number (r^2's error is some 2^-48 of 1 / v, which would be subnormal
+    // from 2^102 on, r^2 itself infinite below 2^-128).  Otherwise the sum and eps take an even power of two, whose root goes
+    // back into r.  (The look costs 1001 x 5120 to 4 bits 7.08 -> 7.18 us; a power of two that suits all rows, which eps
+    // would have to bound, 7.16.)
+    constexpr uint32_t kLeast = (127 - 80) << 23, kMost = (127 + 100) << 23;
+    const Pair v = mean_pair(ss, inv_n, eps);
+    if (__float_as_uint(v.h) - kLeast <= kMost - kLeast) return inv_root_pair(v);
+    const float h = __fadd_rn(ss.h, ss.l);  // (a sum of subnormal squares may come with all of it in l)
+    const int a = min(max(-(((int)(__float_as_uint(fmaxf(h, eps.h)) >> 23) - 127) & ~1), -126), 126);
+    const float up = __uint_as_float((uint32_t)(a + 127) << 23), back = __uint_as_float((uint32_t)(a / 2 + 127) << 23);
+    const Pair r = inv_root_pair(mean_pair({__fmul_rn(h, up), __fmul_rn(__fadd_rn(ss.l, __fsub_rn(ss.h, h)), up)}, inv_n,
+                                           {__fmul_rn(eps.h, up), __fmul_rn(eps.l, up)}));
+    return {__fmul_rn(r.h, back), __fmul_rn(r.l, back)};
 }
 
 struct AddNormParams {

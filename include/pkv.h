@@ -534,7 +534,8 @@ PKV_API int pkv_pool_set_rope(pkv_pool* pool, const double* inv_freq, double msc
  * on the tensor cores' 8- and 4-bit rates.  One step of a layer is
  *   pkv_add_norm -> pkv_mx_qkv_proj -> pkv_decode / pkv_q4_decode / ... -> pkv_mx_quantize of the
  *   attention's output -> pkv_mx_linear (o_proj) -> pkv_add_norm.
- * Any pool names the device (and, for pkv_add_norm, gives eps).
+ * Any pool names the device, and for pkv_add_norm gives eps: a model whose layers' norms have another eps than its
+ * QK-norm makes them a pool of their own (one page will do).
  *
  * A microscaled tensor [rows][cols] (OCP Microscaling Formats (MX) Specification v1.0) holds every
  * group of 32 consecutive values of a row as code * 2^e, with e the least whole number >= -127
@@ -570,8 +571,10 @@ PKV_API int pkv_mx_read(pkv_pool* pool, int type, const void* codes, const void*
  *   h = bf16(x + residual),  y = h / sqrt(mean(h^2) + eps) * w
  * h is rounded once, to bf16, and the norm is that of the rounded h; the sum of squares, the root and
  * the products are carried in pairs of floats (about 2^-44, 2^-40 at least), so that y's one rounding, to
- * out_type, is that of the exact value.  A row with an Inf or a NaN, or whose squares add up beyond fp32's range
- * (values of 2^60 and more), is NaN throughout.  Of an h * w below 2^-126, and of a sum of squares below
+ * out_type, is that of the exact value.  A row with an Inf or a NaN, or whose squares add up to 2^128 or more
+ * (which takes values of 2^64 / sqrt(hidden)), is NaN throughout.  An Inf or a NaN in w, and an h * w of 2^128 or
+ * more, make that y NaN, its whole group in a microscaled out; a y of 2^128 or more counts as 2^128 (1 - 2^-24),
+ * infinite in bf16 (both take weights beyond 2^64).  Of an h * w below 2^-126, and of a sum of squares below
  * 2^-80, fp32's subnormals keep less: with the default eps that shows only in a y below 2^-116.
  *   x             device bf16 [tokens][hidden], x_stride elements between rows (>= hidden, a multiple of 8)
  *   residual      device bf16 [tokens][hidden], or NULL: h = x

@@ -84,3 +84,58 @@ def test_digits_of_the_root(size):
     w[:64:4] = 3.0
     got = norm_of(x.to(torch.bfloat16), w, "mx4", 0.0)
     assert np.array_equal(got[:, :64], np.broadcast_to(np.where(np.arange(64) % 4 == 0, 6.0, 3.0), (128, 64)))
+
+
+@pytest.mark.parametrize("kind", OUTS)
+@pytest.mark.parametrize("hidden", [128, 4096, 16384])
+@pytest.mark.parametrize("size", [2.0 ** 56, 1.0, 2.0 ** -50])
+def test_weights_of_any_size(kind, hidden, size):
+    """An h w of 2^128 or more makes its y NaN, in microscaled form the group; everything else is exact."""
+    if hidden == 16384 and size > 1:
+        size /= 16
+    x = uneven(4, hidden, hidden, size)
+    x[2, ::3] = 0
+    x[3] = float(np.float32(size * 1.53125))
+    w = uneven(1, hidden, 3, 1.0)[0]
+    gen = torch.Generator().manual_seed(4)
+    w *= 2.0 ** torch.randint(-20, 118, (hidden,), generator=gen).float()
+    w[:64] = uneven(1, 64, 5, 1.0)[0]               # (two groups of ordinary ones)
+    w[64:68] = torch.tensor([2.0 ** 68, -(2.0 ** 117), 2.0 ** 64, -(2.0 ** 65)])
+    w = w.to(torch.bfloat16)
+    y, hw = _mx.norm(_mx.f64(x), _mx.f64(w), 1e-6), _mx.f64(x) * _mx.f64(w)
+    assert np.isfinite(y).all() and (np.abs(y) < 2.0 ** 128).all() and (np.abs(hw) < 2.0 ** 128).any(-1).all()
+    y = np.where(np.abs(hw) >= 2.0 ** 128, np.nan, y)
+    check(norm_of(x, w, kind, 1e-6), y, kind, 2.0 ** -40)
+
+
+@pytest.mark.parametrize("kind", OUTS)
+def test_infinite_and_nan_weights(kind):
+    x = uneven(4, 256, 1, 1.0)
+    x[1, 40] = 0
+    x[3, 3] = 2.0 ** 70                              # (a row without a norm)
+    w = uneven(1, 256, 2, 1.0)[0]
+    w[40], w[200] = float("inf"), float("nan")
+    clean = w.clone()
+    clean[40], clean[200] = 1, 1
+    y = _mx.norm(_mx.f64(x), _mx.f64(clean), 1e-6)
+    y[:, [40, 200]], y[3] = np.nan, np.nan
+    check(norm_of(x, w, kind, 1e-6), y, kind, 2.0 ** -40)
+
+
+@pytest.mark.parametrize("kind", OUTS)
+def test_where_squares_leave_the_range(kind):
+    """A row's squares may add up to anything below 2^128; from there on it is NaN."""
+    for hidden, value, finite in [(128, 2.0 ** 60, True), (128, 1.25 * 2.0 ** 60, True), (128, 1.5 * 2.0 ** 60, False),
+                                  (4096, 1.9375 * 2.0 ** 57, True), (4096, 2.0 ** 58, False),
+                                  (32768, 1.375 * 2.0 ** 56, True), (32768, 1.4375 * 2.0 ** 56, False)]:
+        assert (hidden * value ** 2 < 2.0 ** 128) == finite
+        x = torch.ones(2, hidden, dtype=torch.bfloat16)
+        x[1] = value
+        w = torch.ones(hidden, dtype=torch.bfloat16)
+        w[::32] = 2.0                                # (a code without a border beside it)
+        got = norm_of(x, w, kind, 1e-6)
+        assert np.isfinite(got[0]).all()
+        if finite:
+            check(got[1:], _mx.norm(_mx.f64(x[1:]), _mx.f64(w), 1e-6), kind, 2.0 ** -40)
+        else:
+            assert np.isnan(got[1]).all()

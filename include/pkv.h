@@ -619,14 +619,15 @@ PKV_API int pkv_check_errors(pkv_pool* pool, void* stream, uint32_t* flags);
 PKV_API int pkv_set_ctas(pkv_pool* pool, int ctas);
 
 /* Limit, in nanoseconds, of each bounded wait inside the decode attention
- * kernel (the shared-memory ring between its copy warp and its compute warps,
- * and the compute warps' meeting points); default 1e9 (one second).  A wait
- * that runs out makes its CTA stop: it sets PKV_DEVERR_TIMEOUT in the error
- * word, lets the copies it has in flight land (allowing a full second for
- * that, whatever this limit), and exits; the outputs of that call are void,
- * and the pool is ready for the next call.  0 gives up at the first check
- * that finds the awaited data not yet there, which lets a test run the
- * timeout path on purpose.  Applies to calls enqueued after it.
+ * kernels (the shared-memory ring between a copy warp and the compute warps,
+ * and the compute warps' meeting points) and inside the products of
+ * microscaled tensors; default 1e9 (one second).  A wait that runs out sets
+ * PKV_DEVERR_TIMEOUT in the error word, and the outputs of that call are void.
+ * An attention's CTA then stops, once the copies it has in flight have landed;
+ * a product's goes on in step with its copies (both allow a full second for
+ * that, whatever this limit).  The pool is ready for the next call.  0 gives
+ * up at the first check that finds the awaited data not yet there, which lets
+ * a test run the timeout path on purpose.  Applies to calls enqueued after it.
  * Errors: PKV_EINVAL (null, ns < 0). */
 PKV_API int pkv_set_wait_limit(pkv_pool* pool, int64_t ns);
 

@@ -95,22 +95,6 @@ __device__ __forceinline__ int64_t mx_scale_at(int64_t row, int group, int tiles
     return ((row / kMxTileRows) * tiles + group / 4) * kMxTileBytes + 16 * (r % 32) + 4 * (r / 32) + group % 4;
 }
 
-// A role's waits.  After one that ran out (its second passed) the later ones share one more, in which the copies in
-// flight land: the role goes through all of its steps, with void results, and nothing is on its way when it ends.
-struct Waits {
-    uint64_t end = 0;
-    __device__ __forceinline__ bool ok() const { return end == 0; }
-    __device__ __forceinline__ void on(uint32_t bar, uint32_t parity)
-    {
-        if (ok()) {
-            if (!mbar_wait_spin(bar, parity)) end = global_ns() + kWaitLimitNs;
-        } else {
-            const uint64_t now = global_ns();
-            mbar_wait_spin(bar, parity, now < end ? end - now : 0);
-        }
-    }
-};
-
 __device__ __forceinline__ void unpack8(uint4 r, float (&x)[8])
 {
     const uint32_t a[4] = {r.x, r.y, r.z, r.w};

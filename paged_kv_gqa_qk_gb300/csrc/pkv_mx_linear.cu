@@ -51,6 +51,7 @@ struct Params {
     __nv_bfloat16* y[3];
     int seg_end[3];     // cumulative widths; seg_end[2] == out
     uint32_t* err;
+    uint64_t wait_ns;   // limit of a wait
     int tokens, in, out, stages;
 };
 
@@ -119,20 +120,20 @@ __global__ void __launch_bounds__(kThreads)
     pdl_launch_dependents();
 
     if (warp == 0) {
-        bool ok = true;
+        Waits wait(p.wait_ns);
         int st = 0;
         uint32_t parity = 0;
         for (int k = k0 + early; k < k1; ++k) {
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait_spin(bar_empty + 8 * st, parity)))) break;
+            if (!__all_sync(0xffffffffu, wait.on(bar_empty + 8 * st, parity))) break;
             load(k, st);
             if (++st == p.stages) st = 0, parity ^= 1;
         }
-        if (!ok && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+        if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 1) {
         // ---- products (a wait that ran out does not end the loop, which would make its counters differ between
         // lanes).  A stage is looked for before the products of the one before it are issued, which takes as long as
         // the look.
-        Waits wait;
+        Waits wait(p.wait_ns);
         bool there = mbar_try_wait(bar_full, 0);
         int st = 0;
         uint32_t parity = 0;
@@ -164,14 +165,16 @@ __global__ void __launch_bounds__(kThreads)
             if (k1 - k0 > p.stages) umma_commit_warp(bar_empty + 8 * cur);  // (else no stage is loaded again)
         }
         umma_commit_warp(bar_done);
-        if (!wait.ok() && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+        if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     }
     __syncwarp();
 
     // ---- each thread has a feature of every token
     constexpr int kOwn = BN / NS, kVec = kOwn < 4 ? kOwn : 4, kRounds = kOwn / kVec;
     static_assert(kVec >= 2, "two tokens a CTA at least");
-    const bool ok = mbar_wait_spin(bar_done, 0);
+    Waits wait(p.wait_ns);
+    const bool ok = wait.on(bar_done, 0);
+    if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     tc_fence_after();
     if (NS > 1) cluster_wait();
     const int tokens = min(BN, p.tokens - n0), feature = 32 * warp + lane;
@@ -337,6 +340,7 @@ cudaError_t launch_mx_linear(const pkv_pool* pool, const MxLinear& a, cudaStream
     p.x_scales = static_cast<const uint8_t*>(a.x_scales);
     p.w_scales = static_cast<const uint8_t*>(a.w_scales);
     p.err = pool->err;
+    p.wait_ns = pool->wait_ns;
     p.tokens = a.tokens;
     p.in = a.in;
     p.out = p.seg_end[2];

@@ -58,6 +58,7 @@ struct Maps {
 
 struct Params {
     uint32_t* err;
+    uint64_t wait_ns;  // limit of a wait
     int seg_end[3];
     int tokens, in, out, units;  // units: of 64 features in a row of tiles
 };
@@ -160,7 +161,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Ring before;  // the stage whose products used the slot last
         SfRing sf;
         SlotRing slot;
-        Waits wait;
+        Waits wait(p.wait_ns);
         while (walk.next())
             for (int k = 0; k < nk; ++k, slot.next(), sf.next()) {
                 wait.on(bar_landed + 8 * sf.st, sf.parity);
@@ -187,19 +188,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(bar0 + 8 * slot.st);
             }
-        if (!wait.ok() && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+        if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 12) {
         // ---- operands: they complete on the even CTA's barrier
         const uint64_t keep = l2_policy_evict_last();  // both are read again by other pairs
         Ring ring;
-        Waits wait;
+        Waits wait(p.wait_ns);
         bool ok = true;
         while (ok && walk.next()) {
             const int m0 = walk.m * kTileM + (int)rank * 128;
             const int n0 = walk.f * kUnit + (int)rank * (walk.n * kUnit / 2);  // (rows beyond half of the tile are not used)
             for (int k = 0; k < nk; ++k, ring.next()) {
-                if (ring.again) wait.on(bar_empty + 8 * ring.st, ring.parity ^ 1);
-                if (!(ok = __all_sync(0xffffffffu, wait.ok()))) break;
+                if (ring.again) ok = wait.on(bar_empty + 8 * ring.st, ring.parity ^ 1);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const uint32_t a = base + ring.st * S::kStageBytes, bar = bar_full + 8 * ring.st;
                 if (rank == 0) mbar_arrive_expect_tx_warp(bar, 2 * S::kStageBytes);
                 tma_load_2d_pair_warp(a, &maps.x, k * kSpan, m0, bar, keep);
@@ -209,16 +210,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the last stages' products are done with this CTA's ring and barriers before it leaves
         for (int i = 0; i < kStages; ++i, ring.next())
             if (ring.again) wait.on(bar_empty + 8 * ring.st, ring.parity ^ 1);
-        if (!wait.ok() && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+        if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 14) {
         // ---- scales: x's block of 128 tokens and W's two of features, on this CTA's barrier; ahead of the operands
         const uint64_t keep = l2_policy_evict_last();
         SfRing sf;
+        Waits wait(p.wait_ns);
         bool ok = true;
         while (ok && walk.next()) {
             const int mb = walk.m * 2 + (int)rank, nb = walk.f / 2;
             for (int k = 0; k < nk; ++k, sf.next()) {
-                if (sf.again) ok = mbar_wait_spin(bar_taken + 8 * sf.st, sf.parity ^ 1);
+                if (sf.again) ok = wait.on(bar_taken + 8 * sf.st, sf.parity ^ 1);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const uint32_t to = base + S::kSf + sf.st * 3 * S::kSfBlock, bar = bar_landed + 8 * sf.st;
                 mbar_arrive_expect_tx_warp(bar, 3 * S::kSfBlock);
@@ -226,14 +228,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tma_load_2d_warp(to + S::kSfBlock, &maps.sfw, k * S::kSfTiles * 128, nb, bar, keep);
             }
         }
-        if (!ok && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+        if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 13) {
         if (rank == 0) {
             // ---- products of the pair (a wait that ran out does not end the loop, which would make its
             // counters differ between lanes)
             Ring ring;
             SlotRing slot;
-            Waits wait;
+            Waits wait(p.wait_ns);
             bool there = false, scaled = false;
             for (int done = 0; walk.next(); ++done) {
                 const uint32_t half = done & 1, acc = tmem + half * kTileN;
@@ -267,7 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 umma_commit_pair_warp(bar_acc + 8 * half);
             }
-            if (!wait.ok() && lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+            if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
         }
     } else {
         // ---- epilogue: group h writes every other tile; its warp q holds tokens 32 q .. + 31 of this CTA
@@ -276,14 +278,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t box = base + S::kOut + kBox * h, mine = box + row * (2 * kOutCols);
         const int swizzle = row & 7;
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + h * kTileN, free0 = cluster_map(bar_free + 8 * h, 0);
+        Waits wait(p.wait_ns);
         for (int done = 0; walk.next(); ++done) {
             if ((done & 1) != h) continue;
             const int m0 = walk.m * kTileM + (int)rank * 128, rounds = walk.n * (kUnit / kOutCols);
-            const bool ok = named_all(1 + h, 128, mbar_wait_spin(bar_acc + 8 * h, (done / 2) & 1));  // (they leave together)
-            if (!ok) {
-                if (lane == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
-                break;
-            }
+            if (!named_all(1 + h, 128, wait.on(bar_acc + 8 * h, (done / 2) & 1))) break;  // (they leave together)
             tc_fence_after();
 #pragma unroll 1
             for (int r = 0; r < rounds; ++r) {
@@ -319,6 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
         if (issuer) bulk_wait();
+        if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     }
     __syncwarp();
     tc_fence_before();
@@ -370,6 +370,7 @@ cudaError_t launch(const pkv_pool* pool, const MxLinear& a, cudaStream_t s)
         !make_tmap_scales(&m.sfw, a.w_scales, sf_tiles, end / 128, S::kSfTiles, 2))
         return cudaErrorInvalidValue;
     p.err = pool->err;
+    p.wait_ns = pool->wait_ns;
     p.tokens = a.tokens;
     p.in = a.in;
     p.out = end;

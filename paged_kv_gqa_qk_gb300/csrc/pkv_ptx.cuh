@@ -121,6 +121,33 @@ __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, ui
     }
 }
 
+// A role's waits, each with `limit` ns.  One that runs out makes the call's results void, but the role stays in step with the
+// barriers: it goes on waiting for the same phase, and later ones, within one more second in all.  So a copy that lands
+// late is still waited for before its stage is used again, and none is on its way when the CTA ends.
+struct Waits {
+    const uint64_t limit;
+    uint64_t end = 0;  // of the further second
+    __device__ __forceinline__ explicit Waits(uint64_t limit_ns) : limit(limit_ns) {}
+    __device__ __forceinline__ bool ok() const { return end == 0; }
+    // Whether the phase has completed.
+    __device__ __forceinline__ bool on(uint32_t bar, uint32_t parity)
+    {
+        if (mbar_test_wait(bar, parity)) return true;
+        const uint64_t t0 = global_ns();
+        if (limit == 0 && ok()) end = t0 + kWaitLimitNs;
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((it & 1023u) == 0) {
+                const uint64_t now = global_ns();
+                if (ok() && now - t0 > limit)
+                    end = now + kWaitLimitNs;
+                else if (!ok() && now > end)
+                    return false;
+            }
+        }
+    }
+};
+
 // ---- TMA ----------------------------------------------------------------------
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map)
 {

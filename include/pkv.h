@@ -620,7 +620,7 @@ PKV_API int pkv_set_ctas(pkv_pool* pool, int ctas);
 
 /* Limit, in nanoseconds, of each bounded wait inside the decode attention
  * kernels (the shared-memory ring between a copy warp and the compute warps,
- * and the compute warps' meeting points) and inside the products of
+ * and the compute warps' meeting points) and inside the products of bf16 and
  * microscaled tensors; default 1e9 (one second).  A wait that runs out sets
  * PKV_DEVERR_TIMEOUT in the error word, and the outputs of that call are void.
  * An attention's CTA then stops, once the copies it has in flight have landed;

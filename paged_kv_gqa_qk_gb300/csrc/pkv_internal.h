@@ -59,7 +59,7 @@ struct pkv_pool {
     CUtensorMap tmap_v;
     int ctas_per_sm;       // resident attention CTAs per SM (occupancy)
     int ctas_override;     // attention grid size; 0 = one wave (ctas_per_sm x SMs)
-    uint64_t wait_ns;      // limit of a wait in the attentions over rows and in the microscaled products (default 1 s)
+    uint64_t wait_ns;      // limit of a wait in the attentions over rows and in the products (default 1 s)
     // kernel timer: a timed call takes event slot timer_count++ % kTimerSlots (atomic,
     // so host threads sharing the pool take distinct slots)
     int timer_on;          // 0 off, 1 every timed launch, 2 the attention launches only

@@ -80,6 +80,7 @@ struct LinParams {
     __nv_bfloat16* y[3];
     int seg_end[3];     // cumulative widths; seg_end[2] == out
     uint32_t* err;
+    uint64_t wait_ns;   // limit of a wait
     int tokens, in, out, splits;
     int fused;          // 1: the epilogue of LinFuse instead of writing y
     LinFuse f;
@@ -321,29 +322,27 @@ __global__ void __launch_bounds__(kLinThreads, BN == 64 ? 2 : 1)
             tma_load_2d(a, &tmW, (k0 + i) * kBK, m0, fb, pol_w);
             tma_load_2d(a + S::kABytes, &tmX, (k0 + i) * kBK, n0, fb, pol_x);
         }
+        Waits wait(p.wait_ns);
         for (int k = k0 + early; k < k1; ++k) {
             const int i = k - k0, st = i % S::kStages;
-            if (!mbar_wait(bar_empty + 8 * st, ((i / S::kStages) - 1) & 1)) {
-                atomicOr(p.err, PKV_DEVERR_TIMEOUT);
-                break;
-            }
+            if (!wait.on(bar_empty + 8 * st, ((i / S::kStages) - 1) & 1)) break;
             const uint32_t a = base + st * S::kStageBytes, fb = bar_full + 8 * st;
             mbar_arrive_expect_tx(fb, S::kStageBytes);
             tma_load_2d(a, &tmW, k * kBK, m0, fb, pol_w);
             tma_load_2d(a + S::kABytes, &tmX, k * kBK, n0, fb, pol_x);
         }
+        if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     } else if (p.fused && warp >= 2) {
         // ---- the fused epilogue's token table (positions, validity, slots), while the product runs
         fused_tokens(p, reinterpret_cast<int2*>(sbase + S::kTok), BN, n0, m0, warp - 2, lane);
     } else if (warp == 1 && lane == 0) {
         // ---- MMA issuer
         constexpr uint32_t idesc = umma_idesc_bf16(kBM, BN, 0, 0);
+        pdl_wait();  // (no copy is on its way before: the limit counts from here)
+        Waits wait(p.wait_ns);
         for (int k = k0; k < k1; ++k) {
             const int i = k - k0, st = i % S::kStages;
-            if (!mbar_wait_spin(bar_full + 8 * st, (i / S::kStages) & 1)) {
-                atomicOr(p.err, PKV_DEVERR_TIMEOUT);
-                break;
-            }
+            if (!wait.on(bar_full + 8 * st, (i / S::kStages) & 1)) break;
             tc_fence_after();
             const uint32_t a = base + st * S::kStageBytes;
             const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(a + S::kABytes, 16, 1024);
@@ -353,12 +352,15 @@ __global__ void __launch_bounds__(kLinThreads, BN == 64 ? 2 : 1)
             umma_commit(bar_empty + 8 * st);
         }
         umma_commit(bar_done);  // also on a timeout: the epilogue and the release wait for it
+        if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     }
     __syncwarp();
 
     // ---- epilogue: thread (warp w, lane l) holds output feature m0 + 32 w + l for BN tokens
     pdl_wait();  // y may be read by the kernel before this one
-    const bool ok = mbar_wait(bar_done, 0);
+    Waits wait(p.wait_ns);
+    const bool ok = wait.on(bar_done, 0);
+    if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     tc_fence_after();
     int yw, yc;
     __nv_bfloat16* const y = seg_of(p, m0, yw, yc);
@@ -525,6 +527,7 @@ cudaError_t launch_linear(pkv_pool* pool, const void* x, const void* w, int toke
         p.seg_end[i] = end;
     }
     p.err = pool->err;
+    p.wait_ns = pool->wait_ns;
     p.tokens = tokens;
     p.in = in;
     p.out = end;
@@ -541,6 +544,7 @@ cudaError_t launch_qkv_append(pkv_pool* pool, const void* x, const void* w_qkv, 
     p.seg_end[1] = qw + kw;
     p.seg_end[2] = qw + 2 * kw;
     p.err = pool->err;
+    p.wait_ns = pool->wait_ns;
     p.tokens = tokens;
     p.in = hidden;
     p.out = p.seg_end[2];

@@ -55,3 +55,33 @@ def test_microscaled_qkv(pool, kind, tokens):
     x, w = operands(tokens, 1024, 48 * 128, kind, seed=tokens)
     xm, wm = pool.mx_quantize(x, kind), pool.mx_quantize(w, kind)
     runs_out_and_recovers(pool, lambda: list(pool.mx_qkv_proj(xm, wm)))
+
+
+@pytest.mark.parametrize("tokens,n_in,n_out", [(1, 4096, 6144), (64, 4096, 4096), (100, 2048, 1024), (700, 4096, 3200)])
+def test_products_of_bf16(pool, tokens, n_in, n_out):
+    x, w = operands(tokens, n_in, n_out, "mx8", seed=tokens)
+    runs_out_and_recovers(pool, lambda: [pool.linear(x, w)])
+
+
+@pytest.mark.parametrize("tokens", [3, 500])
+def test_qkv_of_bf16(pool, tokens):
+    x, w = operands(tokens, 1024, 48 * 128, "mx8", seed=tokens)
+    runs_out_and_recovers(pool, lambda: list(pool.qkv_proj(x, w)))
+
+
+@pytest.mark.parametrize("tokens", [2, 200])
+def test_projection_with_its_append(pool, tokens):
+    """q and the pool's rows after a call that ran out and one that did not."""
+    x, w = operands(tokens, 1024, 48 * 128, "mx8", seed=tokens)
+    p = pkv.PagedKVPool(*torch.zeros(2, 8, 64 * (tokens + 1), 128, dtype=torch.bfloat16, device=DEV),
+                        cfg=dict(heads=32, kv_heads=8, max_seq=64))
+    ones = torch.ones(128, dtype=torch.bfloat16, device=DEV)
+    positions = (torch.arange(tokens, device=DEV) * 5 % 64).int()
+    table = (torch.arange(tokens, device=DEV).int() + 1).view(-1, 1)
+    q_hat = torch.empty(tokens, 32, 128, device=DEV)
+
+    def call():
+        pkv.pkv_qkv_proj_append(p.handle, x, w, ones, ones, positions, table, q_hat)
+        return [q_hat, p.K, p.V]
+    runs_out_and_recovers(p, call)
+    p.close()

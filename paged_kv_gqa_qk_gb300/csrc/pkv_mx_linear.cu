@@ -27,7 +27,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kBM = 128;        // output features a tile
 constexpr int kSpan = 128;      // bytes of a row a stage
-constexpr int kMaxSplits = 8;   // a portable cluster
 
 template <int kType, int BN, int NS>
 struct Shape {
@@ -296,21 +295,12 @@ cudaError_t launch(const MxLinear& a, Params& p, const CUtensorMap& tmW, const C
 }
 
 template <int kType, int BN>
-cudaError_t launch_bn(const pkv_pool* pool, const MxLinear& a, Params& p, cudaStream_t s)
+cudaError_t launch_bn(const MxLinear& a, Params& p, int splits, cudaStream_t s)
 {
     CUtensorMap tmW, tmX;
-    const int row = mx_row_bytes(kType, a.in), nk = (row + kSpan - 1) / kSpan;
+    const int row = mx_row_bytes(kType, a.in);
     if (!make_tmap_bytes(&tmW, a.w_codes, row, p.out, kBM) || !make_tmap_bytes(&tmX, a.x_codes, row, a.tokens, BN))
         return cudaErrorInvalidValue;
-    // Splits of the input features: while the CTAs run at the same time (two an SM up to 32 tokens), two stages a
-    // CTA are left, and clusters of 8 while they find an SM each (us with 1 / 2 / 4 / 8: one token, 4096 x 6144 in 4
-    // bits 5.8 / 5.4 / 4.7 / 7.1, 4096 x 1024 in 8 bits 7.7 / 5.4 / 4.0 / 3.1, 16 tokens, 4096 x 4096 in 4 bits 5.4 / 4.3 /
-    // 3.5 / 5.1; 64 tokens, 4096 x 4096 in 8 bits 9.4 / 7.2 / 6.9 / 15, 4096 x 6144 10.2 / 8.1 / 11.6)
-    const int64_t tiles = (int64_t)(p.out / kBM) * ((a.tokens + BN - 1) / BN);
-    int splits = 1;
-    while (splits < kMaxSplits && nk / (splits * 2) >= 2 &&
-           tiles * splits * 2 <= (BN <= 32 && splits < 4 ? 2 : 1) * (int64_t)pool->num_sms)
-        splits *= 2;
     switch (splits) {
         case 1: return launch<kType, BN, 1>(a, p, tmW, tmX, s);
         case 2: return launch<kType, BN, 2>(a, p, tmW, tmX, s);
@@ -320,11 +310,13 @@ cudaError_t launch_bn(const pkv_pool* pool, const MxLinear& a, Params& p, cudaSt
 }
 
 template <int kType>
-cudaError_t launch_type(const pkv_pool* pool, const MxLinear& a, Params& p, cudaStream_t s)
+cudaError_t launch_type(const MxLinear& a, Params& p, const MxRoute& r, cudaStream_t s)
 {
-    if (a.tokens <= 16) return launch_bn<kType, 16>(pool, a, p, s);
-    if (a.tokens <= 32) return launch_bn<kType, 32>(pool, a, p, s);
-    return launch_bn<kType, 64>(pool, a, p, s);
+    switch (r.tile) {
+        case 16: return launch_bn<kType, 16>(a, p, r.splits, s);
+        case 32: return launch_bn<kType, 32>(a, p, r.splits, s);
+        default: return launch_bn<kType, 64>(a, p, r.splits, s);
+    }
 }
 
 }  // namespace
@@ -344,13 +336,9 @@ cudaError_t launch_mx_linear(const pkv_pool* pool, const MxLinear& a, cudaStream
     p.tokens = a.tokens;
     p.in = a.in;
     p.out = p.seg_end[2];
-    // Tiles of up to 64 tokens while each finds an SM, and in more turns than one for up to 48 tokens, where the work
-    // is W's bytes (us here / over pairs, in 4 and in 8 bits: 128 tokens, 4096 x 6144 6.9 / 8.4 and 9.8 / 11.9; 333
-    // tokens, 4096 x 1024 5.7 / 6.4 and 7.0 / 9.6, 4096 x 4096 15 / 8.3 and 22 / 11.7; 64 tokens, 4096 x 65536 38 / 31 and
-    // 56 / 55, 32 tokens, 4096 x 16384 8.4 / 14.5 and 12.7 / 20.7)
-    const int64_t tiles = (int64_t)(p.out / kBM) * ((a.tokens + 63) / 64);
-    if (a.tokens > 48 && tiles > pool->num_sms) return launch_mx_pair(pool, a, s);
-    return a.type == PKV_MX8 ? launch_type<PKV_MX8>(pool, a, p, s) : launch_type<PKV_MX4>(pool, a, p, s);
+    const MxRoute r = mx_route(a.type == PKV_MX8 ? a.in : a.in / 2, p.tokens, p.out, pool->num_sms);
+    if (r.pairs) return launch_mx_pair(pool, a, s);
+    return a.type == PKV_MX8 ? launch_type<PKV_MX8>(a, p, r, s) : launch_type<PKV_MX4>(a, p, r, s);
 }
 
 }  // namespace pkv

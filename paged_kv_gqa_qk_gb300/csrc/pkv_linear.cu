@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kLinThreads, BN == 64 ? 2 : 1)
         if (!wait.ok()) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     } else if (p.fused && warp >= 2) {
         // ---- the fused epilogue's token table (positions, validity, slots), while the product runs
+        pdl_wait();  // (the kernel before this one may write positions or the table)
         fused_tokens(p, reinterpret_cast<int2*>(sbase + S::kTok), BN, n0, m0, warp - 2, lane);
     } else if (warp == 1 && lane == 0) {
         // ---- MMA issuer

@@ -242,14 +242,14 @@ struct MxRoute {
 inline MxRoute mx_route(int row_bytes, int tokens, int out, int num_sms)
 {
     // Tiles of up to 64 tokens while each finds an SM, and in more turns than one for up to 48 tokens, where the work
-    // is W's bytes (us with tiles / over pairs, in 4 and in 8 bits: 128 tokens, 4096 x 6144 6.9 / 8.4 and 9.8 / 11.9; 333
-    // tokens, 4096 x 1024 5.7 / 6.4 and 7.0 / 9.6, 4096 x 4096 15 / 8.3 and 22 / 11.7; 64 tokens, 4096 x 65536 38 / 31 and
-    // 56 / 55, 32 tokens, 4096 x 16384 8.4 / 14.5 and 12.7 / 20.7)
+    // is W's bytes (us with tiles / over pairs, in 4 and in 8 bits: 128 tokens, 4096 x 6144 6.8 / 8.4 and 9.8 / 11.6; 333
+    // tokens, 4096 x 1024 5.7 / 6.3 and 7.1 / 9.1, 4096 x 4096 12.6 / 8.4 and 17.7 / 11.5; 64 tokens, 4096 x 65536 31.5 / 29.2
+    // and 52.7 / 52.3, 32 tokens, 4096 x 16384 8.0 / 14.8 and 12.7 / 20.1)
     if (tokens > 48 && (int64_t)(out / 128) * ((tokens + 63) / 64) > num_sms) return {true, 0, 0};
     // Splits of the input features, whose stages are 128 bytes of a row: while the CTAs run at the same time (two an SM up to
     // 32 tokens), two stages a CTA are left, and clusters of 8 while they find an SM each (us with 1 / 2 / 4 / 8: one
-    // token, 4096 x 6144 in 4 bits 5.8 / 5.4 / 4.7 / 7.1, 4096 x 1024 in 8 bits 7.7 / 5.4 / 4.0 / 3.1, 16 tokens, 4096 x 4096
-    // in 4 bits 5.4 / 4.3 / 3.5 / 5.1; 64 tokens, 4096 x 4096 in 8 bits 9.4 / 7.2 / 6.9 / 15, 4096 x 6144 10.2 / 8.1 / 11.6)
+    // token, 4096 x 6144 in 4 bits 5.4 / 4.7 / 4.3 / 6.1, 4096 x 1024 in 8 bits 7.7 / 5.4 / 4.0 / 3.2, 16 tokens, 4096 x 4096
+    // in 4 bits 5.4 / 4.5 / 3.5 / 5.3; 64 tokens, 4096 x 4096 in 8 bits 8.6 / 7.4 / 6.9 / 15, 4096 x 6144 9.4 / 8.0 / 11.6)
     const int tile = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64, stages = (row_bytes + 127) / 128;
     const int64_t tiles = (int64_t)(out / 128) * ((tokens + tile - 1) / tile);
     int splits = 1;

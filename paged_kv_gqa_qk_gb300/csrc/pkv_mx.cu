@@ -195,7 +195,7 @@ struct AddNormParams {
     void* out;
     uint8_t* scales;
     int64_t x_stride;
-    int tokens, hidden, warps;
+    int tokens, hidden;
     Pair inv_n, eps;
 };
 
@@ -266,9 +266,11 @@ __device__ __forceinline__ void scaled_odd(uint64_t hw, uint64_t rh, uint64_t rl
 // A CTA takes tokens blockIdx.x, + gridDim.x, ...; its thread i holds chunks i, i + T, ... of 8 columns of each.
 // Every warp forms the sum of the warps' sums and the root by itself, with one barrier a token.
 //
-// Bound by memory where a residual is added: 8192 x 4096 to 8 bits, 236 MB, in 37.0 us, 6.4 TB/s, to bf16, 268 MB, in
-// 42; without one by instructions, some 23 an element with a token's share of the sums (to 4 bits, 85 MB, in 28 us; 1001
-// x 5120 in 7.1, in three turns of the CTAs that fit).
+// Bound by memory where a residual is added: 8192 x 4096 to 8 bits, 236 MB, in 37.1 us, 6.4 TB/s, to 4, 219 MB, in 35.2, to
+// bf16, 268 MB, in 41.7; without one by instructions, some 23 an element with a token's share of the sums (to 4 bits, 85 MB,
+// in 28.7 us, to 8, 102 MB, in 29.0, to bf16, 134 MB, in 25.2; 1001 x 5120 to 4 bits in 7.2, in three turns of the CTAs that
+// fit).  Four chunks and a residual do not fit 64 registers a thread: 56 bytes of each are spilled above 16384 columns (2048 x
+// 20480 to 8 bits, 295 MB, 58.8 us, 5.0 TB/s).
 template <int kType, bool kAdd, int kChunks>
 __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormParams p)
 {
@@ -472,8 +474,9 @@ cudaError_t launch_add_norm(const pkv_pool* pool, const AddNorm& a, cudaStream_t
     p.inv_n = pair_of(1.0 / a.hidden);
     p.eps = pair_of(pool->cfg.eps);
     const int chunks = a.hidden / 8;
-    // chunks a thread: two (8192 x 4096 to 8 bits us with 1 / 2 / 4: 50 / 37.8 / 59), four where 1024 threads need it,
-    // one for a few short rows (300 x 2048 2.4 / 2.6)
+    // chunks a thread: two (8192 x 4096 with a residual to 8 bits us with 1 / 2 / 4: 48 / 37.0 / 43), four where 1024 threads
+    // need it, one for a few short rows (64 x 1024 to bf16 1.60 / 1.67, 150 x 2048 without a residual 1.67 / 1.77, 300 x 2048
+    // the same)
     const int per = chunks > 2048 ? 4 : chunks <= 256 && a.tokens <= 2 * pool->num_sms ? 1 : 2;
     const unsigned threads = (unsigned)((chunks + 32 * per - 1) / (32 * per) * 32);
     // CTAs for twice the threads that registers let be resident, each loading its next token while it works on one (a CTA a token 42 us)

@@ -13,10 +13,10 @@
 // so that every SM has a part of W to read; each CTA sends its sums of a part of the tokens to
 // each other, which adds those of its tokens in the CTAs' order.
 //
-// Bound by latencies up to some MB of W: one token, 4096 x 6144 in 4 bits, 13.4 MB, 4.6 us, of which 1 from the
+// Bound by latencies up to some MB of W: one token, 4096 x 6144 in 4 bits, 13.4 MB, 4.3 us, of which 1 from the
 // launch to the first copy, 0.9 until it is there, 1 for four stages, 1.1 for the exchange of the sums; by the way from
 // L2 with 64 tokens (4096 x 4096 in 8 bits: 26 MB into 128 SMs, W's and x's part for every tile of W, 1.8 of 6.9 us);
-// by memory beyond (16 tokens, 4096 x 65536 in 8 bits, 277 MB, 41 us, 6.8 TB/s).  Scales by four warps and sums by
+// by memory beyond (16 tokens, 4096 x 65536 in 8 bits, 277 MB, 40 us, 6.9 TB/s).  Scales by four warps and sums by
 // st.async in place of the cluster's barrier took as long here.
 #include "pkv_mx.cuh"
 
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int c = 0; c < BN / kCols; ++c) tmem_wait_ld_regs(v[c]);
     if constexpr (NS == 1) {
         // no cluster: two lanes share their tokens out, so that each writes two features of a token at a time (128 tokens,
-        // 4096 x 6144 in 4 bits 7.2 us, through shared memory as below 7.9)
+        // 4096 x 6144 in 4 bits 6.5 us; 0.9 more through shared memory as below)
         int yw, yc;
         __nv_bfloat16* const y = segment(p, m0, yw, yc) + (int64_t)n0 * yw + yc + (feature & ~1);
         const bool odd = lane & 1;

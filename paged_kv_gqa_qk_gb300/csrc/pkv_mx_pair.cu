@@ -17,9 +17,10 @@
 // of the even CTA issues a stage's four products.  Two groups of four warps write y in bf16
 // through shared memory with TMA, an accumulator each.
 //
-// Measured (of four and two times the measured bf16 rate): 8192 x 4096 x 6144 in 4 bits 62 us, 6.6
-// PFLOP/s (0.88), in 8 bits 122 us, 3.4 (0.9); 2048 tokens 20.8 and 34.3 us; 4096 x 8192 x 8192 79
-// and 173.  A call's start and end take some 7 us in all of them.
+// Measured (of four and two times the measured bf16 rate, which instructions of K = 64 and 32 give; those of
+// K = 96 that 4 bits have besides are not used here): 8192 x 4096 x 6144 in 4 bits 62 us, 6.6 PFLOP/s (0.88), in 8
+// bits 123 us, 3.4 (0.89); 2048 tokens 20.9 and 34.3 us; 4096 x 8192 x 8192 79 and 169.  For a second on end, under the
+// power cap, in 8 bits 130 to 138 and 183 to 195.  A call's start and end take some 7 us in all of them.
 #include <atomic>
 
 #include "pkv_mx.cuh"

@@ -721,7 +721,7 @@ class _Pool:
     def add_norm(self, x, residual, w, out="mx8", residual_out=None, stream=None):
         """The residual's addition and a layer's RMS norm: (out, residual_out) with residual_out = x + residual and out its
         norm.  out: a bf16 tensor or an MxTensor, or the kind of a new one ("bf16", "mx8", "mx4").  residual None: the
-        norm of x, and no residual_out.  residual_out may be residual itself."""
+        norm of x, and no residual_out.  residual_out may be residual itself.  eps is the pool's (cfg)."""
         if isinstance(out, str):
             with _on(stream):
                 out = torch.empty(x.shape, dtype=_BF16, device=x.device) if out == "bf16" else \

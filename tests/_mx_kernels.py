@@ -49,6 +49,7 @@ FEW = [
     ((50, 4224, 1024), (64, 8)), ((50, 4096, 4096), (64, 4)), ((50, 1152, 6144), (64, 2)), ((50, 640, 12800), (64, 1)),
     ((1, 4096, 20480), (16, 1)), ((20, 4096, 20480), (32, 1)), ((40, 4096, 20480), (64, 1)),  # a ring used again, more tiles than SMs
     ((300, 4096, 1280), (64, 2)),
+    ((1, 12288, 4096), (16, 4)), ((20, 4096, 24576), (32, 1)),  # an MLP's widths
 ]
 MANY = [
     ((49, 640, 19584), PAIRS),      # the odd CTA of a pair wholly beyond the tokens; a 4-bit row of two stages and a half
@@ -59,5 +60,6 @@ MANY = [
     ((1025, 4096, 3200), PAIRS),    # features of a tile and a third
     ((700, 16512, 2048), PAIRS),    # a long row
     ((2048, 8192, 1280), PAIRS),
+    ((64, 4096, 24576), PAIRS), ((300, 12288, 4096), PAIRS),  # an MLP's widths
     ((5000, 384, 384), PAIRS),      # many tiles a pair, a stage and a half each in 4 bits
 ]
